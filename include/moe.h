@@ -113,7 +113,8 @@ const char *moe_status_string(int32_t status);
 const char *moe_last_error_string(void);
 
 /* ABI version: major * 10000 + minor * 100 + patch.  2.0.0 made y_perm of
- * bf16 layers fp16 (it was fp32 in 1.x). */
+ * bf16 layers fp16 (it was fp32 in 1.x); 2.1.0 added the MXFP4 calls and the
+ * gradients of the permute and combine steps. */
 int32_t moe_abi_version(void);
 
 /*
@@ -364,6 +365,40 @@ moe_status moe_layer_backward_ex(const moe_config *cfg, const void *x, const voi
                                  moe_stream_t stream);
 
 /*
+ * Gradients of the data-movement steps, for a caller that has its own experts
+ * (or a shard of them) between moe_permute and moe_unpermute_combine; the
+ * whole layer's gradient is moe_layer_backward ("Expert Parallelism (EP)",
+ * section 5: the combine's backward is a dispatch, the dispatch's a combine).
+ * Both take row_of [T, k] as the permute wrote it (each row at most once, -1:
+ * no row), any layout, expert range and dtype that the steps take.  Sums run
+ * in a fixed order: results are bit-identical run to run.  Rows outside
+ * [-1, rows_alloc) flag MOE_ERR_BAD_ROUTING and count as -1.
+ *
+ * moe_unpermute_combine_backward: for out[t] = sum_j topk_w[t, j]
+ * y_perm[row_of[t, j]] and dout [T, D] (dtype),
+ *   dy_perm[row_of[t, j], :] = topk_w[t, j] dout[t, :]   [rows_alloc, D] (dtype,
+ *     rounded once; rows that hold no token are not written),
+ *   dtopk_w[t, j] = <dout[t], y_perm[row_of[t, j]]>      [T, k] fp32 (0 for -1).
+ * y_perm [rows_alloc, D] as moe_unpermute_combine takes it (fp32, or fp16 for
+ * MOE_BF16).
+ */
+moe_status moe_unpermute_combine_backward(const moe_config *cfg, const void *dout,
+                                          const void *y_perm, const int32_t *row_of,
+                                          const float *topk_w, void *dy_perm, float *dtopk_w,
+                                          void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * moe_permute_backward: for x_perm[row_of[t, j]] = x[t],
+ *   dx[t, :] = sum_{j, row_of[t,j] >= 0} dx_perm[row_of[t, j], :]
+ * in fp32 in slot order, rounded once to dtype; dx [T, D] (zeros for a token
+ * without a row).  dx_perm [rows_alloc, D] is dx_perm_dtype: MOE_F32, or
+ * MOE_BF16 in a bf16 config (else MOE_ERR_UNSUPPORTED).
+ */
+moe_status moe_permute_backward(const moe_config *cfg, const void *dx_perm, int32_t dx_perm_dtype,
+                                const int32_t *row_of, void *dx, void *ws, size_t ws_bytes,
+                                moe_stream_t stream);
+
+/*
  * FP8 e4m3 dispatch (page "Expert Parallelism (EP)", llm-infra-atlas: the FP8
  * dispatch of its next steps -- dispatched activations as e4m3 values with
  * scales feeding an FP8 grouped GEMM).  The page does not fix the scale
@@ -428,6 +463,78 @@ moe_status moe_layer_forward_fp8(const moe_config *cfg, const void *x, const voi
                                  const float *bias, const uint8_t *w1_q, const float *w1_scale,
                                  const uint8_t *w3_q, const float *w3_scale, const void *w2,
                                  void *out, void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * MXFP4: microscaled 4-bit floating point (Open Compute Project, "OCP
+ * Microscaling Formats (MX) Specification" 1.0; no counterpart in the pages).
+ * 32 consecutive values of a row share a scale: byte b of `scale` stands for
+ * 2^(b - 127) (e8m0; 255 is NaN), and each value is an e2m1 code, 0, 0.5, 1,
+ * 1.5, 2, 3, 4 or 6 with a sign, two to a byte (the even column in the low
+ * half).  A block with largest magnitude m gets the scale 2^e, e =
+ * max(floor(log2 m) - 2, -127), and the codes of v 2^-e to nearest, ties to the
+ * even code, saturating at 6 (so values in (6, 8) 2^e become 6 2^e).  A block
+ * that holds a NaN or an infinity gets scale 255 and codes 0: its 32 values
+ * read back as NaN.  Codes and scales are exact functions of the input.
+ *
+ * moe_quantize_rows_mxfp4: src [rows, cols] of src_dtype (MOE_F32 or MOE_BF16),
+ * cols a multiple of 32, into codes dst [rows, cols / 2] and scale
+ * [rows, cols / 32] (uint8 both): the form the MXFP4 calls take w1 and w3
+ * (rows = E_local * H_local, cols = D) and w2 (E_local * D, H_local) in.
+ * moe_dequantize_rows_mxfp4: the values back, in dst_dtype; both types hold
+ * every value that the quantiser writes exactly.  Device pointers, 16-byte
+ * aligned.
+ */
+moe_status moe_quantize_rows_mxfp4(const void *src, int32_t src_dtype, int64_t rows, int32_t cols,
+                                   uint8_t *dst, uint8_t *scale, moe_stream_t stream);
+moe_status moe_dequantize_rows_mxfp4(const uint8_t *codes, const uint8_t *scale, int64_t rows,
+                                     int32_t cols, void *dst, int32_t dst_dtype,
+                                     moe_stream_t stream);
+
+/*
+ * moe_permute with the dispatched rows quantised to MXFP4: x [T, D] bf16 in;
+ * x_perm_q [rows_alloc, D / 2] codes and x_scale [rows_alloc, D / 32] scales
+ * out (rows that hold no token are not written).  Counts, offsets, row_of and
+ * token_of_row exactly as moe_permute.  Requires dtype MOE_BF16, and D and
+ * H_local multiples of 32 (else MOE_ERR_UNSUPPORTED).
+ */
+moe_status moe_permute_mxfp4(const moe_config *cfg, const void *x, const int32_t *topk_idx,
+                             int32_t *tokens_per_expert, int32_t *seg_offsets, int32_t *row_of,
+                             int32_t *token_of_row, uint8_t *x_perm_q, uint8_t *x_scale, void *ws,
+                             size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * moe_grouped_swiglu with both GEMMs on MXFP4 operands (fp32 accumulation):
+ *   g = x w1^T, u = x w3^T on the values of the codes,
+ *   h = MXFP4(SiLU(g) u)  (the fp32 result, quantised in blocks of 32 hidden
+ *       units as moe_quantize_rows_mxfp4 does),  y_perm = fp16(h w2^T).
+ * x_perm_q / x_scale as moe_permute_mxfp4 writes them; w1_q, w3_q
+ * [E_local, H_local, D / 2] with w1_scale, w3_scale [E_local, H_local, D / 32],
+ * w2_q [E_local, D, H_local / 2] with w2_scale [E_local, D, H_local / 32];
+ * h_q [rows_alloc, H_local / 2], h_scale [rows_alloc, H_local / 32] and y_perm
+ * fp16 [rows_alloc, D], written for valid rows only.  Same segments, range
+ * check (|y| >= 65520: MOE_ERR_UNSUPPORTED) and requirements as
+ * moe_grouped_swiglu and moe_permute_mxfp4.
+ */
+moe_status moe_grouped_swiglu_mxfp4(const moe_config *cfg, const uint8_t *x_perm_q,
+                                    const uint8_t *x_scale, const int32_t *seg_offsets,
+                                    const int32_t *tokens_per_expert, const uint8_t *w1_q,
+                                    const uint8_t *w1_scale, const uint8_t *w3_q,
+                                    const uint8_t *w3_scale, const uint8_t *w2_q,
+                                    const uint8_t *w2_scale, uint8_t *h_q, uint8_t *h_scale,
+                                    void *y_perm, void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * moe_layer_forward with MXFP4 experts: route (bf16 x, fp32 keys, as
+ * moe_route_topk), moe_permute_mxfp4, moe_grouped_swiglu_mxfp4 and the combine,
+ * on one stream.  Workspace: moe_layer_workspace_size (codes and scales lie in
+ * the x_perm and h buffers).
+ */
+moe_status moe_layer_forward_mxfp4(const moe_config *cfg, const void *x, const void *wg,
+                                   const float *bias, const uint8_t *w1_q,
+                                   const uint8_t *w1_scale, const uint8_t *w3_q,
+                                   const uint8_t *w3_scale, const uint8_t *w2_q,
+                                   const uint8_t *w2_scale, void *out, void *ws, size_t ws_bytes,
+                                   moe_stream_t stream);
 
 /*
  * moe_layer_forward with the combine fused into the grouped GEMM's second

@@ -38,6 +38,9 @@ ABI_SYMBOLS = (
     "moe_host_pipeline_workspace_size", "moe_host_pipeline_create", "moe_host_pipeline_submit",
     "moe_host_pipeline_sync", "moe_host_pipeline_destroy",
     "moe_permute_index", "moe_grouped_swiglu_gather", "moe_layer_forward_gather",
+    "moe_quantize_rows_mxfp4", "moe_dequantize_rows_mxfp4", "moe_permute_mxfp4",
+    "moe_grouped_swiglu_mxfp4", "moe_layer_forward_mxfp4",
+    "moe_unpermute_combine_backward", "moe_permute_backward",
 )
 
 
@@ -96,6 +99,13 @@ def _load() -> ctypes.CDLL:
         "moe_permute_index": (I32, [C, P, P, P, P, P, P, SZ, P]),
         "moe_grouped_swiglu_gather": (I32, [C, P, P, P, P, P, P, P, P, P, P, SZ, P]),
         "moe_layer_forward_gather": (I32, [C, P, P, P, P, P, P, P, P, SZ, P]),
+        "moe_quantize_rows_mxfp4": (I32, [P, I32, I64, I32, P, P, P]),
+        "moe_dequantize_rows_mxfp4": (I32, [P, P, I64, I32, P, I32, P]),
+        "moe_permute_mxfp4": (I32, [C, P, P, P, P, P, P, P, P, P, SZ, P]),
+        "moe_grouped_swiglu_mxfp4": (I32, [C, P, P, P, P, P, P, P, P, P, P, P, P, P, P, SZ, P]),
+        "moe_layer_forward_mxfp4": (I32, [C, P, P, P, P, P, P, P, P, P, P, P, SZ, P]),
+        "moe_unpermute_combine_backward": (I32, [C, P, P, P, P, P, P, P, SZ, P]),
+        "moe_permute_backward": (I32, [C, P, I32, P, P, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -584,6 +594,149 @@ def moe_layer_forward_fp8(cfg: Config, x, wg, bias, w1_q, w1_scale, w3_q, w3_sca
                                       _ptr(w1_scale), _ptr(w3_q), _ptr(w3_scale), _ptr(w2),
                                       _ptr(out), _ptr(ws), ws.numel(), _stream(stream)),
            "moe_layer_forward_fp8")
+
+
+def _mx_tensor(t, name):
+    if t.dtype not in (torch.bfloat16, torch.float32) or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous bf16 or fp32 CUDA tensor")
+    if t.dim() == 0 or t.shape[-1] % 32:
+        raise ValueError(f"{name}: rows of a multiple of 32 values")
+    cols = t.shape[-1]
+    return (t.numel() // cols if cols else 0), cols
+
+
+def moe_quantize_rows_mxfp4(src, dst, scale, stream=None):
+    """MXFP4 codes and e8m0 scales of a bf16 or fp32 tensor viewed as [rows, cols]:
+    dst [..., cols / 2] and scale [..., cols / 32], both uint8."""
+    rows, cols = _mx_tensor(src, "src")
+    _expect(dst, (*src.shape[:-1], cols // 2), torch.uint8, "dst")
+    _expect(scale, (*src.shape[:-1], cols // 32), torch.uint8, "scale")
+    if rows == 0:
+        return
+    _check(_lib.moe_quantize_rows_mxfp4(_ptr(src), MOE_BF16 if src.dtype == torch.bfloat16 else MOE_F32,
+                                        rows, cols, _ptr(dst), _ptr(scale), _stream(stream)),
+           "moe_quantize_rows_mxfp4")
+
+
+def moe_dequantize_rows_mxfp4(codes, scale, dst, stream=None):
+    """The values of MXFP4 codes [..., cols / 2] with scales [..., cols / 32] into a
+    bf16 or fp32 dst [..., cols]."""
+    rows, cols = _mx_tensor(dst, "dst")
+    _expect(codes, (*dst.shape[:-1], cols // 2), torch.uint8, "codes")
+    _expect(scale, (*dst.shape[:-1], cols // 32), torch.uint8, "scale")
+    if rows == 0:
+        return
+    _check(_lib.moe_dequantize_rows_mxfp4(_ptr(codes), _ptr(scale), rows, cols, _ptr(dst),
+                                          MOE_BF16 if dst.dtype == torch.bfloat16 else MOE_F32,
+                                          _stream(stream)), "moe_dequantize_rows_mxfp4")
+
+
+def quantize_weights_mxfp4(w, stream=None):
+    """(codes [..., cols / 2], scales [..., cols / 32]), uint8, of a weight such as
+    w1 [E, H, D] or w2 [E, D, H] (bf16 or fp32; blocks along the last dimension)."""
+    cols = w.shape[-1]
+    q = torch.empty((*w.shape[:-1], cols // 2), dtype=torch.uint8, device=w.device)
+    sc = torch.empty((*w.shape[:-1], cols // 32), dtype=torch.uint8, device=w.device)
+    moe_quantize_rows_mxfp4(w, q, sc, stream)
+    return q, sc
+
+
+def moe_permute_mxfp4(cfg: Config, x, topk_idx, tokens_per_expert, seg_offsets, row_of,
+                      token_of_row, x_perm_q, x_scale, ws, stream=None):
+    """moe_permute with the rows quantised: x_perm_q [rows, D / 2], x_scale [rows, D / 32]."""
+    ra = rows_alloc(cfg)
+    _expect(x, (cfg.T, cfg.D), torch.bfloat16, "x")
+    _expect(topk_idx, (cfg.T, cfg.k), torch.int32, "topk_idx")
+    _expect(tokens_per_expert, (cfg.E,), torch.int32, "tokens_per_expert")
+    _expect(seg_offsets, (cfg.e_local + 1,), torch.int32, "seg_offsets")
+    _expect(row_of, (cfg.T, cfg.k), torch.int32, "row_of")
+    _expect(token_of_row, (ra,), torch.int32, "token_of_row")
+    _expect(x_perm_q, (ra, cfg.D // 2), torch.uint8, "x_perm_q")
+    _expect(x_scale, (ra, cfg.D // 32), torch.uint8, "x_scale")
+    c = cfg.c()
+    _check(_lib.moe_permute_mxfp4(ctypes.byref(c), _ptr(x), _ptr(topk_idx), _ptr(tokens_per_expert),
+                                  _ptr(seg_offsets), _ptr(row_of), _ptr(token_of_row),
+                                  _ptr(x_perm_q), _ptr(x_scale), _ptr(ws), ws.numel(),
+                                  _stream(stream)), "moe_permute_mxfp4")
+
+
+def _expect_mx_weights(cfg: Config, w1_q, w1_scale, w3_q, w3_scale, w2_q, w2_scale):
+    el, D, H = cfg.e_local, cfg.D, cfg.H_local
+    for t, sf, n, m, name in ((w1_q, w1_scale, H, D, "w1"), (w3_q, w3_scale, H, D, "w3"),
+                              (w2_q, w2_scale, D, H, "w2")):
+        _expect(t, (el, n, m // 2), torch.uint8, name + "_q")
+        _expect(sf, (el, n, m // 32), torch.uint8, name + "_scale")
+
+
+def moe_grouped_swiglu_mxfp4(cfg: Config, x_perm_q, x_scale, seg_offsets, tokens_per_expert, w1_q,
+                             w1_scale, w3_q, w3_scale, w2_q, w2_scale, h_q, h_scale, y_perm, ws,
+                             stream=None):
+    ra = rows_alloc(cfg)
+    _expect(x_perm_q, (ra, cfg.D // 2), torch.uint8, "x_perm_q")
+    _expect(x_scale, (ra, cfg.D // 32), torch.uint8, "x_scale")
+    _expect(seg_offsets, (cfg.e_local + 1,), torch.int32, "seg_offsets")
+    _expect(tokens_per_expert, (cfg.E,), torch.int32, "tokens_per_expert")
+    _expect_mx_weights(cfg, w1_q, w1_scale, w3_q, w3_scale, w2_q, w2_scale)
+    _expect(h_q, (ra, cfg.H_local // 2), torch.uint8, "h_q")
+    _expect(h_scale, (ra, cfg.H_local // 32), torch.uint8, "h_scale")
+    _expect(y_perm, (ra, cfg.D), torch.float16, "y_perm")
+    c = cfg.c()
+    _check(_lib.moe_grouped_swiglu_mxfp4(ctypes.byref(c), _ptr(x_perm_q), _ptr(x_scale),
+                                         _ptr(seg_offsets), _ptr(tokens_per_expert), _ptr(w1_q),
+                                         _ptr(w1_scale), _ptr(w3_q), _ptr(w3_scale), _ptr(w2_q),
+                                         _ptr(w2_scale), _ptr(h_q), _ptr(h_scale), _ptr(y_perm),
+                                         _ptr(ws), ws.numel(), _stream(stream)),
+           "moe_grouped_swiglu_mxfp4")
+
+
+def moe_layer_forward_mxfp4(cfg: Config, x, wg, bias, w1_q, w1_scale, w3_q, w3_scale, w2_q,
+                            w2_scale, out, ws, stream=None):
+    """moe_layer_forward with MXFP4 expert weights (see quantize_weights_mxfp4)."""
+    _expect(x, (cfg.T, cfg.D), torch.bfloat16, "x")
+    _expect(wg, (cfg.E, cfg.D), torch.bfloat16, "wg")
+    if bias is not None:
+        _expect(bias, (cfg.E,), torch.float32, "bias")
+    _expect_mx_weights(cfg, w1_q, w1_scale, w3_q, w3_scale, w2_q, w2_scale)
+    _expect(out, (cfg.T, cfg.D), torch.bfloat16, "out")
+    c = cfg.c()
+    _check(_lib.moe_layer_forward_mxfp4(ctypes.byref(c), _ptr(x), _ptr(wg), _ptr(bias), _ptr(w1_q),
+                                        _ptr(w1_scale), _ptr(w3_q), _ptr(w3_scale), _ptr(w2_q),
+                                        _ptr(w2_scale), _ptr(out), _ptr(ws), ws.numel(),
+                                        _stream(stream)), "moe_layer_forward_mxfp4")
+
+
+def moe_unpermute_combine_backward(cfg: Config, dout, y_perm, row_of, topk_w, dy_perm, dtopk_w, ws,
+                                   stream=None):
+    """Gradients of moe_unpermute_combine: dy_perm [rows, D] (rows that hold no token
+    are not written) and dtopk_w [T, k]."""
+    ra = rows_alloc(cfg)
+    _expect(dout, (cfg.T, cfg.D), cfg.torch_dtype, "dout")
+    _expect(y_perm, (ra, cfg.D), cfg.y_dtype, "y_perm")
+    _expect(row_of, (cfg.T, cfg.k), torch.int32, "row_of")
+    _expect(topk_w, (cfg.T, cfg.k), torch.float32, "topk_w")
+    _expect(dy_perm, (ra, cfg.D), cfg.torch_dtype, "dy_perm")
+    _expect(dtopk_w, (cfg.T, cfg.k), torch.float32, "dtopk_w")
+    c = cfg.c()
+    _check(_lib.moe_unpermute_combine_backward(ctypes.byref(c), _ptr(dout), _ptr(y_perm),
+                                               _ptr(row_of), _ptr(topk_w), _ptr(dy_perm),
+                                               _ptr(dtopk_w), _ptr(ws), ws.numel(),
+                                               _stream(stream)), "moe_unpermute_combine_backward")
+
+
+def moe_permute_backward(cfg: Config, dx_perm, row_of, dx, ws, stream=None):
+    """Gradient of moe_permute: dx [T, D] from dx_perm [rows, D] (fp32, or bf16 in a
+    bf16 config)."""
+    ra = rows_alloc(cfg)
+    if dx_perm.dtype not in (torch.float32, cfg.torch_dtype):
+        raise ValueError(f"dx_perm: expected float32 or {cfg.torch_dtype}, got {dx_perm.dtype}")
+    _expect(dx_perm, (ra, cfg.D), dx_perm.dtype, "dx_perm")
+    _expect(row_of, (cfg.T, cfg.k), torch.int32, "row_of")
+    _expect(dx, (cfg.T, cfg.D), cfg.torch_dtype, "dx")
+    c = cfg.c()
+    _check(_lib.moe_permute_backward(ctypes.byref(c), _ptr(dx_perm),
+                                     MOE_BF16 if dx_perm.dtype == torch.bfloat16 else MOE_F32,
+                                     _ptr(row_of), _ptr(dx), _ptr(ws), ws.numel(),
+                                     _stream(stream)), "moe_permute_backward")
 
 
 def moe_grouped_swiglu_gather(cfg: Config, x, token_of_row, seg_offsets, tokens_per_expert, w1,

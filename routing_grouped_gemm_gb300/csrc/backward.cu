@@ -41,10 +41,11 @@ __device__ __forceinline__ void load4(const void *p, size_t i, bool bf16, float 
     }
 }
 
-// One warp per token.  gy[row] = bf16(w_j * dout[t]) for each slot j whose
-// row is in the buffer; dw[t, j] = <dout[t], y_perm[row]> (y_perm fp16, the
-// products and sums fp32: each lane sums its columns in order, then the
-// lanes' sums are added in a fixed butterfly order), 0 for a slot without row.
+// One warp per token.  gy[row] = w_j * dout[t], rounded once to the layer's
+// type, for each slot j whose row is in the buffer; dw[t, j] = <dout[t],
+// y_perm[row]> (y_perm fp16 in a bf16 layer, the products and sums fp32: each
+// lane sums its columns in order, then the lanes' sums are added in a fixed
+// butterfly order), 0 for a slot without row.
 // Blocks per SM the register budget is capped for: 8 (64 registers, no
 // spills) puts one block per 4 tokens of the fine-grained batch (1024 blocks)
 // in a single wave of 152 SMs; uncapped (134 registers) 3 blocks per SM fit.
@@ -63,10 +64,12 @@ static_assert(CBW_VEC == 4 || CBW_VEC == 8, "4 or 8 elements per lane");
 using CbwVec = std::conditional_t<CBW_VEC == 8, uint4, uint2>;
 template <bool BF16>
 __global__ void __launch_bounds__(128, MOE_COMBINE_BWD_MINB)
-combine_bwd_kernel(const void *__restrict__ dout, const __half *__restrict__ y_perm,
+combine_bwd_kernel(const void *__restrict__ dout, const void *__restrict__ y_perm_,
                    const int *__restrict__ row_of, const float *__restrict__ topk_w,
-                   __nv_bfloat16 *__restrict__ gy, float *__restrict__ dw, int T, int k, int D,
+                   void *__restrict__ gy_, float *__restrict__ dw, int T, int k, int D,
                    long long rows_alloc, int *status) {
+    const __half *y_perm = static_cast<const __half *>(y_perm_);
+    __nv_bfloat16 *gy = static_cast<__nv_bfloat16 *>(gy_);
     griddep_launch_dependents();  // the next kernel may be scheduled now
     griddep_wait();               // every input of this kernel is complete
     const int t = (int)(((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5);
@@ -93,39 +96,68 @@ combine_bwd_kernel(const void *__restrict__ dout, const __half *__restrict__ y_p
             if (j >= k) r[u] = -1;
             dot[u] = 0.f;
         }
-        for (int d0 = lane * CBW_VEC; d0 < D; d0 += 32 * CBW_VEC) {
-            float g[CBW_VEC];
-            {
-                float g4[4];
+        if constexpr (!BF16) {
+            const float *yf = static_cast<const float *>(y_perm_);
+            float *gf = static_cast<float *>(gy_);
+            for (int d0 = lane * 4; d0 < D; d0 += 128) {
+                const float4 g = *reinterpret_cast<const float4 *>(
+                    static_cast<const float *>(dout) + (size_t)t * D + d0);
+                // half of the slots at a time: 16-byte pieces, the same bytes in flight
 #pragma unroll
-                for (int q = 0; q < CBW_VEC / 4; ++q) {
-                    load4(dout, (size_t)t * D + d0 + 4 * q, BF16, g4);
+                for (int h = 0; h < BW_SLOTS; h += BW_SLOTS / 2) {
+                    float4 y[BW_SLOTS / 2];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) g[4 * q + i] = g4[i];
+                    for (int u = 0; u < BW_SLOTS / 2; ++u)
+                        if (r[h + u] >= 0)
+                            y[u] = __ldcs(reinterpret_cast<const float4 *>(yf + (size_t)r[h + u] * D + d0));
+#pragma unroll
+                    for (int u = 0; u < BW_SLOTS / 2; ++u) {
+                        if (r[h + u] < 0) continue;
+                        dot[h + u] = fmaf(g.x, y[u].x, dot[h + u]);
+                        dot[h + u] = fmaf(g.y, y[u].y, dot[h + u]);
+                        dot[h + u] = fmaf(g.z, y[u].z, dot[h + u]);
+                        dot[h + u] = fmaf(g.w, y[u].w, dot[h + u]);
+                        const float wj = w[h + u];
+                        *reinterpret_cast<float4 *>(gf + (size_t)r[h + u] * D + d0) =
+                            make_float4(wj * g.x, wj * g.y, wj * g.z, wj * g.w);
+                    }
                 }
             }
-            CbwVec y[BW_SLOTS];
+        } else {
+            for (int d0 = lane * CBW_VEC; d0 < D; d0 += 32 * CBW_VEC) {
+                float g[CBW_VEC];
+                {
+                    float g4[4];
 #pragma unroll
-            for (int u = 0; u < BW_SLOTS; ++u)
-                if (r[u] >= 0)
-                    y[u] = __ldcs(reinterpret_cast<const CbwVec *>(y_perm + (size_t)r[u] * D + d0));
+                    for (int q = 0; q < CBW_VEC / 4; ++q) {
+                        load4(dout, (size_t)t * D + d0 + 4 * q, BF16, g4);
 #pragma unroll
-            for (int u = 0; u < BW_SLOTS; ++u) {
-                if (r[u] < 0) continue;
-                const __half2 *yh = reinterpret_cast<const __half2 *>(&y[u]);
-                uint32_t ow[CBW_VEC / 2];
-#pragma unroll
-                for (int i = 0; i < CBW_VEC / 2; ++i) {
-                    const float2 f = __half22float2(yh[i]);
-                    dot[u] = fmaf(g[2 * i], f.x, dot[u]);
-                    dot[u] = fmaf(g[2 * i + 1], f.y, dot[u]);
-                    __nv_bfloat162 b = __floats2bfloat162_rn(w[u] * g[2 * i], w[u] * g[2 * i + 1]);
-                    ow[i] = *reinterpret_cast<uint32_t *>(&b);
+                        for (int i = 0; i < 4; ++i) g[4 * q + i] = g4[i];
+                    }
                 }
-                if constexpr (CBW_VEC == 8)
-                    *reinterpret_cast<uint4 *>(gy + (size_t)r[u] * D + d0) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
-                else
-                    *reinterpret_cast<uint2 *>(gy + (size_t)r[u] * D + d0) = make_uint2(ow[0], ow[1]);
+                CbwVec y[BW_SLOTS];
+#pragma unroll
+                for (int u = 0; u < BW_SLOTS; ++u)
+                    if (r[u] >= 0)
+                        y[u] = __ldcs(reinterpret_cast<const CbwVec *>(y_perm + (size_t)r[u] * D + d0));
+#pragma unroll
+                for (int u = 0; u < BW_SLOTS; ++u) {
+                    if (r[u] < 0) continue;
+                    const __half2 *yh = reinterpret_cast<const __half2 *>(&y[u]);
+                    uint32_t ow[CBW_VEC / 2];
+#pragma unroll
+                    for (int i = 0; i < CBW_VEC / 2; ++i) {
+                        const float2 f = __half22float2(yh[i]);
+                        dot[u] = fmaf(g[2 * i], f.x, dot[u]);
+                        dot[u] = fmaf(g[2 * i + 1], f.y, dot[u]);
+                        __nv_bfloat162 b = __floats2bfloat162_rn(w[u] * g[2 * i], w[u] * g[2 * i + 1]);
+                        ow[i] = *reinterpret_cast<uint32_t *>(&b);
+                    }
+                    if constexpr (CBW_VEC == 8)
+                        *reinterpret_cast<uint4 *>(gy + (size_t)r[u] * D + d0) = make_uint4(ow[0], ow[1], ow[2], ow[3]);
+                    else
+                        *reinterpret_cast<uint2 *>(gy + (size_t)r[u] * D + d0) = make_uint2(ow[0], ow[1]);
+                }
             }
         }
 #pragma unroll
@@ -140,13 +172,14 @@ combine_bwd_kernel(const void *__restrict__ dout, const __half *__restrict__ y_p
 
 // One warp per token: dx[t] = sum_j dxp[row_of[t, j]] + r[t], fp32 in slot
 // order, rounded once to the output type; r[t] = add[t] when add, else (wg
-// given) sum_j dl[t, e_j] wg[e_j] in slot order.
-template <bool BF16>
+// given) sum_j dl[t, e_j] wg[e_j] in slot order.  PBF16: dxp is bf16.
+template <bool BF16, bool PBF16>
 __global__ void __launch_bounds__(128)
-dispatch_bwd_kernel(const float *__restrict__ dxp, const int *__restrict__ row_of,
+dispatch_bwd_kernel(const void *__restrict__ dxp, const int *__restrict__ row_of,
                     const float *__restrict__ add, const int *__restrict__ topk_idx,
                     const float *__restrict__ dl, const void *__restrict__ wg, int E,
-                    void *__restrict__ dx, int T, int k, int D, long long rows_alloc) {
+                    void *__restrict__ dx, int T, int k, int D, long long rows_alloc,
+                    int *status) {
     griddep_launch_dependents();  // the next kernel may be scheduled now
     griddep_wait();               // every input of this kernel is complete
     const int t = (int)(((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5);
@@ -157,35 +190,51 @@ dispatch_bwd_kernel(const float *__restrict__ dxp, const int *__restrict__ row_o
     float my_g = 0.f;
     if (lane < k) {
         my_r = row_of[(size_t)t * k + lane];
-        if (my_r < 0 || (long long)my_r >= rows_alloc) my_r = -1;
+        if (my_r < -1 || (long long)my_r >= rows_alloc) {
+            raise_flag(status, FLAG_BAD_ROUTING);
+            my_r = -1;
+        }
         if (!add && wg) {
             my_e = topk_idx[(size_t)t * k + lane];
             if (my_e < 0 || my_e >= E) my_e = -1;
             else my_g = dl[(size_t)t * E + my_e];
         }
     }
-    for (int d0 = lane * 4; d0 < D; d0 += 128) {
+    // the shuffles need every lane: the loop is uniform, lanes past the row's
+    // end load and store nothing
+    for (int b0 = 0; b0 < D; b0 += 128) {
+        const int d0 = b0 + lane * 4;
+        const bool in = d0 < D;
         float a[4] = {0.f, 0.f, 0.f, 0.f};
         for (int j0 = 0; j0 < k; j0 += DB_SLOTS) {
             int r[DB_SLOTS];
-            float4 v[DB_SLOTS];
+            using Piece = std::conditional_t<PBF16, uint2, float4>;
+            using Elem = std::conditional_t<PBF16, __nv_bfloat16, float>;
+            Piece v[DB_SLOTS];
 #pragma unroll
             for (int u = 0; u < DB_SLOTS; ++u) {
                 r[u] = __shfl_sync(0xffffffffu, my_r, (j0 + u) & 31);
-                if (j0 + u >= k) r[u] = -1;
+                if (j0 + u >= k || !in) r[u] = -1;
                 if (r[u] >= 0)
-                    v[u] = __ldcs(reinterpret_cast<const float4 *>(dxp + (size_t)r[u] * D + d0));
+                    v[u] = __ldcs(reinterpret_cast<const Piece *>(static_cast<const Elem *>(dxp) +
+                                                                  (size_t)r[u] * D + d0));
             }
 #pragma unroll
             for (int u = 0; u < DB_SLOTS; ++u) {
                 if (r[u] < 0) continue;
-                a[0] += v[u].x; a[1] += v[u].y; a[2] += v[u].z; a[3] += v[u].w;
+                if constexpr (PBF16) {
+                    const __nv_bfloat162 *h2 = reinterpret_cast<const __nv_bfloat162 *>(&v[u]);
+                    a[0] += __low2float(h2[0]); a[1] += __high2float(h2[0]);
+                    a[2] += __low2float(h2[1]); a[3] += __high2float(h2[1]);
+                } else {
+                    a[0] += v[u].x; a[1] += v[u].y; a[2] += v[u].z; a[3] += v[u].w;
+                }
             }
         }
-        if (add) {
+        if (add && in) {
             const float4 v = *reinterpret_cast<const float4 *>(add + (size_t)t * D + d0);
             a[0] += v.x; a[1] += v.y; a[2] += v.z; a[3] += v.w;
-        } else if (wg) {
+        } else if (!add && wg) {
             for (int j0 = 0; j0 < k; j0 += DB_SLOTS) {
                 int e[DB_SLOTS];
                 float g[DB_SLOTS], w[DB_SLOTS][4];
@@ -193,7 +242,7 @@ dispatch_bwd_kernel(const float *__restrict__ dxp, const int *__restrict__ row_o
                 for (int u = 0; u < DB_SLOTS; ++u) {
                     e[u] = __shfl_sync(0xffffffffu, my_e, (j0 + u) & 31);
                     g[u] = __shfl_sync(0xffffffffu, my_g, (j0 + u) & 31);
-                    if (j0 + u >= k) e[u] = -1;
+                    if (j0 + u >= k || !in) e[u] = -1;
                     if (e[u] >= 0) load4(wg, (size_t)e[u] * D + d0, BF16, w[u]);
                 }
 #pragma unroll
@@ -204,6 +253,7 @@ dispatch_bwd_kernel(const float *__restrict__ dxp, const int *__restrict__ row_o
                 }
             }
         }
+        if (!in) continue;
         if (BF16) {
             __nv_bfloat162 lo = __floats2bfloat162_rn(a[0], a[1]);
             __nv_bfloat162 hi = __floats2bfloat162_rn(a[2], a[3]);
@@ -540,30 +590,29 @@ cudaError_t launch_combine_bwd(const void *dout, const void *y_perm, const int *
                                const float *topk_w, void *gy, float *dw, int T, int D, int k,
                                int64_t rows_alloc, int is_bf16, int *status, cudaStream_t stream) {
     if (T == 0) return cudaSuccess;
-    const dim3 grid((unsigned)((T + 3) / 4));  // 4 warps (tokens) per block
+    const dim3 grid((unsigned)((T + 3LL) / 4));  // 4 warps (tokens) per block
     const cudaError_t e =
-        is_bf16 ? launch_pdl(combine_bwd_kernel<true>, grid, dim3(128), 0, stream, dout,
-                             (const __half *)y_perm, row_of, topk_w, (__nv_bfloat16 *)gy, dw, T, k, D, (long long)rows_alloc,
-                             status)
-                : launch_pdl(combine_bwd_kernel<false>, grid, dim3(128), 0, stream, dout,
-                             (const __half *)y_perm, row_of, topk_w, (__nv_bfloat16 *)gy, dw, T, k, D, (long long)rows_alloc,
-                             status);
+        launch_pdl(is_bf16 ? combine_bwd_kernel<true> : combine_bwd_kernel<false>, grid, dim3(128),
+                   0, stream, dout, y_perm, row_of, topk_w, gy, dw, T, k, D, (long long)rows_alloc,
+                   status);
     if (e == cudaSuccess) count_launch();
     return e;
 }
 
-cudaError_t launch_dispatch_bwd(const float *dxp, const int *row_of, const float *add,
+cudaError_t launch_dispatch_bwd(const void *dxp, int dxp_bf16, const int *row_of, const float *add,
                                 const int *topk_idx, const float *dl, const void *wg, int E,
                                 void *dx, int T, int D, int k, int64_t rows_alloc, int is_bf16,
-                                cudaStream_t stream) {
+                                int *status, cudaStream_t stream) {
     if (T == 0) return cudaSuccess;
-    if (k > 32) return cudaErrorInvalidValue;  // one lane per slot
-    const dim3 grid((unsigned)((T + 3) / 4));  // 4 warps (tokens) per block
+    if (k > 32) return cudaErrorInvalidValue;             // one lane per slot
+    if (dxp_bf16 && !is_bf16) return cudaErrorInvalidValue;
+    const dim3 grid((unsigned)((T + 3LL) / 4));  // 4 warps (tokens) per block
     const cudaError_t e =
-        is_bf16 ? launch_pdl(dispatch_bwd_kernel<true>, grid, dim3(128), 0, stream, dxp, row_of, add,
-                             topk_idx, dl, wg, E, dx, T, k, D, (long long)rows_alloc)
-                : launch_pdl(dispatch_bwd_kernel<false>, grid, dim3(128), 0, stream, dxp, row_of,
-                             add, topk_idx, dl, wg, E, dx, T, k, D, (long long)rows_alloc);
+        launch_pdl(dxp_bf16  ? dispatch_bwd_kernel<true, true>
+                   : is_bf16 ? dispatch_bwd_kernel<true, false>
+                             : dispatch_bwd_kernel<false, false>,
+                   grid, dim3(128), 0, stream, dxp, row_of, add, topk_idx, dl, wg, E, dx, T, k, D,
+                   (long long)rows_alloc, status);
     if (e == cudaSuccess) count_launch();
     return e;
 }

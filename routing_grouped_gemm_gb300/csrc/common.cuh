@@ -508,6 +508,53 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32_major(int M, int N, int a_
 }
 
 // ---------------------------------------------------------------------
+// MXFP4 operands (kind::mxf4, block scales in tensor memory)
+// ---------------------------------------------------------------------
+// D[tmem] (+)= (A sfa)[smem] * (B sfb)[smem]^T, K = 64 e2m1 elements (32
+// packed bytes of each K-major row) with an e8m0 scale per 32 of them.
+__device__ __forceinline__ void tc_mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t sfa_tmem, uint32_t sfb_tmem,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], "
+        "p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        : "memory");
+}
+
+// Shared memory to tensor memory: 32 rows of 16 bytes into 4 columns, repeated
+// in the four lane quarters.  With row l holding 4 scales each of operand rows
+// l, l + 32, l + 64 and l + 96, this is the scale layout an MMA reads: column
+// c, lane l: the scales of operand row 32 c + l.
+__device__ __forceinline__ void tc_cp_scales(uint32_t tmem, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
+                 : "memory");
+}
+
+// Descriptor of such a 512-byte block: no swizzle, 8-row groups 128 bytes apart.
+__device__ __forceinline__ uint64_t sdesc_scales(uint32_t smem_addr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((smem_addr & 0x3FFFFu) >> 4);  // start address
+    d |= (uint64_t)(128u >> 4) << 32;               // stride byte offset
+    d |= (uint64_t)1 << 46;                         // descriptor version (tcgen05)
+    return d;
+}
+
+// kind::mxf4, e2m1 operands, e8m0 scales; sf: which 16-bit half of a row's four
+// scales this MMA's K = 64 takes (0 or 2).
+__host__ __device__ constexpr uint32_t idesc_mxf4_f32(int M, int N, int sf) {
+    return ((uint32_t)sf << 4)              // B scale id
+           | (1u << 7)                      // A format: e2m1
+           | (1u << 10)                     // B format: e2m1
+           | ((uint32_t)(N >> 3) << 17)     // N / 8
+           | (1u << 23)                     // scale format: e8m0
+           | ((uint32_t)(M >> 7) << 27)     // M / 128
+           | ((uint32_t)sf << 29);          // A scale id
+}
+
+// ---------------------------------------------------------------------
 // grouped-layout tile table (shared by the grouped GEMM kernels)
 // ---------------------------------------------------------------------
 // For local expert i: rows [base_i, base_i + valid_i) of the permuted

@@ -85,7 +85,8 @@ cudaError_t launch_permute(const void *x, const int *topk_idx, int *tokens_per_e
                            int align_m, int capacity, int64_t rows_alloc, int elem_bytes,
                            int *scratch, int *status, cudaStream_t stream,
                            float *x_scale = nullptr,   // set: bf16 x -> e4m3 x_perm + row scales
-                           float *zero_out = nullptr);  // set: zero rows [T, D] fp32 (fused combine)
+                           float *zero_out = nullptr,  // set: zero rows [T, D] fp32 (fused combine)
+                           uint8_t *x_sf = nullptr);   // set: bf16 x -> MXFP4 x_perm + block scales
 
 // out[i] = bf16(comb[i]) for the fused combine's fp32 accumulator (n % 4 == 0).
 cudaError_t launch_comb_to_bf16(const float *comb, void *out, int64_t n, cudaStream_t stream);
@@ -96,6 +97,28 @@ cudaError_t launch_comb_to_bf16(const float *comb, void *out, int64_t n, cudaStr
 // dispatch), else to row t.
 cudaError_t launch_quantize_rows_e4m3(const void *src, int64_t rows, int cols, const int *row_of,
                                       int k, uint8_t *dst, float *scale, cudaStream_t stream);
+
+// Rows [rows, cols] (cols % 32 == 0) of bf16 or fp32 to MXFP4 codes
+// [rows, cols / 2] and e8m0 scales [rows, cols / 32], and back.
+cudaError_t launch_quantize_rows_mxfp4(const void *src, int64_t rows, int cols, int is_bf16,
+                                       uint8_t *dst, uint8_t *scale, cudaStream_t stream);
+cudaError_t launch_dequantize_rows_mxfp4(const uint8_t *codes, const uint8_t *scale, int64_t rows,
+                                         int cols, int is_bf16, void *dst, cudaStream_t stream);
+// bf16 row t's codes and scales to rows row_of[t, j] (the dispatch; -1: none).
+cudaError_t launch_dispatch_rows_mxfp4(const void *src, int64_t rows, int cols, const int *row_of,
+                                       int k, uint8_t *dst, uint8_t *scale, cudaStream_t stream);
+
+// MXFP4 experts: both GEMMs on e2m1 operands with block scales
+// (kind::mxf4.block_scale), h quantised to MXFP4 in GEMM1's epilogue.
+// D and H_local multiples of 32.
+struct MxWeights {
+    const uint8_t *w1, *w1_scale, *w3, *w3_scale, *w2, *w2_scale;
+};
+cudaError_t launch_grouped_swiglu_mxfp4(const uint8_t *x_perm_q, const uint8_t *x_scale,
+                                        const int *seg_offsets, const int *tokens_per_expert,
+                                        const MxWeights &w, uint8_t *h_q, uint8_t *h_scale,
+                                        void *y_perm, int D, int H_local, int e_first, int E_local,
+                                        int64_t rows_alloc, int *status, cudaStream_t stream);
 
 // out[t] = sum_j w[t, j] y_perm[row_of[t, j]], fp32 in slot order, rounded
 // once; y_perm fp16 with a bf16 out (is_bf16), fp32 with an fp32 out.
@@ -176,9 +199,9 @@ cudaError_t launch_grouped_swiglu_bwd(const void *x_perm, const void *h, const v
                                       int grad_bf16 = 0);  // dw1, dw3, dw2 in bf16 (else fp32)
 int64_t grouped_bwd_smem(int E_local);
 
-// Backward of the combine: gy[row] = bf16(w * dout[t]) (rows without a token
-// untouched) and dw[t, j] = <dout[t], y_perm[row]> (y_perm fp16, as the bf16
-// forward stores it).
+// Backward of the combine: gy[row] = w * dout[t] in the layer's type (rows
+// without a token untouched) and dw[t, j] = <dout[t], y_perm[row]> (y_perm in
+// the type the forward stores it: fp16 in a bf16 layer, else fp32).
 cudaError_t launch_combine_bwd(const void *dout, const void *y_perm, const int *row_of,
                                const float *topk_w, void *gy, float *dw, int T, int D, int k,
                                int64_t rows_alloc, int is_bf16, int *status, cudaStream_t stream);
@@ -186,10 +209,11 @@ cudaError_t launch_combine_bwd(const void *dout, const void *y_perm, const int *
 // Backward of the dispatch: dx[t] = sum_j dxp[row_of[t, j]] + r[t], where
 // r[t] = add[t] when add, else sum_j dl[t, e_j] wg[e_j] (e_j = topk_idx[t, j];
 // the router's part of dx when dl is zero off the selected experts), else 0.
-cudaError_t launch_dispatch_bwd(const float *dxp, const int *row_of, const float *add,
+// dxp is fp32, or bf16 with dxp_bf16 (bf16 layers).
+cudaError_t launch_dispatch_bwd(const void *dxp, int dxp_bf16, const int *row_of, const float *add,
                                 const int *topk_idx, const float *dl, const void *wg, int E,
                                 void *dx, int T, int D, int k, int64_t rows_alloc, int is_bf16,
-                                cudaStream_t stream);
+                                int *status, cudaStream_t stream);
 
 // dl is dense (every expert's logit gets a gradient) only for a softmax
 // over all E without renormalisation; otherwise it is zero off the k

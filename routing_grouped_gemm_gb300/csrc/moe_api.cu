@@ -18,8 +18,9 @@
 
 namespace {
 
-// 2.0.0: y_perm of bf16 layers is fp16 (fp32 up to 1.5.0)
-constexpr int32_t kAbiVersion = 20000;
+// 2.0.0: y_perm of bf16 layers is fp16 (fp32 up to 1.5.0); 2.1.0 adds the
+// MXFP4 calls and the gradients of the permute and combine steps
+constexpr int32_t kAbiVersion = 20100;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 32;
 constexpr int64_t kAlign = 256;
@@ -250,11 +251,12 @@ moe_status do_route(const moe_config *c, const void *x, const void *wg, const fl
 
 moe_status do_permute(const moe_config *c, const void *x, const int32_t *topk_idx, int32_t *tpe,
                       int32_t *seg, int32_t *row_of, int32_t *tor, void *x_perm, const StepWs &w,
-                      cudaStream_t s, float *x_scale = nullptr, float *zero_out = nullptr) {
+                      cudaStream_t s, float *x_scale = nullptr, float *zero_out = nullptr,
+                      uint8_t *x_sf = nullptr) {
     cudaError_t e = moe::launch_permute(x, topk_idx, tpe, seg, row_of, tor, x_perm, c->T, c->D, c->E,
                                         c->k, c->e_first, c->E_local, c->layout, c->align_m,
                                         c->capacity, rows_alloc_of(c), elem_bytes(c), w.scratch,
-                                        &w.status->flags, s, x_scale, zero_out);
+                                        &w.status->flags, s, x_scale, zero_out, x_sf);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_permute");
 }
 
@@ -325,6 +327,32 @@ moe_status do_grouped_fp8(const moe_config *c, const void *x_perm_q, const float
         return arg_fail("moe_grouped_swiglu_fp8: too many local experts for the pair kernel",
                         MOE_ERR_UNSUPPORTED);
     return MOE_OK;
+}
+
+// What the MXFP4 path supports: bf16 activations, rows of D and H_local
+// values in whole blocks of 32 (which are also the 16-byte units of packed
+// codes that TMA needs) and k <= 32 (one lane per slot in the dispatch).
+moe_status mxfp4_supported(const moe_config *c) {
+    if (c->dtype != MOE_BF16)
+        return arg_fail("MXFP4 path: bf16 activations only", MOE_ERR_UNSUPPORTED);
+    if (c->D % 32 || c->H_local % 32)
+        return arg_fail("MXFP4 path: D and H_local must be multiples of 32", MOE_ERR_UNSUPPORTED);
+    return MOE_OK;
+}
+
+moe_status do_grouped_mxfp4(const moe_config *c, const uint8_t *x_perm_q, const uint8_t *x_scale,
+                            const int32_t *seg, const int32_t *tpe, const moe::MxWeights &mw,
+                            uint8_t *h_q, uint8_t *h_scale, void *y_perm, const StepWs &w,
+                            cudaStream_t s) {
+    const cudaError_t e = moe::launch_grouped_swiglu_mxfp4(
+        x_perm_q, x_scale, seg, tpe, mw, h_q, h_scale, y_perm, c->D, c->H_local, c->e_first,
+        c->E_local, rows_alloc_of(c), &w.status->flags, s);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_grouped_swiglu_mxfp4");
+}
+
+bool mx_weights_ok(const moe::MxWeights &w) {
+    return need16(w.w1) && need16(w.w1_scale) && need16(w.w3) && need16(w.w3_scale) &&
+           need16(w.w2) && need16(w.w2_scale);
 }
 
 moe_status do_combine(const moe_config *c, const void *y_perm, const int32_t *row_of,
@@ -779,8 +807,8 @@ MOE_EXPORT moe_status moe_layer_backward_ex(const moe_config *cfg, const void *x
     if (e != cudaSuccess) return cuda_fail(e, "moe_layer_backward: router backward");
     // the router's part of dx: a GEMM where dl is dense, else folded in here
     const bool dense = moe::router_dl_dense(cfg->score, cfg->renorm);
-    e = moe::launch_dispatch_bwd(W.dxp, L.row_of, dense ? W.dxr : nullptr, L.topk_idx, W.dl, wg,
-                                 cfg->E, dx, cfg->T, cfg->D, cfg->k, rows, 1, s);
+    e = moe::launch_dispatch_bwd(W.dxp, 0, L.row_of, dense ? W.dxr : nullptr, L.topk_idx, W.dl, wg,
+                                 cfg->E, dx, cfg->T, cfg->D, cfg->k, rows, 1, flags, s);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_layer_backward: dispatch backward");
 }
 
@@ -870,6 +898,164 @@ MOE_EXPORT moe_status moe_layer_forward_fp8(const moe_config *cfg, const void *x
                              w3_scale, w2, L.h, L.y_perm, L.step, s)) != MOE_OK)
         return st;
     return do_combine(cfg, L.y_perm, L.row_of, L.topk_w, out, L.step, s);
+}
+
+MOE_EXPORT moe_status moe_quantize_rows_mxfp4(const void *src, int32_t src_dtype, int64_t rows,
+                                             int32_t cols, uint8_t *dst, uint8_t *scale,
+                                             moe_stream_t stream) {
+    if (src_dtype != MOE_F32 && src_dtype != MOE_BF16)
+        return arg_fail("moe_quantize_rows_mxfp4: src_dtype must be MOE_F32 or MOE_BF16");
+    if (rows < 0 || cols <= 0 || cols % 32 || rows > INT64_MAX / 4 / cols)
+        return arg_fail("moe_quantize_rows_mxfp4: bad shape");
+    if (rows == 0) return MOE_OK;
+    if (!need16(src) || !need16(dst) || !need16(scale))
+        return arg_fail("moe_quantize_rows_mxfp4: NULL or misaligned tensor");
+    const cudaError_t e = moe::launch_quantize_rows_mxfp4(src, rows, cols, src_dtype == MOE_BF16,
+                                                          dst, scale, (cudaStream_t)stream);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_quantize_rows_mxfp4");
+}
+
+MOE_EXPORT moe_status moe_dequantize_rows_mxfp4(const uint8_t *codes, const uint8_t *scale,
+                                               int64_t rows, int32_t cols, void *dst,
+                                               int32_t dst_dtype, moe_stream_t stream) {
+    if (dst_dtype != MOE_F32 && dst_dtype != MOE_BF16)
+        return arg_fail("moe_dequantize_rows_mxfp4: dst_dtype must be MOE_F32 or MOE_BF16");
+    if (rows < 0 || cols <= 0 || cols % 32 || rows > INT64_MAX / 4 / cols)
+        return arg_fail("moe_dequantize_rows_mxfp4: bad shape");
+    if (rows == 0) return MOE_OK;
+    if (!need16(codes) || !need16(scale) || !need16(dst))
+        return arg_fail("moe_dequantize_rows_mxfp4: NULL or misaligned tensor");
+    const cudaError_t e = moe::launch_dequantize_rows_mxfp4(
+        codes, scale, rows, cols, dst_dtype == MOE_BF16, dst, (cudaStream_t)stream);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_dequantize_rows_mxfp4");
+}
+
+MOE_EXPORT moe_status moe_permute_mxfp4(const moe_config *cfg, const void *x,
+                                        const int32_t *topk_idx, int32_t *tokens_per_expert,
+                                        int32_t *seg_offsets, int32_t *row_of,
+                                        int32_t *token_of_row, uint8_t *x_perm_q, uint8_t *x_scale,
+                                        void *ws, size_t ws_bytes, moe_stream_t stream) {
+    moe_status st = validate(cfg);
+    if (st != MOE_OK) return st;
+    if ((st = mxfp4_supported(cfg)) != MOE_OK) return st;
+    StepWs w;
+    if ((st = carve_step(cfg, ws, ws_bytes, &w)) != MOE_OK) return st;
+    if (!tokens_per_expert || !seg_offsets) return arg_fail("moe_permute_mxfp4: NULL tensor");
+    if (cfg->T > 0 && (!topk_idx || !row_of || !need16(x)))
+        return arg_fail("moe_permute_mxfp4: NULL or misaligned tensor");
+    if (rows_alloc_of(cfg) > 0 && (!token_of_row || !need16(x_perm_q) || !need16(x_scale)))
+        return arg_fail("moe_permute_mxfp4: NULL or misaligned tensor");
+    // without a row there is nothing to quantise: the layout only
+    uint8_t *sf = rows_alloc_of(cfg) > 0 ? x_scale : nullptr;
+    return do_permute(cfg, x, topk_idx, tokens_per_expert, seg_offsets, row_of, token_of_row,
+                      sf ? x_perm_q : nullptr, w, (cudaStream_t)stream, nullptr, nullptr, sf);
+}
+
+MOE_EXPORT moe_status moe_grouped_swiglu_mxfp4(
+    const moe_config *cfg, const uint8_t *x_perm_q, const uint8_t *x_scale,
+    const int32_t *seg_offsets, const int32_t *tokens_per_expert, const uint8_t *w1_q,
+    const uint8_t *w1_scale, const uint8_t *w3_q, const uint8_t *w3_scale, const uint8_t *w2_q,
+    const uint8_t *w2_scale, uint8_t *h_q, uint8_t *h_scale, void *y_perm, void *ws,
+    size_t ws_bytes, moe_stream_t stream) {
+    moe_status st = validate(cfg);
+    if (st != MOE_OK) return st;
+    if ((st = mxfp4_supported(cfg)) != MOE_OK) return st;
+    StepWs w;
+    if ((st = carve_step(cfg, ws, ws_bytes, &w)) != MOE_OK) return st;
+    if (cfg->E_local == 0 || rows_alloc_of(cfg) == 0) return MOE_OK;
+    if (!seg_offsets || !tokens_per_expert)
+        return arg_fail("moe_grouped_swiglu_mxfp4: NULL offsets");
+    const moe::MxWeights mw{w1_q, w1_scale, w3_q, w3_scale, w2_q, w2_scale};
+    if (!need16(x_perm_q) || !need16(x_scale) || !mx_weights_ok(mw) || !need16(h_q) ||
+        !need16(h_scale) || !need16(y_perm))
+        return arg_fail("moe_grouped_swiglu_mxfp4: NULL or misaligned tensor");
+    return do_grouped_mxfp4(cfg, x_perm_q, x_scale, seg_offsets, tokens_per_expert, mw, h_q,
+                            h_scale, y_perm, w, (cudaStream_t)stream);
+}
+
+MOE_EXPORT moe_status moe_layer_forward_mxfp4(
+    const moe_config *cfg, const void *x, const void *wg, const float *bias, const uint8_t *w1_q,
+    const uint8_t *w1_scale, const uint8_t *w3_q, const uint8_t *w3_scale, const uint8_t *w2_q,
+    const uint8_t *w2_scale, void *out, void *ws, size_t ws_bytes, moe_stream_t stream) {
+    moe_status st = validate(cfg);
+    if (st != MOE_OK) return st;
+    if ((st = mxfp4_supported(cfg)) != MOE_OK) return st;
+    if (!ws) return arg_fail("workspace is NULL", MOE_ERR_WORKSPACE);
+    if (!aligned(ws, kAlign)) return arg_fail("workspace must be 256-byte aligned", MOE_ERR_WORKSPACE);
+    if ((int64_t)ws_bytes < layer_ws_layout(cfg, nullptr, nullptr))
+        return arg_fail("workspace too small for moe_layer_forward_mxfp4", MOE_ERR_WORKSPACE);
+    if (cfg->T == 0) return MOE_OK;
+    if (!need16(x) || !need16(wg) || !need16(out) || (bias && !aligned(bias, 4)))
+        return arg_fail("moe_layer_forward_mxfp4: NULL or misaligned tensor");
+    const moe::MxWeights mw{w1_q, w1_scale, w3_q, w3_scale, w2_q, w2_scale};
+    if (cfg->E_local > 0 && !mx_weights_ok(mw))
+        return arg_fail("moe_layer_forward_mxfp4: NULL or misaligned expert weights");
+    LayerWs L;
+    carve_step(cfg, ws, ws_bytes, &L.step);
+    layer_ws_layout(cfg, static_cast<char *>(ws), &L);
+    // codes and scales of a row take D / 2 + D / 32 of its 2 D bytes in the
+    // x_perm buffer (h likewise); a multiple of 16 codes bytes comes first
+    const int64_t rows = rows_alloc_of(cfg);
+    uint8_t *xq = static_cast<uint8_t *>(L.x_perm), *xs = xq + rows * (cfg->D / 2);
+    uint8_t *hq = static_cast<uint8_t *>(L.h), *hs = hq + rows * (cfg->H_local / 2);
+    cudaStream_t s = (cudaStream_t)stream;
+    if ((st = do_route(cfg, x, wg, bias, nullptr, L.topk_idx, L.topk_w, L.step, s)) != MOE_OK)
+        return st;
+    if ((st = do_permute(cfg, x, L.topk_idx, L.tpe, L.seg_off, L.row_of, L.token_of_row,
+                         rows > 0 ? xq : nullptr, L.step, s, nullptr, nullptr,
+                         rows > 0 ? xs : nullptr)) != MOE_OK)
+        return st;
+    if (cfg->E_local > 0 && rows > 0 &&
+        (st = do_grouped_mxfp4(cfg, xq, xs, L.seg_off, L.tpe, mw, hq, hs, L.y_perm, L.step, s)) !=
+            MOE_OK)
+        return st;
+    return do_combine(cfg, L.y_perm, L.row_of, L.topk_w, out, L.step, s);
+}
+
+MOE_EXPORT moe_status moe_unpermute_combine_backward(const moe_config *cfg, const void *dout,
+                                                     const void *y_perm, const int32_t *row_of,
+                                                     const float *topk_w, void *dy_perm,
+                                                     float *dtopk_w, void *ws, size_t ws_bytes,
+                                                     moe_stream_t stream) {
+    moe_status st = validate(cfg);
+    if (st != MOE_OK) return st;
+    StepWs w;
+    if ((st = carve_step(cfg, ws, ws_bytes, &w)) != MOE_OK) return st;
+    if (cfg->T == 0) return MOE_OK;
+    const int64_t rows = rows_alloc_of(cfg);
+    if (!need16(dout) || !row_of || !topk_w || !dtopk_w || !aligned(row_of, 4) ||
+        !aligned(topk_w, 4) || !aligned(dtopk_w, 4) ||
+        (rows > 0 && (!need16(y_perm) || !need16(dy_perm))))
+        return arg_fail("moe_unpermute_combine_backward: NULL or misaligned tensor");
+    const cudaError_t e = moe::launch_combine_bwd(dout, y_perm, row_of, topk_w, dy_perm, dtopk_w,
+                                                  cfg->T, cfg->D, cfg->k, rows,
+                                                  cfg->dtype == MOE_BF16, &w.status->flags,
+                                                  (cudaStream_t)stream);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_unpermute_combine_backward");
+}
+
+MOE_EXPORT moe_status moe_permute_backward(const moe_config *cfg, const void *dx_perm,
+                                           int32_t dx_perm_dtype, const int32_t *row_of, void *dx,
+                                           void *ws, size_t ws_bytes, moe_stream_t stream) {
+    if (dx_perm_dtype != MOE_F32 && dx_perm_dtype != MOE_BF16)
+        return arg_fail("moe_permute_backward: dx_perm_dtype must be MOE_F32 or MOE_BF16");
+    moe_status st = validate(cfg);
+    if (st != MOE_OK) return st;
+    if (dx_perm_dtype == MOE_BF16 && cfg->dtype != MOE_BF16)
+        return arg_fail("moe_permute_backward: a bf16 dx_perm needs a bf16 config",
+                        MOE_ERR_UNSUPPORTED);
+    StepWs w;
+    if ((st = carve_step(cfg, ws, ws_bytes, &w)) != MOE_OK) return st;
+    if (cfg->T == 0) return MOE_OK;
+    const int64_t rows = rows_alloc_of(cfg);
+    if (!row_of || !aligned(row_of, 4) || !need16(dx) || (rows > 0 && !need16(dx_perm)))
+        return arg_fail("moe_permute_backward: NULL or misaligned tensor");
+    const cudaError_t e = moe::launch_dispatch_bwd(dx_perm, dx_perm_dtype == MOE_BF16, row_of,
+                                                   nullptr, nullptr, nullptr, nullptr, cfg->E, dx,
+                                                   cfg->T, cfg->D, cfg->k, rows,
+                                                   cfg->dtype == MOE_BF16, &w.status->flags,
+                                                   (cudaStream_t)stream);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_permute_backward");
 }
 
 MOE_EXPORT moe_status moe_layer_forward_fused(const moe_config *cfg, const void *x, const void *wg,

@@ -36,6 +36,7 @@
 #include "common.cuh"
 #include "e4m3_row.cuh"
 #include "launch.h"
+#include "mxfp4_row.cuh"
 
 namespace moe {
 namespace {
@@ -529,7 +530,10 @@ __device__ __forceinline__ void derive_offsets(const int *__restrict__ blk_cnt, 
 #endif
 constexpr int IC_WARPS = MOE_IC_WARPS;
 static_assert(PB_TOKENS % IC_WARPS == 0, "a block's tokens lie in one count block");
-template <bool kFp8, bool kDerive>
+// What the copy of a token's row writes: the row itself, its e4m3 codes with
+// one fp32 scale, or its MXFP4 codes with one e8m0 scale per 32 values.
+enum : int { COPY_PLAIN = 0, COPY_E4M3 = 1, COPY_MXFP4 = 2 };
+template <int kCopy, bool kDerive>
 __global__ void __launch_bounds__(32 * IC_WARPS)
 permute_index_copy_kernel(const uint4 *__restrict__ x, const int *__restrict__ topk_idx,
                           const int2 *__restrict__ wmeta, const int *__restrict__ blk_base,
@@ -540,7 +544,7 @@ permute_index_copy_kernel(const uint4 *__restrict__ x, const int *__restrict__ t
                           long long rows_alloc, int cols, float *__restrict__ x_scale,
                           const int *__restrict__ blk_cnt, int nblk, int layout, int align_m,
                           int capacity, int *__restrict__ tpe_out, int *__restrict__ seg_out,
-                          int *status) {
+                          uint8_t *__restrict__ x_sf, int *status) {
     griddep_launch_dependents();  // the next kernel may be scheduled now
     griddep_wait();               // every input of this kernel is complete
     const int t = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
@@ -566,7 +570,7 @@ permute_index_copy_kernel(const uint4 *__restrict__ x, const int *__restrict__ t
     const int e = lane < k ? topk_idx[(size_t)t * k + lane] : -1;
     const uint4 *src = x + (size_t)t * vpr;
     uint4 buf[IC_UNROLL];
-    if (!kFp8 && x_perm) {
+    if (kCopy == COPY_PLAIN && x_perm) {
 #pragma unroll
         for (int u = 0; u < IC_UNROLL; ++u) {  // the first chunk of x[t] is in flight meanwhile
             const int v = u * 32 + lane;
@@ -599,9 +603,14 @@ permute_index_copy_kernel(const uint4 *__restrict__ x, const int *__restrict__ t
     for (long long r = (long long)seg_offsets[E_local] + (long long)t * 32 + lane; r < rows_alloc;
          r += (long long)T * 32)
         token_of_row[r] = -1;
-    if (kFp8) {
+    if (kCopy == COPY_E4M3) {
         quantize_row_e4m3_warp(src, cols, my_row, k, reinterpret_cast<uint8_t *>(x_perm), x_scale,
                                lane);
+        return;
+    }
+    if (kCopy == COPY_MXFP4) {
+        quantize_row_mxfp4_warp(reinterpret_cast<const __nv_bfloat16 *>(src), cols, my_row, k,
+                                reinterpret_cast<uint8_t *>(x_perm), x_sf, lane);
         return;
     }
     if (zero_out) {  // the fused combine's accumulator row of this token starts at zero
@@ -819,7 +828,7 @@ cudaError_t launch_permute(const void *x, const int *topk_idx, int *tokens_per_e
                            int T, int D, int E, int k, int e_first, int E_local, int layout,
                            int align_m, int capacity, int64_t rows_alloc, int elem_bytes,
                            int *scratch, int *status, cudaStream_t stream, float *x_scale,
-                           float *zero_out) {
+                           float *zero_out, uint8_t *x_sf) {
     const int nblk = (T + PB_TOKENS - 1) / PB_TOKENS;
     unsigned *ticket = reinterpret_cast<unsigned *>(scratch);
     int *blk_cnt = scratch + SCR_HEAD;
@@ -828,6 +837,7 @@ cudaError_t launch_permute(const void *x, const int *topk_idx, int *tokens_per_e
     const size_t mask_smem = sizeof(uint32_t) * PB_WARPS * (size_t)E;
     cudaError_t err;
     if (x_scale && (D % 8 || k > 32)) return cudaErrorInvalidValue;  // before any launch
+    if (x_sf && (D % 32 || k > 32)) return cudaErrorInvalidValue;
     if (nblk > 0 && (int64_t)nblk * E <= CS_MAX_CELLS) {
         // small count matrices: the copy blocks derive the offsets themselves
         const bool derive = (int64_t)nblk * E <= DERIVE_MAX_CELLS;
@@ -849,10 +859,12 @@ cudaError_t launch_permute(const void *x, const int *topk_idx, int *tokens_per_e
         const int blocks = (T + warps_per_block - 1) / warps_per_block;
         const size_t csmem =
             derive ? sizeof(int) * (2 * (size_t)E + E_local + 1 + warps_per_block) : 0;
-        auto copy_kernel = x_scale ? (derive ? permute_index_copy_kernel<true, true>
-                                             : permute_index_copy_kernel<true, false>)
-                                   : (derive ? permute_index_copy_kernel<false, true>
-                                             : permute_index_copy_kernel<false, false>);
+        auto copy_kernel = x_sf      ? (derive ? permute_index_copy_kernel<COPY_MXFP4, true>
+                                               : permute_index_copy_kernel<COPY_MXFP4, false>)
+                           : x_scale ? (derive ? permute_index_copy_kernel<COPY_E4M3, true>
+                                               : permute_index_copy_kernel<COPY_E4M3, false>)
+                                     : (derive ? permute_index_copy_kernel<COPY_PLAIN, true>
+                                               : permute_index_copy_kernel<COPY_PLAIN, false>);
         if (csmem > 0 && (err = ensure_smem((const void *)copy_kernel, csmem)) != cudaSuccess)
             return err;
         if ((err = launch_pdl(copy_kernel, dim3(blocks), dim3(32 * warps_per_block), csmem, stream,
@@ -861,7 +873,7 @@ cudaError_t launch_permute(const void *x, const int *topk_idx, int *tokens_per_e
                               (uint4 *)x_perm, T, k, E, e_first, E_local, D * elem_bytes / 16,
                               (float4 *)zero_out, D / 4, (const int *)tokens_per_expert,
                               (long long)rows_alloc, D, x_scale, (const int *)blk_cnt, nblk,
-                              layout, align_m, capacity, tokens_per_expert, seg_offsets,
+                              layout, align_m, capacity, tokens_per_expert, seg_offsets, x_sf,
                               status)) != cudaSuccess)
             return err;
         count_launch();
@@ -908,6 +920,8 @@ cudaError_t launch_permute(const void *x, const int *topk_idx, int *tokens_per_e
     }
     if (x_scale)  // FP8 dispatch: the copy quantises each token row once
         return launch_quantize_rows_e4m3(x, T, D, row_of, k, (uint8_t *)x_perm, x_scale, stream);
+    if (x_sf)  // MXFP4 dispatch: likewise
+        return launch_dispatch_rows_mxfp4(x, T, D, row_of, k, (uint8_t *)x_perm, x_sf, stream);
     if (!x_perm) return cudaSuccess;  // the layout only
     const int vpr = D * elem_bytes / 16;
     const int warps_per_block = 8;
