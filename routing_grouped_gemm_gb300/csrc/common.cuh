@@ -73,6 +73,20 @@ __device__ __forceinline__ uint32_t smem_u32(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// True in one lane of a converged warp.  A block guarded by it right where it
+// is entered stays warp-uniform for the compiler, so the operands of TMA and
+// tcgen05 instructions in it can live in uniform registers; under `lane == 0`
+// each is moved there anew for every instruction.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
+}
+
 __device__ __forceinline__ uint32_t lanemask_lt() {
     uint32_t m;
     asm("mov.u32 %0, %%lanemask_lt;" : "=r"(m));
@@ -350,6 +364,25 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
                  : "memory");
 }
 
+// Barrier of `threads` threads (whole warps, all of them in this call) that
+// also tells each whether `ok` held for every one.
+__device__ __forceinline__ bool bar_and(int id, int threads, bool ok) {
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %3, 0;\n\t"
+        "barrier.cta.red.and.pred q, %1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"(id), "r"(threads), "r"((uint32_t)ok)
+        : "memory");
+    return all != 0;
+}
+
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+    asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
 // Every thread of every CTA of the cluster; the warp is reconverged first
 // because the .aligned forms require it.
 __device__ __forceinline__ void cluster_sync() {
@@ -510,26 +543,28 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32_major(int M, int N, int a_
 // ---------------------------------------------------------------------
 // MXFP4 operands (kind::mxf4, block scales in tensor memory)
 // ---------------------------------------------------------------------
-// D[tmem] (+)= (A sfa)[smem] * (B sfb)[smem]^T, K = 64 e2m1 elements (32
-// packed bytes of each K-major row) with an e8m0 scale per 32 of them.
-__device__ __forceinline__ void tc_mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                            uint32_t idesc, uint32_t sfa_tmem, uint32_t sfb_tmem,
-                                            uint32_t accumulate) {
+// D[tmem, both CTAs] (+)= (A sfa)[smem, 128 rows per CTA] * (B sfb)[smem, N/2
+// rows per CTA]^T, K = 64 e2m1 elements (32 packed bytes of each K-major row)
+// with an e8m0 scale per 32 of them.  Each CTA's tensor memory holds the scales
+// of its own 128 rows of A and of all N rows of B.
+__device__ __forceinline__ void tc_mma_mxf4_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                                 uint32_t idesc, uint32_t sfa_tmem,
+                                                 uint32_t sfb_tmem, uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], "
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], "
         "p;\n\t}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
         : "memory");
 }
 
-// Shared memory to tensor memory: 32 rows of 16 bytes into 4 columns, repeated
-// in the four lane quarters.  With row l holding 4 scales each of operand rows
-// l, l + 32, l + 64 and l + 96, this is the scale layout an MMA reads: column
-// c, lane l: the scales of operand row 32 c + l.
-__device__ __forceinline__ void tc_cp_scales(uint32_t tmem, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
+// Shared memory to tensor memory, in both CTAs of the pair: 32 rows of 16 bytes
+// into 4 columns, repeated in the four lane quarters.  With row l holding 4
+// scales each of operand rows l, l + 32, l + 64 and l + 96, this is the scale
+// layout an MMA reads: column c, lane l: the scales of operand row 32 c + l.
+__device__ __forceinline__ void tc_cp_scales_pair(uint32_t tmem, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
                  : "memory");
 }
 

@@ -1,4 +1,5 @@
-// MXFP4 m-grouped SwiGLU expert FFN (tcgen05 kind::mxf4, block scales).
+// MXFP4 m-grouped SwiGLU expert FFN on CTA pairs (tcgen05 kind::mxf4, block
+// scales).
 //
 // Same contract as grouped_tc.cu over operands of e2m1 codes with one e8m0
 // scale per 32 elements of K (mxfp4_row.cuh):
@@ -8,23 +9,30 @@
 // fp32; h is rounded once, from the fp32 result straight to MXFP4 (GEMM2's
 // operand), and y once to fp16, as the other bf16 layers store it.
 //
-// Each GEMM is one persistent launch of one CTA per SM over 128 x 192 output
-// tiles, K in blocks of 256 elements (128 packed bytes, a 128-byte swizzled
-// row):
-//   * GEMM1's 192 columns are the gate and the up products of the same 96
-//     hidden units, so the epilogue has both in one lane; a lane holds one
-//     row, so a block of 32 hidden units is 32 registers of one thread and
-//     its maximum needs no exchange;
-//   * N = 192 leaves 128 of the 512 tensor-memory columns beside two
-//     accumulators: the scales of five K blocks (24 columns each), one buffer
-//     per pipeline stage, so scales are never overwritten under an MMA;
+// At 4 bits the tensor cores take a K = 64 step in the time of a bf16 K = 16
+// one, so a tile's operands, which come from L2, bound long calls and the
+// weights, which come from HBM, short ones.  Both ask for few operand rows per
+// product:
+//   * the weights are the M operand, 256 rows on a pair of CTAs
+//     (cta_group::2), and the tokens the N operand, up to 192 of an expert's
+//     rows, split evenly over its tiles in steps of 16: a ragged segment costs
+//     its own rows and no more, a decode batch loads 16;
+//   * of GEMM1's 256 rows each CTA holds 64 rows of w1 and the same 64 of w3,
+//     so a tile gives h of 128 hidden units;
+//   * two accumulators of 192 columns leave 128 of the 512 tensor-memory
+//     columns for scales: five buffers of 24 (a K block of 256 of 128 weight
+//     rows and of the tokens), one per pipeline stage, so scales are never
+//     overwritten under an MMA and nothing waits for that but the stage itself;
 //   * scales are read in their natural [rows, K / 32] layout, which is not the
 //     order the tensor cores want (four scales each of rows l, l + 32, l + 64
-//     and l + 96 together): four warps gather them, one per stage in flight,
-//     into 512-byte blocks that tcgen05.cp spreads over tensor memory;
-//   * a tile of at most 64 valid rows loads only those (16-row boxes); the
-//     other rows of the operand are whatever the stage held -- every code is a
-//     finite number and their scales are set to 1 -- and are not stored;
+//     and l + 96 together).  Three warps fetch them, 32 bytes of a row -- one
+//     sector, four K blocks -- at a time, and store them as 512-byte blocks for
+//     tcgen05.cp, in a ring of their own with one fence and one arrival for four
+//     K blocks;
+//   * the accumulator's lanes are weight rows and its columns tokens, so the
+//     epilogues turn it around in shared memory, 32 tokens at a time: for h a
+//     thread then has 16 gates and ups of one token (half of a block, its
+//     maximum one shuffle away), for y 16-byte pieces of a token's row;
 //   * every mbarrier wait is bounded (FLAG_TIMEOUT).
 #include <cuda.h>
 
@@ -37,355 +45,645 @@
 namespace moe {
 namespace {
 
-constexpr int X_BM = 128;             // token rows per tile
-constexpr int X_BN = 192;             // output columns per tile (GEMM1: 96 gate, 96 up)
-constexpr int X_UNITS = X_BN / 2;     // hidden units per GEMM1 tile
+constexpr int X_BM = 256;             // weight rows per pair tile, 128 per CTA
+constexpr int X_BN = 192;             // most tokens per tile
+constexpr int X_UNITS = X_BM / 2;     // hidden units per GEMM1 tile
 constexpr int X_BK = 256;             // K elements per stage
 constexpr int X_ROW = X_BK / 2;       // bytes of a row's K block: the swizzle span
-constexpr int X_A_BYTES = X_BM * X_ROW;
-constexpr int X_B_BYTES = X_BN * X_ROW;
+constexpr int X_W_BYTES = 128 * X_ROW;
+constexpr int X_T_BYTES = X_BN / 2 * X_ROW;
 constexpr int X_SF_BLOCK = 512;       // 128 rows x 4 scales
-constexpr int X_SF_BYTES = 6 * X_SF_BLOCK;  // two K halves of A's block, then of B's two
-constexpr int X_STAGE_BYTES = X_A_BYTES + X_B_BYTES + X_SF_BYTES;
-constexpr int X_MAX_STAGES = 5;
-constexpr int X_EPI_WARPS = 4;
-constexpr int X_SF_WARPS = 4;
-constexpr int X_THREADS = 64 + 32 * (X_EPI_WARPS + X_SF_WARPS);
+constexpr int X_SF_BYTES = 6 * X_SF_BLOCK;  // two K halves of the weights' block, then of the tokens' two
+constexpr int X_STAGE_BYTES = X_W_BYTES + X_T_BYTES;
+constexpr int X_STAGES = 5;
+// Warps: TMA, MMA, scale copies, scale fetchers, epilogue.
+constexpr int X_GROUP = 4;            // K blocks whose scales are fetched together (32 bytes of a row)
+constexpr int X_GROUP_BYTES = X_GROUP * X_SF_BYTES;
+constexpr int X_SF_WARPS = 3;         // one group each in shared memory, one each in flight
+constexpr int X_EPI_GROUPS = 2;       // of four warps (the TMEM lane quarters), alternate chunks of a tile
+constexpr int X_EPI_WARPS = 4 * X_EPI_GROUPS;
+constexpr int X_THREADS = 32 * (3 + X_SF_WARPS + X_EPI_WARPS);
 constexpr int X_TMEM_COLS = 512;
 constexpr int X_SF_COL = 2 * X_BN;    // scale buffers start here
-constexpr int X_SF_COLS = 24;         // per stage: 2 x 4 for A, 2 x 8 for B
-static_assert(X_SF_COL + X_MAX_STAGES * X_SF_COLS <= X_TMEM_COLS, "tensor memory columns");
-static_assert(X_STAGE_BYTES % 1024 == 0, "stages keep the swizzle's alignment");
-constexpr int X_NBARS = 2 * X_MAX_STAGES + 5;
+constexpr int X_SF_COLS = 24;         // 2 x 4 of the weights, 2 x 8 of the tokens
+static_assert(X_SF_COL + X_STAGES * X_SF_COLS <= X_TMEM_COLS, "tensor memory columns");
+static_assert(X_STAGE_BYTES % 1024 == 0 && X_T_BYTES % 1024 == 0, "the swizzle's alignment");
+constexpr int X_NBARS = 2 * X_STAGES + 2 * X_SF_WARPS + 6;
 constexpr int X_SMEM_MAX = 227 * 1024;
+// GEMM1's turning buffer, per epilogue group: 32 tokens x (64 gates, 64 ups, 4 of padding)
+constexpr int X_TURN_LD = 132;
+constexpr int X_TURN1 = X_EPI_GROUPS * 32 * X_TURN_LD * 4;
+// GEMM2's: per warp 32 tokens x 32 columns fp16
+constexpr int X_TURN2 = X_EPI_WARPS * 32 * 64;
+constexpr int X_EPI_BAR = 1;          // named barriers of the epilogue: one per group
 
 struct MxParams {
     int E_local, e_first, rows_alloc;
-    int stages;
     int K, nk;            // reduction length (D or H_local) and its 256-blocks
-    int nt, n_out;        // tiles along N; columns of the output (H_local or D)
+    int nt, n_out;        // tiles along the weight rows; columns of the output (H_local or D)
     const int *seg_off, *tpe;
-    const uint8_t *a_sf;          // [rows_alloc, K / 32]
-    const uint8_t *b_sf0, *b_sf1; // w1 and w3 [E_local, H_local, D / 32], or w2 twice
+    const uint8_t *t_sf;          // tokens' scales [rows_alloc, K / 32]
+    const uint8_t *w_sf0, *w_sf1; // of w1 and w3 [E_local, H_local, D / 32], or of w2 twice
     uint8_t *hq, *hsf;            // GEMM1: codes [rows, H / 2], scales [rows, H / 32]
     __half *y;                    // GEMM2: [rows, D]
     int *status;
 };
 
-size_t mx_smem_bytes(int stages, int E_local) {
-    return 1024 + (size_t)stages * X_STAGE_BYTES + (X_NBARS + 1) * sizeof(uint64_t) + 16 +
-           sizeof(int) * (3 * (size_t)E_local + 1);
+size_t mx_smem_bytes(bool gemm1, int E_local) {
+    return 1024 + (size_t)X_STAGES * X_STAGE_BYTES + X_SF_WARPS * X_GROUP_BYTES + (gemm1 ? X_TURN1 : X_TURN2) +
+           (X_NBARS + 1) * sizeof(uint64_t) + 16 + sizeof(int) * (4 * (size_t)E_local + 1);
 }
 
-struct MxTile {
-    int expert, row0, nvalid, nt;
+// The experts' rows in shared memory: first row, rows, first token tile and
+// rows per token tile.
+struct MxTable {
+    int *base, *valid, *first, *per;
 };
 
-__device__ __forceinline__ MxTile decode_tile(int v, const MxParams &p, const int *s_mtoff,
-                                              const int *s_base, const int *s_valid) {
-    MxTile c;
-    const int mt = v / p.nt;
-    c.nt = v - mt * p.nt;
-    c.expert = tile_expert(s_mtoff, p.E_local, mt);
-    const int lm = mt - s_mtoff[c.expert];
-    c.row0 = s_base[c.expert] + lm * X_BM;
-    c.nvalid = min(X_BM, s_valid[c.expert] - lm * X_BM);
-    return c;
+// A warp's way through the tiles of its pair: tile v = token tile * nt +
+// weight tile, an expert's rows in equal token tiles (a multiple of 16, at
+// most X_BN), weight tiles inner.  Every step is n_pairs tiles on, so a few
+// additions and the next experts' entries replace a division and a search.
+struct MxTile {
+    int tt, nt;                    // token tile (over all experts), weight tile
+    int expert, row0, nvalid;      // expert, first row, rows
+    int n;                         // the MMA's N: nvalid rounded up to 16
+
+    __device__ __forceinline__ void place(const MxTable &t) {
+        while (t.first[expert + 1] <= tt) ++expert;
+        const int per = t.per[expert], lead = (tt - t.first[expert]) * per;
+        row0 = t.base[expert] + lead;
+        nvalid = min(per, t.valid[expert] - lead);
+        n = (nvalid + 15) & ~15;
+    }
+    __device__ __forceinline__ MxTile(int v, int nts, int total, const MxTable &t)
+        : tt(v / nts), nt(v - v / nts * nts), expert(0), row0(0), nvalid(0), n(16) {
+        if (v < total) place(t);
+    }
+    // n_pairs on, in units of token tiles (dt) and weight tiles (dn)
+    __device__ __forceinline__ void step(int dt, int dn, int nts, bool more, const MxTable &t) {
+        tt += dt;
+        nt += dn;
+        if (nt >= nts) {
+            nt -= nts;
+            ++tt;
+        }
+        if (more) place(t);
+    }
+};
+
+// Builds the table by one warp, 32 experts at a time; returns the number of
+// token tiles.  Offsets outside [0, rows_alloc] or decreasing flag
+// FLAG_BAD_ROUTING and empty the segment.
+__device__ __forceinline__ void build_mx_table(int lane, const MxParams &p, const MxTable &t,
+                                               int *status) {
+    int run = 0;
+    for (int e0 = 0; e0 < p.E_local; e0 += 32) {
+        const int e = e0 + lane;
+        int b = 0, v = 0, tiles = 0;
+        if (e < p.E_local) {
+            b = p.seg_off[e];
+            const int end = p.seg_off[e + 1];
+            int c = p.tpe[p.e_first + e];
+            if (b < 0 || end < b || end > p.rows_alloc || c < 0) {
+                raise_flag(status, FLAG_BAD_ROUTING);
+                c = 0;
+            }
+            v = max(0, min(c, end - b));
+            tiles = (v + X_BN - 1) / X_BN;
+        }
+        int incl = tiles;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int n = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += n;
+        }
+        if (e < p.E_local) {
+            t.base[e] = b;
+            t.valid[e] = v;
+            t.first[e] = run + incl - tiles;
+            t.per[e] = tiles ? ((v + tiles - 1) / tiles + 15) & ~15 : 16;
+        }
+        run += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) t.first[p.E_local] = run;
 }
 
 // SiLU(g) = g / (1 + e^-g) with the fast approximate division (2 ulp in fp32,
 // far below the 4-bit rounding); 0 where e^-g overflows, as SiLU is there.
 __device__ __forceinline__ float mx_silu(float g) { return __fdividef(g, 1.f + __expf(-g)); }
 
-// The 8 scales of a row's K block kb: bytes [8 kb, 8 kb + 8) of its `ld`
-// scales, 1.0 (byte 127) past the end (the codes there are zeros).
-__device__ __forceinline__ uint2 load_scales(const uint8_t *row, int kb, int ld) {
-    const int b = kb * 8;
-    uint2 v = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
-    if ((ld & 7) == 0) {
-        v = *reinterpret_cast<const uint2 *>(row + b);
-    } else if ((ld & 3) == 0) {
-        v.x = *reinterpret_cast<const uint32_t *>(row + b);
-        if (b + 4 < ld) v.y = *reinterpret_cast<const uint32_t *>(row + b + 4);
-    } else {
-        uint32_t w[2] = {0, 0};
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            w[i >> 2] |= (b + i < ld ? (uint32_t)row[b + i] : 127u) << (8 * (i & 3));
-        v = make_uint2(w[0], w[1]);
+constexpr uint32_t kMxOnes = 0x7f7f7f7fu;  // four scales of 1
+
+// Bytes [32 kg, 32 kg + 32) of row `row` of scales [.., ld] (`total` bytes in
+// all, 16-byte aligned), 1.0 past the row's end (the codes there are zeros).
+__device__ __forceinline__ void load_scales32(const uint8_t *__restrict__ base, size_t row, int ld,
+                                              size_t total, int kg, uint32_t (&v)[8]) {
+    const int n = ld - 32 * kg;  // bytes left in the row
+    const size_t off = row * ld + 32 * kg;
+    if ((ld & 15) == 0) {
+        const uint4 *q = reinterpret_cast<const uint4 *>(base + off);
+        const uint4 a = q[0];
+        uint4 b = make_uint4(kMxOnes, kMxOnes, kMxOnes, kMxOnes);
+        if (n > 16) b = q[1];
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        return;
     }
-    return v;
+    if ((ld & 3) == 0) {
+        const uint32_t *q = reinterpret_cast<const uint32_t *>(base + off);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 4 * i < n ? q[i] : kMxOnes;
+        return;
+    }
+    // rows at any byte: the aligned words around the 32 bytes, shifted together
+    const size_t a = off & ~(size_t)3;
+    const int sh = 8 * (int)(off & 3);
+    const int words = (min(n, 32) + (sh >> 3) + 3) / 4;
+    uint32_t w[9];
+#pragma unroll
+    for (int i = 0; i < 9; ++i)
+        w[i] = i < words && a + 4 * i + 4 <= total ? *reinterpret_cast<const uint32_t *>(base + a + 4 * i)
+                                                   : 0u;
+    if (a + 4 * words > total)  // the array's last, partial word
+        for (size_t at = total & ~(size_t)3; at < total; ++at) {
+            const int i = (int)(at - a) / 4;
+#pragma unroll
+            for (int j = 0; j < 9; ++j)
+                if (j == i) w[j] |= (uint32_t)base[at] << (8 * (int)(at & 3));
+        }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        v[i] = __funnelshift_r(w[i], w[i + 1], sh);
+        const int left = n - 4 * i;
+        if (left <= 0) v[i] = kMxOnes;
+        else if (left < 4) v[i] = (v[i] & ((1u << (8 * left)) - 1u)) | (kMxOnes << (8 * left));
+    }
 }
 
 template <bool kGemm1>
 __global__ void __launch_bounds__(X_THREADS, 1)
-grouped_mx_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA16,
-                  const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
+grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constant__ CUtensorMap tmT16,
+                  const __grid_constant__ CUtensorMap tmT32, const __grid_constant__ CUtensorMap tmT64,
+                  const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CUtensorMap tmW1,
                   const MxParams p) {
     griddep_launch_dependents();  // the next kernel may be scheduled now
-    griddep_wait();               // every input of this kernel is complete
+    if (cluster_nctarank() != 2) {  // every role below assumes a CTA pair
+        griddep_wait();
+        if (threadIdx.x == 0) raise_flag(p.status, FLAG_LAUNCH);
+        return;
+    }
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(ring + p.stages * X_STAGE_BYTES);
-    uint64_t *full = bars;                       // TMA bytes + the stage's scale warp -> MMA
-    uint64_t *empty = bars + X_MAX_STAGES;       // MMA -> TMA and scale warps
-    uint64_t *tfull = bars + 2 * X_MAX_STAGES;   // [2] MMA -> epilogue
-    uint64_t *tempty = tfull + 2;                // [2] epilogue -> MMA
-    uint64_t *drain = tempty + 2;                // MMA completion at exit
+    uint8_t *sfs = ring + X_STAGES * X_STAGE_BYTES;  // [X_SF_WARPS] groups of scales
+    uint8_t *turn = sfs + X_SF_WARPS * X_GROUP_BYTES;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(turn + (kGemm1 ? X_TURN1 : X_TURN2));
+    uint64_t *full = bars;                       // leader: both CTAs' TMA bytes, scales in TMEM -> MMA
+    uint64_t *empty = bars + X_STAGES;           // MMA -> each CTA's TMA, the leader's scale copies
+    uint64_t *tfull = bars + 2 * X_STAGES;       // [2] MMA -> each CTA's epilogue
+    uint64_t *tempty = tfull + 2;                // [2] leader: both epilogues -> MMA
+    uint64_t *drain = tempty + 2;                // [2] leader: MMA's and copies' completion at exit
+    uint64_t *sfull = drain + 2;                 // [X_SF_WARPS] leader: both CTAs' group of scales -> copies
+    uint64_t *sempty = sfull + X_SF_WARPS;       // [X_SF_WARPS] copies -> each CTA's scale warp
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + X_NBARS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    int *s_base = reinterpret_cast<int *>(tmem_slot + 4);
-    int *s_valid = s_base + p.E_local;
-    int *s_mtoff = s_valid + p.E_local;
+    MxTable table;
+    table.base = reinterpret_cast<int *>(tmem_slot + 4);
+    table.valid = table.base + p.E_local;
+    table.per = table.valid + p.E_local;
+    table.first = table.per + p.E_local;  // [E_local + 1]
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int stages = p.stages;
-    if (warp == 0) {
-        build_tile_table(lane, p.E_local, p.e_first, p.rows_alloc, X_BM, p.seg_off, p.tpe, s_base,
-                         s_valid, s_mtoff, blockIdx.x == 0 ? p.status : nullptr);
+    // warp-uniform for the compiler too
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const int pair_id = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
+    // barriers and tensor memory need no input: ready before the wait for the
+    // previous kernel, the table after it
+    if (warp == 1) {
         if (lane == 0) {
-            for (int s = 0; s < stages; ++s) {
+            for (int s = 0; s < X_STAGES; ++s) {
                 mbar_init(&full[s], 2);
                 mbar_init(&empty[s], 1);
             }
             for (int a = 0; a < 2; ++a) {
                 mbar_init(&tfull[a], 1);
-                mbar_init(&tempty[a], X_EPI_WARPS);
+                mbar_init(&tempty[a], 2 * X_EPI_WARPS);
+                mbar_init(&drain[a], 1);
             }
-            mbar_init(drain, 1);
+            for (int g = 0; g < X_SF_WARPS; ++g) {
+                mbar_init(&sfull[g], 2);
+                mbar_init(&sempty[g], 1);
+            }
             *abort_flag = 0;
             fence_mbarrier_init();
-            prefetch_tmap(&tmA);
-            prefetch_tmap(&tmA16);
-            prefetch_tmap(&tmB0);
-            if (kGemm1) prefetch_tmap(&tmB1);
         }
-    } else if (warp == 1) {
-        tmem_alloc(tmem_slot, X_TMEM_COLS);
-        tmem_relinquish();
+        __syncwarp();
+    } else if (warp == 2) {
+        tmem_alloc_pair(tmem_slot, X_TMEM_COLS);
+        tmem_relinquish_pair();
+    } else if (warp == 3 && lane == 0) {
+        prefetch_tmap(&tmT8);
+        prefetch_tmap(&tmT16);
+        prefetch_tmap(&tmT32);
+        prefetch_tmap(&tmT64);
+        prefetch_tmap(&tmW0);
+        if (kGemm1) prefetch_tmap(&tmW1);
     }
+    griddep_wait();  // every input of this kernel is complete
+    if (warp == 0) build_mx_table(lane, p, table, blockIdx.x == 0 ? p.status : nullptr);
     tc_fence_before();
     __syncthreads();
+    cluster_sync();  // the peer's barriers exist before anything arrives on them
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    const int total = s_mtoff[p.E_local] * p.nt;
+    const int total = table.first[p.E_local] * p.nt;
+    const uint32_t full_leader = mapa_shared(smem_u32(&full[0]), 0);
+    const int dt = n_pairs / p.nt, dn = n_pairs - dt * p.nt;  // a step of n_pairs tiles
 
     if (warp == 0) {
-        if (lane == 0) {
-            // ---------------- TMA producer ----------------
-            int s = 0;
-            uint32_t ph = 0;
-            bool ok = true;
-            for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
-                const MxTile c = decode_tile(tile, p, s_mtoff, s_base, s_valid);
-                const int n16 = c.nvalid <= 64 ? (c.nvalid + 15) / 16 : 0;  // 16-row boxes of A
-                const uint32_t tx = (n16 ? n16 * 16 * X_ROW : X_A_BYTES) + X_B_BYTES;
-                for (int kb = 0; kb < p.nk; ++kb) {
-                    if (!mbar_wait_bounded(&empty[s], ph ^ 1u, abort_flag)) { ok = false; break; }
-                    mbar_arrive_expect_tx(&full[s], tx);
-                    uint8_t *sa = ring + s * X_STAGE_BYTES;
-                    uint8_t *sb = sa + X_A_BYTES;
-                    if (n16)
-                        for (int i = 0; i < n16; ++i)
-                            tma_load_2d(sa + i * 16 * X_ROW, &tmA16, &full[s], kb * X_ROW,
-                                        c.row0 + 16 * i);
-                    else
-                        tma_load_2d(sa, &tmA, &full[s], kb * X_ROW, c.row0);
-                    if (kGemm1) {
-                        tma_load_3d(sb, &tmB0, &full[s], kb * X_ROW, c.nt * X_UNITS, c.expert);
-                        tma_load_3d(sb + X_B_BYTES / 2, &tmB1, &full[s], kb * X_ROW,
-                                    c.nt * X_UNITS, c.expert);
-                    } else {
-                        tma_load_3d(sb, &tmB0, &full[s], kb * X_ROW, c.nt * X_BN, c.expert);
-                    }
-                    if (++s == stages) { s = 0; ph ^= 1u; }
+        // ---------------- TMA producer (both CTAs) ----------------
+        // the whole warp walks the tiles and waits, one lane issues
+        int s = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        MxTile c(pair_id, p.nt, total, table);
+        for (int tile = pair_id; ok && tile < total;) {
+            const int trows = c.n / 2;  // this CTA's token rows: a multiple of 8, at most 96
+            const int trow = c.row0 + (int)rank * trows;
+            const int wrow = kGemm1 ? c.nt * X_UNITS + (int)rank * 64 : c.nt * X_BM + (int)rank * 128;
+            const uint32_t tx = 2u * (uint32_t)(X_W_BYTES + trows * X_ROW);
+            for (int kb = 0; kb < p.nk; ++kb) {
+                if (!__all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], ph ^ 1u, abort_flag))) {
+                    ok = false;
+                    break;
                 }
+                if (elect_one()) {
+                    if (leader) mbar_arrive_expect_tx(&full[s], tx);
+                    uint8_t *sw = ring + s * X_STAGE_BYTES;
+                    uint8_t *st = sw + X_W_BYTES;
+                    const uint32_t fb = full_leader + (uint32_t)(s * sizeof(uint64_t));
+                    tma_load_3d_pair(sw, &tmW0, fb, kb * X_ROW, wrow, c.expert);
+                    if (kGemm1)
+                        tma_load_3d_pair(sw + X_W_BYTES / 2, &tmW1, fb, kb * X_ROW, wrow, c.expert);
+                    int at = 0;
+                    if (trows & 64) {
+                        tma_load_2d_pair(st, &tmT64, fb, kb * X_ROW, trow);
+                        at = 64;
+                    }
+                    if (trows & 32) {
+                        tma_load_2d_pair(st + at * X_ROW, &tmT32, fb, kb * X_ROW, trow + at);
+                        at += 32;
+                    }
+                    if (trows & 16) {
+                        tma_load_2d_pair(st + at * X_ROW, &tmT16, fb, kb * X_ROW, trow + at);
+                        at += 16;
+                    }
+                    if (trows & 8)
+                        tma_load_2d_pair(st + at * X_ROW, &tmT8, fb, kb * X_ROW, trow + at);
+                }
+                __syncwarp();
+                if (++s == X_STAGES) { s = 0; ph ^= 1u; }
             }
+            tile += n_pairs;
+            c.step(dt, dn, p.nt, tile < total, table);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            // ---------------- MMA issuer ----------------
+        if (leader) {
+            // ---------------- MMA issuer (leader CTA) ----------------
             int s = 0;
             uint32_t ph = 0;
             bool ok = true;
             int it = 0;
-            for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x, ++it) {
+            const uint64_t w_desc0 = sdesc_kmajor_sw128(smem_u32(ring));
+            MxTile c(pair_id, p.nt, total, table);
+            for (int tile = pair_id; ok && tile < total; ++it) {
                 const int acc = it & 1;
-                if (!mbar_wait_bounded(&tempty[acc], ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag))
+                const uint32_t id0 = idesc_mxf4_f32(X_BM, c.n, 0), id2 = idesc_mxf4_f32(X_BM, c.n, 2);
+                if (!__all_sync(0xffffffffu, mbar_wait_bounded(
+                                                 &tempty[acc], ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag)))
                     break;
-                tc_fence_after();
                 const uint32_t d_tmem = tmem_base + (uint32_t)(acc * X_BN);
                 for (int kb = 0; kb < p.nk; ++kb) {
-                    if (!mbar_wait_bounded(&full[s], ph, abort_flag)) { ok = false; break; }
+                    if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[s], ph, abort_flag))) {
+                        ok = false;
+                        break;
+                    }
                     tc_fence_after();
-                    const uint32_t a_addr = smem_u32(ring + s * X_STAGE_BYTES);
-                    const uint32_t b_addr = a_addr + X_A_BYTES;
-                    const uint32_t f_addr = b_addr + X_B_BYTES;
-                    const uint32_t sfa = tmem_base + (uint32_t)(X_SF_COL + s * X_SF_COLS);
-                    const uint32_t sfb = sfa + 8;
-                    // blocks 0, 1: A's K halves; 2 + 2 half + rows / 128: B's.  The
-                    // copies and the MMAs of one thread execute in issue order.
-#pragma unroll
-                    for (int b = 0; b < 6; ++b)
-                        tc_cp_scales(sfa + 4 * b, sdesc_scales(f_addr + b * X_SF_BLOCK));
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        tc_mma_mxf4(d_tmem, sdesc_kmajor_sw128(a_addr + kk * 32),
-                                    sdesc_kmajor_sw128(b_addr + kk * 32),
-                                    idesc_mxf4_f32(X_BM, X_BN, 2 * (kk & 1)), sfa + 4 * (kk >> 1),
-                                    sfb + 8 * (kk >> 1), (kb | kk) != 0 ? 1u : 0u);
-                    tc_commit(&empty[s]);
-                    if (++s == stages) { s = 0; ph ^= 1u; }
+                    if (elect_one()) {
+                        // Descriptors count in 16 bytes and do not carry out of their
+                        // address field: all of shared memory is below 2^18.
+                        const uint64_t w_desc = w_desc0 + (uint64_t)(s * (X_STAGE_BYTES / 16));
+                        const uint64_t t_desc = w_desc + X_W_BYTES / 16;
+                        const uint32_t sfw = tmem_base + (uint32_t)(X_SF_COL + s * X_SF_COLS);
+                        const uint32_t sft = sfw + 8;
+                        tc_mma_mxf4_pair(d_tmem, w_desc, t_desc, id0, sfw, sft, kb != 0 ? 1u : 0u);
+                        tc_mma_mxf4_pair(d_tmem, w_desc + 2, t_desc + 2, id2, sfw, sft, 1u);
+                        tc_mma_mxf4_pair(d_tmem, w_desc + 4, t_desc + 4, id0, sfw + 4, sft + 8, 1u);
+                        tc_mma_mxf4_pair(d_tmem, w_desc + 6, t_desc + 6, id2, sfw + 4, sft + 8, 1u);
+                        tc_commit_pair(&empty[s], 0x3);
+                        if (kb == p.nk - 1) tc_commit_pair(&tfull[acc], 0x3);
+                    }
+                    __syncwarp();
+                    if (++s == X_STAGES) { s = 0; ph ^= 1u; }
                 }
-                if (!ok) break;
-                tc_commit(&tfull[acc]);
+                tile += n_pairs;
+                c.step(dt, dn, p.nt, tile < total, table);
             }
-            // every MMA issued here completes before TMEM is freed
-            tc_commit(drain);
+            // every MMA issued here completes before either CTA frees TMEM
+            if (elect_one()) tc_commit_pair(&drain[0], 0x1);
+            __syncwarp();
             volatile int local_abort = 0;
-            mbar_wait_bounded(drain, 0u, &local_abort);
+            mbar_wait_bounded(&drain[0], 0u, &local_abort);
         }
-    } else if (warp < 2 + X_EPI_WARPS) {
-        // ---------------- epilogue (warps 2..5) ----------------
+    } else if (warp == 2) {
+        if (leader) {
+            // ---------------- scale copies (leader CTA) ----------------
+            // A K block's scales go to the tensor memory of both CTAs as soon as
+            // the stage's last MMAs have completed; their completion is the
+            // second of the two arrivals that the stage's MMAs wait for.
+            int s = 0, sg = 0;
+            uint32_t ph = 0, phg = 0;
+            bool ok = true;
+            const uint64_t f_desc0 = sdesc_scales(smem_u32(sfs));
+            MxTile c(pair_id, p.nt, total, table);
+            for (int tile = pair_id; ok && tile < total;) {
+                const bool wide = c.n > 128;
+                for (int kb = 0; kb < p.nk; ++kb) {
+                    const int k4 = kb % X_GROUP;
+                    bool got = true;
+                    // the peer's scales were written by its threads: cluster acquire
+                    if (k4 == 0) got = mbar_wait_bounded(&sfull[sg], phg, abort_flag, true);
+                    got = got && mbar_wait_bounded(&empty[s], ph ^ 1u, abort_flag);
+                    if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+                    tc_fence_after();
+                    const bool last = k4 == X_GROUP - 1 || kb == p.nk - 1;
+                    if (elect_one()) {
+                        const uint64_t f_desc =
+                            f_desc0 + (uint64_t)(sg * (X_GROUP_BYTES / 16) + k4 * (X_SF_BYTES / 16));
+                        const uint32_t sfw = tmem_base + (uint32_t)(X_SF_COL + s * X_SF_COLS);
+                        const uint32_t sft = sfw + 8;
+                        // blocks 0, 1: the weights' K halves; 2 + 2 half + token / 128: the tokens'
+                        constexpr uint64_t kBlk = X_SF_BLOCK / 16;
+                        tc_cp_scales_pair(sfw, f_desc);
+                        tc_cp_scales_pair(sfw + 4, f_desc + kBlk);
+                        tc_cp_scales_pair(sft, f_desc + 2 * kBlk);
+                        tc_cp_scales_pair(sft + 8, f_desc + 4 * kBlk);
+                        if (wide) {
+                            tc_cp_scales_pair(sft + 4, f_desc + 3 * kBlk);
+                            tc_cp_scales_pair(sft + 12, f_desc + 5 * kBlk);
+                        }
+                        tc_commit_pair(&full[s], 0x1);
+                        if (last) tc_commit_pair(&sempty[sg], 0x3);
+                    }
+                    __syncwarp();
+                    if (++s == X_STAGES) { s = 0; ph ^= 1u; }
+                    if (last && ++sg == X_SF_WARPS) { sg = 0; phg ^= 1u; }
+                }
+                tile += n_pairs;
+                c.step(dt, dn, p.nt, tile < total, table);
+            }
+            if (elect_one()) tc_commit_pair(&drain[1], 0x1);
+            __syncwarp();
+            volatile int local_abort = 0;
+            mbar_wait_bounded(&drain[1], 0u, &local_abort);
+        }
+    } else if (warp >= 3 + X_SF_WARPS) {
+        // ---------------- epilogue (both CTAs) ----------------
         const int q = warp & 3;  // TMEM lane quarter this warp may access
-        const int r = q * 32 + lane;
+        const int ew = warp - 3 - X_SF_WARPS, eg = ew >> 2;
+        const uint32_t tempty_leader = mapa_shared(smem_u32(&tempty[0]), 0);
         int it = 0;
-        for (int tile = blockIdx.x; tile < total; tile += gridDim.x, ++it) {
-            const MxTile c = decode_tile(tile, p, s_mtoff, s_base, s_valid);
+        bool over = false;  // a stored y beyond the fp16 range
+        MxTile c(pair_id, p.nt, total, table);
+        for (int tile = pair_id; tile < total; ++it) {
             const int acc = it & 1;
             const bool got = mbar_wait_bounded(&tfull[acc], (uint32_t)(it >> 1) & 1u, abort_flag);
-            if (!__all_sync(0xffffffffu, got)) break;
+            // a group's warps go on, or stop, together
+            if (!bar_and(X_EPI_BAR + eg, 128, got)) break;
             tc_fence_after();
-            const bool row_ok = r < c.nvalid;
             const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * X_BN);
-            if (q * 32 < c.nvalid) {
-                if (kGemm1) {
-                    const size_t row = (size_t)(c.row0 + (row_ok ? r : 0));
-#pragma unroll 1
-                    for (int b = 0; b < X_UNITS / 32; ++b) {
-                        const int unit = c.nt * X_UNITS + b * 32;
-                        if (unit >= p.n_out) break;  // uniform: H_local is a multiple of 32
-                        uint32_t g[32], u[32];
-                        tmem_ld_32x32b_x32(tb + b * 32, g);
-                        tmem_ld_32x32b_x32(tb + X_UNITS + b * 32, u);
-                        tc_wait_ld();
-                        float h[32];
-                        uint32_t top = 0;
+            if (kGemm1) {
+                // lanes 0-63 are the gates of units `unit0`.., 64-127 their ups
+                const int unit0 = c.nt * X_UNITS + (int)rank * 64;
+                const int tok = (q & 1) * 16 + (lane >> 1);   // of the 32 in the buffer
+                const int unit = unit0 + (q >> 1) * 32 + (lane & 1) * 16;
+                float *buf = reinterpret_cast<float *>(turn) + eg * (32 * X_TURN_LD);
+                for (int t0 = 32 * eg; t0 < c.nvalid; t0 += 32 * X_EPI_GROUPS) {
+                    uint32_t d[32];
+                    tmem_ld_32x32b_x32(tb + t0, d);
+                    tc_wait_ld();
+                    bar_sync(X_EPI_BAR + eg, 128);  // the group has read its last chunk
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            h[i] = mx_silu(__uint_as_float(g[i])) * __uint_as_float(u[i]);
-                            top = max(top, abs_bits(h[i]));
-                        }
-                        const uint32_t sb = mx_scale_byte(top);
-                        const float inv = mx_inv_scale(sb);
-                        uint32_t w[4];
+                    for (int j = 0; j < 32; ++j)
+                        buf[j * X_TURN_LD + q * 32 + lane] = __uint_as_float(d[j]);
+                    bar_sync(X_EPI_BAR + eg, 128);
+                    const float *src = buf + tok * X_TURN_LD + (q >> 1) * 32 + (lane & 1) * 16;
+                    float h[16];
+                    uint32_t top = 0;
 #pragma unroll
-                        for (int v = 0; v < 4; ++v)
-                            w[v] = mx_codes8(*reinterpret_cast<const float(*)[8]>(h + 8 * v), inv);
-                        if (row_ok) {
-                            *reinterpret_cast<uint4 *>(p.hq + row * (size_t)(p.n_out / 2) + unit / 2) =
-                                make_uint4(w[0], w[1], w[2], w[3]);
+                    for (int v = 0; v < 4; ++v) {
+                        const float4 g = *reinterpret_cast<const float4 *>(src + 4 * v);
+                        const float4 u = *reinterpret_cast<const float4 *>(src + 64 + 4 * v);
+                        h[4 * v] = mx_silu(g.x) * u.x;
+                        h[4 * v + 1] = mx_silu(g.y) * u.y;
+                        h[4 * v + 2] = mx_silu(g.z) * u.z;
+                        h[4 * v + 3] = mx_silu(g.w) * u.w;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) top = max(top, abs_bits(h[i]));
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    const uint32_t sb = mx_scale_byte(top);
+                    const float inv = mx_inv_scale(sb);
+                    if (t0 + tok < c.nvalid && unit < p.n_out) {
+                        const size_t row = (size_t)(c.row0 + t0 + tok);
+                        *reinterpret_cast<uint2 *>(p.hq + row * (size_t)(p.n_out / 2) + unit / 2) =
+                            make_uint2(mx_codes8(*reinterpret_cast<const float(*)[8]>(h), inv),
+                                       mx_codes8(*reinterpret_cast<const float(*)[8]>(h + 8), inv));
+                        if ((lane & 1) == 0)
                             p.hsf[row * (size_t)(p.n_out / 32) + unit / 32] = (uint8_t)sb;
-                        }
                     }
-                } else {
-                    __half *yrow = p.y + (size_t)(c.row0 + (row_ok ? r : 0)) * p.n_out;
-                    bool over = false;  // a stored value beyond the fp16 range
-#pragma unroll 1
-                    for (int b = 0; b < X_BN / 32; ++b) {
-                        const int col0 = c.nt * X_BN + b * 32;
-                        if (col0 >= p.n_out) break;  // uniform: D is a multiple of 32
+                }
+            } else {
+                // lane = column of y; 32 columns of the warp, 32 tokens at a time
+                const int col0 = c.nt * X_BM + (int)rank * 128 + q * 32;
+                __half *buf = reinterpret_cast<__half *>(turn + ew * (32 * 64));
+                if (col0 < p.n_out) {  // uniform: D is a multiple of 32
+                    for (int t0 = 32 * eg; t0 < c.nvalid; t0 += 32 * X_EPI_GROUPS) {
                         uint32_t d[32];
-                        tmem_ld_32x32b_x32(tb + b * 32, d);
+                        tmem_ld_32x32b_x32(tb + t0, d);
                         tc_wait_ld();
-                        if (!row_ok) continue;
+                        __syncwarp();  // the last chunk has been read
 #pragma unroll
-                        for (int v = 0; v < 4; ++v) {
-                            uint32_t w[4];
+                        for (int j = 0; j < 32; ++j) {
+                            const float v = __uint_as_float(d[j]);
+                            over |= t0 + j < c.nvalid && fabsf(v) >= kHalfOverflow;
+                            buf[j * 32 + lane] = __float2half_rn(v);
+                        }
+                        __syncwarp();
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float lo = __uint_as_float(d[v * 8 + 2 * i]);
-                                const float hi = __uint_as_float(d[v * 8 + 2 * i + 1]);
-                                over |= fabsf(lo) >= kHalfOverflow || fabsf(hi) >= kHalfOverflow;
-                                w[i] = pack_half2(lo, hi);
-                            }
-                            *reinterpret_cast<uint4 *>(yrow + col0 + v * 8) =
-                                make_uint4(w[0], w[1], w[2], w[3]);
+                        for (int i = 0; i < 4; ++i) {
+                            const int tok = 8 * i + (lane >> 2);
+                            if (t0 + tok < c.nvalid)
+                                *reinterpret_cast<uint4 *>(
+                                    p.y + (size_t)(c.row0 + t0 + tok) * p.n_out + col0 + (lane & 3) * 8) =
+                                    *reinterpret_cast<const uint4 *>(buf + tok * 32 + (lane & 3) * 8);
                         }
                     }
-                    if (__any_sync(0xffffffffu, over) && lane == 0) raise_flag(p.status, FLAG_RANGE);
                 }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&tempty[acc]);
+            if (lane == 0) mbar_arrive_cluster(tempty_leader + (uint32_t)(acc * sizeof(uint64_t)));
+            tile += n_pairs;
+            c.step(dt, dn, p.nt, tile < total, table);
         }
+        if (!kGemm1 && __any_sync(0xffffffffu, over) && lane == 0) raise_flag(p.status, FLAG_RANGE);
     } else {
-        // ---------------- scales (warps 6..9) ----------------
-        // Warp g fills the stages n with n % 4 == g.  Lane l fetches the 8
-        // scales of the stage's K block for operand rows l, l + 32, ... (in
-        // flight while the stage is still busy) and stores, for each K half of
-        // 128 and each 128 rows, the 16 bytes of rows l, +32, +64, +96.
-        const int gw = warp - 2 - X_EPI_WARPS;
-        const int ld = p.K / 32;
-        int s = 0;
-        uint32_t ph = 0, n = 0;
-        bool ok = true;
-        for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
-            const MxTile c = decode_tile(tile, p, s_mtoff, s_base, s_valid);
-            for (int kb = 0; kb < p.nk; ++kb, ++n) {
-                if ((int)(n % X_SF_WARPS) == gw) {
-                    uint2 a[4], b[8];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        a[i] = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
-                        if (lane + 32 * i < c.nvalid)
-                            a[i] = load_scales(p.a_sf + (size_t)(c.row0 + lane + 32 * i) * ld, kb, ld);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        b[i] = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
-                        if (i >= X_BN / 32) continue;
-                        // operand row lane + 32 i: a gate or an up row, or a row of w2
-                        const bool up = kGemm1 && i >= X_UNITS / 32;
-                        const int wr = kGemm1 ? c.nt * X_UNITS + lane + 32 * (up ? i - X_UNITS / 32 : i)
-                                              : c.nt * X_BN + lane + 32 * i;
-                        if (wr < p.n_out)
-                            b[i] = load_scales((up ? p.b_sf1 : p.b_sf0) +
-                                                   ((size_t)c.expert * p.n_out + wr) * ld, kb, ld);
-                    }
-                    bool got = true;
-                    if (lane == 0) got = mbar_wait_bounded(&empty[s], ph ^ 1u, abort_flag);
-                    if (!__shfl_sync(0xffffffffu, got, 0)) { ok = false; break; }
-                    uint4 *f = reinterpret_cast<uint4 *>(ring + s * X_STAGE_BYTES + X_A_BYTES + X_B_BYTES) + lane;
-                    f[0] = make_uint4(a[0].x, a[1].x, a[2].x, a[3].x);
-                    f[32] = make_uint4(a[0].y, a[1].y, a[2].y, a[3].y);
-                    f[64] = make_uint4(b[0].x, b[1].x, b[2].x, b[3].x);
-                    f[96] = make_uint4(b[4].x, b[5].x, b[6].x, b[7].x);
-                    f[128] = make_uint4(b[0].y, b[1].y, b[2].y, b[3].y);
-                    f[160] = make_uint4(b[4].y, b[5].y, b[6].y, b[7].y);
-                    fence_proxy_async_smem();  // tcgen05.cp reads them through the async proxy
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&full[s]);
-                }
-                if (++s == stages) { s = 0; ph ^= 1u; }
+        // ---------------- scale fetchers (both CTAs) ----------------
+        // Warp w takes every third group of four K blocks, whole: 32 bytes of
+        // each of the CTA's 128 weight rows and of the tile's tokens (all of
+        // them: each CTA's half of the MMA needs all).  Lane l serves rows
+        // l, l + 32, ...  A group's loads are issued when the warp's last one
+        // is stored, and are done before the next fence and arrival, which
+        // would wait for them.
+        const int w = warp - 3;
+        const int ld = p.K / 32, ng = (p.nk + X_GROUP - 1) / X_GROUP;
+        const size_t t_total = (size_t)p.rows_alloc * ld, w_total = (size_t)p.E_local * p.n_out * ld;
+        const uint32_t sfull_leader = mapa_shared(smem_u32(&sfull[w]), 0);
+        uint4 *f = reinterpret_cast<uint4 *>(sfs + w * X_GROUP_BYTES) + lane;
+        uint32_t ph = 0;
+        MxTile c(pair_id, p.nt, total, table);
+        int kg = w;
+        for (int tile = pair_id;; kg += X_SF_WARPS) {
+            while (kg >= ng && tile < total) {
+                kg -= ng;
+                tile += n_pairs;
+                c.step(dt, dn, p.nt, tile < total, table);
             }
+            if (tile >= total) break;
+            uint32_t wv[4][8], tv[8][8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int wr = kGemm1 ? c.nt * X_UNITS + (int)rank * 64 + (i & 1) * 32 + lane
+                                      : c.nt * X_BM + (int)rank * 128 + i * 32 + lane;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) wv[i][j] = kMxOnes;
+                if (wr < p.n_out)
+                    load_scales32(kGemm1 && i >= 2 ? p.w_sf1 : p.w_sf0,
+                                  (size_t)c.expert * p.n_out + wr, ld, w_total, kg, wv[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) tv[i][j] = kMxOnes;
+                if (i < X_BN / 32 && i * 32 + lane < c.nvalid)
+                    load_scales32(p.t_sf, (size_t)(c.row0 + i * 32 + lane), ld, t_total, kg, tv[i]);
+            }
+            // lane 0 waits for the group's room, the warp follows it
+            bool got = true;
+            if (lane == 0) got = mbar_wait_bounded(&sempty[w], ph ^ 1u, abort_flag);
+            if (!__shfl_sync(0xffffffffu, got, 0)) break;
+            ph ^= 1u;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {  // K block j / 2 of the group, its half j % 2
+                uint4 *d = f + (j / 2) * (X_SF_BYTES / 16);
+                const int h = j & 1;
+                d[32 * h] = make_uint4(wv[0][j], wv[1][j], wv[2][j], wv[3][j]);
+                d[32 * (2 + 2 * h)] = make_uint4(tv[0][j], tv[1][j], tv[2][j], tv[3][j]);
+                if (c.n > 128)
+                    d[32 * (3 + 2 * h)] = make_uint4(tv[4][j], tv[5][j], tv[6][j], tv[7][j]);
+            }
+            fence_proxy_async_smem();  // tcgen05.cp reads them through the async proxy
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(sfull_leader);
         }
     }
 
     tc_fence_before();
     __syncthreads();
+    // after an abort loads may be in flight for stages the MMA warp never
+    // consumed; the peer waits at the cluster barrier too
+    if (threadIdx.x == 0 && *abort_flag) settle_inflight_copies();
+    cluster_sync();  // the leader's MMAs (which read both CTAs' smem) are done
     if (threadIdx.x == 0 && *abort_flag) {
-        // loads may be in flight for stages the MMA warp never consumed
-        settle_inflight_copies();
         raise_flag(p.status, FLAG_TIMEOUT);
         atomicCAS(p.status + 1, 0, 1 + blockIdx.x);
     }
-    __syncthreads();
-    if (warp == 1) {
+    if (warp == 2) {
         tc_fence_after();
-        tmem_dealloc(tmem_base, X_TMEM_COLS);
+        tmem_dealloc_pair(tmem_base, X_TMEM_COLS);
     }
+}
+
+// Clusters of two that fit at once on the current device (0 if none).
+template <bool kGemm1>
+int max_mx_clusters(size_t smem) {
+    constexpr int kMaxDev = 64;
+    static int cached[kMaxDev] = {0};
+    static size_t cached_smem[kMaxDev] = {0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return 0;
+    if (cached[dev] > 0 && cached_smem[dev] == smem) return cached[dev];
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * 256);
+    cfg.blockDim = dim3(X_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, (void *)grouped_mx_kernel<kGemm1>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    cached[dev] = n;
+    cached_smem[dev] = smem;
+    return n;
+}
+
+struct MxMaps {
+    CUtensorMap t8, t16, t32, t64, w0, w1;
+};
+
+bool token_maps(MxMaps *m, const uint8_t *codes, int K, int64_t rows) {
+    return make_tmap_tile(&m->t8, codes, 1, K / 2, rows, 0, X_ROW, 8, 128) &&
+           make_tmap_tile(&m->t16, codes, 1, K / 2, rows, 0, X_ROW, 16, 128) &&
+           make_tmap_tile(&m->t32, codes, 1, K / 2, rows, 0, X_ROW, 32, 128) &&
+           make_tmap_tile(&m->t64, codes, 1, K / 2, rows, 0, X_ROW, 64, 128);
+}
+
+template <bool kGemm1>
+cudaError_t launch_mx(const MxMaps &m, const MxParams &p, long long token_tiles, cudaStream_t stream) {
+    const size_t smem = mx_smem_bytes(kGemm1, p.E_local);
+    static_assert(1024 + X_STAGES * X_STAGE_BYTES + X_SF_WARPS * X_GROUP_BYTES + X_TURN1 +
+                          (X_NBARS + 1) * 8 + 16 + 4 * (4 * 1024 + 1) <= X_SMEM_MAX,
+                  "the table of 1024 experts fits beside the ring");
+    cudaError_t e = ensure_smem((const void *)grouped_mx_kernel<kGemm1>, smem);
+    if (e != cudaSuccess) return e;
+    const int clusters = max_mx_clusters<kGemm1>(smem);
+    if (clusters <= 0) return cudaErrorInvalidConfiguration;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (unsigned)std::min<long long>(clusters, token_tiles * p.nt));
+    cfg.blockDim = dim3(X_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = MOE_PDL ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, grouped_mx_kernel<kGemm1>, m.t8, m.t16, m.t32, m.t64, m.w0, m.w1, p);
+    if (e == cudaSuccess) count_launch();
+    return e;
 }
 
 }  // namespace
@@ -397,33 +695,20 @@ cudaError_t launch_grouped_swiglu_mxfp4(const uint8_t *x_perm_q, const uint8_t *
                                         int64_t rows_alloc, int *status, cudaStream_t stream) {
     if (E_local == 0 || rows_alloc == 0) return cudaSuccess;
     if (D % 32 || H_local % 32) return cudaErrorInvalidValue;
-    // five stages leave room for the table of about 850 experts, four for any
-    int stages = X_MAX_STAGES;
-    while (stages > 1 && mx_smem_bytes(stages, E_local) > X_SMEM_MAX) --stages;
-    const size_t smem = mx_smem_bytes(stages, E_local);
-    cudaError_t e = ensure_smem((const void *)grouped_mx_kernel<true>, smem);
-    if (e == cudaSuccess) e = ensure_smem((const void *)grouped_mx_kernel<false>, smem);
-    if (e != cudaSuccess) return e;
-    const int sms = sm_count();
-    if (sms <= 0) return cudaErrorInvalidDevice;
-
-    CUtensorMap x, x16, b0, b1, h, h16, b2;
-    if (!make_tmap_tile(&x, x_perm_q, 1, D / 2, rows_alloc, 0, X_ROW, X_BM, 128) ||
-        !make_tmap_tile(&x16, x_perm_q, 1, D / 2, rows_alloc, 0, X_ROW, 16, 128) ||
-        !make_tmap_tile(&b0, w.w1, 1, D / 2, H_local, E_local, X_ROW, X_UNITS, 128) ||
-        !make_tmap_tile(&b1, w.w3, 1, D / 2, H_local, E_local, X_ROW, X_UNITS, 128) ||
-        !make_tmap_tile(&h, h_q, 1, H_local / 2, rows_alloc, 0, X_ROW, X_BM, 128) ||
-        !make_tmap_tile(&h16, h_q, 1, H_local / 2, rows_alloc, 0, X_ROW, 16, 128) ||
-        !make_tmap_tile(&b2, w.w2, 1, H_local / 2, D, E_local, X_ROW, X_BN, 128))
+    MxMaps m1, m2;
+    if (!token_maps(&m1, x_perm_q, D, rows_alloc) || !token_maps(&m2, h_q, H_local, rows_alloc) ||
+        !make_tmap_tile(&m1.w0, w.w1, 1, D / 2, H_local, E_local, X_ROW, 64, 128) ||
+        !make_tmap_tile(&m1.w1, w.w3, 1, D / 2, H_local, E_local, X_ROW, 64, 128) ||
+        !make_tmap_tile(&m2.w0, w.w2, 1, H_local / 2, D, E_local, X_ROW, 128, 128))
         return cudaErrorInvalidValue;
+    m2.w1 = m2.w0;
 
-    // m-tiles: at most one partial tile per expert beside the whole ones
-    const long long mt = std::min<long long>(rows_alloc, rows_alloc / X_BM + E_local);
+    // token tiles: at most one partial tile per expert beside the whole ones
+    const long long tt = std::min<long long>(rows_alloc, rows_alloc / X_BN + E_local);
     MxParams p{};
     p.E_local = E_local;
     p.e_first = e_first;
     p.rows_alloc = (int)rows_alloc;
-    p.stages = stages;
     p.seg_off = seg_offsets;
     p.tpe = tokens_per_expert;
     p.status = status;
@@ -433,28 +718,23 @@ cudaError_t launch_grouped_swiglu_mxfp4(const uint8_t *x_perm_q, const uint8_t *
     p1.nk = (D + X_BK - 1) / X_BK;
     p1.n_out = H_local;
     p1.nt = (H_local + X_UNITS - 1) / X_UNITS;
-    p1.a_sf = x_scale;
-    p1.b_sf0 = w.w1_scale;
-    p1.b_sf1 = w.w3_scale;
+    p1.t_sf = x_scale;
+    p1.w_sf0 = w.w1_scale;
+    p1.w_sf1 = w.w3_scale;
     p1.hq = h_q;
     p1.hsf = h_scale;
-    e = launch_pdl(grouped_mx_kernel<true>, dim3((unsigned)std::min<long long>(sms, mt * p1.nt)),
-                   dim3(X_THREADS), smem, stream, x, x16, b0, b1, p1);
+    const cudaError_t e = launch_mx<true>(m1, p1, tt, stream);
     if (e != cudaSuccess) return e;
-    count_launch();
 
     MxParams p2 = p;
     p2.K = H_local;
     p2.nk = (H_local + X_BK - 1) / X_BK;
     p2.n_out = D;
-    p2.nt = (D + X_BN - 1) / X_BN;
-    p2.a_sf = h_scale;
-    p2.b_sf0 = p2.b_sf1 = w.w2_scale;
+    p2.nt = (D + X_BM - 1) / X_BM;
+    p2.t_sf = h_scale;
+    p2.w_sf0 = p2.w_sf1 = w.w2_scale;
     p2.y = static_cast<__half *>(y_perm);
-    e = launch_pdl(grouped_mx_kernel<false>, dim3((unsigned)std::min<long long>(sms, mt * p2.nt)),
-                   dim3(X_THREADS), smem, stream, h, h16, b2, b2, p2);
-    if (e == cudaSuccess) count_launch();
-    return e;
+    return launch_mx<false>(m2, p2, tt, stream);
 }
 
 }  // namespace moe
