@@ -383,6 +383,14 @@ __device__ __forceinline__ void bar_sync(int id, int threads) {
     asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+// The same without ordering, for an arrival that publishes no memory: a release
+// waits until the thread's stores in flight (a tile's output) have landed, about
+// 2500 cycles after the epilogue of a grouped MXFP4 tile.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+                 : "memory");
+}
+
 // Every thread of every CTA of the cluster; the warp is reconverged first
 // because the .aligned forms require it.
 __device__ __forceinline__ void cluster_sync() {

@@ -175,49 +175,68 @@ __device__ __forceinline__ float mx_silu(float g) { return __fdividef(g, 1.f + _
 
 constexpr uint32_t kMxOnes = 0x7f7f7f7fu;  // four scales of 1
 
-// Bytes [32 kg, 32 kg + 32) of row `row` of scales [.., ld] (`total` bytes in
-// all, 16-byte aligned), 1.0 past the row's end (the codes there are zeros).
-__device__ __forceinline__ void load_scales32(const uint8_t *__restrict__ base, size_t row, int ld,
-                                              size_t total, int kg, uint32_t (&v)[8]) {
-    const int n = ld - 32 * kg;  // bytes left in the row
-    const size_t off = row * ld + 32 * kg;
+// Bytes [32 kg, 32 kg + 32) of each of N rows of scales [.., ld] (`total` bytes
+// in all, 16-byte aligned), 1.0 past the row's end (the codes there are zeros)
+// and for a row that is not `there`.  The rows' alignment is looked at once, not
+// row by row, so that every load is issued before any of them is used.
+template <int N>
+__device__ __forceinline__ void load_scales32(const uint8_t *const (&base)[N], const size_t (&row)[N],
+                                              const bool (&there)[N], int ld, const size_t (&total)[N],
+                                              int kg, uint32_t (&v)[N][8]) {
+    const int n = ld - 32 * kg;  // bytes left in a row
     if ((ld & 15) == 0) {
-        const uint4 *q = reinterpret_cast<const uint4 *>(base + off);
-        const uint4 a = q[0];
-        uint4 b = make_uint4(kMxOnes, kMxOnes, kMxOnes, kMxOnes);
-        if (n > 16) b = q[1];
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+#pragma unroll
+        for (int r = 0; r < N; ++r) {
+            const uint4 *q = reinterpret_cast<const uint4 *>(base[r] + row[r] * ld + 32 * kg);
+            uint4 a = make_uint4(kMxOnes, kMxOnes, kMxOnes, kMxOnes), b = a;
+            if (there[r]) a = q[0];
+            if (there[r] && n > 16) b = q[1];
+            v[r][0] = a.x; v[r][1] = a.y; v[r][2] = a.z; v[r][3] = a.w;
+            v[r][4] = b.x; v[r][5] = b.y; v[r][6] = b.z; v[r][7] = b.w;
+        }
         return;
     }
     if ((ld & 3) == 0) {
-        const uint32_t *q = reinterpret_cast<const uint32_t *>(base + off);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 4 * i < n ? q[i] : kMxOnes;
+        for (int r = 0; r < N; ++r) {
+            const uint32_t *q = reinterpret_cast<const uint32_t *>(base[r] + row[r] * ld + 32 * kg);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                uint32_t x = kMxOnes;
+                if (there[r] && 4 * i < n) x = q[i];
+                v[r][i] = x;
+            }
+        }
         return;
     }
     // rows at any byte: the aligned words around the 32 bytes, shifted together
-    const size_t a = off & ~(size_t)3;
-    const int sh = 8 * (int)(off & 3);
-    const int words = (min(n, 32) + (sh >> 3) + 3) / 4;
-    uint32_t w[9];
 #pragma unroll
-    for (int i = 0; i < 9; ++i)
-        w[i] = i < words && a + 4 * i + 4 <= total ? *reinterpret_cast<const uint32_t *>(base + a + 4 * i)
-                                                   : 0u;
-    if (a + 4 * words > total)  // the array's last, partial word
-        for (size_t at = total & ~(size_t)3; at < total; ++at) {
-            const int i = (int)(at - a) / 4;
+    for (int r = 0; r < N; ++r) {
+        const size_t off = row[r] * ld + 32 * kg, a = off & ~(size_t)3;
+        const int sh = 8 * (int)(off & 3);
+        const int words = there[r] ? (min(n, 32) + (sh >> 3) + 3) / 4 : 0;
+        const uint8_t *src = base[r] + a;
+        uint32_t w[9];
 #pragma unroll
-            for (int j = 0; j < 9; ++j)
-                if (j == i) w[j] |= (uint32_t)base[at] << (8 * (int)(at & 3));
+        for (int i = 0; i < 9; ++i) {
+            w[i] = 0;
+            if (i < words && a + 4 * i + 4 <= total[r])
+                w[i] = *reinterpret_cast<const uint32_t *>(src + 4 * i);
         }
+        if (words && a + 4 * words > total[r])  // the array's last, partial word
+            for (size_t at = total[r] & ~(size_t)3; at < total[r]; ++at) {
+                const int i = (int)(at - a) / 4;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        v[i] = __funnelshift_r(w[i], w[i + 1], sh);
-        const int left = n - 4 * i;
-        if (left <= 0) v[i] = kMxOnes;
-        else if (left < 4) v[i] = (v[i] & ((1u << (8 * left)) - 1u)) | (kMxOnes << (8 * left));
+                for (int j = 0; j < 9; ++j)
+                    if (j == i) w[j] |= (uint32_t)base[r][at] << (8 * (int)(at & 3));
+            }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[r][i] = __funnelshift_r(w[i], w[i + 1], sh);
+            const int left = there[r] ? n - 4 * i : 0;
+            if (left <= 0) v[r][i] = kMxOnes;
+            else if (left < 4) v[r][i] = (v[r][i] & ((1u << (8 * left)) - 1u)) | (kMxOnes << (8 * left));
+        }
     }
 }
 
@@ -463,16 +482,29 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
             if (!bar_and(X_EPI_BAR + eg, 128, got)) break;
             tc_fence_after();
             const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * X_BN);
+            // The accumulator is the MMA's again once this warp has its last chunk
+            // in registers; nothing in memory goes with that.
+            auto release = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_cluster_relaxed(tempty_leader + (uint32_t)(acc * sizeof(uint64_t)));
+            };
+            const int step = 32 * X_EPI_GROUPS;
+            const bool none = 32 * eg >= c.nvalid ||
+                              (!kGemm1 && c.nt * X_BM + (int)rank * 128 + q * 32 >= p.n_out);
+            if (none) release();
             if (kGemm1) {
                 // lanes 0-63 are the gates of units `unit0`.., 64-127 their ups
                 const int unit0 = c.nt * X_UNITS + (int)rank * 64;
                 const int tok = (q & 1) * 16 + (lane >> 1);   // of the 32 in the buffer
                 const int unit = unit0 + (q >> 1) * 32 + (lane & 1) * 16;
                 float *buf = reinterpret_cast<float *>(turn) + eg * (32 * X_TURN_LD);
-                for (int t0 = 32 * eg; t0 < c.nvalid; t0 += 32 * X_EPI_GROUPS) {
+                for (int t0 = 32 * eg; t0 < c.nvalid; t0 += step) {
                     uint32_t d[32];
                     tmem_ld_32x32b_x32(tb + t0, d);
                     tc_wait_ld();
+                    if (t0 + step >= c.nvalid) release();
                     bar_sync(X_EPI_BAR + eg, 128);  // the group has read its last chunk
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
@@ -508,11 +540,12 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
                 // lane = column of y; 32 columns of the warp, 32 tokens at a time
                 const int col0 = c.nt * X_BM + (int)rank * 128 + q * 32;
                 __half *buf = reinterpret_cast<__half *>(turn + ew * (32 * 64));
-                if (col0 < p.n_out) {  // uniform: D is a multiple of 32
-                    for (int t0 = 32 * eg; t0 < c.nvalid; t0 += 32 * X_EPI_GROUPS) {
+                if (!none) {  // (D is a multiple of 32: a warp's columns are all there or none is)
+                    for (int t0 = 32 * eg; t0 < c.nvalid; t0 += step) {
                         uint32_t d[32];
                         tmem_ld_32x32b_x32(tb + t0, d);
                         tc_wait_ld();
+                        if (t0 + step >= c.nvalid) release();
                         __syncwarp();  // the last chunk has been read
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {
@@ -532,9 +565,6 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
                     }
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(tempty_leader + (uint32_t)(acc * sizeof(uint64_t)));
             tile += n_pairs;
             c.step(dt, dn, p.nt, tile < total, table);
         }
@@ -562,24 +592,30 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
                 c.step(dt, dn, p.nt, tile < total, table);
             }
             if (tile >= total) break;
-            uint32_t wv[4][8], tv[8][8];
+            // 4 weight rows and up to 6 tokens of this lane
+            constexpr int kRows = 4 + X_BN / 32;
+            const uint8_t *base[kRows];
+            size_t row[kRows], all[kRows];
+            bool there[kRows];
+            uint32_t v[kRows][8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int wr = kGemm1 ? c.nt * X_UNITS + (int)rank * 64 + (i & 1) * 32 + lane
-                                      : c.nt * X_BM + (int)rank * 128 + i * 32 + lane;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) wv[i][j] = kMxOnes;
-                if (wr < p.n_out)
-                    load_scales32(kGemm1 && i >= 2 ? p.w_sf1 : p.w_sf0,
-                                  (size_t)c.expert * p.n_out + wr, ld, w_total, kg, wv[i]);
+            for (int i = 0; i < kRows; ++i) {
+                if (i < 4) {
+                    const int wr = kGemm1 ? c.nt * X_UNITS + (int)rank * 64 + (i & 1) * 32 + lane
+                                          : c.nt * X_BM + (int)rank * 128 + i * 32 + lane;
+                    there[i] = wr < p.n_out;
+                    base[i] = kGemm1 && i >= 2 ? p.w_sf1 : p.w_sf0;
+                    row[i] = (size_t)c.expert * p.n_out + wr;
+                    all[i] = w_total;
+                } else {
+                    const int tr = (i - 4) * 32 + lane;
+                    there[i] = tr < c.nvalid;
+                    base[i] = p.t_sf;
+                    row[i] = (size_t)(c.row0 + tr);
+                    all[i] = t_total;
+                }
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) tv[i][j] = kMxOnes;
-                if (i < X_BN / 32 && i * 32 + lane < c.nvalid)
-                    load_scales32(p.t_sf, (size_t)(c.row0 + i * 32 + lane), ld, t_total, kg, tv[i]);
-            }
+            load_scales32<kRows>(base, row, there, ld, all, kg, v);
             // lane 0 waits for the group's room, the warp follows it
             bool got = true;
             if (lane == 0) got = mbar_wait_bounded(&sempty[w], ph ^ 1u, abort_flag);
@@ -589,10 +625,10 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
             for (int j = 0; j < 8; ++j) {  // K block j / 2 of the group, its half j % 2
                 uint4 *d = f + (j / 2) * (X_SF_BYTES / 16);
                 const int h = j & 1;
-                d[32 * h] = make_uint4(wv[0][j], wv[1][j], wv[2][j], wv[3][j]);
-                d[32 * (2 + 2 * h)] = make_uint4(tv[0][j], tv[1][j], tv[2][j], tv[3][j]);
-                if (c.n > 128)
-                    d[32 * (3 + 2 * h)] = make_uint4(tv[4][j], tv[5][j], tv[6][j], tv[7][j]);
+                d[32 * h] = make_uint4(v[0][j], v[1][j], v[2][j], v[3][j]);
+                d[32 * (2 + 2 * h)] = make_uint4(v[4][j], v[5][j], v[6][j], v[7][j]);
+                if (c.n > 128)  // (rows 192 on do not exist)
+                    d[32 * (3 + 2 * h)] = make_uint4(v[8][j], v[9][j], kMxOnes, kMxOnes);
             }
             fence_proxy_async_smem();  // tcgen05.cp reads them through the async proxy
             __syncwarp();
