@@ -25,7 +25,7 @@
 //     overwritten under an MMA and nothing waits for that but the stage itself;
 //   * scales are read in their natural [rows, K / 32] layout, which is not the
 //     order the tensor cores want (four scales each of rows l, l + 32, l + 64
-//     and l + 96 together).  Three warps fetch them, 32 bytes of a row -- one
+//     and l + 96 together).  Warps fetch them, 32 bytes of a row -- one
 //     sector, four K blocks -- at a time, and store them as 512-byte blocks for
 //     tcgen05.cp, in a ring of their own with one fence and one arrival for four
 //     K blocks;
@@ -59,7 +59,8 @@ constexpr int X_STAGES = 5;
 // Warps: TMA, MMA, scale copies, scale fetchers, epilogue.
 constexpr int X_GROUP = 4;            // K blocks whose scales are fetched together (32 bytes of a row)
 constexpr int X_GROUP_BYTES = X_GROUP * X_SF_BYTES;
-constexpr int X_SF_WARPS = 3;         // one group each in shared memory, one each in flight
+constexpr int X_SLOTS = 3;            // groups in shared memory
+constexpr int X_SF_WARPS = 2 * X_SLOTS;  // per slot one for the weights' scales, one for the tokens'
 constexpr int X_EPI_GROUPS = 2;       // of four warps (the TMEM lane quarters), alternate chunks of a tile
 constexpr int X_EPI_WARPS = 4 * X_EPI_GROUPS;
 constexpr int X_THREADS = 32 * (3 + X_SF_WARPS + X_EPI_WARPS);
@@ -68,7 +69,7 @@ constexpr int X_SF_COL = 2 * X_BN;    // scale buffers start here
 constexpr int X_SF_COLS = 24;         // 2 x 4 of the weights, 2 x 8 of the tokens
 static_assert(X_SF_COL + X_STAGES * X_SF_COLS <= X_TMEM_COLS, "tensor memory columns");
 static_assert(X_STAGE_BYTES % 1024 == 0 && X_T_BYTES % 1024 == 0, "the swizzle's alignment");
-constexpr int X_NBARS = 2 * X_STAGES + 2 * X_SF_WARPS + 6;
+constexpr int X_NBARS = 2 * X_STAGES + 2 * X_SLOTS + 6;
 constexpr int X_SMEM_MAX = 227 * 1024;
 // GEMM1's turning buffer, per epilogue group: 32 tokens x (64 gates, 64 ups, 4 of padding)
 constexpr int X_TURN_LD = 132;
@@ -90,7 +91,7 @@ struct MxParams {
 };
 
 size_t mx_smem_bytes(bool gemm1, int E_local) {
-    return 1024 + (size_t)X_STAGES * X_STAGE_BYTES + X_SF_WARPS * X_GROUP_BYTES + (gemm1 ? X_TURN1 : X_TURN2) +
+    return 1024 + (size_t)X_STAGES * X_STAGE_BYTES + X_SLOTS * X_GROUP_BYTES + (gemm1 ? X_TURN1 : X_TURN2) +
            (X_NBARS + 1) * sizeof(uint64_t) + 16 + sizeof(int) * (4 * (size_t)E_local + 1);
 }
 
@@ -240,6 +241,81 @@ __device__ __forceinline__ void load_scales32(const uint8_t *const (&base)[N], c
     }
 }
 
+// What a scale warp works with: its room in shared memory, the barriers of that
+// and its place among the pair's tiles.
+struct ScaleWarp {
+    uint8_t *room;
+    uint64_t *empty;
+    uint32_t full_leader;
+    volatile int *abort_flag;
+    int slot, lane, pair_id, n_pairs, total, dt, dn, rank;
+};
+
+// Takes every X_SLOTS-th group of four K blocks: 32 bytes of each of the CTA's
+// 128 weight rows, or of the tile's tokens (all of them: each CTA's half of the
+// MMA needs all).  Lane l serves rows l, l + 32, ...  A group's loads are issued
+// when the warp's last one is stored, and are done before the next fence and
+// arrival, which would wait for them.
+template <bool kGemm1, bool kTokens>
+__device__ __forceinline__ void fetch_scales(const ScaleWarp &f, const MxParams &p, const MxTable &table) {
+    constexpr int kRows = kTokens ? X_BN / 32 : 4;
+    const int lane = f.lane, ld = p.K / 32, ng = (p.nk + X_GROUP - 1) / X_GROUP;
+    const size_t all = (kTokens ? (size_t)p.rows_alloc : (size_t)p.E_local * p.n_out) * ld;
+    uint32_t ph = 0;
+    MxTile c(f.pair_id, p.nt, f.total, table);
+    int kg = f.slot;
+    for (int tile = f.pair_id;; kg += X_SLOTS) {
+        while (kg >= ng && tile < f.total) {
+            kg -= ng;
+            tile += f.n_pairs;
+            c.step(f.dt, f.dn, p.nt, tile < f.total, table);
+        }
+        if (tile >= f.total) break;
+        const uint8_t *base[kRows];
+        size_t row[kRows], total[kRows];
+        bool there[kRows];
+        uint32_t v[kRows][8];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            if (kTokens) {
+                const int r = i * 32 + lane;
+                there[i] = r < c.nvalid;
+                base[i] = p.t_sf;
+                row[i] = (size_t)(c.row0 + r);
+            } else {
+                const int r = kGemm1 ? c.nt * X_UNITS + f.rank * 64 + (i & 1) * 32 + lane
+                                     : c.nt * X_BM + f.rank * 128 + i * 32 + lane;
+                there[i] = r < p.n_out;
+                base[i] = kGemm1 && i >= 2 ? p.w_sf1 : p.w_sf0;
+                row[i] = (size_t)c.expert * p.n_out + r;
+            }
+            total[i] = all;
+        }
+        load_scales32<kRows>(base, row, there, ld, total, kg, v);
+        // lane 0 waits for the group's room, the warp follows it
+        bool got = true;
+        if (lane == 0) got = mbar_wait_bounded(f.empty, ph ^ 1u, f.abort_flag);
+        if (!__shfl_sync(0xffffffffu, got, 0)) break;
+        ph ^= 1u;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {  // K block j / 2 of the group, its half h = j % 2
+            // blocks of 512 bytes: 0, 1: the weights' K halves; 2 + 2 h + token / 128: the tokens'
+            uint4 *d = reinterpret_cast<uint4 *>(f.room + (j / 2) * X_SF_BYTES) + lane;
+            const int h = j & 1;
+            if constexpr (kTokens) {
+                d[32 * (2 + 2 * h)] = make_uint4(v[0][j], v[1][j], v[2][j], v[3][j]);
+                if (c.n > 128)  // (rows 192 on do not exist)
+                    d[32 * (3 + 2 * h)] = make_uint4(v[4][j], v[5][j], kMxOnes, kMxOnes);
+            } else {
+                d[32 * h] = make_uint4(v[0][j], v[1][j], v[2][j], v[3][j]);
+            }
+        }
+        fence_proxy_async_smem();  // tcgen05.cp reads them through the async proxy
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(f.full_leader);
+    }
+}
+
 template <bool kGemm1>
 __global__ void __launch_bounds__(X_THREADS, 1)
 grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constant__ CUtensorMap tmT16,
@@ -254,16 +330,16 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
     }
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint8_t *sfs = ring + X_STAGES * X_STAGE_BYTES;  // [X_SF_WARPS] groups of scales
-    uint8_t *turn = sfs + X_SF_WARPS * X_GROUP_BYTES;
+    uint8_t *sfs = ring + X_STAGES * X_STAGE_BYTES;  // [X_SLOTS] groups of scales
+    uint8_t *turn = sfs + X_SLOTS * X_GROUP_BYTES;
     uint64_t *bars = reinterpret_cast<uint64_t *>(turn + (kGemm1 ? X_TURN1 : X_TURN2));
     uint64_t *full = bars;                       // leader: both CTAs' TMA bytes, scales in TMEM -> MMA
     uint64_t *empty = bars + X_STAGES;           // MMA -> each CTA's TMA, the leader's scale copies
     uint64_t *tfull = bars + 2 * X_STAGES;       // [2] MMA -> each CTA's epilogue
     uint64_t *tempty = tfull + 2;                // [2] leader: both epilogues -> MMA
     uint64_t *drain = tempty + 2;                // [2] leader: MMA's and copies' completion at exit
-    uint64_t *sfull = drain + 2;                 // [X_SF_WARPS] leader: both CTAs' group of scales -> copies
-    uint64_t *sempty = sfull + X_SF_WARPS;       // [X_SF_WARPS] copies -> each CTA's scale warp
+    uint64_t *sfull = drain + 2;                 // [X_SLOTS] leader: both CTAs' group of scales -> copies
+    uint64_t *sempty = sfull + X_SLOTS;          // [X_SLOTS] copies -> each CTA's scale warp
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + X_NBARS);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     MxTable table;
@@ -290,8 +366,8 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
                 mbar_init(&tempty[a], 2 * X_EPI_WARPS);
                 mbar_init(&drain[a], 1);
             }
-            for (int g = 0; g < X_SF_WARPS; ++g) {
-                mbar_init(&sfull[g], 2);
+            for (int g = 0; g < X_SLOTS; ++g) {
+                mbar_init(&sfull[g], 4);  // two warps of each CTA
                 mbar_init(&sempty[g], 1);
             }
             *abort_flag = 0;
@@ -457,7 +533,7 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
                     }
                     __syncwarp();
                     if (++s == X_STAGES) { s = 0; ph ^= 1u; }
-                    if (last && ++sg == X_SF_WARPS) { sg = 0; phg ^= 1u; }
+                    if (last && ++sg == X_SLOTS) { sg = 0; phg ^= 1u; }
                 }
                 tile += n_pairs;
                 c.step(dt, dn, p.nt, tile < total, table);
@@ -571,69 +647,14 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
         if (!kGemm1 && __any_sync(0xffffffffu, over) && lane == 0) raise_flag(p.status, FLAG_RANGE);
     } else {
         // ---------------- scale fetchers (both CTAs) ----------------
-        // Warp w takes every third group of four K blocks, whole: 32 bytes of
-        // each of the CTA's 128 weight rows and of the tile's tokens (all of
-        // them: each CTA's half of the MMA needs all).  Lane l serves rows
-        // l, l + 32, ...  A group's loads are issued when the warp's last one
-        // is stored, and are done before the next fence and arrival, which
-        // would wait for them.
-        const int w = warp - 3;
-        const int ld = p.K / 32, ng = (p.nk + X_GROUP - 1) / X_GROUP;
-        const size_t t_total = (size_t)p.rows_alloc * ld, w_total = (size_t)p.E_local * p.n_out * ld;
-        const uint32_t sfull_leader = mapa_shared(smem_u32(&sfull[w]), 0);
-        uint4 *f = reinterpret_cast<uint4 *>(sfs + w * X_GROUP_BYTES) + lane;
-        uint32_t ph = 0;
-        MxTile c(pair_id, p.nt, total, table);
-        int kg = w;
-        for (int tile = pair_id;; kg += X_SF_WARPS) {
-            while (kg >= ng && tile < total) {
-                kg -= ng;
-                tile += n_pairs;
-                c.step(dt, dn, p.nt, tile < total, table);
-            }
-            if (tile >= total) break;
-            // 4 weight rows and up to 6 tokens of this lane
-            constexpr int kRows = 4 + X_BN / 32;
-            const uint8_t *base[kRows];
-            size_t row[kRows], all[kRows];
-            bool there[kRows];
-            uint32_t v[kRows][8];
-#pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-                if (i < 4) {
-                    const int wr = kGemm1 ? c.nt * X_UNITS + (int)rank * 64 + (i & 1) * 32 + lane
-                                          : c.nt * X_BM + (int)rank * 128 + i * 32 + lane;
-                    there[i] = wr < p.n_out;
-                    base[i] = kGemm1 && i >= 2 ? p.w_sf1 : p.w_sf0;
-                    row[i] = (size_t)c.expert * p.n_out + wr;
-                    all[i] = w_total;
-                } else {
-                    const int tr = (i - 4) * 32 + lane;
-                    there[i] = tr < c.nvalid;
-                    base[i] = p.t_sf;
-                    row[i] = (size_t)(c.row0 + tr);
-                    all[i] = t_total;
-                }
-            }
-            load_scales32<kRows>(base, row, there, ld, all, kg, v);
-            // lane 0 waits for the group's room, the warp follows it
-            bool got = true;
-            if (lane == 0) got = mbar_wait_bounded(&sempty[w], ph ^ 1u, abort_flag);
-            if (!__shfl_sync(0xffffffffu, got, 0)) break;
-            ph ^= 1u;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {  // K block j / 2 of the group, its half j % 2
-                uint4 *d = f + (j / 2) * (X_SF_BYTES / 16);
-                const int h = j & 1;
-                d[32 * h] = make_uint4(v[0][j], v[1][j], v[2][j], v[3][j]);
-                d[32 * (2 + 2 * h)] = make_uint4(v[4][j], v[5][j], v[6][j], v[7][j]);
-                if (c.n > 128)  // (rows 192 on do not exist)
-                    d[32 * (3 + 2 * h)] = make_uint4(v[8][j], v[9][j], kMxOnes, kMxOnes);
-            }
-            fence_proxy_async_smem();  // tcgen05.cp reads them through the async proxy
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(sfull_leader);
-        }
+        const int w = warp - 3, slot = w >> 1;
+        const ScaleWarp f{sfs + slot * X_GROUP_BYTES, &sempty[slot],
+                          mapa_shared(smem_u32(&sfull[slot]), 0), abort_flag, slot, lane,
+                          pair_id, n_pairs, total, dt, dn, (int)rank};
+        if (w & 1)
+            fetch_scales<kGemm1, true>(f, p, table);
+        else
+            fetch_scales<kGemm1, false>(f, p, table);
     }
 
     tc_fence_before();
@@ -696,7 +717,7 @@ bool token_maps(MxMaps *m, const uint8_t *codes, int K, int64_t rows) {
 template <bool kGemm1>
 cudaError_t launch_mx(const MxMaps &m, const MxParams &p, long long token_tiles, cudaStream_t stream) {
     const size_t smem = mx_smem_bytes(kGemm1, p.E_local);
-    static_assert(1024 + X_STAGES * X_STAGE_BYTES + X_SF_WARPS * X_GROUP_BYTES + X_TURN1 +
+    static_assert(1024 + X_STAGES * X_STAGE_BYTES + X_SLOTS * X_GROUP_BYTES + X_TURN1 +
                           (X_NBARS + 1) * 8 + 16 + 4 * (4 * 1024 + 1) <= X_SMEM_MAX,
                   "the table of 1024 experts fits beside the ring");
     cudaError_t e = ensure_smem((const void *)grouped_mx_kernel<kGemm1>, smem);
