@@ -383,6 +383,16 @@ __device__ __forceinline__ void bar_sync(int id, int threads) {
     asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+// The same with release at CTA scope: orders this CTA's shared memory, which is
+// all that is published where the other CTA of the pair only goes on to issue an
+// operation whose half in this SM reads it (after fence.proxy.async).  At cluster
+// scope the release also waits for the SM's global stores: 2300-3000 cycles
+// beside a tile's epilogue against about 100.
+__device__ __forceinline__ void mbar_arrive_cluster_cta(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+                 : "memory");
+}
+
 // The same without ordering, for an arrival that publishes no memory: a release
 // waits until the thread's stores in flight (a tile's output) have landed, about
 // 2500 cycles after the epilogue of a grouped MXFP4 tile.

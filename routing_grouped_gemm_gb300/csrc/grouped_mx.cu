@@ -254,8 +254,7 @@ struct ScaleWarp {
 // Takes every X_SLOTS-th group of four K blocks: 32 bytes of each of the CTA's
 // 128 weight rows, or of the tile's tokens (all of them: each CTA's half of the
 // MMA needs all).  Lane l serves rows l, l + 32, ...  A group's loads are issued
-// when the warp's last one is stored, and are done before the next fence and
-// arrival, which would wait for them.
+// when the warp's last one is stored.
 template <bool kGemm1, bool kTokens>
 __device__ __forceinline__ void fetch_scales(const ScaleWarp &f, const MxParams &p, const MxTable &table) {
     constexpr int kRows = kTokens ? X_BN / 32 : 4;
@@ -312,7 +311,7 @@ __device__ __forceinline__ void fetch_scales(const ScaleWarp &f, const MxParams 
         }
         fence_proxy_async_smem();  // tcgen05.cp reads them through the async proxy
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(f.full_leader);
+        if (lane == 0) mbar_arrive_cluster_cta(f.full_leader);
     }
 }
 
@@ -507,8 +506,7 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
                 for (int kb = 0; kb < p.nk; ++kb) {
                     const int k4 = kb % X_GROUP;
                     bool got = true;
-                    // the peer's scales were written by its threads: cluster acquire
-                    if (k4 == 0) got = mbar_wait_bounded(&sfull[sg], phg, abort_flag, true);
+                    if (k4 == 0) got = mbar_wait_bounded(&sfull[sg], phg, abort_flag);
                     got = got && mbar_wait_bounded(&empty[s], ph ^ 1u, abort_flag);
                     if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
                     tc_fence_after();
