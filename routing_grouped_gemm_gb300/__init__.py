@@ -139,6 +139,21 @@ class Config:
     n_group: int = 0           # > 1: group-limited routing over n_group expert groups
     topk_group: int = 0
 
+    def __setattr__(self, name, value):
+        self.__dict__.pop("_ref", None)   # what ref() keeps describes the old values
+        object.__setattr__(self, name, value)
+
+    def __getstate__(self):               # copies and pickles go without the pointer
+        return {k: v for k, v in self.__dict__.items() if k != "_ref"}
+
+    def ref(self):
+        """(pointer to the C struct, rows of the permuted buffers), built once for these values."""
+        r = self.__dict__.get("_ref")
+        if r is None:
+            p = ctypes.pointer(self.c())
+            r = self.__dict__["_ref"] = (p, int(_lib.moe_rows_alloc(p)))
+        return r
+
     def c(self) -> moe_config:
         el = self.E - self.e_first if self.E_local < 0 else self.E_local
         return moe_config(self.T, self.D, self.H_local, self.E, self.k, self.e_first, el,
@@ -182,8 +197,7 @@ def validate_config(cfg: Config) -> int:
 
 
 def rows_alloc(cfg: Config) -> int:
-    c = cfg.c()
-    return int(_lib.moe_rows_alloc(ctypes.byref(c)))
+    return cfg.ref()[1]
 
 
 def workspace_size(cfg: Config) -> int:
@@ -234,7 +248,7 @@ def _ptr(t) -> int:
 
 def _stream(stream) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream
 
 
@@ -246,7 +260,7 @@ def _check(st: int, what: str):
 def _expect(t, shape, dtype, name):
     if t is None:
         raise ValueError(f"{name} is required")
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+    if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{name}: expected {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -266,8 +280,7 @@ def moe_route_topk(cfg: Config, x, wg, bias, logits_out, topk_idx, topk_w, ws, s
         _expect(logits_out, (cfg.T, cfg.E), torch.float32, "logits_out")
     _expect(topk_idx, (cfg.T, cfg.k), torch.int32, "topk_idx")
     _expect(topk_w, (cfg.T, cfg.k), torch.float32, "topk_w")
-    c = cfg.c()
-    _check(_lib.moe_route_topk(ctypes.byref(c), _ptr(x), _ptr(wg), _ptr(bias), _ptr(logits_out),
+    _check(_lib.moe_route_topk(cfg.ref()[0], _ptr(x), _ptr(wg), _ptr(bias), _ptr(logits_out),
                                _ptr(topk_idx), _ptr(topk_w), _ptr(ws), ws.numel(), _stream(stream)),
            "moe_route_topk")
 
@@ -282,8 +295,7 @@ def moe_permute(cfg: Config, x, topk_idx, tokens_per_expert, seg_offsets, row_of
     _expect(row_of, (cfg.T, cfg.k), torch.int32, "row_of")
     _expect(token_of_row, (ra,), torch.int32, "token_of_row")
     _expect(x_perm, (ra, cfg.D), cfg.torch_dtype, "x_perm")
-    c = cfg.c()
-    _check(_lib.moe_permute(ctypes.byref(c), _ptr(x), _ptr(topk_idx), _ptr(tokens_per_expert),
+    _check(_lib.moe_permute(cfg.ref()[0], _ptr(x), _ptr(topk_idx), _ptr(tokens_per_expert),
                             _ptr(seg_offsets), _ptr(row_of), _ptr(token_of_row), _ptr(x_perm),
                             _ptr(ws), ws.numel(), _stream(stream)), "moe_permute")
 
@@ -297,8 +309,7 @@ def moe_permute_index(cfg: Config, topk_idx, tokens_per_expert, seg_offsets, row
     _expect(seg_offsets, (cfg.e_local + 1,), torch.int32, "seg_offsets")
     _expect(row_of, (cfg.T, cfg.k), torch.int32, "row_of")
     _expect(token_of_row, (ra,), torch.int32, "token_of_row")
-    c = cfg.c()
-    _check(_lib.moe_permute_index(ctypes.byref(c), _ptr(topk_idx), _ptr(tokens_per_expert),
+    _check(_lib.moe_permute_index(cfg.ref()[0], _ptr(topk_idx), _ptr(tokens_per_expert),
                                   _ptr(seg_offsets), _ptr(row_of), _ptr(token_of_row), _ptr(ws),
                                   ws.numel(), _stream(stream)), "moe_permute_index")
 
@@ -322,8 +333,7 @@ def moe_permute_noalloc(cfg: Config, x, topk_idx, tokens_per_expert, seg_offsets
     _expect(x_perm, (ra, cfg.D), cfg.torch_dtype, "x_perm")
     if device_flags is not None:
         _expect(device_flags, (1,), torch.int32, "device_flags")
-    c = cfg.c()
-    _check(_lib.moe_permute_noalloc(ctypes.byref(c), _ptr(x), _ptr(topk_idx),
+    _check(_lib.moe_permute_noalloc(cfg.ref()[0], _ptr(x), _ptr(topk_idx),
                                     _ptr(tokens_per_expert), _ptr(seg_offsets), _ptr(row_of),
                                     _ptr(token_of_row), _ptr(x_perm), _ptr(device_flags),
                                     _stream(stream)), "moe_permute_noalloc")
@@ -342,8 +352,7 @@ def moe_grouped_swiglu(cfg: Config, x_perm, seg_offsets, tokens_per_expert, w1, 
     _expect(w2, (el, cfg.D, cfg.H_local), dt, "w2")
     _expect(h, (ra, cfg.H_local), dt, "h")
     _expect(y_perm, (ra, cfg.D), cfg.y_dtype, "y_perm")
-    c = cfg.c()
-    _check(_lib.moe_grouped_swiglu(ctypes.byref(c), _ptr(x_perm), _ptr(seg_offsets),
+    _check(_lib.moe_grouped_swiglu(cfg.ref()[0], _ptr(x_perm), _ptr(seg_offsets),
                                    _ptr(tokens_per_expert), _ptr(w1), _ptr(w3), _ptr(w2), _ptr(h),
                                    _ptr(y_perm), _ptr(ws), ws.numel(), _stream(stream)),
            "moe_grouped_swiglu")
@@ -356,8 +365,7 @@ def moe_unpermute_combine(cfg: Config, y_perm, row_of, topk_w, out, ws, stream=N
     _expect(row_of, (cfg.T, cfg.k), torch.int32, "row_of")
     _expect(topk_w, (cfg.T, cfg.k), torch.float32, "topk_w")
     _expect(out, (cfg.T, cfg.D), dt, "out")
-    c = cfg.c()
-    _check(_lib.moe_unpermute_combine(ctypes.byref(c), _ptr(y_perm), _ptr(row_of), _ptr(topk_w),
+    _check(_lib.moe_unpermute_combine(cfg.ref()[0], _ptr(y_perm), _ptr(row_of), _ptr(topk_w),
                                       _ptr(out), _ptr(ws), ws.numel(), _stream(stream)),
            "moe_unpermute_combine")
 
@@ -373,8 +381,7 @@ def moe_layer_forward(cfg: Config, x, wg, bias, w1, w3, w2, out, ws, stream=None
     _expect(w3, (el, cfg.H_local, cfg.D), dt, "w3")
     _expect(w2, (el, cfg.D, cfg.H_local), dt, "w2")
     _expect(out, (cfg.T, cfg.D), dt, "out")
-    c = cfg.c()
-    _check(_lib.moe_layer_forward(ctypes.byref(c), _ptr(x), _ptr(wg), _ptr(bias), _ptr(w1),
+    _check(_lib.moe_layer_forward(cfg.ref()[0], _ptr(x), _ptr(wg), _ptr(bias), _ptr(w1),
                                   _ptr(w3), _ptr(w2), _ptr(out), _ptr(ws), ws.numel(),
                                   _stream(stream)), "moe_layer_forward")
 
@@ -393,8 +400,7 @@ def moe_layer_forward_host(cfg: Config, x_host, wg, bias, w1, w3, w2, out_host, 
     _expect(w1, (el, cfg.H_local, cfg.D), dt, "w1")
     _expect(w3, (el, cfg.H_local, cfg.D), dt, "w3")
     _expect(w2, (el, cfg.D, cfg.H_local), dt, "w2")
-    c = cfg.c()
-    _check(_lib.moe_layer_forward_host(ctypes.byref(c), x_host.data_ptr(), _ptr(wg), _ptr(bias),
+    _check(_lib.moe_layer_forward_host(cfg.ref()[0], x_host.data_ptr(), _ptr(wg), _ptr(bias),
                                        _ptr(w1), _ptr(w3), _ptr(w2), out_host.data_ptr(), _ptr(ws),
                                        ws.numel(), _stream(stream)), "moe_layer_forward_host")
 
@@ -476,8 +482,7 @@ def moe_layer_forward_train(cfg: Config, x, wg, bias, w1, w3, w2, out, ws, strea
     _expect(w3, (el, cfg.H_local, cfg.D), dt, "w3")
     _expect(w2, (el, cfg.D, cfg.H_local), dt, "w2")
     _expect(out, (cfg.T, cfg.D), dt, "out")
-    c = cfg.c()
-    _check(_lib.moe_layer_forward_train(ctypes.byref(c), _ptr(x), _ptr(wg), _ptr(bias), _ptr(w1),
+    _check(_lib.moe_layer_forward_train(cfg.ref()[0], _ptr(x), _ptr(wg), _ptr(bias), _ptr(w1),
                                         _ptr(w3), _ptr(w2), _ptr(out), _ptr(ws), ws.numel(),
                                         _stream(stream)), "moe_layer_forward_train")
 
@@ -503,8 +508,7 @@ def moe_layer_backward(cfg: Config, x, wg, w1, w3, w2, dout, dx, dwg, dbias, dw1
     _expect(dw1, (el, cfg.H_local, cfg.D), wdt, "dw1")
     _expect(dw3, (el, cfg.H_local, cfg.D), wdt, "dw3")
     _expect(dw2, (el, cfg.D, cfg.H_local), wdt, "dw2")
-    c = cfg.c()
-    _check(_lib.moe_layer_backward_ex(ctypes.byref(c), _ptr(x), _ptr(wg), _ptr(w1), _ptr(w3),
+    _check(_lib.moe_layer_backward_ex(cfg.ref()[0], _ptr(x), _ptr(wg), _ptr(w1), _ptr(w3),
                                       _ptr(w2), _ptr(dout), _ptr(dx), _ptr(dwg), _ptr(dbias),
                                       _ptr(dw1), _ptr(dw3), _ptr(dw2),
                                       MOE_BF16 if wdt == torch.bfloat16 else MOE_F32, _ptr(ws),
@@ -546,8 +550,7 @@ def moe_permute_fp8(cfg: Config, x, topk_idx, tokens_per_expert, seg_offsets, ro
     _expect(token_of_row, (ra,), torch.int32, "token_of_row")
     _expect(x_perm_q, (ra, cfg.D), torch.uint8, "x_perm_q")
     _expect(x_scale, (ra,), torch.float32, "x_scale")
-    c = cfg.c()
-    _check(_lib.moe_permute_fp8(ctypes.byref(c), _ptr(x), _ptr(topk_idx), _ptr(tokens_per_expert),
+    _check(_lib.moe_permute_fp8(cfg.ref()[0], _ptr(x), _ptr(topk_idx), _ptr(tokens_per_expert),
                                 _ptr(seg_offsets), _ptr(row_of), _ptr(token_of_row),
                                 _ptr(x_perm_q), _ptr(x_scale), _ptr(ws), ws.numel(),
                                 _stream(stream)), "moe_permute_fp8")
@@ -568,8 +571,7 @@ def moe_grouped_swiglu_fp8(cfg: Config, x_perm_q, x_scale, seg_offsets, tokens_p
     _expect(w2, (el, cfg.D, cfg.H_local), torch.bfloat16, "w2")
     _expect(h, (ra, cfg.H_local), torch.bfloat16, "h")
     _expect(y_perm, (ra, cfg.D), cfg.y_dtype, "y_perm")
-    c = cfg.c()
-    _check(_lib.moe_grouped_swiglu_fp8(ctypes.byref(c), _ptr(x_perm_q), _ptr(x_scale),
+    _check(_lib.moe_grouped_swiglu_fp8(cfg.ref()[0], _ptr(x_perm_q), _ptr(x_scale),
                                        _ptr(seg_offsets), _ptr(tokens_per_expert), _ptr(w1_q),
                                        _ptr(w1_scale), _ptr(w3_q), _ptr(w3_scale), _ptr(w2),
                                        _ptr(h), _ptr(y_perm), _ptr(ws), ws.numel(),
@@ -589,8 +591,7 @@ def moe_layer_forward_fp8(cfg: Config, x, wg, bias, w1_q, w1_scale, w3_q, w3_sca
     _expect(w3_scale, (el, cfg.H_local), torch.float32, "w3_scale")
     _expect(w2, (el, cfg.D, cfg.H_local), torch.bfloat16, "w2")
     _expect(out, (cfg.T, cfg.D), torch.bfloat16, "out")
-    c = cfg.c()
-    _check(_lib.moe_layer_forward_fp8(ctypes.byref(c), _ptr(x), _ptr(wg), _ptr(bias), _ptr(w1_q),
+    _check(_lib.moe_layer_forward_fp8(cfg.ref()[0], _ptr(x), _ptr(wg), _ptr(bias), _ptr(w1_q),
                                       _ptr(w1_scale), _ptr(w3_q), _ptr(w3_scale), _ptr(w2),
                                       _ptr(out), _ptr(ws), ws.numel(), _stream(stream)),
            "moe_layer_forward_fp8")
@@ -653,8 +654,7 @@ def moe_permute_mxfp4(cfg: Config, x, topk_idx, tokens_per_expert, seg_offsets, 
     _expect(token_of_row, (ra,), torch.int32, "token_of_row")
     _expect(x_perm_q, (ra, cfg.D // 2), torch.uint8, "x_perm_q")
     _expect(x_scale, (ra, cfg.D // 32), torch.uint8, "x_scale")
-    c = cfg.c()
-    _check(_lib.moe_permute_mxfp4(ctypes.byref(c), _ptr(x), _ptr(topk_idx), _ptr(tokens_per_expert),
+    _check(_lib.moe_permute_mxfp4(cfg.ref()[0], _ptr(x), _ptr(topk_idx), _ptr(tokens_per_expert),
                                   _ptr(seg_offsets), _ptr(row_of), _ptr(token_of_row),
                                   _ptr(x_perm_q), _ptr(x_scale), _ptr(ws), ws.numel(),
                                   _stream(stream)), "moe_permute_mxfp4")
@@ -680,8 +680,7 @@ def moe_grouped_swiglu_mxfp4(cfg: Config, x_perm_q, x_scale, seg_offsets, tokens
     _expect(h_q, (ra, cfg.H_local // 2), torch.uint8, "h_q")
     _expect(h_scale, (ra, cfg.H_local // 32), torch.uint8, "h_scale")
     _expect(y_perm, (ra, cfg.D), torch.float16, "y_perm")
-    c = cfg.c()
-    _check(_lib.moe_grouped_swiglu_mxfp4(ctypes.byref(c), _ptr(x_perm_q), _ptr(x_scale),
+    _check(_lib.moe_grouped_swiglu_mxfp4(cfg.ref()[0], _ptr(x_perm_q), _ptr(x_scale),
                                          _ptr(seg_offsets), _ptr(tokens_per_expert), _ptr(w1_q),
                                          _ptr(w1_scale), _ptr(w3_q), _ptr(w3_scale), _ptr(w2_q),
                                          _ptr(w2_scale), _ptr(h_q), _ptr(h_scale), _ptr(y_perm),
@@ -698,8 +697,7 @@ def moe_layer_forward_mxfp4(cfg: Config, x, wg, bias, w1_q, w1_scale, w3_q, w3_s
         _expect(bias, (cfg.E,), torch.float32, "bias")
     _expect_mx_weights(cfg, w1_q, w1_scale, w3_q, w3_scale, w2_q, w2_scale)
     _expect(out, (cfg.T, cfg.D), torch.bfloat16, "out")
-    c = cfg.c()
-    _check(_lib.moe_layer_forward_mxfp4(ctypes.byref(c), _ptr(x), _ptr(wg), _ptr(bias), _ptr(w1_q),
+    _check(_lib.moe_layer_forward_mxfp4(cfg.ref()[0], _ptr(x), _ptr(wg), _ptr(bias), _ptr(w1_q),
                                         _ptr(w1_scale), _ptr(w3_q), _ptr(w3_scale), _ptr(w2_q),
                                         _ptr(w2_scale), _ptr(out), _ptr(ws), ws.numel(),
                                         _stream(stream)), "moe_layer_forward_mxfp4")
@@ -716,8 +714,7 @@ def moe_unpermute_combine_backward(cfg: Config, dout, y_perm, row_of, topk_w, dy
     _expect(topk_w, (cfg.T, cfg.k), torch.float32, "topk_w")
     _expect(dy_perm, (ra, cfg.D), cfg.torch_dtype, "dy_perm")
     _expect(dtopk_w, (cfg.T, cfg.k), torch.float32, "dtopk_w")
-    c = cfg.c()
-    _check(_lib.moe_unpermute_combine_backward(ctypes.byref(c), _ptr(dout), _ptr(y_perm),
+    _check(_lib.moe_unpermute_combine_backward(cfg.ref()[0], _ptr(dout), _ptr(y_perm),
                                                _ptr(row_of), _ptr(topk_w), _ptr(dy_perm),
                                                _ptr(dtopk_w), _ptr(ws), ws.numel(),
                                                _stream(stream)), "moe_unpermute_combine_backward")
@@ -732,8 +729,7 @@ def moe_permute_backward(cfg: Config, dx_perm, row_of, dx, ws, stream=None):
     _expect(dx_perm, (ra, cfg.D), dx_perm.dtype, "dx_perm")
     _expect(row_of, (cfg.T, cfg.k), torch.int32, "row_of")
     _expect(dx, (cfg.T, cfg.D), cfg.torch_dtype, "dx")
-    c = cfg.c()
-    _check(_lib.moe_permute_backward(ctypes.byref(c), _ptr(dx_perm),
+    _check(_lib.moe_permute_backward(cfg.ref()[0], _ptr(dx_perm),
                                      MOE_BF16 if dx_perm.dtype == torch.bfloat16 else MOE_F32,
                                      _ptr(row_of), _ptr(dx), _ptr(ws), ws.numel(),
                                      _stream(stream)), "moe_permute_backward")
@@ -754,8 +750,7 @@ def moe_grouped_swiglu_gather(cfg: Config, x, token_of_row, seg_offsets, tokens_
     _expect(w2, (el, cfg.D, cfg.H_local), dt, "w2")
     _expect(h, (ra, cfg.H_local), dt, "h")
     _expect(y_perm, (ra, cfg.D), cfg.y_dtype, "y_perm")
-    c = cfg.c()
-    _check(_lib.moe_grouped_swiglu_gather(ctypes.byref(c), _ptr(x), _ptr(token_of_row),
+    _check(_lib.moe_grouped_swiglu_gather(cfg.ref()[0], _ptr(x), _ptr(token_of_row),
                                           _ptr(seg_offsets), _ptr(tokens_per_expert), _ptr(w1),
                                           _ptr(w3), _ptr(w2), _ptr(h), _ptr(y_perm), _ptr(ws),
                                           ws.numel(), _stream(stream)), "moe_grouped_swiglu_gather")
@@ -774,8 +769,7 @@ def moe_layer_forward_gather(cfg: Config, x, wg, bias, w1, w3, w2, out, ws, stre
     _expect(w3, (el, cfg.H_local, cfg.D), dt, "w3")
     _expect(w2, (el, cfg.D, cfg.H_local), dt, "w2")
     _expect(out, (cfg.T, cfg.D), dt, "out")
-    c = cfg.c()
-    _check(_lib.moe_layer_forward_gather(ctypes.byref(c), _ptr(x), _ptr(wg), _ptr(bias), _ptr(w1),
+    _check(_lib.moe_layer_forward_gather(cfg.ref()[0], _ptr(x), _ptr(wg), _ptr(bias), _ptr(w1),
                                          _ptr(w3), _ptr(w2), _ptr(out), _ptr(ws), ws.numel(),
                                          _stream(stream)), "moe_layer_forward_gather")
 
@@ -793,8 +787,7 @@ def moe_layer_forward_fused(cfg: Config, x, wg, bias, w1, w3, w2, out, ws, strea
     _expect(w3, (el, cfg.H_local, cfg.D), dt, "w3")
     _expect(w2, (el, cfg.D, cfg.H_local), dt, "w2")
     _expect(out, (cfg.T, cfg.D), dt, "out")
-    c = cfg.c()
-    _check(_lib.moe_layer_forward_fused(ctypes.byref(c), _ptr(x), _ptr(wg), _ptr(bias), _ptr(w1),
+    _check(_lib.moe_layer_forward_fused(cfg.ref()[0], _ptr(x), _ptr(wg), _ptr(bias), _ptr(w1),
                                         _ptr(w3), _ptr(w2), _ptr(out), _ptr(ws), ws.numel(),
                                         _stream(stream)), "moe_layer_forward_fused")
 

@@ -85,15 +85,28 @@ combine_bwd_kernel(const void *__restrict__ dout, const void *__restrict__ y_per
             my_r = -1;
         }
     }
-    for (int j0 = 0; j0 < k; j0 += BW_SLOTS) {
+    // lane i takes the i-th slot that has a row; the others' weight gradient is 0
+    int row = 0, slot = 0, n = 0;
+    float wt = 0.f;
+    for (uint32_t m = __ballot_sync(0xffffffffu, my_r >= 0); m; m &= m - 1, ++n) {
+        const int src = __ffs(m) - 1;
+        const int r = __shfl_sync(0xffffffffu, my_r, src);
+        const float w = __shfl_sync(0xffffffffu, my_w, src);
+        if (lane == n) {
+            row = r;
+            wt = w;
+            slot = src;
+        }
+    }
+    if (lane < k && my_r < 0) dw[(size_t)t * k + lane] = 0.f;
+    for (int j0 = 0; j0 < n; j0 += BW_SLOTS) {
         int r[BW_SLOTS];
         float w[BW_SLOTS], dot[BW_SLOTS];
 #pragma unroll
         for (int u = 0; u < BW_SLOTS; ++u) {
-            const int j = j0 + u;
-            r[u] = __shfl_sync(0xffffffffu, my_r, j & 31);
-            w[u] = __shfl_sync(0xffffffffu, my_w, j & 31);
-            if (j >= k) r[u] = -1;
+            r[u] = __shfl_sync(0xffffffffu, row, (j0 + u) & 31);
+            w[u] = __shfl_sync(0xffffffffu, wt, (j0 + u) & 31);
+            if (j0 + u >= n) r[u] = -1;
             dot[u] = 0.f;
         }
         if constexpr (!BF16) {
@@ -165,21 +178,21 @@ combine_bwd_kernel(const void *__restrict__ dout, const void *__restrict__ y_per
             float v = dot[u];
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-            if (lane == 0 && j0 + u < k) dw[(size_t)t * k + j0 + u] = v;
+            const int sl = __shfl_sync(0xffffffffu, slot, (j0 + u) & 31);
+            if (lane == 0 && j0 + u < n) dw[(size_t)t * k + sl] = v;
         }
     }
 }
 
 // One warp per token: dx[t] = sum_j dxp[row_of[t, j]] + r[t], fp32 in slot
 // order, rounded once to the output type; r[t] = add[t] when add, else (wg
-// given) sum_j dl[t, e_j] wg[e_j] in slot order.  PBF16: dxp is bf16.
-template <bool BF16, bool PBF16>
+// given) sum_j dl[t, e_j] wg[e_j] in slot order.
+template <bool BF16>
 __global__ void __launch_bounds__(128)
-dispatch_bwd_kernel(const void *__restrict__ dxp, const int *__restrict__ row_of,
+dispatch_bwd_kernel(const float *__restrict__ dxp, const int *__restrict__ row_of,
                     const float *__restrict__ add, const int *__restrict__ topk_idx,
                     const float *__restrict__ dl, const void *__restrict__ wg, int E,
-                    void *__restrict__ dx, int T, int k, int D, long long rows_alloc,
-                    int *status) {
+                    void *__restrict__ dx, int T, int k, int D, long long rows_alloc) {
     griddep_launch_dependents();  // the next kernel may be scheduled now
     griddep_wait();               // every input of this kernel is complete
     const int t = (int)(((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5);
@@ -190,10 +203,7 @@ dispatch_bwd_kernel(const void *__restrict__ dxp, const int *__restrict__ row_of
     float my_g = 0.f;
     if (lane < k) {
         my_r = row_of[(size_t)t * k + lane];
-        if (my_r < -1 || (long long)my_r >= rows_alloc) {
-            raise_flag(status, FLAG_BAD_ROUTING);
-            my_r = -1;
-        }
+        if (my_r < 0 || (long long)my_r >= rows_alloc) my_r = -1;
         if (!add && wg) {
             my_e = topk_idx[(size_t)t * k + lane];
             if (my_e < 0 || my_e >= E) my_e = -1;
@@ -208,27 +218,18 @@ dispatch_bwd_kernel(const void *__restrict__ dxp, const int *__restrict__ row_of
         float a[4] = {0.f, 0.f, 0.f, 0.f};
         for (int j0 = 0; j0 < k; j0 += DB_SLOTS) {
             int r[DB_SLOTS];
-            using Piece = std::conditional_t<PBF16, uint2, float4>;
-            using Elem = std::conditional_t<PBF16, __nv_bfloat16, float>;
-            Piece v[DB_SLOTS];
+            float4 v[DB_SLOTS];
 #pragma unroll
             for (int u = 0; u < DB_SLOTS; ++u) {
                 r[u] = __shfl_sync(0xffffffffu, my_r, (j0 + u) & 31);
                 if (j0 + u >= k || !in) r[u] = -1;
                 if (r[u] >= 0)
-                    v[u] = __ldcs(reinterpret_cast<const Piece *>(static_cast<const Elem *>(dxp) +
-                                                                  (size_t)r[u] * D + d0));
+                    v[u] = __ldcs(reinterpret_cast<const float4 *>(dxp + (size_t)r[u] * D + d0));
             }
 #pragma unroll
             for (int u = 0; u < DB_SLOTS; ++u) {
                 if (r[u] < 0) continue;
-                if constexpr (PBF16) {
-                    const __nv_bfloat162 *h2 = reinterpret_cast<const __nv_bfloat162 *>(&v[u]);
-                    a[0] += __low2float(h2[0]); a[1] += __high2float(h2[0]);
-                    a[2] += __low2float(h2[1]); a[3] += __high2float(h2[1]);
-                } else {
-                    a[0] += v[u].x; a[1] += v[u].y; a[2] += v[u].z; a[3] += v[u].w;
-                }
+                a[0] += v[u].x; a[1] += v[u].y; a[2] += v[u].z; a[3] += v[u].w;
             }
         }
         if (add && in) {
@@ -265,6 +266,98 @@ dispatch_bwd_kernel(const void *__restrict__ dxp, const int *__restrict__ row_of
             *reinterpret_cast<float4 *>(static_cast<float *>(dx) + (size_t)t * D + d0) =
                 make_float4(a[0], a[1], a[2], a[3]);
         }
+    }
+}
+
+// Backward of the dispatch by itself: dx[t] = sum_j dxp[row_of[t, j]] in fp32 in
+// slot order, rounded once.  Every row of dxp is read once, so memory bounds it,
+// and next to that the instructions spent per 16 bytes: the slots that have a
+// row are gathered once per token (a shard's -1 slots cost nothing after that)
+// and up to PB_ROWS of them stay in registers over the whole row.  A lane holds
+// 16 bytes of dx's row; a token's row is split over `parts` warps.
+// (65536 rows of 4096 bf16 of a shard with half of the experts, D = 4096: 115 us;
+// with every slot handled in the column loop, 8 bytes a lane, 247 us.)
+constexpr int PB_ROWS = 8;      // 16-byte loads of a lane in flight
+constexpr int PB_MIN_PARTS = 4; // 121 us with one warp per token
+
+template <typename In, typename Out>
+__global__ void __launch_bounds__(256, 4)
+permute_bwd_kernel(const In *__restrict__ dxp, const int *__restrict__ row_of, Out *__restrict__ dx,
+                   int T, int k, int D, int parts, long long rows_alloc, int *status) {
+    griddep_launch_dependents();  // the next kernel may be scheduled now
+    griddep_wait();               // every input of this kernel is complete
+    constexpr int kVec = 16 / sizeof(Out);          // elements of dx per lane
+    constexpr int kIn = kVec * sizeof(In) / 16;     // 16-byte pieces of dxp per lane and row
+    constexpr int kRows = PB_ROWS / kIn;            // rows whose loads are issued together
+    const long long wid = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    const int t = (int)(wid / parts), part = (int)(wid - (long long)t * parts);
+    const int lane = threadIdx.x & 31;
+    if (t >= T) return;
+    int my_r = -1;
+    if (lane < k) {
+        my_r = row_of[(size_t)t * k + lane];
+        if (my_r < -1 || (long long)my_r >= rows_alloc) {
+            if (part == 0) raise_flag(status, FLAG_BAD_ROUTING);
+            my_r = -1;
+        }
+    }
+    // lane i takes the i-th slot that has a row
+    int mine = 0, n = 0;
+    for (uint32_t m = __ballot_sync(0xffffffffu, my_r >= 0); m; m &= m - 1, ++n) {
+        const int r = __shfl_sync(0xffffffffu, my_r, __ffs(m) - 1);
+        if (lane == n) mine = r;
+    }
+    int r[kRows];
+    auto rows_from = [&](int j0) {
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) r[u] = __shfl_sync(0xffffffffu, mine, (j0 + u) & 31);
+    };
+    rows_from(0);
+    // uniform (the shuffles need every lane): lanes past the row's end load and store nothing
+    for (int b0 = part * 32 * kVec; b0 < D; b0 += parts * 32 * kVec) {
+        const int d0 = b0 + lane * kVec;
+        const bool in = d0 < D;
+        float a[kVec] = {};
+        for (int j0 = 0; j0 < n; j0 += kRows) {
+            if (n > kRows) rows_from(j0);
+            uint4 v[kRows][kIn];
+#pragma unroll
+            for (int u = 0; u < kRows; ++u) {
+                const uint4 *p = reinterpret_cast<const uint4 *>(dxp + (size_t)r[u] * D + d0);
+#pragma unroll
+                for (int i = 0; i < kIn; ++i)
+                    if (in && j0 + u < n) v[u][i] = __ldcs(p + i);
+            }
+#pragma unroll
+            for (int u = 0; u < kRows; ++u) {
+                if (j0 + u >= n) break;
+#pragma unroll
+                for (int i = 0; i < kIn; ++i) {
+                    const uint32_t w[4] = {v[u][i].x, v[u][i].y, v[u][i].z, v[u][i].w};
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        if constexpr (sizeof(In) == 2) {
+                            a[i * 8 + 2 * h] += __uint_as_float(w[h] << 16);
+                            a[i * 8 + 2 * h + 1] += __uint_as_float(w[h] & 0xffff0000u);
+                        } else {
+                            a[i * 4 + h] += __uint_as_float(w[h]);
+                        }
+                    }
+                }
+            }
+        }
+        if (!in) continue;
+        uint32_t o[4];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            if constexpr (sizeof(Out) == 2) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(a[2 * h], a[2 * h + 1]);
+                o[h] = *reinterpret_cast<const uint32_t *>(&b);
+            } else {
+                o[h] = __float_as_uint(a[h]);
+            }
+        }
+        *reinterpret_cast<uint4 *>(dx + (size_t)t * D + d0) = make_uint4(o[0], o[1], o[2], o[3]);
     }
 }
 
@@ -599,20 +692,42 @@ cudaError_t launch_combine_bwd(const void *dout, const void *y_perm, const int *
     return e;
 }
 
-cudaError_t launch_dispatch_bwd(const void *dxp, int dxp_bf16, const int *row_of, const float *add,
+cudaError_t launch_dispatch_bwd(const float *dxp, const int *row_of, const float *add,
                                 const int *topk_idx, const float *dl, const void *wg, int E,
                                 void *dx, int T, int D, int k, int64_t rows_alloc, int is_bf16,
-                                int *status, cudaStream_t stream) {
+                                cudaStream_t stream) {
     if (T == 0) return cudaSuccess;
-    if (k > 32) return cudaErrorInvalidValue;             // one lane per slot
-    if (dxp_bf16 && !is_bf16) return cudaErrorInvalidValue;
+    if (k > 32) return cudaErrorInvalidValue;  // one lane per slot
     const dim3 grid((unsigned)((T + 3LL) / 4));  // 4 warps (tokens) per block
     const cudaError_t e =
-        launch_pdl(dxp_bf16  ? dispatch_bwd_kernel<true, true>
-                   : is_bf16 ? dispatch_bwd_kernel<true, false>
-                             : dispatch_bwd_kernel<false, false>,
-                   grid, dim3(128), 0, stream, dxp, row_of, add, topk_idx, dl, wg, E, dx, T, k, D,
-                   (long long)rows_alloc, status);
+        launch_pdl(is_bf16 ? dispatch_bwd_kernel<true> : dispatch_bwd_kernel<false>, grid, dim3(128),
+                   0, stream, dxp, row_of, add, topk_idx, dl, wg, E, dx, T, k, D,
+                   (long long)rows_alloc);
+    if (e == cudaSuccess) count_launch();
+    return e;
+}
+
+cudaError_t launch_permute_bwd(const void *dxp, int dxp_bf16, const int *row_of, void *dx, int T,
+                               int D, int k, int64_t rows_alloc, int is_bf16, int *status,
+                               cudaStream_t stream) {
+    if (T == 0) return cudaSuccess;
+    if (k > 32 || (dxp_bf16 && !is_bf16)) return cudaErrorInvalidValue;
+    // at least two blocks of 8 warps per SM, at most a warp per 32 16-byte pieces of dx
+    const int pieces = (D * (is_bf16 ? 2 : 4) + 511) / 512;
+        const int parts = std::min(pieces, std::max(PB_MIN_PARTS, 2 * 8 * 152 / T));
+    const dim3 grid((unsigned)(((long long)T * parts + 7) / 8));
+    const long long rows = rows_alloc;
+    cudaError_t e;
+    if (dxp_bf16)
+        e = launch_pdl(permute_bwd_kernel<__nv_bfloat16, __nv_bfloat16>, grid, dim3(256), 0, stream,
+                       (const __nv_bfloat16 *)dxp, row_of, (__nv_bfloat16 *)dx, T, k, D, parts, rows,
+                       status);
+    else if (is_bf16)
+        e = launch_pdl(permute_bwd_kernel<float, __nv_bfloat16>, grid, dim3(256), 0, stream,
+                       (const float *)dxp, row_of, (__nv_bfloat16 *)dx, T, k, D, parts, rows, status);
+    else
+        e = launch_pdl(permute_bwd_kernel<float, float>, grid, dim3(256), 0, stream,
+                       (const float *)dxp, row_of, (float *)dx, T, k, D, parts, rows, status);
     if (e == cudaSuccess) count_launch();
     return e;
 }

@@ -46,40 +46,49 @@ namespace moe {
 namespace {
 
 constexpr int X_BM = 256;             // weight rows per pair tile, 128 per CTA
-constexpr int X_BN = 192;             // most tokens per tile
 constexpr int X_UNITS = X_BM / 2;     // hidden units per GEMM1 tile
 constexpr int X_BK = 256;             // K elements per stage
 constexpr int X_ROW = X_BK / 2;       // bytes of a row's K block: the swizzle span
 constexpr int X_W_BYTES = 128 * X_ROW;
-constexpr int X_T_BYTES = X_BN / 2 * X_ROW;
 constexpr int X_SF_BLOCK = 512;       // 128 rows x 4 scales
 constexpr int X_SF_BYTES = 6 * X_SF_BLOCK;  // two K halves of the weights' block, then of the tokens' two
-constexpr int X_STAGE_BYTES = X_W_BYTES + X_T_BYTES;
-constexpr int X_STAGES = 5;
-// Warps: TMA, MMA, scale copies, scale fetchers, epilogue.
+#ifndef MOE_MX_MAXST
+#define MOE_MX_MAXST 6
+#endif
+constexpr int X_MAX_STAGES = MOE_MX_MAXST;
 constexpr int X_GROUP = 4;            // K blocks whose scales are fetched together (32 bytes of a row)
 constexpr int X_GROUP_BYTES = X_GROUP * X_SF_BYTES;
-constexpr int X_SLOTS = 3;            // groups in shared memory
+constexpr int X_SLOTS = 2;            // groups in shared memory
 constexpr int X_SF_WARPS = 2 * X_SLOTS;  // per slot one for the weights' scales, one for the tokens'
-constexpr int X_EPI_GROUPS = 2;       // of four warps (the TMEM lane quarters), alternate chunks of a tile
+// Warps: TMA, MMA, scale copies, scale fetchers, epilogue.
+constexpr int X_EPI_GROUPS = 2;       // of four warps (the TMEM lane quarters), taking chunks of a tile in turn
 constexpr int X_EPI_WARPS = 4 * X_EPI_GROUPS;
 constexpr int X_THREADS = 32 * (3 + X_SF_WARPS + X_EPI_WARPS);
 constexpr int X_TMEM_COLS = 512;
-constexpr int X_SF_COL = 2 * X_BN;    // scale buffers start here
-constexpr int X_SF_COLS = 24;         // 2 x 4 of the weights, 2 x 8 of the tokens
-static_assert(X_SF_COL + X_STAGES * X_SF_COLS <= X_TMEM_COLS, "tensor memory columns");
-static_assert(X_STAGE_BYTES % 1024 == 0 && X_T_BYTES % 1024 == 0, "the swizzle's alignment");
-constexpr int X_NBARS = 2 * X_STAGES + 2 * X_SLOTS + 6;
+constexpr int X_SF_COLS = 24;         // of a K block: 2 x 4 of the weights, 2 x 8 of the tokens
+constexpr int X_NBARS = 2 * X_MAX_STAGES + 2 * X_SLOTS + 6;
 constexpr int X_SMEM_MAX = 227 * 1024;
+constexpr int X_CHUNK = 32;           // tokens that an epilogue group turns around at a time
 // GEMM1's turning buffer, per epilogue group: 32 tokens x (64 gates, 64 ups, 4 of padding)
 constexpr int X_TURN_LD = 132;
-constexpr int X_TURN1 = X_EPI_GROUPS * 32 * X_TURN_LD * 4;
+constexpr int X_TURN1 = X_EPI_GROUPS * X_CHUNK * X_TURN_LD * 4;
 // GEMM2's: per warp 32 tokens x 32 columns fp16
 constexpr int X_TURN2 = X_EPI_WARPS * 32 * 64;
 constexpr int X_EPI_BAR = 1;          // named barriers of the epilogue: one per group
 
+// What follows from the most tokens of a tile, kBN (a multiple of 16).
+template <int kBN>
+struct MxShape {
+    static constexpr int kTBytes = kBN / 2 * X_ROW;         // a CTA's tokens of a stage
+    static constexpr int kStage = X_W_BYTES + kTBytes;
+    static constexpr int kSfCol = 2 * kBN;                  // scale buffers start behind two accumulators
+    static constexpr int kSfBufs = (X_TMEM_COLS - kSfCol) / X_SF_COLS;
+    static_assert(kBN % 16 == 0 && kBN <= 256 && kTBytes % 1024 == 0 && kSfBufs >= 2, "tile shape");
+};
+
 struct MxParams {
     int E_local, e_first, rows_alloc;
+    int stages;           // of the ring
     int K, nk;            // reduction length (D or H_local) and its 256-blocks
     int nt, n_out;        // tiles along the weight rows; columns of the output (H_local or D)
     const int *seg_off, *tpe;
@@ -90,9 +99,11 @@ struct MxParams {
     int *status;
 };
 
-size_t mx_smem_bytes(bool gemm1, int E_local) {
-    return 1024 + (size_t)X_STAGES * X_STAGE_BYTES + X_SLOTS * X_GROUP_BYTES + (gemm1 ? X_TURN1 : X_TURN2) +
-           (X_NBARS + 1) * sizeof(uint64_t) + 16 + sizeof(int) * (4 * (size_t)E_local + 1);
+template <bool kGemm1, int kBN>
+size_t mx_smem_bytes(int stages, int E_local) {
+    return 1024 + (size_t)stages * MxShape<kBN>::kStage + X_SLOTS * X_GROUP_BYTES +
+           (kGemm1 ? X_TURN1 : X_TURN2) + (X_NBARS + 1) * sizeof(uint64_t) + 16 +
+           sizeof(int) * (4 * (size_t)E_local + 1);
 }
 
 // The experts' rows in shared memory: first row, rows, first token tile and
@@ -103,7 +114,7 @@ struct MxTable {
 
 // A warp's way through the tiles of its pair: tile v = token tile * nt +
 // weight tile, an expert's rows in equal token tiles (a multiple of 16, at
-// most X_BN), weight tiles inner.  Every step is n_pairs tiles on, so a few
+// most kBN), weight tiles inner.  Every step is n_pairs tiles on, so a few
 // additions and the next experts' entries replace a division and a search.
 struct MxTile {
     int tt, nt;                    // token tile (over all experts), weight tile
@@ -136,6 +147,7 @@ struct MxTile {
 // Builds the table by one warp, 32 experts at a time; returns the number of
 // token tiles.  Offsets outside [0, rows_alloc] or decreasing flag
 // FLAG_BAD_ROUTING and empty the segment.
+template <int kBN>
 __device__ __forceinline__ void build_mx_table(int lane, const MxParams &p, const MxTable &t,
                                                int *status) {
     int run = 0;
@@ -151,7 +163,7 @@ __device__ __forceinline__ void build_mx_table(int lane, const MxParams &p, cons
                 c = 0;
             }
             v = max(0, min(c, end - b));
-            tiles = (v + X_BN - 1) / X_BN;
+            tiles = (v + kBN - 1) / kBN;
         }
         int incl = tiles;
 #pragma unroll
@@ -255,9 +267,10 @@ struct ScaleWarp {
 // 128 weight rows, or of the tile's tokens (all of them: each CTA's half of the
 // MMA needs all).  Lane l serves rows l, l + 32, ...  A group's loads are issued
 // when the warp's last one is stored.
-template <bool kGemm1, bool kTokens>
+template <bool kGemm1, bool kTokens, int kBN>
 __device__ __forceinline__ void fetch_scales(const ScaleWarp &f, const MxParams &p, const MxTable &table) {
-    constexpr int kRows = kTokens ? X_BN / 32 : 4;
+    constexpr int kRows = kTokens ? (kBN + 31) / 32 : 4;
+    static_assert(kRows <= 8, "two blocks of 128 tokens");
     const int lane = f.lane, ld = p.K / 32, ng = (p.nk + X_GROUP - 1) / X_GROUP;
     const size_t all = (kTokens ? (size_t)p.rows_alloc : (size_t)p.E_local * p.n_out) * ld;
     uint32_t ph = 0;
@@ -302,9 +315,10 @@ __device__ __forceinline__ void fetch_scales(const ScaleWarp &f, const MxParams 
             uint4 *d = reinterpret_cast<uint4 *>(f.room + (j / 2) * X_SF_BYTES) + lane;
             const int h = j & 1;
             if constexpr (kTokens) {
-                d[32 * (2 + 2 * h)] = make_uint4(v[0][j], v[1][j], v[2][j], v[3][j]);
-                if (c.n > 128)  // (rows 192 on do not exist)
-                    d[32 * (3 + 2 * h)] = make_uint4(v[4][j], v[5][j], kMxOnes, kMxOnes);
+                auto of = [&](int i) { return i < kRows ? v[i < kRows ? i : 0][j] : kMxOnes; };
+                d[32 * (2 + 2 * h)] = make_uint4(of(0), of(1), of(2), of(3));
+                if (kBN > 128 && c.n > 128)
+                    d[32 * (3 + 2 * h)] = make_uint4(of(4), of(5), of(6), of(7));
             } else {
                 d[32 * h] = make_uint4(v[0][j], v[1][j], v[2][j], v[3][j]);
             }
@@ -315,7 +329,7 @@ __device__ __forceinline__ void fetch_scales(const ScaleWarp &f, const MxParams 
     }
 }
 
-template <bool kGemm1>
+template <bool kGemm1, int kBN>
 __global__ void __launch_bounds__(X_THREADS, 1)
 grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constant__ CUtensorMap tmT16,
                   const __grid_constant__ CUtensorMap tmT32, const __grid_constant__ CUtensorMap tmT64,
@@ -327,14 +341,17 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
         if (threadIdx.x == 0) raise_flag(p.status, FLAG_LAUNCH);
         return;
     }
+    using Shape = MxShape<kBN>;
+    const int stages = p.stages;
+    const int sf_bufs = min(Shape::kSfBufs, stages);
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint8_t *sfs = ring + X_STAGES * X_STAGE_BYTES;  // [X_SLOTS] groups of scales
+    uint8_t *sfs = ring + stages * Shape::kStage;  // [X_SLOTS] groups of scales
     uint8_t *turn = sfs + X_SLOTS * X_GROUP_BYTES;
     uint64_t *bars = reinterpret_cast<uint64_t *>(turn + (kGemm1 ? X_TURN1 : X_TURN2));
     uint64_t *full = bars;                       // leader: both CTAs' TMA bytes, scales in TMEM -> MMA
-    uint64_t *empty = bars + X_STAGES;           // MMA -> each CTA's TMA, the leader's scale copies
-    uint64_t *tfull = bars + 2 * X_STAGES;       // [2] MMA -> each CTA's epilogue
+    uint64_t *empty = bars + X_MAX_STAGES;       // MMA -> each CTA's TMA, the leader's scale copies
+    uint64_t *tfull = bars + 2 * X_MAX_STAGES;   // [2] MMA -> each CTA's epilogue
     uint64_t *tempty = tfull + 2;                // [2] leader: both epilogues -> MMA
     uint64_t *drain = tempty + 2;                // [2] leader: MMA's and copies' completion at exit
     uint64_t *sfull = drain + 2;                 // [X_SLOTS] leader: both CTAs' group of scales -> copies
@@ -356,7 +373,7 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
     // previous kernel, the table after it
     if (warp == 1) {
         if (lane == 0) {
-            for (int s = 0; s < X_STAGES; ++s) {
+            for (int s = 0; s < stages; ++s) {
                 mbar_init(&full[s], 2);
                 mbar_init(&empty[s], 1);
             }
@@ -385,7 +402,7 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
         if (kGemm1) prefetch_tmap(&tmW1);
     }
     griddep_wait();  // every input of this kernel is complete
-    if (warp == 0) build_mx_table(lane, p, table, blockIdx.x == 0 ? p.status : nullptr);
+    if (warp == 0) build_mx_table<kBN>(lane, p, table, blockIdx.x == 0 ? p.status : nullptr);
     tc_fence_before();
     __syncthreads();
     cluster_sync();  // the peer's barriers exist before anything arrives on them
@@ -403,7 +420,7 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
         bool ok = true;
         MxTile c(pair_id, p.nt, total, table);
         for (int tile = pair_id; ok && tile < total;) {
-            const int trows = c.n / 2;  // this CTA's token rows: a multiple of 8, at most 96
+            const int trows = c.n / 2;  // this CTA's token rows: a multiple of 8, below 128
             const int trow = c.row0 + (int)rank * trows;
             const int wrow = kGemm1 ? c.nt * X_UNITS + (int)rank * 64 : c.nt * X_BM + (int)rank * 128;
             const uint32_t tx = 2u * (uint32_t)(X_W_BYTES + trows * X_ROW);
@@ -414,7 +431,7 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
                 }
                 if (elect_one()) {
                     if (leader) mbar_arrive_expect_tx(&full[s], tx);
-                    uint8_t *sw = ring + s * X_STAGE_BYTES;
+                    uint8_t *sw = ring + s * Shape::kStage;
                     uint8_t *st = sw + X_W_BYTES;
                     const uint32_t fb = full_leader + (uint32_t)(s * sizeof(uint64_t));
                     tma_load_3d_pair(sw, &tmW0, fb, kb * X_ROW, wrow, c.expert);
@@ -437,7 +454,7 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
                         tma_load_2d_pair(st + at * X_ROW, &tmT8, fb, kb * X_ROW, trow + at);
                 }
                 __syncwarp();
-                if (++s == X_STAGES) { s = 0; ph ^= 1u; }
+                if (++s == stages) { s = 0; ph ^= 1u; }
             }
             tile += n_pairs;
             c.step(dt, dn, p.nt, tile < total, table);
@@ -445,7 +462,7 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
     } else if (warp == 1) {
         if (leader) {
             // ---------------- MMA issuer (leader CTA) ----------------
-            int s = 0;
+            int s = 0, sb = 0;  // stage, scale buffer
             uint32_t ph = 0;
             bool ok = true;
             int it = 0;
@@ -457,7 +474,7 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
                 if (!__all_sync(0xffffffffu, mbar_wait_bounded(
                                                  &tempty[acc], ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag)))
                     break;
-                const uint32_t d_tmem = tmem_base + (uint32_t)(acc * X_BN);
+                const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kBN);
                 for (int kb = 0; kb < p.nk; ++kb) {
                     if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[s], ph, abort_flag))) {
                         ok = false;
@@ -467,9 +484,9 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
                     if (elect_one()) {
                         // Descriptors count in 16 bytes and do not carry out of their
                         // address field: all of shared memory is below 2^18.
-                        const uint64_t w_desc = w_desc0 + (uint64_t)(s * (X_STAGE_BYTES / 16));
+                        const uint64_t w_desc = w_desc0 + (uint64_t)(s * (Shape::kStage / 16));
                         const uint64_t t_desc = w_desc + X_W_BYTES / 16;
-                        const uint32_t sfw = tmem_base + (uint32_t)(X_SF_COL + s * X_SF_COLS);
+                        const uint32_t sfw = tmem_base + (uint32_t)(Shape::kSfCol + sb * X_SF_COLS);
                         const uint32_t sft = sfw + 8;
                         tc_mma_mxf4_pair(d_tmem, w_desc, t_desc, id0, sfw, sft, kb != 0 ? 1u : 0u);
                         tc_mma_mxf4_pair(d_tmem, w_desc + 2, t_desc + 2, id2, sfw, sft, 1u);
@@ -479,7 +496,8 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
                         if (kb == p.nk - 1) tc_commit_pair(&tfull[acc], 0x3);
                     }
                     __syncwarp();
-                    if (++s == X_STAGES) { s = 0; ph ^= 1u; }
+                    if (++s == stages) { s = 0; ph ^= 1u; }
+                    if (++sb == sf_bufs) sb = 0;
                 }
                 tile += n_pairs;
                 c.step(dt, dn, p.nt, tile < total, table);
@@ -494,10 +512,12 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
         if (leader) {
             // ---------------- scale copies (leader CTA) ----------------
             // A K block's scales go to the tensor memory of both CTAs as soon as
-            // the stage's last MMAs have completed; their completion is the
-            // second of the two arrivals that the stage's MMAs wait for.
-            int s = 0, sg = 0;
-            uint32_t ph = 0, phg = 0;
+            // the last MMAs that read the buffer, sf_bufs K blocks back, have
+            // completed; their completion is the second of the two arrivals that
+            // the stage's MMAs wait for.
+            int s = 0, sg = 0, sb = 0;
+            int s2 = 0, lag = sf_bufs;  // the stage sf_bufs K blocks back
+            uint32_t ph2 = 0, phg = 0;
             bool ok = true;
             const uint64_t f_desc0 = sdesc_scales(smem_u32(sfs));
             MxTile c(pair_id, p.nt, total, table);
@@ -507,14 +527,19 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
                     const int k4 = kb % X_GROUP;
                     bool got = true;
                     if (k4 == 0) got = mbar_wait_bounded(&sfull[sg], phg, abort_flag);
-                    got = got && mbar_wait_bounded(&empty[s], ph ^ 1u, abort_flag);
+                    if (lag > 0) {
+                        --lag;
+                    } else {
+                        got = got && mbar_wait_bounded(&empty[s2], ph2, abort_flag);
+                        if (++s2 == stages) { s2 = 0; ph2 ^= 1u; }
+                    }
                     if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
                     tc_fence_after();
                     const bool last = k4 == X_GROUP - 1 || kb == p.nk - 1;
                     if (elect_one()) {
                         const uint64_t f_desc =
                             f_desc0 + (uint64_t)(sg * (X_GROUP_BYTES / 16) + k4 * (X_SF_BYTES / 16));
-                        const uint32_t sfw = tmem_base + (uint32_t)(X_SF_COL + s * X_SF_COLS);
+                        const uint32_t sfw = tmem_base + (uint32_t)(Shape::kSfCol + sb * X_SF_COLS);
                         const uint32_t sft = sfw + 8;
                         // blocks 0, 1: the weights' K halves; 2 + 2 half + token / 128: the tokens'
                         constexpr uint64_t kBlk = X_SF_BLOCK / 16;
@@ -530,7 +555,8 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
                         if (last) tc_commit_pair(&sempty[sg], 0x3);
                     }
                     __syncwarp();
-                    if (++s == X_STAGES) { s = 0; ph ^= 1u; }
+                    if (++s == stages) s = 0;
+                    if (++sb == sf_bufs) sb = 0;
                     if (last && ++sg == X_SLOTS) { sg = 0; phg ^= 1u; }
                 }
                 tile += n_pairs;
@@ -555,7 +581,7 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
             // a group's warps go on, or stop, together
             if (!bar_and(X_EPI_BAR + eg, 128, got)) break;
             tc_fence_after();
-            const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * X_BN);
+            const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kBN);
             // The accumulator is the MMA's again once this warp has its last chunk
             // in registers; nothing in memory goes with that.
             auto release = [&]() {
@@ -564,17 +590,17 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
                 if (lane == 0)
                     mbar_arrive_cluster_relaxed(tempty_leader + (uint32_t)(acc * sizeof(uint64_t)));
             };
-            const int step = 32 * X_EPI_GROUPS;
-            const bool none = 32 * eg >= c.nvalid ||
+            constexpr int step = X_CHUNK * X_EPI_GROUPS;
+            const bool none = X_CHUNK * eg >= c.nvalid ||
                               (!kGemm1 && c.nt * X_BM + (int)rank * 128 + q * 32 >= p.n_out);
             if (none) release();
             if (kGemm1) {
                 // lanes 0-63 are the gates of units `unit0`.., 64-127 their ups
                 const int unit0 = c.nt * X_UNITS + (int)rank * 64;
-                const int tok = (q & 1) * 16 + (lane >> 1);   // of the 32 in the buffer
-                const int unit = unit0 + (q >> 1) * 32 + (lane & 1) * 16;
-                float *buf = reinterpret_cast<float *>(turn) + eg * (32 * X_TURN_LD);
-                for (int t0 = 32 * eg; t0 < c.nvalid; t0 += step) {
+                const int tok = (q & 1) * 16 + (lane >> 1);    // of the chunk in the buffer
+                const int unit = (q >> 1) * 32 + (lane & 1) * 16;
+                float *buf = reinterpret_cast<float *>(turn) + eg * (X_CHUNK * X_TURN_LD);
+                for (int t0 = X_CHUNK * eg; t0 < c.nvalid; t0 += step) {
                     uint32_t d[32];
                     tmem_ld_32x32b_x32(tb + t0, d);
                     tc_wait_ld();
@@ -584,7 +610,7 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
                     for (int j = 0; j < 32; ++j)
                         buf[j * X_TURN_LD + q * 32 + lane] = __uint_as_float(d[j]);
                     bar_sync(X_EPI_BAR + eg, 128);
-                    const float *src = buf + tok * X_TURN_LD + (q >> 1) * 32 + (lane & 1) * 16;
+                    const float *src = buf + tok * X_TURN_LD + unit;
                     float h[16];
                     uint32_t top = 0;
 #pragma unroll
@@ -598,16 +624,17 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
                     }
 #pragma unroll
                     for (int i = 0; i < 16; ++i) top = max(top, abs_bits(h[i]));
-                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));  // the block's other half
                     const uint32_t sb = mx_scale_byte(top);
                     const float inv = mx_inv_scale(sb);
-                    if (t0 + tok < c.nvalid && unit < p.n_out) {
+                    if (t0 + tok < c.nvalid && unit0 + unit < p.n_out) {
                         const size_t row = (size_t)(c.row0 + t0 + tok);
-                        *reinterpret_cast<uint2 *>(p.hq + row * (size_t)(p.n_out / 2) + unit / 2) =
+                        *reinterpret_cast<uint2 *>(p.hq + row * (size_t)(p.n_out / 2) +
+                                                   (unit0 + unit) / 2) =
                             make_uint2(mx_codes8(*reinterpret_cast<const float(*)[8]>(h), inv),
                                        mx_codes8(*reinterpret_cast<const float(*)[8]>(h + 8), inv));
                         if ((lane & 1) == 0)
-                            p.hsf[row * (size_t)(p.n_out / 32) + unit / 32] = (uint8_t)sb;
+                            p.hsf[row * (size_t)(p.n_out / 32) + (unit0 + unit) / 32] = (uint8_t)sb;
                     }
                 }
             } else {
@@ -615,7 +642,7 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
                 const int col0 = c.nt * X_BM + (int)rank * 128 + q * 32;
                 __half *buf = reinterpret_cast<__half *>(turn + ew * (32 * 64));
                 if (!none) {  // (D is a multiple of 32: a warp's columns are all there or none is)
-                    for (int t0 = 32 * eg; t0 < c.nvalid; t0 += step) {
+                    for (int t0 = X_CHUNK * eg; t0 < c.nvalid; t0 += step) {
                         uint32_t d[32];
                         tmem_ld_32x32b_x32(tb + t0, d);
                         tc_wait_ld();
@@ -650,9 +677,9 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
                           mapa_shared(smem_u32(&sfull[slot]), 0), abort_flag, slot, lane,
                           pair_id, n_pairs, total, dt, dn, (int)rank};
         if (w & 1)
-            fetch_scales<kGemm1, true>(f, p, table);
+            fetch_scales<kGemm1, true, kBN>(f, p, table);
         else
-            fetch_scales<kGemm1, false>(f, p, table);
+            fetch_scales<kGemm1, false, kBN>(f, p, table);
     }
 
     tc_fence_before();
@@ -672,7 +699,7 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
 }
 
 // Clusters of two that fit at once on the current device (0 if none).
-template <bool kGemm1>
+template <bool kGemm1, int kBN>
 int max_mx_clusters(size_t smem) {
     constexpr int kMaxDev = 64;
     static int cached[kMaxDev] = {0};
@@ -692,7 +719,7 @@ int max_mx_clusters(size_t smem) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, (void *)grouped_mx_kernel<kGemm1>, &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&n, (void *)grouped_mx_kernel<kGemm1, kBN>, &cfg) != cudaSuccess) {
         cudaGetLastError();
         return 0;
     }
@@ -712,15 +739,18 @@ bool token_maps(MxMaps *m, const uint8_t *codes, int K, int64_t rows) {
            make_tmap_tile(&m->t64, codes, 1, K / 2, rows, 0, X_ROW, 64, 128);
 }
 
-template <bool kGemm1>
-cudaError_t launch_mx(const MxMaps &m, const MxParams &p, long long token_tiles, cudaStream_t stream) {
-    const size_t smem = mx_smem_bytes(kGemm1, p.E_local);
-    static_assert(1024 + X_STAGES * X_STAGE_BYTES + X_SLOTS * X_GROUP_BYTES + X_TURN1 +
+template <bool kGemm1, int kBN>
+cudaError_t launch_mx(const MxMaps &m, MxParams p, long long token_tiles, cudaStream_t stream) {
+    static_assert(1024 + 4 * MxShape<kBN>::kStage + X_SLOTS * X_GROUP_BYTES + X_TURN1 +
                           (X_NBARS + 1) * 8 + 16 + 4 * (4 * 1024 + 1) <= X_SMEM_MAX,
-                  "the table of 1024 experts fits beside the ring");
-    cudaError_t e = ensure_smem((const void *)grouped_mx_kernel<kGemm1>, smem);
+                  "four stages fit beside the table of 1024 experts");
+    int stages = X_MAX_STAGES;  // as many as fit beside the table of the experts
+    while (mx_smem_bytes<kGemm1, kBN>(stages, p.E_local) > X_SMEM_MAX) --stages;
+    p.stages = stages;
+    const size_t smem = mx_smem_bytes<kGemm1, kBN>(stages, p.E_local);
+    cudaError_t e = ensure_smem((const void *)grouped_mx_kernel<kGemm1, kBN>, smem);
     if (e != cudaSuccess) return e;
-    const int clusters = max_mx_clusters<kGemm1>(smem);
+    const int clusters = max_mx_clusters<kGemm1, kBN>(smem);
     if (clusters <= 0) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (unsigned)std::min<long long>(clusters, token_tiles * p.nt));
@@ -736,7 +766,7 @@ cudaError_t launch_mx(const MxMaps &m, const MxParams &p, long long token_tiles,
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = MOE_PDL ? 2 : 1;
-    e = cudaLaunchKernelEx(&cfg, grouped_mx_kernel<kGemm1>, m.t8, m.t16, m.t32, m.t64, m.w0, m.w1, p);
+    e = cudaLaunchKernelEx(&cfg, grouped_mx_kernel<kGemm1, kBN>, m.t8, m.t16, m.t32, m.t64, m.w0, m.w1, p);
     if (e == cudaSuccess) count_launch();
     return e;
 }
@@ -758,8 +788,12 @@ cudaError_t launch_grouped_swiglu_mxfp4(const uint8_t *x_perm_q, const uint8_t *
         return cudaErrorInvalidValue;
     m2.w1 = m2.w0;
 
+#ifndef MOE_MX_BN
+#define MOE_MX_BN 208
+#endif
+    constexpr int kBN = MOE_MX_BN;
     // token tiles: at most one partial tile per expert beside the whole ones
-    const long long tt = std::min<long long>(rows_alloc, rows_alloc / X_BN + E_local);
+    const long long tt = std::min<long long>(rows_alloc, rows_alloc / kBN + E_local);
     MxParams p{};
     p.E_local = E_local;
     p.e_first = e_first;
@@ -778,7 +812,7 @@ cudaError_t launch_grouped_swiglu_mxfp4(const uint8_t *x_perm_q, const uint8_t *
     p1.w_sf1 = w.w3_scale;
     p1.hq = h_q;
     p1.hsf = h_scale;
-    const cudaError_t e = launch_mx<true>(m1, p1, tt, stream);
+    const cudaError_t e = launch_mx<true, kBN>(m1, p1, tt, stream);
     if (e != cudaSuccess) return e;
 
     MxParams p2 = p;
@@ -789,7 +823,7 @@ cudaError_t launch_grouped_swiglu_mxfp4(const uint8_t *x_perm_q, const uint8_t *
     p2.t_sf = h_scale;
     p2.w_sf0 = p2.w_sf1 = w.w2_scale;
     p2.y = static_cast<__half *>(y_perm);
-    return launch_mx<false>(m2, p2, tt, stream);
+    return launch_mx<false, kBN>(m2, p2, tt, stream);
 }
 
 }  // namespace moe

@@ -209,11 +209,16 @@ cudaError_t launch_combine_bwd(const void *dout, const void *y_perm, const int *
 // Backward of the dispatch: dx[t] = sum_j dxp[row_of[t, j]] + r[t], where
 // r[t] = add[t] when add, else sum_j dl[t, e_j] wg[e_j] (e_j = topk_idx[t, j];
 // the router's part of dx when dl is zero off the selected experts), else 0.
-// dxp is fp32, or bf16 with dxp_bf16 (bf16 layers).
-cudaError_t launch_dispatch_bwd(const void *dxp, int dxp_bf16, const int *row_of, const float *add,
+cudaError_t launch_dispatch_bwd(const float *dxp, const int *row_of, const float *add,
                                 const int *topk_idx, const float *dl, const void *wg, int E,
                                 void *dx, int T, int D, int k, int64_t rows_alloc, int is_bf16,
-                                int *status, cudaStream_t stream);
+                                cudaStream_t stream);
+
+// The same without the router's part, for moe_permute_backward: dxp fp32, or
+// bf16 with dxp_bf16 (bf16 layers); rows outside [-1, rows_alloc) are flagged.
+cudaError_t launch_permute_bwd(const void *dxp, int dxp_bf16, const int *row_of, void *dx, int T,
+                               int D, int k, int64_t rows_alloc, int is_bf16, int *status,
+                               cudaStream_t stream);
 
 // dl is dense (every expert's logit gets a gradient) only for a softmax
 // over all E without renormalisation; otherwise it is zero off the k

@@ -807,8 +807,8 @@ MOE_EXPORT moe_status moe_layer_backward_ex(const moe_config *cfg, const void *x
     if (e != cudaSuccess) return cuda_fail(e, "moe_layer_backward: router backward");
     // the router's part of dx: a GEMM where dl is dense, else folded in here
     const bool dense = moe::router_dl_dense(cfg->score, cfg->renorm);
-    e = moe::launch_dispatch_bwd(W.dxp, 0, L.row_of, dense ? W.dxr : nullptr, L.topk_idx, W.dl, wg,
-                                 cfg->E, dx, cfg->T, cfg->D, cfg->k, rows, 1, flags, s);
+    e = moe::launch_dispatch_bwd(W.dxp, L.row_of, dense ? W.dxr : nullptr, L.topk_idx, W.dl, wg,
+                                 cfg->E, dx, cfg->T, cfg->D, cfg->k, rows, 1, s);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_layer_backward: dispatch backward");
 }
 
@@ -1050,11 +1050,10 @@ MOE_EXPORT moe_status moe_permute_backward(const moe_config *cfg, const void *dx
     const int64_t rows = rows_alloc_of(cfg);
     if (!row_of || !aligned(row_of, 4) || !need16(dx) || (rows > 0 && !need16(dx_perm)))
         return arg_fail("moe_permute_backward: NULL or misaligned tensor");
-    const cudaError_t e = moe::launch_dispatch_bwd(dx_perm, dx_perm_dtype == MOE_BF16, row_of,
-                                                   nullptr, nullptr, nullptr, nullptr, cfg->E, dx,
-                                                   cfg->T, cfg->D, cfg->k, rows,
-                                                   cfg->dtype == MOE_BF16, &w.status->flags,
-                                                   (cudaStream_t)stream);
+    const cudaError_t e = moe::launch_permute_bwd(dx_perm, dx_perm_dtype == MOE_BF16, row_of, dx,
+                                                  cfg->T, cfg->D, cfg->k, rows,
+                                                  cfg->dtype == MOE_BF16, &w.status->flags,
+                                                  (cudaStream_t)stream);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_permute_backward");
 }
 

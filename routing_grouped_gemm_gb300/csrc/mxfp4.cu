@@ -16,7 +16,10 @@ namespace moe {
 namespace {
 
 // 8-value pieces of a thread that are in flight together.
-constexpr int MX_UNROLL = 4;
+#ifndef MOE_MXQ_UNROLL
+#define MOE_MXQ_UNROLL 4
+#endif
+constexpr int MX_UNROLL = MOE_MXQ_UNROLL;
 
 template <typename T>
 __global__ void __launch_bounds__(256)
@@ -43,23 +46,19 @@ quantize_rows_mxfp4_kernel(const T *__restrict__ src, long long n8, uint32_t *__
     }
 }
 
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&f)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t *>(&h);
-    }
+// 8 values held as bf16 (two to a word) to a bf16 or an fp32 row.
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const uint32_t (&w)[4]) {
     __stcs(reinterpret_cast<uint4 *>(p), make_uint4(w[0], w[1], w[2], w[3]));
 }
-__device__ __forceinline__ void store8(float *p, const float (&f)[8]) {
-    __stcs(reinterpret_cast<float4 *>(p), make_float4(f[0], f[1], f[2], f[3]));
-    __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(f[4], f[5], f[6], f[7]));
+__device__ __forceinline__ void store8(float *p, const uint32_t (&w)[4]) {
+    uint4 *o = reinterpret_cast<uint4 *>(p);
+    __stcs(o, make_uint4(w[0] << 16, w[0] & 0xffff0000u, w[1] << 16, w[1] & 0xffff0000u));
+    __stcs(o + 1, make_uint4(w[2] << 16, w[2] & 0xffff0000u, w[3] << 16, w[3] & 0xffff0000u));
 }
 
 // Every value is exact in bf16 as in fp32 (two significant bits, exponents of
 // the binary32 range) but beyond scale byte 252, which the quantiser never
-// writes: there 6 * 2^126 and more round to infinity as binary32 does.
+// writes: there a value above the range becomes infinite.
 template <typename T>
 __global__ void __launch_bounds__(256)
 dequantize_rows_mxfp4_kernel(const uint32_t *__restrict__ codes, const uint8_t *__restrict__ scale,
@@ -71,18 +70,16 @@ dequantize_rows_mxfp4_kernel(const uint32_t *__restrict__ codes, const uint8_t *
 #pragma unroll
     for (int u = 0; u < MX_UNROLL; ++u) {
         const long long i = base + u * 256;
-        q[u] = i < n8 ? codes[i] : 0u;
+        q[u] = i < n8 ? __ldcs(codes + i) : 0u;
         b[u] = i < n8 ? scale[i >> 2] : 0u;
     }
 #pragma unroll
     for (int u = 0; u < MX_UNROLL; ++u) {
         const long long i = base + u * 256;
         if (i >= n8) continue;
-        const float s = mx_scale(b[u]);
-        float f[8];
-#pragma unroll
-        for (int v = 0; v < 8; ++v) f[v] = mx_value((q[u] >> (4 * v)) & 15u) * s;
-        store8(dst + i * 8, f);
+        uint32_t w[4];
+        mx_values8(q[u], mx_scale_bf16x2(b[u]), w);
+        store8(dst + i * 8, w);
     }
 }
 
@@ -97,7 +94,7 @@ dispatch_rows_mxfp4_kernel(const __nv_bfloat16 *__restrict__ src, long long rows
     const int lane = threadIdx.x & 31;
     if (t >= rows) return;
     const int my_row = lane < k ? row_of[(size_t)t * k + lane] : -1;
-    quantize_row_mxfp4_warp(src + (size_t)t * cols, cols, my_row, k, dst, scale, lane);
+    quantize_row_mxfp4_warp(src + (size_t)t * cols, cols, 0, 256, my_row, k, dst, scale, lane);
 }
 
 bool grid_of(long long n8, unsigned *blocks) {

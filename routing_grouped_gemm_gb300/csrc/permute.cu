@@ -544,10 +544,16 @@ permute_index_copy_kernel(const uint4 *__restrict__ x, const int *__restrict__ t
                           long long rows_alloc, int cols, float *__restrict__ x_scale,
                           const int *__restrict__ blk_cnt, int nblk, int layout, int align_m,
                           int capacity, int *__restrict__ tpe_out, int *__restrict__ seg_out,
-                          uint8_t *__restrict__ x_sf, int *status) {
+                          uint8_t *__restrict__ x_sf, int parts_, int *status) {
     griddep_launch_dependents();  // the next kernel may be scheduled now
     griddep_wait();               // every input of this kernel is complete
-    const int t = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    // The MXFP4 copy of a small batch gives each token `parts` warps, which take
+    // its row's columns in turn, and launches further warps that only mark
+    // padding rows (`fill` of `fills`); otherwise one warp per token does both.
+    const int parts = kCopy == COPY_MXFP4 ? parts_ : 1;
+    const int wid = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    const int t = wid / parts, part = wid - t * parts;
+    const int fill = wid, fills = kCopy == COPY_MXFP4 ? gridDim.x * IC_WARPS : T;
     const int lane = threadIdx.x & 31;
     // offsets: derived here (kDerive; the whole block takes part before any
     // warp leaves), or written by the count kernel's last block
@@ -560,14 +566,16 @@ permute_index_copy_kernel(const uint4 *__restrict__ x, const int *__restrict__ t
         s_pre = s_tot + E;
         int *s_off = s_pre + E;
         int *s_wsum = s_off + E_local + 1;
-        derive_offsets(blk_cnt, nblk, (blockIdx.x * (blockDim.x >> 5)) / PB_TOKENS, E, e_first,
+        derive_offsets(blk_cnt, nblk,
+                       min(nblk - 1, blockIdx.x * (int)(blockDim.x >> 5) / parts / PB_TOKENS), E, e_first,
                        E_local, layout, align_m, capacity, s_tot, s_pre, s_off, s_wsum, tpe_out,
                        seg_out, status);
         seg_offsets = s_off;
         tokens_per_expert = s_tot;
     }
-    if (t >= T) return;
-    const int e = lane < k ? topk_idx[(size_t)t * k + lane] : -1;
+    if (kCopy != COPY_MXFP4 && t >= T) return;
+    const bool token = t < T;
+    const int e = token && lane < k ? topk_idx[(size_t)t * k + lane] : -1;
     const uint4 *src = x + (size_t)t * vpr;
     uint4 buf[IC_UNROLL];
     if (kCopy == COPY_PLAIN && x_perm) {
@@ -591,17 +599,17 @@ permute_index_copy_kernel(const uint4 *__restrict__ x, const int *__restrict__ t
         const int cand = first + m.y + __popc((uint32_t)m.x & ((1u << (t & 31)) - 1u));
         if (cand < seg_offsets[i + 1]) {
             my_row = cand;
-            token_of_row[cand] = t;
+            if (part == 0) token_of_row[cand] = t;
         }
     }
-    if (lane < k) row_of[(size_t)t * k + lane] = my_row;
-    for (int s = t; s < E_local; s += T) {
+    if (token && part == 0 && lane < k) row_of[(size_t)t * k + lane] = my_row;
+    for (int s = fill; s < E_local; s += fills) {
         const int lo = seg_offsets[s], hi = seg_offsets[s + 1];
         const int used = min(tokens_per_expert[e_first + s], hi - lo);
         for (int r = lo + used + lane; r < hi; r += 32) token_of_row[r] = -1;
     }
-    for (long long r = (long long)seg_offsets[E_local] + (long long)t * 32 + lane; r < rows_alloc;
-         r += (long long)T * 32)
+    for (long long r = (long long)seg_offsets[E_local] + (long long)fill * 32 + lane; r < rows_alloc;
+         r += (long long)fills * 32)
         token_of_row[r] = -1;
     if (kCopy == COPY_E4M3) {
         quantize_row_e4m3_warp(src, cols, my_row, k, reinterpret_cast<uint8_t *>(x_perm), x_scale,
@@ -609,8 +617,12 @@ permute_index_copy_kernel(const uint4 *__restrict__ x, const int *__restrict__ t
         return;
     }
     if (kCopy == COPY_MXFP4) {
-        quantize_row_mxfp4_warp(reinterpret_cast<const __nv_bfloat16 *>(src), cols, my_row, k,
-                                reinterpret_cast<uint8_t *>(x_perm), x_sf, lane);
+        const __nv_bfloat16 *xr = reinterpret_cast<const __nv_bfloat16 *>(src);
+        uint8_t *xq = reinterpret_cast<uint8_t *>(x_perm);
+        if (token && parts == 1)  // the strides known
+            quantize_row_mxfp4_warp(xr, cols, 0, 256, my_row, k, xq, x_sf, lane);
+        else if (token)
+            quantize_row_mxfp4_warp(xr, cols, part * 256, parts * 256, my_row, k, xq, x_sf, lane);
         return;
     }
     if (zero_out) {  // the fused combine's accumulator row of this token starts at zero
@@ -684,11 +696,14 @@ constexpr int CB_SLOTS = 8;  // slots whose loads are issued together
 // y_perm is read once: its loads are evict-first (ld.global.cs), which
 // measured 39 against 45 us with the default policy on the fine-grained step.
 
-#ifndef MOE_COMBINE_PARTS
-#define MOE_COMBINE_PARTS 1
-#endif
-constexpr int CB_PARTS = MOE_COMBINE_PARTS;  // warps per token (1: 45 us, 2: 52 us, 4: 51 us
-                                              // on the fine-grained step, fp32 y_perm)
+// Warps per token.  One where the tokens alone fill the GPU (two or four were
+// slower there: fine-grained step, fp32 y_perm, 45 against 52 and 51 us); a
+// smaller batch splits each row into whole 32-vector chunks, up to one warp per
+// chunk, until there are CB_MIN_WARPS of them (a decode batch of 128 tokens,
+// D = 7168: 41 us with one warp per token).  Each output element is summed by
+// one lane in slot order either way: the same bits.
+constexpr int CB_MIN_WARPS = 2 * 8 * 152;
+
 // 32-vector chunks of the row whose loads one warp issues together
 #ifndef MOE_COMBINE_CHUNKS
 #define MOE_COMBINE_CHUNKS 1
@@ -713,22 +728,25 @@ constexpr int CB_WPB = MOE_COMBINE_WPB;  // warps per block
 // y_perm is fp16 for bf16 layers (out bf16) and fp32 for fp32 layers.  The
 // loop over 16-byte output vectors is uniform across the warp (the shuffles
 // inside need every lane), with per-lane predicates for the row tail.
-template <bool BF16>
-__global__ void __launch_bounds__(32 * CB_WPB, MOE_COMBINE_MINB)
+// kSplit: `parts` warps per token (an instantiation of its own: with the count
+// known to be one, the row loop keeps its 64 registers without spills).
+template <bool BF16, bool kSplit>
+__global__ void __launch_bounds__(32 * CB_WPB, kSplit ? 2 : MOE_COMBINE_MINB)
 combine_kernel(const void *__restrict__ y, const int *__restrict__ row_of,
                const float *__restrict__ topk_w, void *__restrict__ out, int T, int k, int D,
-               long long rows_alloc, int *status) {
+               int parts_, long long rows_alloc, int *status) {
+    const int parts = kSplit ? parts_ : 1;
     griddep_launch_dependents();  // the next kernel may be scheduled now
     griddep_wait();               // every input of this kernel is complete
-    // One warp per (token, part): a token's row is split into CB_PARTS parts
-    // of whole 32-vector chunks, so the grid has CB_PARTS x T warps.
+    // One warp per (token, part): a token's row is split into `parts` parts of
+    // whole 32-vector chunks.
     constexpr int EPV = BF16 ? 8 : 4;      // output (and y) elements per 16-byte vector
     const int vpr = D / EPV;               // 16-byte vectors per output row and per y row
     const int nchunk = (vpr + 31) / 32;
     const int lane = threadIdx.x & 31;
     const long long wid = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-    const int t = (int)(wid / CB_PARTS);
-    const int part = (int)(wid - (long long)t * CB_PARTS);
+    const int t = (int)(wid / parts);
+    const int part = (int)(wid - (long long)t * parts);
     if (t >= T) return;
     const uint4 *yv = static_cast<const uint4 *>(y);
     int my_row = -1;
@@ -741,7 +759,20 @@ combine_kernel(const void *__restrict__ y, const int *__restrict__ row_of,
             my_row = -1;
         }
     }
-    const int c_lo = part * nchunk / CB_PARTS, c_hi = (part + 1) * nchunk / CB_PARTS;
+    // the first CB_SLOTS slots' rows and weights stay in registers over the row
+    int rj[CB_SLOTS];
+    float wj[CB_SLOTS];
+    auto slots_from = [&](int j0) {
+#pragma unroll
+        for (int u = 0; u < CB_SLOTS; ++u) {
+            rj[u] = __shfl_sync(0xffffffffu, my_row, (j0 + u) & 31);
+            wj[u] = __shfl_sync(0xffffffffu, my_w, (j0 + u) & 31);
+            if (j0 + u >= k) rj[u] = -1;
+        }
+    };
+    slots_from(0);
+    const int c_lo = (int)((long long)part * nchunk / parts);
+    const int c_hi = (int)((long long)(part + 1) * nchunk / parts);
     for (int c = c_lo; c < c_hi; c += CB_CHUNKS) {
         int v[CB_CHUNKS];
         bool act[CB_CHUNKS];
@@ -755,14 +786,9 @@ combine_kernel(const void *__restrict__ y, const int *__restrict__ row_of,
         }
         for (int j0 = 0; j0 < k; j0 += CB_SLOTS) {
             uint4 val[CB_SLOTS][CB_CHUNKS];
-            float wj[CB_SLOTS];
-            int rj[CB_SLOTS];
+            if (k > CB_SLOTS) slots_from(j0);
 #pragma unroll
             for (int u = 0; u < CB_SLOTS; ++u) {
-                const int j = j0 + u;
-                rj[u] = __shfl_sync(0xffffffffu, my_row, j & 31);
-                wj[u] = __shfl_sync(0xffffffffu, my_w, j & 31);
-                if (j >= k) rj[u] = -1;
 #pragma unroll
                 for (int q = 0; q < CB_CHUNKS; ++q)
                     if (act[q] && rj[u] >= 0) val[u][q] = __ldcs(yv + (size_t)rj[u] * vpr + v[q]);
@@ -856,7 +882,19 @@ cudaError_t launch_permute(const void *x, const int *topk_idx, int *tokens_per_e
             return err;
         count_launch();
         const int warps_per_block = IC_WARPS;
-        const int blocks = (T + warps_per_block - 1) / warps_per_block;
+        // MXFP4: warps per token, a power of two, so that a block's tokens stay in
+        // one count block: as many as it takes for two blocks per SM, at most one
+        // per 256 values of the row; and enough blocks to mark the padding rows in
+        // a few steps each (one token of the fine-grained layer leaves 8128: 254
+        // steps for one warp)
+        int parts = 1;
+        long long blocks = ((long long)T + warps_per_block - 1) / warps_per_block;
+        if (x_sf) {
+            while (parts < IC_WARPS && 2 * parts * 256 <= D && 2LL * parts * T <= 2 * IC_WARPS * 152)
+                parts *= 2;
+            blocks = ((long long)T * parts + warps_per_block - 1) / warps_per_block;
+            blocks = std::max(blocks, std::min<long long>(76, rows_alloc / (32 * warps_per_block * 4)));
+        }
         const size_t csmem =
             derive ? sizeof(int) * (2 * (size_t)E + E_local + 1 + warps_per_block) : 0;
         auto copy_kernel = x_sf      ? (derive ? permute_index_copy_kernel<COPY_MXFP4, true>
@@ -867,14 +905,14 @@ cudaError_t launch_permute(const void *x, const int *topk_idx, int *tokens_per_e
                                                : permute_index_copy_kernel<COPY_PLAIN, false>);
         if (csmem > 0 && (err = ensure_smem((const void *)copy_kernel, csmem)) != cudaSuccess)
             return err;
-        if ((err = launch_pdl(copy_kernel, dim3(blocks), dim3(32 * warps_per_block), csmem, stream,
+        if ((err = launch_pdl(copy_kernel, dim3((unsigned)blocks), dim3(32 * warps_per_block), csmem, stream,
                               (const uint4 *)x, topk_idx, (const int2 *)wmeta,
                               (const int *)blk_base, (const int *)seg_offsets, row_of, token_of_row,
                               (uint4 *)x_perm, T, k, E, e_first, E_local, D * elem_bytes / 16,
                               (float4 *)zero_out, D / 4, (const int *)tokens_per_expert,
                               (long long)rows_alloc, D, x_scale, (const int *)blk_cnt, nblk,
                               layout, align_m, capacity, tokens_per_expert, seg_offsets, x_sf,
-                              status)) != cudaSuccess)
+                              parts, status)) != cudaSuccess)
             return err;
         count_launch();
         return cudaGetLastError();
@@ -969,13 +1007,15 @@ cudaError_t launch_combine(const void *y_perm, const int *row_of, const float *t
                            cudaStream_t stream) {
     if (T == 0) return cudaSuccess;
     const int warps_per_block = CB_WPB;
-    const long long warps = (long long)T * CB_PARTS;
+    const int nchunk = (D / (is_bf16 ? 8 : 4) + 31) / 32;
+    const int parts = std::max(1, std::min(nchunk, CB_MIN_WARPS / T));
+    const long long warps = (long long)T * parts;
     const int blocks = (int)((warps + warps_per_block - 1) / warps_per_block);
-    const cudaError_t err =
-        is_bf16 ? launch_pdl(combine_kernel<true>, dim3(blocks), dim3(32 * warps_per_block), 0, stream,
-                             y_perm, row_of, topk_w, out, T, k, D, (long long)rows_alloc, status)
-                : launch_pdl(combine_kernel<false>, dim3(blocks), dim3(32 * warps_per_block), 0, stream,
-                             y_perm, row_of, topk_w, out, T, k, D, (long long)rows_alloc, status);
+    const cudaError_t err = launch_pdl(
+        is_bf16 ? (parts > 1 ? combine_kernel<true, true> : combine_kernel<true, false>)
+                : (parts > 1 ? combine_kernel<false, true> : combine_kernel<false, false>),
+        dim3(blocks), dim3(32 * warps_per_block), 0, stream, y_perm, row_of, topk_w, out, T, k, D,
+        parts, (long long)rows_alloc, status);
     if (err != cudaSuccess) return err;
     count_launch();
     return cudaSuccess;
