@@ -37,6 +37,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "common.cuh"
 #include "launch.h"
@@ -52,10 +53,7 @@ constexpr int X_ROW = X_BK / 2;       // bytes of a row's K block: the swizzle s
 constexpr int X_W_BYTES = 128 * X_ROW;
 constexpr int X_SF_BLOCK = 512;       // 128 rows x 4 scales
 constexpr int X_SF_BYTES = 6 * X_SF_BLOCK;  // two K halves of the weights' block, then of the tokens' two
-#ifndef MOE_MX_MAXST
-#define MOE_MX_MAXST 6
-#endif
-constexpr int X_MAX_STAGES = MOE_MX_MAXST;
+constexpr int X_MAX_STAGES = 8;
 constexpr int X_GROUP = 4;            // K blocks whose scales are fetched together (32 bytes of a row)
 constexpr int X_GROUP_BYTES = X_GROUP * X_SF_BYTES;
 constexpr int X_SLOTS = 2;            // groups in shared memory
@@ -68,12 +66,8 @@ constexpr int X_TMEM_COLS = 512;
 constexpr int X_SF_COLS = 24;         // of a K block: 2 x 4 of the weights, 2 x 8 of the tokens
 constexpr int X_NBARS = 2 * X_MAX_STAGES + 2 * X_SLOTS + 6;
 constexpr int X_SMEM_MAX = 227 * 1024;
-constexpr int X_CHUNK = 32;           // tokens that an epilogue group turns around at a time
-// GEMM1's turning buffer, per epilogue group: 32 tokens x (64 gates, 64 ups, 4 of padding)
-constexpr int X_TURN_LD = 132;
-constexpr int X_TURN1 = X_EPI_GROUPS * X_CHUNK * X_TURN_LD * 4;
-// GEMM2's: per warp 32 tokens x 32 columns fp16
-constexpr int X_TURN2 = X_EPI_WARPS * 32 * 64;
+constexpr int X_TURN_LD = 132;        // GEMM1's turning buffer: a token's 64 gates, 64 ups, 4 of padding
+constexpr int X_TURN2 = X_EPI_WARPS * 32 * 64;  // GEMM2's: per warp 32 tokens x 32 columns fp16
 constexpr int X_EPI_BAR = 1;          // named barriers of the epilogue: one per group
 
 // What follows from the most tokens of a tile, kBN (a multiple of 16).
@@ -83,6 +77,10 @@ struct MxShape {
     static constexpr int kStage = X_W_BYTES + kTBytes;
     static constexpr int kSfCol = 2 * kBN;                  // scale buffers start behind two accumulators
     static constexpr int kSfBufs = (X_TMEM_COLS - kSfCol) / X_SF_COLS;
+    // tokens that an epilogue group of GEMM1 turns around at a time: 16 where
+    // calls wait for weights and the room is better spent on two more stages
+    static constexpr int kChunk1 = kBN > 144 ? 32 : 16;
+    static constexpr int kTurn1 = X_EPI_GROUPS * kChunk1 * X_TURN_LD * 4;
     static_assert(kBN % 16 == 0 && kBN <= 256 && kTBytes % 1024 == 0 && kSfBufs >= 2, "tile shape");
 };
 
@@ -102,7 +100,7 @@ struct MxParams {
 template <bool kGemm1, int kBN>
 size_t mx_smem_bytes(int stages, int E_local) {
     return 1024 + (size_t)stages * MxShape<kBN>::kStage + X_SLOTS * X_GROUP_BYTES +
-           (kGemm1 ? X_TURN1 : X_TURN2) + (X_NBARS + 1) * sizeof(uint64_t) + 16 +
+           (kGemm1 ? MxShape<kBN>::kTurn1 : X_TURN2) + (X_NBARS + 1) * sizeof(uint64_t) + 16 +
            sizeof(int) * (4 * (size_t)E_local + 1);
 }
 
@@ -348,7 +346,7 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
     uint8_t *ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *sfs = ring + stages * Shape::kStage;  // [X_SLOTS] groups of scales
     uint8_t *turn = sfs + X_SLOTS * X_GROUP_BYTES;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(turn + (kGemm1 ? X_TURN1 : X_TURN2));
+    uint64_t *bars = reinterpret_cast<uint64_t *>(turn + (kGemm1 ? Shape::kTurn1 : X_TURN2));
     uint64_t *full = bars;                       // leader: both CTAs' TMA bytes, scales in TMEM -> MMA
     uint64_t *empty = bars + X_MAX_STAGES;       // MMA -> each CTA's TMA, the leader's scale copies
     uint64_t *tfull = bars + 2 * X_MAX_STAGES;   // [2] MMA -> each CTA's epilogue
@@ -419,6 +417,7 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
         uint32_t ph = 0;
         bool ok = true;
         MxTile c(pair_id, p.nt, total, table);
+        MxTile next = c;  // found while the first K block of a tile is on its way
         for (int tile = pair_id; ok && tile < total;) {
             const int trows = c.n / 2;  // this CTA's token rows: a multiple of 8, below 128
             const int trow = c.row0 + (int)rank * trows;
@@ -455,9 +454,10 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
                 }
                 __syncwarp();
                 if (++s == stages) { s = 0; ph ^= 1u; }
+                if (kb == 0) next.step(dt, dn, p.nt, tile + n_pairs < total, table);
             }
             tile += n_pairs;
-            c.step(dt, dn, p.nt, tile < total, table);
+            c = next;
         }
     } else if (warp == 1) {
         if (leader) {
@@ -468,6 +468,7 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
             int it = 0;
             const uint64_t w_desc0 = sdesc_kmajor_sw128(smem_u32(ring));
             MxTile c(pair_id, p.nt, total, table);
+            MxTile next = c;
             for (int tile = pair_id; ok && tile < total; ++it) {
                 const int acc = it & 1;
                 const uint32_t id0 = idesc_mxf4_f32(X_BM, c.n, 0), id2 = idesc_mxf4_f32(X_BM, c.n, 2);
@@ -498,9 +499,10 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
                     __syncwarp();
                     if (++s == stages) { s = 0; ph ^= 1u; }
                     if (++sb == sf_bufs) sb = 0;
+                    if (kb == 0) next.step(dt, dn, p.nt, tile + n_pairs < total, table);
                 }
                 tile += n_pairs;
-                c.step(dt, dn, p.nt, tile < total, table);
+                c = next;
             }
             // every MMA issued here completes before either CTA frees TMEM
             if (elect_one()) tc_commit_pair(&drain[0], 0x1);
@@ -521,6 +523,7 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
             bool ok = true;
             const uint64_t f_desc0 = sdesc_scales(smem_u32(sfs));
             MxTile c(pair_id, p.nt, total, table);
+            MxTile next = c;
             for (int tile = pair_id; ok && tile < total;) {
                 const bool wide = c.n > 128;
                 for (int kb = 0; kb < p.nk; ++kb) {
@@ -558,9 +561,10 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
                     if (++s == stages) s = 0;
                     if (++sb == sf_bufs) sb = 0;
                     if (last && ++sg == X_SLOTS) { sg = 0; phg ^= 1u; }
+                    if (kb == 0) next.step(dt, dn, p.nt, tile + n_pairs < total, table);
                 }
                 tile += n_pairs;
-                c.step(dt, dn, p.nt, tile < total, table);
+                c = next;
             }
             if (elect_one()) tc_commit_pair(&drain[1], 0x1);
             __syncwarp();
@@ -590,31 +594,34 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
                 if (lane == 0)
                     mbar_arrive_cluster_relaxed(tempty_leader + (uint32_t)(acc * sizeof(uint64_t)));
             };
-            constexpr int step = X_CHUNK * X_EPI_GROUPS;
-            const bool none = X_CHUNK * eg >= c.nvalid ||
+            constexpr int kChunk = kGemm1 ? Shape::kChunk1 : 32;
+            constexpr int step = kChunk * X_EPI_GROUPS;
+            const bool none = kChunk * eg >= c.nvalid ||
                               (!kGemm1 && c.nt * X_BM + (int)rank * 128 + q * 32 >= p.n_out);
             if (none) release();
             if (kGemm1) {
                 // lanes 0-63 are the gates of units `unit0`.., 64-127 their ups
                 const int unit0 = c.nt * X_UNITS + (int)rank * 64;
-                const int tok = (q & 1) * 16 + (lane >> 1);    // of the chunk in the buffer
-                const int unit = (q >> 1) * 32 + (lane & 1) * 16;
-                float *buf = reinterpret_cast<float *>(turn) + eg * (X_CHUNK * X_TURN_LD);
-                for (int t0 = X_CHUNK * eg; t0 < c.nvalid; t0 += step) {
-                    uint32_t d[32];
-                    tmem_ld_32x32b_x32(tb + t0, d);
+                constexpr int kLanes = 64 / kChunk;            // lanes that share a block of 32 units
+                constexpr int kUnits = 32 / kLanes;            // units of a lane
+                const int tok = (q & 1) * (kChunk / 2) + lane / kLanes;  // of the chunk in the buffer
+                const int unit = (q >> 1) * 32 + lane % kLanes * kUnits;
+                float *buf = reinterpret_cast<float *>(turn) + eg * (kChunk * X_TURN_LD);
+                for (int t0 = kChunk * eg; t0 < c.nvalid; t0 += step) {
+                    uint32_t d[kChunk];
+                    tmem_ld_32x32b(tb + t0, d);
                     tc_wait_ld();
                     if (t0 + step >= c.nvalid) release();
                     bar_sync(X_EPI_BAR + eg, 128);  // the group has read its last chunk
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
+                    for (int j = 0; j < kChunk; ++j)
                         buf[j * X_TURN_LD + q * 32 + lane] = __uint_as_float(d[j]);
                     bar_sync(X_EPI_BAR + eg, 128);
                     const float *src = buf + tok * X_TURN_LD + unit;
-                    float h[16];
+                    float h[kUnits];
                     uint32_t top = 0;
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) {
+                    for (int v = 0; v < kUnits / 4; ++v) {
                         const float4 g = *reinterpret_cast<const float4 *>(src + 4 * v);
                         const float4 u = *reinterpret_cast<const float4 *>(src + 64 + 4 * v);
                         h[4 * v] = mx_silu(g.x) * u.x;
@@ -623,36 +630,66 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
                         h[4 * v + 3] = mx_silu(g.w) * u.w;
                     }
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) top = max(top, abs_bits(h[i]));
-                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));  // the block's other half
+                    for (int i = 0; i < kUnits; ++i) top = max(top, abs_bits(h[i]));
+#pragma unroll
+                    for (int o = 1; o < kLanes; o *= 2)  // the block's other units
+                        top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
                     const uint32_t sb = mx_scale_byte(top);
                     const float inv = mx_inv_scale(sb);
                     if (t0 + tok < c.nvalid && unit0 + unit < p.n_out) {
                         const size_t row = (size_t)(c.row0 + t0 + tok);
-                        *reinterpret_cast<uint2 *>(p.hq + row * (size_t)(p.n_out / 2) +
-                                                   (unit0 + unit) / 2) =
-                            make_uint2(mx_codes8(*reinterpret_cast<const float(*)[8]>(h), inv),
-                                       mx_codes8(*reinterpret_cast<const float(*)[8]>(h + 8), inv));
-                        if ((lane & 1) == 0)
+                        uint32_t *to = reinterpret_cast<uint32_t *>(
+                            p.hq + row * (size_t)(p.n_out / 2) + (unit0 + unit) / 2);
+                        const uint32_t c0 = mx_codes8(*reinterpret_cast<const float(*)[8]>(h), inv);
+                        if constexpr (kUnits == 16)
+                            *reinterpret_cast<uint2 *>(to) = make_uint2(
+                                c0, mx_codes8(*reinterpret_cast<const float(*)[8]>(h + 8), inv));
+                        else
+                            *to = c0;
+                        if (lane % kLanes == 0)
                             p.hsf[row * (size_t)(p.n_out / 32) + (unit0 + unit) / 32] = (uint8_t)sb;
                     }
                 }
             } else {
-                // lane = column of y; 32 columns of the warp, 32 tokens at a time
+                // The warp's 32 columns of y, 32 tokens at a time: loaded as the
+                // fragments of 8 x 8 matrices (a column of y by tokens), rounded to
+                // fp16 and stored transposed, a token's 8 columns in 16 bytes; 16-byte
+                // unit u of token t is kept at u ^ (t / 2 & 3), free of bank conflicts
+                // both ways.  (One STS per value instead: 583 against 250 cycles a chunk.)
                 const int col0 = c.nt * X_BM + (int)rank * 128 + q * 32;
-                __half *buf = reinterpret_cast<__half *>(turn + ew * (32 * 64));
+                uint8_t *buf = turn + ew * (32 * 64);
+                const int mr = lane & 7, mf = lane >> 3;   // the address this lane gives: token, unit
+                const uint32_t st = smem_u32(buf) + mr * 64 + ((mf ^ (mr >> 1 & 3)) << 4);
                 if (!none) {  // (D is a multiple of 32: a warp's columns are all there or none is)
-                    for (int t0 = X_CHUNK * eg; t0 < c.nvalid; t0 += step) {
-                        uint32_t d[32];
-                        tmem_ld_32x32b_x32(tb + t0, d);
+                    for (int t0 = kChunk * eg; t0 < c.nvalid; t0 += step) {
+                        uint32_t d0[16], d1[16];
+                        tmem_ld_16x256b_x4(tb + t0, d0);
+                        tmem_ld_16x256b_x4(tb + (16u << 16) + t0, d1);
                         tc_wait_ld();
                         if (t0 + step >= c.nvalid) release();
+                        // only stored values count: columns past the tile's tokens hold anything
+                        if (t0 + kChunk <= c.nvalid) {
+                            float top = 0.f;
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                top = fmaxf(top, fmaxf(fabsf(__uint_as_float(d0[i])), fabsf(__uint_as_float(d1[i]))));
+                            over |= top >= kHalfOverflow;
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const bool held = t0 + 8 * (i >> 2) + 2 * (lane & 3) + (i & 1) < c.nvalid;
+                                over |= held && (fabsf(__uint_as_float(d0[i])) >= kHalfOverflow ||
+                                                 fabsf(__uint_as_float(d1[i])) >= kHalfOverflow);
+                            }
+                        }
                         __syncwarp();  // the last chunk has been read
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const float v = __uint_as_float(d[j]);
-                            over |= t0 + j < c.nvalid && fabsf(v) >= kHalfOverflow;
-                            buf[j * 32 + lane] = __float2half_rn(v);
+                        for (int i = 0; i < 4; ++i) {
+                            auto half2 = [](const uint32_t (&d)[16], int j) {
+                                return pack_half2(__uint_as_float(d[j]), __uint_as_float(d[j + 1]));
+                            };
+                            stmatrix_x4_trans(st + i * (8 * 64), half2(d0, 4 * i), half2(d0, 4 * i + 2),
+                                              half2(d1, 4 * i), half2(d1, 4 * i + 2));
                         }
                         __syncwarp();
 #pragma unroll
@@ -661,7 +698,8 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
                             if (t0 + tok < c.nvalid)
                                 *reinterpret_cast<uint4 *>(
                                     p.y + (size_t)(c.row0 + t0 + tok) * p.n_out + col0 + (lane & 3) * 8) =
-                                    *reinterpret_cast<const uint4 *>(buf + tok * 32 + (lane & 3) * 8);
+                                    *reinterpret_cast<const uint4 *>(
+                                        buf + tok * 64 + (((lane & 3) ^ (tok >> 1 & 3)) << 4));
                         }
                     }
                 }
@@ -741,7 +779,7 @@ bool token_maps(MxMaps *m, const uint8_t *codes, int K, int64_t rows) {
 
 template <bool kGemm1, int kBN>
 cudaError_t launch_mx(const MxMaps &m, MxParams p, long long token_tiles, cudaStream_t stream) {
-    static_assert(1024 + 4 * MxShape<kBN>::kStage + X_SLOTS * X_GROUP_BYTES + X_TURN1 +
+    static_assert(1024 + 4 * MxShape<kBN>::kStage + X_SLOTS * X_GROUP_BYTES + MxShape<kBN>::kTurn1 +
                           (X_NBARS + 1) * 8 + 16 + 4 * (4 * 1024 + 1) <= X_SMEM_MAX,
                   "four stages fit beside the table of 1024 experts");
     int stages = X_MAX_STAGES;  // as many as fit beside the table of the experts
@@ -771,13 +809,23 @@ cudaError_t launch_mx(const MxMaps &m, MxParams p, long long token_tiles, cudaSt
     return e;
 }
 
+template <int kBN>
+cudaError_t launch_mx_both(const MxMaps &m1, const MxMaps &m2, const MxParams &p1, const MxParams &p2,
+                           cudaStream_t stream) {
+    // token tiles: at most one partial tile per expert beside the whole ones
+    const long long tt = std::min<long long>(p1.rows_alloc, p1.rows_alloc / kBN + p1.E_local);
+    const cudaError_t e = launch_mx<true, kBN>(m1, p1, tt, stream);
+    return e == cudaSuccess ? launch_mx<false, kBN>(m2, p2, tt, stream) : e;
+}
+
 }  // namespace
 
 cudaError_t launch_grouped_swiglu_mxfp4(const uint8_t *x_perm_q, const uint8_t *x_scale,
                                         const int *seg_offsets, const int *tokens_per_expert,
                                         const MxWeights &w, uint8_t *h_q, uint8_t *h_scale,
                                         void *y_perm, int D, int H_local, int e_first, int E_local,
-                                        int64_t rows_alloc, int *status, cudaStream_t stream) {
+                                        int64_t rows_alloc, double avg_rows, int *status,
+                                        cudaStream_t stream) {
     if (E_local == 0 || rows_alloc == 0) return cudaSuccess;
     if (D % 32 || H_local % 32) return cudaErrorInvalidValue;
     MxMaps m1, m2;
@@ -788,12 +836,6 @@ cudaError_t launch_grouped_swiglu_mxfp4(const uint8_t *x_perm_q, const uint8_t *
         return cudaErrorInvalidValue;
     m2.w1 = m2.w0;
 
-#ifndef MOE_MX_BN
-#define MOE_MX_BN 208
-#endif
-    constexpr int kBN = MOE_MX_BN;
-    // token tiles: at most one partial tile per expert beside the whole ones
-    const long long tt = std::min<long long>(rows_alloc, rows_alloc / kBN + E_local);
     MxParams p{};
     p.E_local = E_local;
     p.e_first = e_first;
@@ -812,8 +854,6 @@ cudaError_t launch_grouped_swiglu_mxfp4(const uint8_t *x_perm_q, const uint8_t *
     p1.w_sf1 = w.w3_scale;
     p1.hq = h_q;
     p1.hsf = h_scale;
-    const cudaError_t e = launch_mx<true, kBN>(m1, p1, tt, stream);
-    if (e != cudaSuccess) return e;
 
     MxParams p2 = p;
     p2.K = H_local;
@@ -823,7 +863,20 @@ cudaError_t launch_grouped_swiglu_mxfp4(const uint8_t *x_perm_q, const uint8_t *
     p2.t_sf = h_scale;
     p2.w_sf0 = p2.w_sf1 = w.w2_scale;
     p2.y = static_cast<__half *>(y_perm);
-    return launch_mx<false, kBN>(m2, p2, tt, stream);
+
+    // Tokens per tile: 208 is the most that two accumulators leave room for; a
+    // smaller tile needs less of the ring per stage and so has more stages, which
+    // is worth it where it costs no further tile: the smallest of 32, 144 and 208
+    // that takes an average expert's rows (and a standard deviation more) in as
+    // few tiles as 208.  Grouped call on GB300, by tile: a decode batch (4 rows
+    // per expert) 850 us with 32, 886 with 208; 8192 tokens over 256 experts (256
+    // rows) 1260 us with 144, 1356 with 208; fine-grained (384 rows) 138 us with
+    // 144, 123 with 208.
+    const double rows = avg_rows + sqrt((double)avg_rows);
+    auto tiles = [&](int bn) { return std::max(1LL, (long long)std::ceil(rows / bn)); };
+    if (tiles(32) == tiles(208)) return launch_mx_both<32>(m1, m2, p1, p2, stream);
+    if (tiles(144) == tiles(208)) return launch_mx_both<144>(m1, m2, p1, p2, stream);
+    return launch_mx_both<208>(m1, m2, p1, p2, stream);
 }
 
 }  // namespace moe

@@ -110,7 +110,8 @@ cudaError_t launch_dispatch_rows_mxfp4(const void *src, int64_t rows, int cols, 
 
 // MXFP4 experts: both GEMMs on e2m1 operands with block scales
 // (kind::mxf4.block_scale), h quantised to MXFP4 in GEMM1's epilogue.
-// D and H_local multiples of 32.
+// D and H_local multiples of 32; avg_rows: rows an expert has on average (picks
+// the tile, not the result).
 struct MxWeights {
     const uint8_t *w1, *w1_scale, *w3, *w3_scale, *w2, *w2_scale;
 };
@@ -118,7 +119,8 @@ cudaError_t launch_grouped_swiglu_mxfp4(const uint8_t *x_perm_q, const uint8_t *
                                         const int *seg_offsets, const int *tokens_per_expert,
                                         const MxWeights &w, uint8_t *h_q, uint8_t *h_scale,
                                         void *y_perm, int D, int H_local, int e_first, int E_local,
-                                        int64_t rows_alloc, int *status, cudaStream_t stream);
+                                        int64_t rows_alloc, double avg_rows, int *status,
+                                        cudaStream_t stream);
 
 // out[t] = sum_j w[t, j] y_perm[row_of[t, j]], fp32 in slot order, rounded
 // once; y_perm fp16 with a bf16 out (is_bf16), fp32 with an fp32 out.

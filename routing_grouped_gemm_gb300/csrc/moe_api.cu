@@ -346,7 +346,7 @@ moe_status do_grouped_mxfp4(const moe_config *c, const uint8_t *x_perm_q, const 
                             cudaStream_t s) {
     const cudaError_t e = moe::launch_grouped_swiglu_mxfp4(
         x_perm_q, x_scale, seg, tpe, mw, h_q, h_scale, y_perm, c->D, c->H_local, c->e_first,
-        c->E_local, rows_alloc_of(c), &w.status->flags, s);
+        c->E_local, rows_alloc_of(c), (double)c->T * c->k / c->E, &w.status->flags, s);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_grouped_swiglu_mxfp4");
 }
 
