@@ -266,6 +266,14 @@ def _expect(t, shape, dtype, name):
         raise ValueError(f"{name} must be a CUDA tensor")
 
 
+def _arg(t, shape, dtype, name) -> int:
+    """The address of a tensor that is what _expect and _ptr ask for, in one step."""
+    if t is not None and t.shape == shape and t.dtype is dtype and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    _expect(t, shape, dtype, name)
+    return _ptr(t)
+
+
 # --------------------------------------------------------------------------
 # the ABI calls (same names as include/moe.h)
 # --------------------------------------------------------------------------
@@ -359,15 +367,13 @@ def moe_grouped_swiglu(cfg: Config, x_perm, seg_offsets, tokens_per_expert, w1, 
 
 
 def moe_unpermute_combine(cfg: Config, y_perm, row_of, topk_w, out, ws, stream=None):
-    ra = rows_alloc(cfg)
-    dt = cfg.torch_dtype
-    _expect(y_perm, (ra, cfg.D), cfg.y_dtype, "y_perm")
-    _expect(row_of, (cfg.T, cfg.k), torch.int32, "row_of")
-    _expect(topk_w, (cfg.T, cfg.k), torch.float32, "topk_w")
-    _expect(out, (cfg.T, cfg.D), dt, "out")
-    _check(_lib.moe_unpermute_combine(cfg.ref()[0], _ptr(y_perm), _ptr(row_of), _ptr(topk_w),
-                                      _ptr(out), _ptr(ws), ws.numel(), _stream(stream)),
-           "moe_unpermute_combine")
+    c, ra = cfg.ref()
+    _check(_lib.moe_unpermute_combine(
+        c, _arg(y_perm, (ra, cfg.D), cfg.y_dtype, "y_perm"),
+        _arg(row_of, (cfg.T, cfg.k), torch.int32, "row_of"),
+        _arg(topk_w, (cfg.T, cfg.k), torch.float32, "topk_w"),
+        _arg(out, (cfg.T, cfg.D), cfg.torch_dtype, "out"), _ptr(ws), ws.numel(), _stream(stream)),
+        "moe_unpermute_combine")
 
 
 def moe_layer_forward(cfg: Config, x, wg, bias, w1, w3, w2, out, ws, stream=None):
@@ -598,38 +604,37 @@ def moe_layer_forward_fp8(cfg: Config, x, wg, bias, w1_q, w1_scale, w3_q, w3_sca
 
 
 def _mx_tensor(t, name):
+    """(rows, cols, dtype) of a tensor taken as rows of whole blocks."""
     if t.dtype not in (torch.bfloat16, torch.float32) or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous bf16 or fp32 CUDA tensor")
     if t.dim() == 0 or t.shape[-1] % 32:
         raise ValueError(f"{name}: rows of a multiple of 32 values")
     cols = t.shape[-1]
-    return (t.numel() // cols if cols else 0), cols
+    return (t.numel() // cols if cols else 0), cols, MOE_BF16 if t.dtype == torch.bfloat16 else MOE_F32
 
 
 def moe_quantize_rows_mxfp4(src, dst, scale, stream=None):
     """MXFP4 codes and e8m0 scales of a bf16 or fp32 tensor viewed as [rows, cols]:
     dst [..., cols / 2] and scale [..., cols / 32], both uint8."""
-    rows, cols = _mx_tensor(src, "src")
-    _expect(dst, (*src.shape[:-1], cols // 2), torch.uint8, "dst")
-    _expect(scale, (*src.shape[:-1], cols // 32), torch.uint8, "scale")
+    rows, cols, dt = _mx_tensor(src, "src")
+    q = _arg(dst, (*src.shape[:-1], cols // 2), torch.uint8, "dst")
+    sc = _arg(scale, (*src.shape[:-1], cols // 32), torch.uint8, "scale")
     if rows == 0:
         return
-    _check(_lib.moe_quantize_rows_mxfp4(_ptr(src), MOE_BF16 if src.dtype == torch.bfloat16 else MOE_F32,
-                                        rows, cols, _ptr(dst), _ptr(scale), _stream(stream)),
+    _check(_lib.moe_quantize_rows_mxfp4(src.data_ptr(), dt, rows, cols, q, sc, _stream(stream)),
            "moe_quantize_rows_mxfp4")
 
 
 def moe_dequantize_rows_mxfp4(codes, scale, dst, stream=None):
     """The values of MXFP4 codes [..., cols / 2] with scales [..., cols / 32] into a
     bf16 or fp32 dst [..., cols]."""
-    rows, cols = _mx_tensor(dst, "dst")
-    _expect(codes, (*dst.shape[:-1], cols // 2), torch.uint8, "codes")
-    _expect(scale, (*dst.shape[:-1], cols // 32), torch.uint8, "scale")
+    rows, cols, dt = _mx_tensor(dst, "dst")
+    q = _arg(codes, (*dst.shape[:-1], cols // 2), torch.uint8, "codes")
+    sc = _arg(scale, (*dst.shape[:-1], cols // 32), torch.uint8, "scale")
     if rows == 0:
         return
-    _check(_lib.moe_dequantize_rows_mxfp4(_ptr(codes), _ptr(scale), rows, cols, _ptr(dst),
-                                          MOE_BF16 if dst.dtype == torch.bfloat16 else MOE_F32,
-                                          _stream(stream)), "moe_dequantize_rows_mxfp4")
+    _check(_lib.moe_dequantize_rows_mxfp4(q, sc, rows, cols, dst.data_ptr(), dt, _stream(stream)),
+           "moe_dequantize_rows_mxfp4")
 
 
 def quantize_weights_mxfp4(w, stream=None):
@@ -645,94 +650,78 @@ def quantize_weights_mxfp4(w, stream=None):
 def moe_permute_mxfp4(cfg: Config, x, topk_idx, tokens_per_expert, seg_offsets, row_of,
                       token_of_row, x_perm_q, x_scale, ws, stream=None):
     """moe_permute with the rows quantised: x_perm_q [rows, D / 2], x_scale [rows, D / 32]."""
-    ra = rows_alloc(cfg)
-    _expect(x, (cfg.T, cfg.D), torch.bfloat16, "x")
-    _expect(topk_idx, (cfg.T, cfg.k), torch.int32, "topk_idx")
-    _expect(tokens_per_expert, (cfg.E,), torch.int32, "tokens_per_expert")
-    _expect(seg_offsets, (cfg.e_local + 1,), torch.int32, "seg_offsets")
-    _expect(row_of, (cfg.T, cfg.k), torch.int32, "row_of")
-    _expect(token_of_row, (ra,), torch.int32, "token_of_row")
-    _expect(x_perm_q, (ra, cfg.D // 2), torch.uint8, "x_perm_q")
-    _expect(x_scale, (ra, cfg.D // 32), torch.uint8, "x_scale")
-    _check(_lib.moe_permute_mxfp4(cfg.ref()[0], _ptr(x), _ptr(topk_idx), _ptr(tokens_per_expert),
-                                  _ptr(seg_offsets), _ptr(row_of), _ptr(token_of_row),
-                                  _ptr(x_perm_q), _ptr(x_scale), _ptr(ws), ws.numel(),
-                                  _stream(stream)), "moe_permute_mxfp4")
+    c, ra = cfg.ref()
+    T, D, k, i32, u8 = cfg.T, cfg.D, cfg.k, torch.int32, torch.uint8
+    _check(_lib.moe_permute_mxfp4(
+        c, _arg(x, (T, D), torch.bfloat16, "x"), _arg(topk_idx, (T, k), i32, "topk_idx"),
+        _arg(tokens_per_expert, (cfg.E,), i32, "tokens_per_expert"),
+        _arg(seg_offsets, (cfg.e_local + 1,), i32, "seg_offsets"),
+        _arg(row_of, (T, k), i32, "row_of"), _arg(token_of_row, (ra,), i32, "token_of_row"),
+        _arg(x_perm_q, (ra, D // 2), u8, "x_perm_q"), _arg(x_scale, (ra, D // 32), u8, "x_scale"),
+        _ptr(ws), ws.numel(), _stream(stream)), "moe_permute_mxfp4")
 
 
-def _expect_mx_weights(cfg: Config, w1_q, w1_scale, w3_q, w3_scale, w2_q, w2_scale):
-    el, D, H = cfg.e_local, cfg.D, cfg.H_local
-    for t, sf, n, m, name in ((w1_q, w1_scale, H, D, "w1"), (w3_q, w3_scale, H, D, "w3"),
-                              (w2_q, w2_scale, D, H, "w2")):
-        _expect(t, (el, n, m // 2), torch.uint8, name + "_q")
-        _expect(sf, (el, n, m // 32), torch.uint8, name + "_scale")
+def _mx_weights(cfg: Config, w1_q, w1_scale, w3_q, w3_scale, w2_q, w2_scale):
+    el, D, H, u8 = cfg.e_local, cfg.D, cfg.H_local, torch.uint8
+    return (_arg(w1_q, (el, H, D // 2), u8, "w1_q"), _arg(w1_scale, (el, H, D // 32), u8, "w1_scale"),
+            _arg(w3_q, (el, H, D // 2), u8, "w3_q"), _arg(w3_scale, (el, H, D // 32), u8, "w3_scale"),
+            _arg(w2_q, (el, D, H // 2), u8, "w2_q"), _arg(w2_scale, (el, D, H // 32), u8, "w2_scale"))
 
 
 def moe_grouped_swiglu_mxfp4(cfg: Config, x_perm_q, x_scale, seg_offsets, tokens_per_expert, w1_q,
                              w1_scale, w3_q, w3_scale, w2_q, w2_scale, h_q, h_scale, y_perm, ws,
                              stream=None):
-    ra = rows_alloc(cfg)
-    _expect(x_perm_q, (ra, cfg.D // 2), torch.uint8, "x_perm_q")
-    _expect(x_scale, (ra, cfg.D // 32), torch.uint8, "x_scale")
-    _expect(seg_offsets, (cfg.e_local + 1,), torch.int32, "seg_offsets")
-    _expect(tokens_per_expert, (cfg.E,), torch.int32, "tokens_per_expert")
-    _expect_mx_weights(cfg, w1_q, w1_scale, w3_q, w3_scale, w2_q, w2_scale)
-    _expect(h_q, (ra, cfg.H_local // 2), torch.uint8, "h_q")
-    _expect(h_scale, (ra, cfg.H_local // 32), torch.uint8, "h_scale")
-    _expect(y_perm, (ra, cfg.D), torch.float16, "y_perm")
-    _check(_lib.moe_grouped_swiglu_mxfp4(cfg.ref()[0], _ptr(x_perm_q), _ptr(x_scale),
-                                         _ptr(seg_offsets), _ptr(tokens_per_expert), _ptr(w1_q),
-                                         _ptr(w1_scale), _ptr(w3_q), _ptr(w3_scale), _ptr(w2_q),
-                                         _ptr(w2_scale), _ptr(h_q), _ptr(h_scale), _ptr(y_perm),
-                                         _ptr(ws), ws.numel(), _stream(stream)),
-           "moe_grouped_swiglu_mxfp4")
+    """moe_grouped_swiglu on MXFP4 operands; h_q [rows, H / 2] and h_scale [rows, H / 32]
+    receive SiLU(gate) * up, quantised."""
+    c, ra = cfg.ref()
+    D, H, i32, u8 = cfg.D, cfg.H_local, torch.int32, torch.uint8
+    _check(_lib.moe_grouped_swiglu_mxfp4(
+        c, _arg(x_perm_q, (ra, D // 2), u8, "x_perm_q"), _arg(x_scale, (ra, D // 32), u8, "x_scale"),
+        _arg(seg_offsets, (cfg.e_local + 1,), i32, "seg_offsets"),
+        _arg(tokens_per_expert, (cfg.E,), i32, "tokens_per_expert"),
+        *_mx_weights(cfg, w1_q, w1_scale, w3_q, w3_scale, w2_q, w2_scale),
+        _arg(h_q, (ra, H // 2), u8, "h_q"), _arg(h_scale, (ra, H // 32), u8, "h_scale"),
+        _arg(y_perm, (ra, D), torch.float16, "y_perm"), _ptr(ws), ws.numel(), _stream(stream)),
+        "moe_grouped_swiglu_mxfp4")
 
 
 def moe_layer_forward_mxfp4(cfg: Config, x, wg, bias, w1_q, w1_scale, w3_q, w3_scale, w2_q,
                             w2_scale, out, ws, stream=None):
     """moe_layer_forward with MXFP4 expert weights (see quantize_weights_mxfp4)."""
-    _expect(x, (cfg.T, cfg.D), torch.bfloat16, "x")
-    _expect(wg, (cfg.E, cfg.D), torch.bfloat16, "wg")
-    if bias is not None:
-        _expect(bias, (cfg.E,), torch.float32, "bias")
-    _expect_mx_weights(cfg, w1_q, w1_scale, w3_q, w3_scale, w2_q, w2_scale)
-    _expect(out, (cfg.T, cfg.D), torch.bfloat16, "out")
-    _check(_lib.moe_layer_forward_mxfp4(cfg.ref()[0], _ptr(x), _ptr(wg), _ptr(bias), _ptr(w1_q),
-                                        _ptr(w1_scale), _ptr(w3_q), _ptr(w3_scale), _ptr(w2_q),
-                                        _ptr(w2_scale), _ptr(out), _ptr(ws), ws.numel(),
-                                        _stream(stream)), "moe_layer_forward_mxfp4")
+    bf = torch.bfloat16
+    _check(_lib.moe_layer_forward_mxfp4(
+        cfg.ref()[0], _arg(x, (cfg.T, cfg.D), bf, "x"), _arg(wg, (cfg.E, cfg.D), bf, "wg"),
+        0 if bias is None else _arg(bias, (cfg.E,), torch.float32, "bias"),
+        *_mx_weights(cfg, w1_q, w1_scale, w3_q, w3_scale, w2_q, w2_scale),
+        _arg(out, (cfg.T, cfg.D), bf, "out"), _ptr(ws), ws.numel(), _stream(stream)),
+        "moe_layer_forward_mxfp4")
 
 
 def moe_unpermute_combine_backward(cfg: Config, dout, y_perm, row_of, topk_w, dy_perm, dtopk_w, ws,
                                    stream=None):
     """Gradients of moe_unpermute_combine: dy_perm [rows, D] (rows that hold no token
     are not written) and dtopk_w [T, k]."""
-    ra = rows_alloc(cfg)
-    _expect(dout, (cfg.T, cfg.D), cfg.torch_dtype, "dout")
-    _expect(y_perm, (ra, cfg.D), cfg.y_dtype, "y_perm")
-    _expect(row_of, (cfg.T, cfg.k), torch.int32, "row_of")
-    _expect(topk_w, (cfg.T, cfg.k), torch.float32, "topk_w")
-    _expect(dy_perm, (ra, cfg.D), cfg.torch_dtype, "dy_perm")
-    _expect(dtopk_w, (cfg.T, cfg.k), torch.float32, "dtopk_w")
-    _check(_lib.moe_unpermute_combine_backward(cfg.ref()[0], _ptr(dout), _ptr(y_perm),
-                                               _ptr(row_of), _ptr(topk_w), _ptr(dy_perm),
-                                               _ptr(dtopk_w), _ptr(ws), ws.numel(),
-                                               _stream(stream)), "moe_unpermute_combine_backward")
+    c, ra = cfg.ref()
+    T, D, k, dt = cfg.T, cfg.D, cfg.k, cfg.torch_dtype
+    _check(_lib.moe_unpermute_combine_backward(
+        c, _arg(dout, (T, D), dt, "dout"), _arg(y_perm, (ra, D), cfg.y_dtype, "y_perm"),
+        _arg(row_of, (T, k), torch.int32, "row_of"), _arg(topk_w, (T, k), torch.float32, "topk_w"),
+        _arg(dy_perm, (ra, D), dt, "dy_perm"), _arg(dtopk_w, (T, k), torch.float32, "dtopk_w"),
+        _ptr(ws), ws.numel(), _stream(stream)), "moe_unpermute_combine_backward")
 
 
 def moe_permute_backward(cfg: Config, dx_perm, row_of, dx, ws, stream=None):
     """Gradient of moe_permute: dx [T, D] from dx_perm [rows, D] (fp32, or bf16 in a
     bf16 config)."""
-    ra = rows_alloc(cfg)
-    if dx_perm.dtype not in (torch.float32, cfg.torch_dtype):
-        raise ValueError(f"dx_perm: expected float32 or {cfg.torch_dtype}, got {dx_perm.dtype}")
-    _expect(dx_perm, (ra, cfg.D), dx_perm.dtype, "dx_perm")
-    _expect(row_of, (cfg.T, cfg.k), torch.int32, "row_of")
-    _expect(dx, (cfg.T, cfg.D), cfg.torch_dtype, "dx")
-    _check(_lib.moe_permute_backward(cfg.ref()[0], _ptr(dx_perm),
-                                     MOE_BF16 if dx_perm.dtype == torch.bfloat16 else MOE_F32,
-                                     _ptr(row_of), _ptr(dx), _ptr(ws), ws.numel(),
-                                     _stream(stream)), "moe_permute_backward")
+    c, ra = cfg.ref()
+    dt = cfg.torch_dtype
+    if dx_perm.dtype not in (torch.float32, dt):
+        raise ValueError(f"dx_perm: expected float32 or {dt}, got {dx_perm.dtype}")
+    _check(_lib.moe_permute_backward(
+        c, _arg(dx_perm, (ra, cfg.D), dx_perm.dtype, "dx_perm"),
+        MOE_BF16 if dx_perm.dtype == torch.bfloat16 else MOE_F32,
+        _arg(row_of, (cfg.T, cfg.k), torch.int32, "row_of"), _arg(dx, (cfg.T, cfg.D), dt, "dx"),
+        _ptr(ws), ws.numel(), _stream(stream)), "moe_permute_backward")
 
 
 def moe_grouped_swiglu_gather(cfg: Config, x, token_of_row, seg_offsets, tokens_per_expert, w1,

@@ -399,13 +399,14 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
         prefetch_tmap(&tmW0);
         if (kGemm1) prefetch_tmap(&tmW1);
     }
-    griddep_wait();  // every input of this kernel is complete
-    if (warp == 0) build_mx_table<kBN>(lane, p, table, blockIdx.x == 0 ? p.status : nullptr);
     tc_fence_before();
     __syncthreads();
     cluster_sync();  // the peer's barriers exist before anything arrives on them
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
+    griddep_wait();  // every input of this kernel is complete
+    if (warp == 0) build_mx_table<kBN>(lane, p, table, blockIdx.x == 0 ? p.status : nullptr);
+    __syncthreads();
     const int total = table.first[p.E_local] * p.nt;
     const uint32_t full_leader = mapa_shared(smem_u32(&full[0]), 0);
     const int dt = n_pairs / p.nt, dn = n_pairs - dt * p.nt;  // a step of n_pairs tiles
@@ -417,7 +418,6 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
         uint32_t ph = 0;
         bool ok = true;
         MxTile c(pair_id, p.nt, total, table);
-        MxTile next = c;  // found while the first K block of a tile is on its way
         for (int tile = pair_id; ok && tile < total;) {
             const int trows = c.n / 2;  // this CTA's token rows: a multiple of 8, below 128
             const int trow = c.row0 + (int)rank * trows;
@@ -454,10 +454,9 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
                 }
                 __syncwarp();
                 if (++s == stages) { s = 0; ph ^= 1u; }
-                if (kb == 0) next.step(dt, dn, p.nt, tile + n_pairs < total, table);
             }
             tile += n_pairs;
-            c = next;
+            c.step(dt, dn, p.nt, tile < total, table);
         }
     } else if (warp == 1) {
         if (leader) {
@@ -468,7 +467,6 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
             int it = 0;
             const uint64_t w_desc0 = sdesc_kmajor_sw128(smem_u32(ring));
             MxTile c(pair_id, p.nt, total, table);
-            MxTile next = c;
             for (int tile = pair_id; ok && tile < total; ++it) {
                 const int acc = it & 1;
                 const uint32_t id0 = idesc_mxf4_f32(X_BM, c.n, 0), id2 = idesc_mxf4_f32(X_BM, c.n, 2);
@@ -499,10 +497,9 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
                     __syncwarp();
                     if (++s == stages) { s = 0; ph ^= 1u; }
                     if (++sb == sf_bufs) sb = 0;
-                    if (kb == 0) next.step(dt, dn, p.nt, tile + n_pairs < total, table);
                 }
                 tile += n_pairs;
-                c = next;
+                c.step(dt, dn, p.nt, tile < total, table);
             }
             // every MMA issued here completes before either CTA frees TMEM
             if (elect_one()) tc_commit_pair(&drain[0], 0x1);
@@ -523,7 +520,6 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
             bool ok = true;
             const uint64_t f_desc0 = sdesc_scales(smem_u32(sfs));
             MxTile c(pair_id, p.nt, total, table);
-            MxTile next = c;
             for (int tile = pair_id; ok && tile < total;) {
                 const bool wide = c.n > 128;
                 for (int kb = 0; kb < p.nk; ++kb) {
@@ -561,10 +557,9 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
                     if (++s == stages) s = 0;
                     if (++sb == sf_bufs) sb = 0;
                     if (last && ++sg == X_SLOTS) { sg = 0; phg ^= 1u; }
-                    if (kb == 0) next.step(dt, dn, p.nt, tile + n_pairs < total, table);
                 }
                 tile += n_pairs;
-                c = next;
+                c.step(dt, dn, p.nt, tile < total, table);
             }
             if (elect_one()) tc_commit_pair(&drain[1], 0x1);
             __syncwarp();
@@ -770,11 +765,15 @@ struct MxMaps {
     CUtensorMap t8, t16, t32, t64, w0, w1;
 };
 
-bool token_maps(MxMaps *m, const uint8_t *codes, int K, int64_t rows) {
-    return make_tmap_tile(&m->t8, codes, 1, K / 2, rows, 0, X_ROW, 8, 128) &&
-           make_tmap_tile(&m->t16, codes, 1, K / 2, rows, 0, X_ROW, 16, 128) &&
-           make_tmap_tile(&m->t32, codes, 1, K / 2, rows, 0, X_ROW, 32, 128) &&
-           make_tmap_tile(&m->t64, codes, 1, K / 2, rows, 0, X_ROW, 64, 128);
+// Token boxes of 8, 16, 32 and 64 rows; a tile of at most 32 tokens loads 8 or
+// 16 per CTA, and the others only have to be valid.
+bool token_maps(MxMaps *m, const uint8_t *codes, int K, int64_t rows, int bn) {
+    if (!make_tmap_tile(&m->t8, codes, 1, K / 2, rows, 0, X_ROW, 8, 128) ||
+        !make_tmap_tile(&m->t16, codes, 1, K / 2, rows, 0, X_ROW, 16, 128))
+        return false;
+    m->t32 = m->t64 = m->t16;
+    return bn <= 32 || (make_tmap_tile(&m->t32, codes, 1, K / 2, rows, 0, X_ROW, 32, 128) &&
+                        make_tmap_tile(&m->t64, codes, 1, K / 2, rows, 0, X_ROW, 64, 128));
 }
 
 template <bool kGemm1, int kBN>
@@ -828,14 +827,6 @@ cudaError_t launch_grouped_swiglu_mxfp4(const uint8_t *x_perm_q, const uint8_t *
                                         cudaStream_t stream) {
     if (E_local == 0 || rows_alloc == 0) return cudaSuccess;
     if (D % 32 || H_local % 32) return cudaErrorInvalidValue;
-    MxMaps m1, m2;
-    if (!token_maps(&m1, x_perm_q, D, rows_alloc) || !token_maps(&m2, h_q, H_local, rows_alloc) ||
-        !make_tmap_tile(&m1.w0, w.w1, 1, D / 2, H_local, E_local, X_ROW, 64, 128) ||
-        !make_tmap_tile(&m1.w1, w.w3, 1, D / 2, H_local, E_local, X_ROW, 64, 128) ||
-        !make_tmap_tile(&m2.w0, w.w2, 1, H_local / 2, D, E_local, X_ROW, 128, 128))
-        return cudaErrorInvalidValue;
-    m2.w1 = m2.w0;
-
     MxParams p{};
     p.E_local = E_local;
     p.e_first = e_first;
@@ -874,9 +865,19 @@ cudaError_t launch_grouped_swiglu_mxfp4(const uint8_t *x_perm_q, const uint8_t *
     // 144, 123 with 208.
     const double rows = avg_rows + sqrt((double)avg_rows);
     auto tiles = [&](int bn) { return std::max(1LL, (long long)std::ceil(rows / bn)); };
-    if (tiles(32) == tiles(208)) return launch_mx_both<32>(m1, m2, p1, p2, stream);
-    if (tiles(144) == tiles(208)) return launch_mx_both<144>(m1, m2, p1, p2, stream);
-    return launch_mx_both<208>(m1, m2, p1, p2, stream);
+    const int bn = tiles(32) == tiles(208) ? 32 : tiles(144) == tiles(208) ? 144 : 208;
+
+    MxMaps m1, m2;
+    if (!token_maps(&m1, x_perm_q, D, rows_alloc, bn) ||
+        !token_maps(&m2, h_q, H_local, rows_alloc, bn) ||
+        !make_tmap_tile(&m1.w0, w.w1, 1, D / 2, H_local, E_local, X_ROW, 64, 128) ||
+        !make_tmap_tile(&m1.w1, w.w3, 1, D / 2, H_local, E_local, X_ROW, 64, 128) ||
+        !make_tmap_tile(&m2.w0, w.w2, 1, H_local / 2, D, E_local, X_ROW, 128, 128))
+        return cudaErrorInvalidValue;
+    m2.w1 = m2.w0;
+    return bn == 32    ? launch_mx_both<32>(m1, m2, p1, p2, stream)
+           : bn == 144 ? launch_mx_both<144>(m1, m2, p1, p2, stream)
+                       : launch_mx_both<208>(m1, m2, p1, p2, stream);
 }
 
 }  // namespace moe
