@@ -142,42 +142,45 @@ struct MxTile {
     }
 };
 
-// Builds the table by one warp, 32 experts at a time; returns the number of
-// token tiles.  Offsets outside [0, rows_alloc] or decreasing flag
-// FLAG_BAD_ROUTING and empty the segment.
+// An expert's first row, rows and token tiles (kept in `first` until the scan),
+// by every thread of the block, so that E_local = 256 waits for one load and not
+// for eight in a row (prologue after the wait 11000 cycles with one warp, 3000).
+// Offsets outside [0, rows_alloc] or decreasing flag FLAG_BAD_ROUTING and empty
+// the segment.
 template <int kBN>
-__device__ __forceinline__ void build_mx_table(int lane, const MxParams &p, const MxTable &t,
-                                               int *status) {
-    int run = 0;
-    for (int e0 = 0; e0 < p.E_local; e0 += 32) {
-        const int e = e0 + lane;
-        int b = 0, v = 0, tiles = 0;
-        if (e < p.E_local) {
-            b = p.seg_off[e];
-            const int end = p.seg_off[e + 1];
-            int c = p.tpe[p.e_first + e];
-            if (b < 0 || end < b || end > p.rows_alloc || c < 0) {
-                raise_flag(status, FLAG_BAD_ROUTING);
-                c = 0;
-            }
-            v = max(0, min(c, end - b));
-            tiles = (v + kBN - 1) / kBN;
+__device__ __forceinline__ void read_mx_table(const MxParams &p, const MxTable &t, int *status) {
+    for (int e = threadIdx.x; e < p.E_local; e += X_THREADS) {
+        const int b = p.seg_off[e], end = p.seg_off[e + 1];
+        int c = p.tpe[p.e_first + e];
+        if (b < 0 || end < b || end > p.rows_alloc || c < 0) {
+            raise_flag(status, FLAG_BAD_ROUTING);
+            c = 0;
         }
+        const int v = max(0, min(c, end - b));
+        const int tiles = (v + kBN - 1) / kBN;
+        t.base[e] = b;
+        t.valid[e] = v;
+        t.first[e] = tiles;
+        t.per[e] = tiles ? ((v + tiles - 1) / tiles + 15) & ~15 : 16;
+    }
+}
+
+// Exclusive scan of the tile counts by one warp.
+__device__ __forceinline__ void scan_mx_table(int lane, int E_local, const MxTable &t) {
+    int run = 0;
+    for (int e0 = 0; e0 < E_local; e0 += 32) {
+        const int e = e0 + lane;
+        const int tiles = e < E_local ? t.first[e] : 0;
         int incl = tiles;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int n = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += n;
         }
-        if (e < p.E_local) {
-            t.base[e] = b;
-            t.valid[e] = v;
-            t.first[e] = run + incl - tiles;
-            t.per[e] = tiles ? ((v + tiles - 1) / tiles + 15) & ~15 : 16;
-        }
+        if (e < E_local) t.first[e] = run + incl - tiles;
         run += __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (lane == 0) t.first[p.E_local] = run;
+    if (lane == 0) t.first[E_local] = run;
 }
 
 // SiLU(g) = g / (1 + e^-g) with the fast approximate division (2 ulp in fp32,
@@ -405,7 +408,9 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     griddep_wait();  // every input of this kernel is complete
-    if (warp == 0) build_mx_table<kBN>(lane, p, table, blockIdx.x == 0 ? p.status : nullptr);
+    read_mx_table<kBN>(p, table, blockIdx.x == 0 ? p.status : nullptr);
+    __syncthreads();
+    if (warp == 0) scan_mx_table(lane, p.E_local, table);
     __syncthreads();
     const int total = table.first[p.E_local] * p.nt;
     const uint32_t full_leader = mapa_shared(smem_u32(&full[0]), 0);
@@ -650,7 +655,8 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
                 // fragments of 8 x 8 matrices (a column of y by tokens), rounded to
                 // fp16 and stored transposed, a token's 8 columns in 16 bytes; 16-byte
                 // unit u of token t is kept at u ^ (t / 2 & 3), free of bank conflicts
-                // both ways.  (One STS per value instead: 583 against 250 cycles a chunk.)
+                // both ways.  (One STS per value instead: a long Zipf-skewed call 883
+                // against 849 us.)
                 const int col0 = c.nt * X_BM + (int)rank * 128 + q * 32;
                 uint8_t *buf = turn + ew * (32 * 64);
                 const int mr = lane & 7, mf = lane >> 3;   // the address this lane gives: token, unit

@@ -245,6 +245,11 @@ ALL = [1, 15, 16, 17, 31, 33, 0, 64, 65, 96, 127, 128, 129, 0, 255, 256, 257, 30
     ([140, 2], 2048, 1408, 128),      # sizes of the fine-grained layer
     (ALL, 320, 192, 128),
     (ALL, 320, 224, 1),
+    # averages that take the tile of 208 tokens: tiles full, one row over, one row
+    ([416, 0, 417, 385, 400, 350], 288, 160, 128),
+    ([208, 209, 160, 63, 1, 320], 768, 128, 1),
+    # few rows on average (tiles of 32), one expert with several tiles
+    ([0, 1, 100, 0, 32, 33, 2, 0, 0, 1, 0, 16, 0, 0, 3, 0, 0, 5], 224, 288, 64),
 ])
 def test_grouped(moe, counts, D, H, align):
     cfg, seg, xq, xs, w, out = _grouped_case(moe, counts, D, H, align, D + H)
