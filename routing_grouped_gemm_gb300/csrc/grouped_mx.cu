@@ -14,15 +14,17 @@
 // weights, which come from HBM, short ones.  Both ask for few operand rows per
 // product:
 //   * the weights are the M operand, 256 rows on a pair of CTAs
-//     (cta_group::2), and the tokens the N operand, up to 192 of an expert's
-//     rows, split evenly over its tiles in steps of 16: a ragged segment costs
-//     its own rows and no more, a decode batch loads 16;
+//     (cta_group::2), and the tokens the N operand, up to 32, 144 or 208 of an
+//     expert's rows (the launch says when which), split evenly over its tiles in
+//     steps of 16: a ragged segment costs its own rows and no more, a decode
+//     batch loads 16;
 //   * of GEMM1's 256 rows each CTA holds 64 rows of w1 and the same 64 of w3,
 //     so a tile gives h of 128 hidden units;
-//   * two accumulators of 192 columns leave 128 of the 512 tensor-memory
-//     columns for scales: five buffers of 24 (a K block of 256 of 128 weight
-//     rows and of the tokens), one per pipeline stage, so scales are never
-//     overwritten under an MMA and nothing waits for that but the stage itself;
+//   * two accumulators leave at least 96 of the 512 tensor-memory columns for
+//     scales: four or more buffers of 24 (a K block of 256 of 128 weight rows
+//     and of the tokens), taken in turn.  The warp that copies scales refills one
+//     when the MMAs that many K blocks back have completed, which the ring's own
+//     barriers tell, so the buffers and the stages differ in number freely;
 //   * scales are read in their natural [rows, K / 32] layout, which is not the
 //     order the tensor cores want (four scales each of rows l, l + 32, l + 64
 //     and l + 96 together).  Warps fetch them, 32 bytes of a row -- one
@@ -30,9 +32,9 @@
 //     tcgen05.cp, in a ring of their own with one fence and one arrival for four
 //     K blocks;
 //   * the accumulator's lanes are weight rows and its columns tokens, so the
-//     epilogues turn it around in shared memory, 32 tokens at a time: for h a
-//     thread then has 16 gates and ups of one token (half of a block, its
-//     maximum one shuffle away), for y 16-byte pieces of a token's row;
+//     epilogues turn it around in shared memory, 16 or 32 tokens at a time: for
+//     h a thread then has 8 or 16 gates and ups of one token (part of a block,
+//     its maximum one or two shuffles away), for y pieces of a token's row;
 //   * every mbarrier wait is bounded (FLAG_TIMEOUT).
 #include <cuda.h>
 
@@ -144,7 +146,7 @@ struct MxTile {
 
 // An expert's first row, rows and token tiles (kept in `first` until the scan),
 // by every thread of the block, so that E_local = 256 waits for one load and not
-// for eight in a row (prologue after the wait 11000 cycles with one warp, 3000).
+// for eight in a row.
 // Offsets outside [0, rows_alloc] or decreasing flag FLAG_BAD_ROUTING and empty
 // the segment.
 template <int kBN>
@@ -602,10 +604,18 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
             if (kGemm1) {
                 // lanes 0-63 are the gates of units `unit0`.., 64-127 their ups
                 const int unit0 = c.nt * X_UNITS + (int)rank * 64;
-                constexpr int kLanes = 64 / kChunk;            // lanes that share a block of 32 units
-                constexpr int kUnits = 32 / kLanes;            // units of a lane
-                const int tok = (q & 1) * (kChunk / 2) + lane / kLanes;  // of the chunk in the buffer
-                const int unit = (q >> 1) * 32 + lane % kLanes * kUnits;
+                // A lane turns kUnits of a token's 64, kLanes share a block of 32 and
+                // 2 kLanes a token, so that the warp stores whole 32-byte sectors of h
+                // and both of a token's scales at once (16 bytes and a byte at a time: a
+                // long Zipf-skewed call 844 against 834 us, others the same).  Units 32
+                // on are kept with their 8s swapped in pairs (column ^ 8): the two
+                // blocks' lanes would read the same banks.
+                constexpr int kLanes = 64 / kChunk;
+                constexpr int kUnits = 32 / kLanes;
+                const int tok = q * (kChunk / 4) + lane / (2 * kLanes);  // of the chunk in the buffer
+                const int blk = lane / kLanes & 1, first = lane % kLanes * kUnits;
+                const int unit = blk * 32 + first;
+                const bool both = (p.n_out & 63) == 0;  // a token's two scales lie on 2 bytes
                 float *buf = reinterpret_cast<float *>(turn) + eg * (kChunk * X_TURN_LD);
                 for (int t0 = kChunk * eg; t0 < c.nvalid; t0 += step) {
                     uint32_t d[kChunk];
@@ -615,15 +625,16 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
                     bar_sync(X_EPI_BAR + eg, 128);  // the group has read its last chunk
 #pragma unroll
                     for (int j = 0; j < kChunk; ++j)
-                        buf[j * X_TURN_LD + q * 32 + lane] = __uint_as_float(d[j]);
+                        buf[j * X_TURN_LD + q * 32 + (lane ^ (q & 1) << 3)] = __uint_as_float(d[j]);
                     bar_sync(X_EPI_BAR + eg, 128);
-                    const float *src = buf + tok * X_TURN_LD + unit;
+                    const float *src = buf + tok * X_TURN_LD + blk * 32;
                     float h[kUnits];
                     uint32_t top = 0;
 #pragma unroll
                     for (int v = 0; v < kUnits / 4; ++v) {
-                        const float4 g = *reinterpret_cast<const float4 *>(src + 4 * v);
-                        const float4 u = *reinterpret_cast<const float4 *>(src + 64 + 4 * v);
+                        const int at = (first + 4 * v) ^ blk << 3;
+                        const float4 g = *reinterpret_cast<const float4 *>(src + at);
+                        const float4 u = *reinterpret_cast<const float4 *>(src + 64 + at);
                         h[4 * v] = mx_silu(g.x) * u.x;
                         h[4 * v + 1] = mx_silu(g.y) * u.y;
                         h[4 * v + 2] = mx_silu(g.z) * u.z;
@@ -636,6 +647,7 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
                         top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
                     const uint32_t sb = mx_scale_byte(top);
                     const float inv = mx_inv_scale(sb);
+                    const uint32_t sb1 = __shfl_down_sync(0xffffffffu, sb, kLanes);  // the second block's
                     if (t0 + tok < c.nvalid && unit0 + unit < p.n_out) {
                         const size_t row = (size_t)(c.row0 + t0 + tok);
                         uint32_t *to = reinterpret_cast<uint32_t *>(
@@ -646,8 +658,12 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
                                 c0, mx_codes8(*reinterpret_cast<const float(*)[8]>(h + 8), inv));
                         else
                             *to = c0;
-                        if (lane % kLanes == 0)
-                            p.hsf[row * (size_t)(p.n_out / 32) + (unit0 + unit) / 32] = (uint8_t)sb;
+                        uint8_t *sf = p.hsf + row * (size_t)(p.n_out / 32) + (unit0 + unit) / 32;
+                        if (both) {
+                            if (unit == 0) *reinterpret_cast<uint16_t *>(sf) = (uint16_t)(sb | sb1 << 8);
+                        } else if (first == 0) {
+                            *sf = (uint8_t)sb;
+                        }
                     }
                 }
             } else {
