@@ -126,7 +126,8 @@ def test_rows_in_more_dimensions_and_none(moe):
 
 @pytest.mark.parametrize("T,E,k,D,align,e_first,E_local,masked", [
     (700, 16, 4, 512, 128, 0, 16, False), (333, 5, 2, 352, 1, 1, 3, False), (1, 8, 8, 32, 128, 0, 8, False),
-    (40, 8, 3, 1056, 64, 0, 8, True), (20000, 256, 2, 64, 128, 0, 256, False), (50, 4, 1, 64, 128, 4, 0, False)])
+    (40, 8, 3, 1056, 64, 0, 8, True), (20000, 256, 2, 64, 128, 0, 256, False), (50, 4, 1, 64, 128, 4, 0, False),
+    (5000, 256, 2, 64, 128, 0, 256, False), (5000, 256, 2, 64, 1, 200, 56, False), (0, 8, 2, 64, 128, 0, 8, False)])
 def test_dispatch(moe, T, E, k, D, align, e_first, E_local, masked):
     idx = _dev(moe_inputs.random_topk_idx(T, E, k, seed=T))
     x = _spread((T, D), T).to(torch.bfloat16)
@@ -150,6 +151,43 @@ def test_dispatch(moe, T, E, k, D, align, e_first, E_local, masked):
     assert np.array_equal(_np(xs)[held], sc[tor[held]])
     assert np.array_equal(mx.values(_np(xq)[held], _np(xs)[held]), v[tor[held]])
     assert (_np(xq)[~held] == 0xAA).all() and (_np(xs)[~held] == 0xAA).all()
+
+
+@pytest.mark.parametrize("T,E,k,cap", [(60, 8, 3, 9), (3000, 256, 4, 32), (5000, 16, 2, 0)])
+def test_rows_past_the_capacity_are_dropped(moe, T, E, k, cap):
+    """Masked layout: an expert's first `capacity` tokens are kept, the rest have no
+    row, the status says so, and the layer is still its steps."""
+    D, H = 128, 64
+    cfg, x, wg, w = _layer(moe, T, D, H, E, k, seed=T, layout=1, capacity=cap)
+    ra, ws = moe.rows_alloc(cfg), moe.alloc_workspace(cfg, layer=True)
+    idx = torch.empty((T, k), dtype=torch.int32, device="cuda")
+    tw = torch.empty((T, k), dtype=torch.float32, device="cuda")
+    moe.moe_route_topk(cfg, x, wg, None, None, idx, tw, ws)
+    lay = [torch.full(n, -7, dtype=torch.int32, device="cuda") for n in ((E,), (E + 1,), (T, k), (ra,))]
+    want = [torch.empty_like(t) for t in lay]
+    xq = torch.full((ra, D // 2), 0xAA, dtype=torch.uint8, device="cuda")
+    xs = torch.full((ra, D // 32), 0xAA, dtype=torch.uint8, device="cuda")
+    moe.moe_permute_mxfp4(cfg, x, idx, *lay, xq, xs, ws)
+    assert moe.moe_get_device_status(ws) == moe.MOE_ERR_CAPACITY
+    moe.moe_permute_index(cfg, idx, *want, ws)
+    assert moe.moe_get_device_status(ws) == moe.MOE_ERR_CAPACITY
+    for p, q in zip(lay, want):
+        assert torch.equal(p, q)
+    tor = _np(lay[3])
+    held = tor >= 0
+    assert held.sum() == np.minimum(_np(lay[0]), cap).sum() < T * k
+    v, sc = mx.quantize(_f64(x))
+    assert np.array_equal(_np(xs)[held], sc[tor[held]])
+    assert np.array_equal(mx.values(_np(xq)[held], _np(xs)[held]), v[tor[held]])
+    assert (_np(xq)[~held] == 0xAA).all() and (_np(xs)[~held] == 0xAA).all()
+    hq, hs = torch.empty((ra, H // 2), dtype=torch.uint8, device="cuda"), torch.empty((ra, H // 32), dtype=torch.uint8, device="cuda")
+    y, steps, out = torch.empty((ra, D), dtype=torch.float16, device="cuda"), torch.empty_like(x), torch.empty_like(x)
+    moe.moe_grouped_swiglu_mxfp4(cfg, xq, xs, lay[1], lay[0], *w[0], *w[1], *w[2], hq, hs, y, ws)
+    moe.moe_unpermute_combine(cfg, y, lay[2], tw, steps, ws)
+    assert moe.moe_get_device_status(ws) == moe.MOE_OK
+    moe.moe_layer_forward_mxfp4(cfg, x, wg, None, *w[0], *w[1], *w[2], out, ws)
+    assert moe.moe_get_device_status(ws) == moe.MOE_ERR_CAPACITY
+    assert torch.equal(out, steps)
 
 
 # ---------------------------------------------------------------------------
