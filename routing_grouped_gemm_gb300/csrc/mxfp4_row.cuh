@@ -115,6 +115,7 @@ __device__ __forceinline__ uint32_t mx_amax_quad(const float (&f)[8]) {
 // time and has the loads of kMxBatch of those in flight before it uses the
 // first: with one, each step of a row waited for memory in turn.
 constexpr int kMxBatch = 8;
+static_assert(kMxBatch == 8, "two stores of four steps' scales");
 
 __device__ __forceinline__ void quantize_row_mxfp4_warp(const __nv_bfloat16 *__restrict__ x,
                                                         int cols, int c_first, int c_step,
@@ -138,6 +139,10 @@ __device__ __forceinline__ void quantize_row_mxfp4_warp(const __nv_bfloat16 *__r
             b[u] = mx_scale_byte(mx_amax_quad(f));
             q[u] = mx_codes8(f, mx_inv_scale(b[u]));
         }
+        // a block's lanes all hold its scale: each stores that of another step
+        const int i = lane & 3, cs = c0 + i * c_step + (lane & ~3) * 8;
+        const uint32_t b0 = i & 2 ? (i & 1 ? b[3] : b[2]) : (i & 1 ? b[1] : b[0]);
+        const uint32_t b1 = i & 2 ? (i & 1 ? b[7] : b[6]) : (i & 1 ? b[5] : b[4]);
         for (int j = 0; j < n_dst; ++j) {
             const int r = __shfl_sync(0xffffffffu, my_row, j);
             if (r < 0) continue;
@@ -147,8 +152,9 @@ __device__ __forceinline__ void quantize_row_mxfp4_warp(const __nv_bfloat16 *__r
                 const int c = c0 + u * c_step + lane * 8;
                 if (c >= cols) continue;
                 *reinterpret_cast<uint32_t *>(qr + c / 2) = q[u];
-                if ((lane & 3) == 0) sr[c / 32] = (uint8_t)b[u];
             }
+            if (cs < cols) sr[cs / 32] = (uint8_t)b0;
+            if (cs + 4 * c_step < cols) sr[(cs + 4 * c_step) / 32] = (uint8_t)b1;
         }
     }
 }
