@@ -364,14 +364,16 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
                  : "memory");
 }
 
-// Barrier of `threads` threads (whole warps, all of them in this call) that
-// also tells each whether `ok` held for every one.
+// Barrier of `threads` threads that also tells each whether `ok` held for every
+// one.  Aligned, as __syncthreads is: whole warps come to it, each together, but
+// different warps may come from different code.  (Without .aligned the compiler
+// takes what follows for divergent.)
 __device__ __forceinline__ bool bar_and(int id, int threads, bool ok) {
     uint32_t all;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %3, 0;\n\t"
-        "barrier.cta.red.and.pred q, %1, %2, p;\n\t"
+        "barrier.cta.red.and.aligned.pred q, %1, %2, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(all)
         : "r"(id), "r"(threads), "r"((uint32_t)ok)
@@ -380,7 +382,7 @@ __device__ __forceinline__ bool bar_and(int id, int threads, bool ok) {
 }
 
 __device__ __forceinline__ void bar_sync(int id, int threads) {
-    asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+    asm volatile("barrier.cta.sync.aligned %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 // The same with release at CTA scope: orders this CTA's shared memory, which is

@@ -145,13 +145,15 @@ struct MxTile {
 };
 
 // An expert's first row, rows and token tiles (kept in `first` until the scan),
-// by every thread of the block, so that E_local = 256 waits for one load and not
-// for eight in a row.
+// by every warp but the scale fetchers, so that E_local = 256 waits for one load
+// and not for eight in a row.
 // Offsets outside [0, rows_alloc] or decreasing flag FLAG_BAD_ROUTING and empty
 // the segment.
 template <int kBN>
 __device__ __forceinline__ void read_mx_table(const MxParams &p, const MxTable &t, int *status) {
-    for (int e = threadIdx.x; e < p.E_local; e += X_THREADS) {
+    const int warp = threadIdx.x >> 5;
+    const int first = threadIdx.x - (warp < 3 ? 0 : 32 * X_SF_WARPS);
+    for (int e = first; e < p.E_local; e += X_THREADS - 32 * X_SF_WARPS) {
         const int b = p.seg_off[e], end = p.seg_off[e + 1];
         int c = p.tpe[p.e_first + e];
         if (b < 0 || end < b || end > p.rows_alloc || c < 0) {
@@ -191,14 +193,14 @@ __device__ __forceinline__ float mx_silu(float g) { return __fdividef(g, 1.f + _
 
 constexpr uint32_t kMxOnes = 0x7f7f7f7fu;  // four scales of 1
 
-// Bytes [32 kg, 32 kg + 32) of each of N rows of scales [.., ld] (`total` bytes
-// in all, 16-byte aligned), 1.0 past the row's end (the codes there are zeros)
-// and for a row that is not `there`.  The rows' alignment is looked at once, not
-// row by row, so that every load is issued before any of them is used.
+// Bytes [32 kg, 32 kg + 32) of each of N rows of scales [.., ld], ld a multiple
+// of 4 (the array 16-byte aligned); 1.0 past the row's end (the codes there are
+// zeros) and for a row that is not `there`.  The rows' alignment is looked at
+// once, not row by row, so that every load is issued before any is used.
 template <int N>
 __device__ __forceinline__ void load_scales32(const uint8_t *const (&base)[N], const size_t (&row)[N],
-                                              const bool (&there)[N], int ld, const size_t (&total)[N],
-                                              int kg, uint32_t (&v)[N][8]) {
+                                              const bool (&there)[N], int ld, int kg,
+                                              uint32_t (&v)[N][8]) {
     const int n = ld - 32 * kg;  // bytes left in a row
     if ((ld & 15) == 0) {
 #pragma unroll
@@ -212,46 +214,14 @@ __device__ __forceinline__ void load_scales32(const uint8_t *const (&base)[N], c
         }
         return;
     }
-    if ((ld & 3) == 0) {
-#pragma unroll
-        for (int r = 0; r < N; ++r) {
-            const uint32_t *q = reinterpret_cast<const uint32_t *>(base[r] + row[r] * ld + 32 * kg);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                uint32_t x = kMxOnes;
-                if (there[r] && 4 * i < n) x = q[i];
-                v[r][i] = x;
-            }
-        }
-        return;
-    }
-    // rows at any byte: the aligned words around the 32 bytes, shifted together
 #pragma unroll
     for (int r = 0; r < N; ++r) {
-        const size_t off = row[r] * ld + 32 * kg, a = off & ~(size_t)3;
-        const int sh = 8 * (int)(off & 3);
-        const int words = there[r] ? (min(n, 32) + (sh >> 3) + 3) / 4 : 0;
-        const uint8_t *src = base[r] + a;
-        uint32_t w[9];
-#pragma unroll
-        for (int i = 0; i < 9; ++i) {
-            w[i] = 0;
-            if (i < words && a + 4 * i + 4 <= total[r])
-                w[i] = *reinterpret_cast<const uint32_t *>(src + 4 * i);
-        }
-        if (words && a + 4 * words > total[r])  // the array's last, partial word
-            for (size_t at = total[r] & ~(size_t)3; at < total[r]; ++at) {
-                const int i = (int)(at - a) / 4;
-#pragma unroll
-                for (int j = 0; j < 9; ++j)
-                    if (j == i) w[j] |= (uint32_t)base[r][at] << (8 * (int)(at & 3));
-            }
+        const uint32_t *q = reinterpret_cast<const uint32_t *>(base[r] + row[r] * ld + 32 * kg);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            v[r][i] = __funnelshift_r(w[i], w[i + 1], sh);
-            const int left = there[r] ? n - 4 * i : 0;
-            if (left <= 0) v[r][i] = kMxOnes;
-            else if (left < 4) v[r][i] = (v[r][i] & ((1u << (8 * left)) - 1u)) | (kMxOnes << (8 * left));
+            uint32_t x = kMxOnes;
+            if (there[r] && 4 * i < n) x = q[i];
+            v[r][i] = x;
         }
     }
 }
@@ -263,31 +233,43 @@ struct ScaleWarp {
     uint64_t *empty;
     uint32_t full_leader;
     volatile int *abort_flag;
-    int slot, lane, pair_id, n_pairs, total, dt, dn, rank;
+    int slot, lane, pair_id, n_pairs, dt, dn, rank;
 };
 
 // Takes every X_SLOTS-th group of four K blocks: 32 bytes of each of the CTA's
 // 128 weight rows, or of the tile's tokens (all of them: each CTA's half of the
 // MMA needs all).  Lane l serves rows l, l + 32, ...  A group's loads are issued
 // when the warp's last one is stored.
-template <bool kGemm1, bool kTokens, int kBN>
+// The first round is a dry one, before the wait for the previous kernel and the
+// table: no row is there and nothing is announced, but its instructions come from
+// memory while there is nothing else to do.  Between the table and the first MMA
+// of a fine-grained GEMM2 lay 6.6 us, 3 of them for the instructions up to the
+// loads, and for rows at any byte, unrolled, 13 (grouped call 119.8 against 117
+// us with the dry round, 37 against 27 for a small shard of such rows).
+// kWords: ld is a multiple of 4.
+template <bool kGemm1, bool kTokens, int kBN, bool kWords>
 __device__ __forceinline__ void fetch_scales(const ScaleWarp &f, const MxParams &p, const MxTable &table) {
     constexpr int kRows = kTokens ? (kBN + 31) / 32 : 4;
     static_assert(kRows <= 8, "two blocks of 128 tokens");
     const int lane = f.lane, ld = p.K / 32, ng = (p.nk + X_GROUP - 1) / X_GROUP;
     const size_t all = (kTokens ? (size_t)p.rows_alloc : (size_t)p.E_local * p.n_out) * ld;
-    uint32_t ph = 0;
-    MxTile c(f.pair_id, p.nt, f.total, table);
-    int kg = f.slot;
-    for (int tile = f.pair_id;; kg += X_SLOTS) {
-        while (kg >= ng && tile < f.total) {
-            kg -= ng;
-            tile += f.n_pairs;
-            c.step(f.dt, f.dn, p.nt, tile < f.total, table);
+    uint32_t ph = 0, tail = 0;  // tail: the array's last word, where that is a part of one
+    MxTile c(f.pair_id, p.nt, 0, table);
+    int kg = f.slot, tile = f.pair_id, total = 0;
+    int rows_there = 0;  // of the weights (no token is in a tile without rows)
+    int dry;
+    asm volatile("mov.s32 %0, 1;" : "=r"(dry));  // unknown to the compiler: one code for all rounds
+    for (;;) {
+        if (!dry) {
+            while (kg >= ng && tile < total) {
+                kg -= ng;
+                tile += f.n_pairs;
+                c.step(f.dt, f.dn, p.nt, tile < total, table);
+            }
+            if (tile >= total) break;
         }
-        if (tile >= f.total) break;
         const uint8_t *base[kRows];
-        size_t row[kRows], total[kRows];
+        size_t row[kRows];
         bool there[kRows];
         uint32_t v[kRows][8];
 #pragma unroll
@@ -300,35 +282,82 @@ __device__ __forceinline__ void fetch_scales(const ScaleWarp &f, const MxParams 
             } else {
                 const int r = kGemm1 ? c.nt * X_UNITS + f.rank * 64 + (i & 1) * 32 + lane
                                      : c.nt * X_BM + f.rank * 128 + i * 32 + lane;
-                there[i] = r < p.n_out;
+                there[i] = r < rows_there;
                 base[i] = kGemm1 && i >= 2 ? p.w_sf1 : p.w_sf0;
                 row[i] = (size_t)c.expert * p.n_out + r;
             }
-            total[i] = all;
         }
-        load_scales32<kRows>(base, row, there, ld, total, kg, v);
-        // lane 0 waits for the group's room, the warp follows it
-        bool got = true;
-        if (lane == 0) got = mbar_wait_bounded(f.empty, ph ^ 1u, f.abort_flag);
-        if (!__shfl_sync(0xffffffffu, got, 0)) break;
-        ph ^= 1u;
+        // rows at any byte: the aligned words around the 32 bytes, shifted; the
+        // first are asked for here, and bring most of the others' sectors
+        auto word = [&](int i, int at) {
+            const size_t a = ((row[i] * ld + 32 * kg) & ~(size_t)3) + 4 * at;
+            const int end = (int)((row[i] * ld) & 3) + min(ld - 32 * kg, 32);
+            if (!there[i] || 4 * at >= end) return 0u;
+            return a + 4 <= all ? *reinterpret_cast<const uint32_t *>(base[i] + a) : tail;
+        };
+        if constexpr (kWords) {
+            load_scales32<kRows>(base, row, there, ld, kg, v);
+        } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {  // K block j / 2 of the group, its half h = j % 2
-            // blocks of 512 bytes: 0, 1: the weights' K halves; 2 + 2 h + token / 128: the tokens'
+            for (int i = 0; i < kRows; ++i) v[i][0] = word(i, 0);
+        }
+        if (!dry) {
+            // lane 0 waits for the group's room, the warp follows it
+            bool got = true;
+            if (lane == 0) got = mbar_wait_bounded(f.empty, ph ^ 1u, f.abort_flag);
+            if (!__shfl_sync(0xffffffffu, got, 0)) break;
+            ph ^= 1u;
+        }
+        // K block j / 2 of the group, its half h = j % 2, in blocks of 512 bytes:
+        // 0, 1: the weights' K halves; 2 + 2 h + token / 128: the tokens'
+        auto store = [&](int j, auto &&of) {
             uint4 *d = reinterpret_cast<uint4 *>(f.room + (j / 2) * X_SF_BYTES) + lane;
             const int h = j & 1;
             if constexpr (kTokens) {
-                auto of = [&](int i) { return i < kRows ? v[i < kRows ? i : 0][j] : kMxOnes; };
                 d[32 * (2 + 2 * h)] = make_uint4(of(0), of(1), of(2), of(3));
                 if (kBN > 128 && c.n > 128)
                     d[32 * (3 + 2 * h)] = make_uint4(of(4), of(5), of(6), of(7));
             } else {
-                d[32 * h] = make_uint4(v[0][j], v[1][j], v[2][j], v[3][j]);
+                d[32 * h] = make_uint4(of(0), of(1), of(2), of(3));
             }
+        };
+        if constexpr (kWords) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                store(j, [&](int i) { return i < kRows ? v[i < kRows ? i : 0][j] : kMxOnes; });
+        } else {
+#pragma unroll 1
+            for (int j = 0; j < 8; ++j) {
+                const int left = ld - 32 * kg - 4 * j;  // bytes of the row from here on
+                const uint32_t keep = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) {
+                    const uint32_t next = word(i, j + 1);
+                    v[i][1] = __funnelshift_r(v[i][0], next, 8 * (uint32_t)((row[i] * ld) & 3));
+                    v[i][1] = there[i] ? (v[i][1] & keep) | (kMxOnes & ~keep) : kMxOnes;
+                    v[i][0] = next;
+                }
+                store(j, [&](int i) { return i < kRows ? v[i < kRows ? i : 0][1] : kMxOnes; });
+            }
+        }
+        if (dry) {
+            dry = 0;
+            griddep_wait();             // every input of this kernel is complete
+            bar_sync(0, X_THREADS);     // the table is read
+            bar_sync(0, X_THREADS);     // and scanned
+            total = table.first[p.E_local] * p.nt;
+            if (tile < total) c.place(table);
+            rows_there = p.n_out;
+            if (!kWords && kTokens && (all & 3)) {
+                const size_t a = all & ~(size_t)3;
+                for (int i = 0; i < (int)(all & 3); ++i) tail |= (uint32_t)p.t_sf[a + i] << (8 * i);
+            }
+            continue;
         }
         fence_proxy_async_smem();  // tcgen05.cp reads them through the async proxy
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster_cta(f.full_leader);
+        kg += X_SLOTS;
     }
 }
 
@@ -409,14 +438,17 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
     cluster_sync();  // the peer's barriers exist before anything arrives on them
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    griddep_wait();  // every input of this kernel is complete
-    read_mx_table<kBN>(p, table, blockIdx.x == 0 ? p.status : nullptr);
-    __syncthreads();
-    if (warp == 0) scan_mx_table(lane, p.E_local, table);
-    __syncthreads();
-    const int total = table.first[p.E_local] * p.nt;
-    const uint32_t full_leader = mapa_shared(smem_u32(&full[0]), 0);
     const int dt = n_pairs / p.nt, dn = n_pairs - dt * p.nt;  // a step of n_pairs tiles
+    int total = 0;
+    if (warp < 3 || warp >= 3 + X_SF_WARPS) {  // (the scale fetchers: after their dry round)
+        griddep_wait();                        // every input of this kernel is complete
+        read_mx_table<kBN>(p, table, blockIdx.x == 0 ? p.status : nullptr);
+        bar_sync(0, X_THREADS);
+        if (warp == 0) scan_mx_table(lane, p.E_local, table);
+        bar_sync(0, X_THREADS);
+        total = table.first[p.E_local] * p.nt;
+    }
+    const uint32_t full_leader = mapa_shared(smem_u32(&full[0]), 0);
 
     if (warp == 0) {
         // ---------------- TMA producer (both CTAs) ----------------
@@ -730,11 +762,18 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
         const int w = warp - 3, slot = w >> 1;
         const ScaleWarp f{sfs + slot * X_GROUP_BYTES, &sempty[slot],
                           mapa_shared(smem_u32(&sfull[slot]), 0), abort_flag, slot, lane,
-                          pair_id, n_pairs, total, dt, dn, (int)rank};
-        if (w & 1)
-            fetch_scales<kGemm1, true, kBN>(f, p, table);
-        else
-            fetch_scales<kGemm1, false, kBN>(f, p, table);
+                          pair_id, n_pairs, dt, dn, (int)rank};
+        if ((p.K / 32 & 3) == 0) {
+            if (w & 1)
+                fetch_scales<kGemm1, true, kBN, true>(f, p, table);
+            else
+                fetch_scales<kGemm1, false, kBN, true>(f, p, table);
+        } else {
+            if (w & 1)
+                fetch_scales<kGemm1, true, kBN, false>(f, p, table);
+            else
+                fetch_scales<kGemm1, false, kBN, false>(f, p, table);
+        }
     }
 
     tc_fence_before();
