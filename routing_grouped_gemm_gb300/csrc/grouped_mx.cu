@@ -342,11 +342,11 @@ __device__ __forceinline__ void fetch_scales(const ScaleWarp &f, const MxParams 
         }
         if (dry) {
             dry = 0;
-            griddep_wait();             // every input of this kernel is complete
-            bar_sync(0, X_THREADS);     // the table is read
-            bar_sync(0, X_THREADS);     // and scanned
+            bar_sync(0, X_THREADS);  // the table is read
+            bar_sync(0, X_THREADS);  // and scanned
             total = table.first[p.E_local] * p.nt;
             if (tile < total) c.place(table);
+            griddep_wait();          // every input of this kernel is complete
             rows_there = p.n_out;
             if (!kWords && kTokens && (all & 3)) {
                 const size_t a = all & ~(size_t)3;
@@ -367,7 +367,9 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
                   const __grid_constant__ CUtensorMap tmT32, const __grid_constant__ CUtensorMap tmT64,
                   const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CUtensorMap tmW1,
                   const MxParams p) {
-    griddep_launch_dependents();  // the next kernel may be scheduled now
+    // The next kernel may be scheduled now; GEMM2 once GEMM1's inputs are complete,
+    // so that it can read the experts' table, one of them, before its own wait.
+    if (!kGemm1) griddep_launch_dependents();
     if (cluster_nctarank() != 2) {  // every role below assumes a CTA pair
         griddep_wait();
         if (threadIdx.x == 0) raise_flag(p.status, FLAG_LAUNCH);
@@ -441,7 +443,10 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
     const int dt = n_pairs / p.nt, dn = n_pairs - dt * p.nt;  // a step of n_pairs tiles
     int total = 0;
     if (warp < 3 || warp >= 3 + X_SF_WARPS) {  // (the scale fetchers: after their dry round)
-        griddep_wait();                        // every input of this kernel is complete
+        if (kGemm1) {
+            griddep_wait();  // every input of this kernel is complete
+            griddep_launch_dependents();
+        }
         read_mx_table<kBN>(p, table, blockIdx.x == 0 ? p.status : nullptr);
         bar_sync(0, X_THREADS);
         if (warp == 0) scan_mx_table(lane, p.E_local, table);
@@ -457,6 +462,7 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
         uint32_t ph = 0;
         bool ok = true;
         MxTile c(pair_id, p.nt, total, table);
+        if (!kGemm1) griddep_wait();  // h is complete
         for (int tile = pair_id; ok && tile < total;) {
             const int trows = c.n / 2;  // this CTA's token rows: a multiple of 8, below 128
             const int trow = c.row0 + (int)rank * trows;
