@@ -364,6 +364,15 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
                  : "memory");
 }
 
+// 32 bytes (aligned as such) in one load: one request for a sector, not two.
+__device__ __forceinline__ void ld_global_32(const void *src, uint32_t (&v)[8]) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+                   "=r"(v[7])
+                 : "l"(src)
+                 : "memory");
+}
+
 // Barrier of `threads` threads that also tells each whether `ok` held for every
 // one.  Aligned, as __syncthreads is: whole warps come to it, each together, but
 // different warps may come from different code.  (Without .aligned the compiler

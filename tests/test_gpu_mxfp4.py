@@ -361,6 +361,24 @@ def test_grouped_flags(moe):
     assert np.isfinite(y[:4]).all() and np.isnan(y[4:]).all()
 
 
+def test_grouped_scales_on_16_bytes(moe):
+    """Scales whose arrays start on 16 bytes and not on 32: the same bits."""
+    counts = [40, 0, 7, 161]
+    cfg, seg, xq, xs, w, out = _grouped_case(moe, counts, 1024, 1024, 16, 5)
+    ws = moe.alloc_workspace(cfg)
+    _call(moe, cfg, seg, counts, xq, xs, w, out, ws)
+    want = {k: v.clone() for k, v in out.items()}
+
+    def moved(t):
+        b = torch.empty(t.numel() + 16, dtype=torch.uint8, device="cuda")[16:].view(t.shape)
+        return b.copy_(t)
+    out["hs"] = moved(torch.full_like(out["hs"], 0xAA))
+    _call(moe, cfg, seg, counts, xq, moved(xs), [(q, moved(s)) for q, s in w], out, ws)
+    assert moe.moe_get_device_status(ws) == moe.MOE_OK
+    for k in out:
+        assert torch.equal(out[k].view(torch.uint8), want[k].view(torch.uint8)), k
+
+
 def test_grouped_many_experts(moe):
     """1024 experts, the largest table, most of them empty."""
     E, D, H = 1024, 64, 32
