@@ -10,9 +10,12 @@
 // operand), and y once to fp16, as the other bf16 layers store it.
 //
 // At 4 bits the tensor cores take a K = 64 step in the time of a bf16 K = 16
-// one, so a tile's operands, which come from L2, bound long calls and the
-// weights, which come from HBM, short ones.  Both ask for few operand rows per
-// product:
+// one, so everything around them counts: decode calls run at the weights' HBM
+// time (256 experts' 5.9 GB in 853 us), long ones at 45% tensor pipe
+// (4096 tokens x 6, 64 experts of 2048 x 1408: 115 us, 3.7 PFLOP/s), held by
+// operands and scales from L2, the epilogue's stores and the launches' ends, no
+// one of which is worth more than a few percent by itself.  So, few operand
+// rows per product:
 //   * the weights are the M operand, 256 rows on a pair of CTAs
 //     (cta_group::2), and the tokens the N operand, up to 32, 144 or 208 of an
 //     expert's rows (the launch says when which), split evenly over its tiles in
