@@ -370,9 +370,14 @@ __device__ __forceinline__ void fetch_scales(const ScaleWarp &f, const MxParams 
             }
             continue;
         }
-        fence_proxy_async_smem();  // tcgen05.cp reads them through the async proxy
+        // tcgen05.cp, issued by the leader's copy warp, reads them through the async
+        // proxy; the leader acquires at cluster scope
+        fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_cta(f.full_leader);
+        if (lane == 0) {
+            fence_release_smem_cluster();
+            mbar_arrive_cluster_relaxed(f.full_leader);
+        }
         kg += X_SLOTS;
     }
 }
@@ -586,7 +591,7 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
                 for (int kb = 0; kb < p.nk; ++kb) {
                     const int k4 = kb % X_GROUP;
                     bool got = true;
-                    if (k4 == 0) got = mbar_wait_bounded(&sfull[sg], phg, abort_flag);
+                    if (k4 == 0) got = mbar_wait_bounded(&sfull[sg], phg, abort_flag, true);
                     if (lag > 0) {
                         --lag;
                     } else {
