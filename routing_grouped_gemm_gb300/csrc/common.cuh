@@ -404,9 +404,11 @@ __device__ __forceinline__ void fence_release_smem_cluster() {
     asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
 }
 
-// mbar_arrive_cluster() without ordering, after fence_release_smem_cluster() or
-// for an arrival that publishes no memory: a release waits until the thread's stores in flight (a tile's output) have landed, about
-// 2500 cycles after the epilogue of a grouped MXFP4 tile.
+// mbar_arrive_cluster() without ordering: after fence_release_smem_cluster(), or
+// between tcgen05.fence::before_thread_sync and the ::after_thread_sync of a thread
+// that waits at cluster scope, which order the tensor memory that is handed over.
+// A release waits until the thread's stores in flight (a tile's output) have
+// landed, about 2500 cycles after the epilogue of a grouped MXFP4 tile.
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                  : "memory");

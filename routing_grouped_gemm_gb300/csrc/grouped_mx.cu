@@ -536,8 +536,9 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
             for (int tile = pair_id; ok && tile < total; ++it) {
                 const int acc = it & 1;
                 const uint32_t id0 = idesc_mxf4_f32(X_BM, c.n, 0), id2 = idesc_mxf4_f32(X_BM, c.n, 2);
-                if (!__all_sync(0xffffffffu, mbar_wait_bounded(
-                                                 &tempty[acc], ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag)))
+                // the peer's epilogue arrives here too: at cluster scope
+                if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tempty[acc], ((uint32_t)(it >> 1) & 1u) ^ 1u,
+                                                               abort_flag, true)))
                     break;
                 const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kBN);
                 for (int kb = 0; kb < p.nk; ++kb) {
@@ -647,8 +648,9 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
             if (!bar_and(X_EPI_BAR + eg, 128, got)) break;
             tc_fence_after();
             const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kBN);
-            // The accumulator is the MMA's again once this warp has its last chunk
-            // in registers; nothing in memory goes with that.
+            // The accumulator is the MMA's again once every warp has its last chunk in
+            // registers: tensor memory only, so the tcgen05 fences around a relaxed
+            // arrival are all it takes.
             auto release = [&]() {
                 tc_fence_before();
                 __syncwarp();

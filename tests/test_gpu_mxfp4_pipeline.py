@@ -70,20 +70,8 @@ def _tile_rule(rows):
     return 32 if n(32) == n(208) else 144 if n(144) == n(208) else 208
 
 
-@pytest.mark.parametrize("bn,E,D,H,align", [
-    (32, 12, 4352, 2336, 128),    # 17 and 10 K blocks; h's scale rows of 73 bytes
-    (32, 16, 2336, 4352, 1),
-    (144, 20, 2304, 2080, 16),    # 9 K blocks each way; h's scale rows of 65 bytes
-    (144, 20, 2080, 2304, 1),
-    (208, 20, 2304, 2016, 1),     # h's scale rows of 63 bytes
-    (208, 16, 4096, 2560, 128),   # 16 and 10 K blocks, scale rows on 16 bytes
-])
-def test_pairs_take_several_tiles(moe, bn, E, D, H, align):  # noqa: F811
-    counts = _tokens(bn, E, D + H)
-    assert _tile_rule(sum(counts) / E) == bn
-    tiles = sum(-(-c // bn) for c in counts)
-    assert tiles * -(-H // 128) > 2 * PAIRS and tiles * -(-D // 256) > 2 * PAIRS
-    cfg, seg, xq, xs, w, out = _grouped_case(moe, counts, D, H, align, bn + D, span=8)
+def _run(moe, counts, D, H, align, seed):
+    cfg, seg, xq, xs, w, out = _grouped_case(moe, counts, D, H, align, seed, span=8)
     ws = moe.alloc_workspace(cfg)
     _call(moe, cfg, seg, counts, xq, xs, w, out, ws)
     assert moe.moe_get_device_status(ws) == moe.MOE_OK
@@ -105,3 +93,30 @@ def test_pairs_take_several_tiles(moe, bn, E, D, H, align):  # noqa: F811
     assert moe.moe_get_device_status(ws) == moe.MOE_OK
     for k, v in out.items():
         assert torch.equal(v.view(torch.uint8), first[k].view(torch.uint8)), k
+
+
+@pytest.mark.parametrize("bn,E,D,H,align", [
+    (32, 12, 4352, 2336, 128),    # 17 and 10 K blocks; h's scale rows of 73 bytes
+    (32, 16, 2336, 4352, 1),
+    (144, 20, 2304, 2080, 16),    # 9 K blocks each way; h's scale rows of 65 bytes
+    (144, 20, 2080, 2304, 1),
+    (208, 20, 2304, 2016, 1),     # h's scale rows of 63 bytes
+    (208, 16, 4096, 2560, 128),   # 16 and 10 K blocks, scale rows on 16 bytes
+])
+def test_pairs_take_several_tiles(moe, bn, E, D, H, align):  # noqa: F811
+    counts = _tokens(bn, E, D + H)
+    assert _tile_rule(sum(counts) / E) == bn
+    tiles = sum(-(-c // bn) for c in counts)
+    assert tiles * -(-H // 128) > 2 * PAIRS and tiles * -(-D // 256) > 2 * PAIRS
+    _run(moe, counts, D, H, align, bn + D)
+
+
+@pytest.mark.parametrize("bn,E", [(32, 256), (144, 90), (208, 90)])
+def test_accumulators_change_hands(moe, bn, E):  # noqa: F811
+    """GEMM1 tiles of one K block: their products take less than their epilogues, and both
+    accumulators wait for it at every tile."""
+    counts = _tokens(bn, E, E + bn)
+    assert _tile_rule(sum(counts) / E) == bn
+    tiles = sum(-(-c // bn) for c in counts)
+    assert tiles * 4 > 4 * PAIRS and tiles > PAIRS
+    _run(moe, counts, 256, 512, 1, bn)
