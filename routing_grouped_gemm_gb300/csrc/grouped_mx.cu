@@ -643,7 +643,9 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
         MxTile c(pair_id, p.nt, total, table);
         for (int tile = pair_id; tile < total; ++it) {
             const int acc = it & 1;
-            const bool got = mbar_wait_bounded(&tfull[acc], (uint32_t)(it >> 1) & 1u, abort_flag);
+            // the warp together (the aligned barriers and loads below need it so)
+            const bool got = __all_sync(
+                0xffffffffu, mbar_wait_bounded(&tfull[acc], (uint32_t)(it >> 1) & 1u, abort_flag));
             // a group's warps go on, or stop, together
             if (!bar_and(X_EPI_BAR + eg, 128, got)) break;
             tc_fence_after();
