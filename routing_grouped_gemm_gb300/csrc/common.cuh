@@ -170,6 +170,15 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity
     }
 }
 
+// A warp's wait, before its CTA frees tensor memory or leaves, for what it has
+// issued (bar's first phase).  It runs to its own limit even when *abort is set
+// already, and a wait that runs out sets *abort: the CTA then settles and reports
+// it like any other.
+__device__ __forceinline__ void wait_drained(uint64_t *bar, volatile int *abort) {
+    volatile int ran_out = 0;
+    if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar, 0u, &ran_out))) *abort = 1;
+}
+
 // ---------------------------------------------------------------------
 // Counters in global memory shared by the CTAs of one launch
 // ---------------------------------------------------------------------

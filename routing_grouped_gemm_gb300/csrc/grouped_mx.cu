@@ -571,8 +571,7 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
             // every MMA issued here completes before either CTA frees TMEM
             if (elect_one()) tc_commit_pair(&drain[0], 0x1);
             __syncwarp();
-            volatile int local_abort = 0;
-            mbar_wait_bounded(&drain[0], 0u, &local_abort);
+            wait_drained(&drain[0], abort_flag);
         }
     } else if (warp == 2) {
         if (leader) {
@@ -630,8 +629,7 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
             }
             if (elect_one()) tc_commit_pair(&drain[1], 0x1);
             __syncwarp();
-            volatile int local_abort = 0;
-            mbar_wait_bounded(&drain[1], 0u, &local_abort);
+            wait_drained(&drain[1], abort_flag);
         }
     } else if (warp >= 3 + X_SF_WARPS) {
         // ---------------- epilogue (both CTAs) ----------------
