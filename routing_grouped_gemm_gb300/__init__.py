@@ -140,19 +140,20 @@ class Config:
     topk_group: int = 0
 
     def __setattr__(self, name, value):
-        self.__dict__.pop("_ref", None)   # what ref() keeps describes the old values
         object.__setattr__(self, name, value)
+        self.__dict__["_set"] = object()  # what ref() began to build before this is not these values'
 
     def __getstate__(self):               # copies and pickles go without the pointer
-        return {k: v for k, v in self.__dict__.items() if k != "_ref"}
+        return {k: v for k, v in self.__dict__.items() if k not in ("_set", "_ref")}
 
     def ref(self):
         """(pointer to the C struct, rows of the permuted buffers), built once for these values."""
-        r = self.__dict__.get("_ref")
-        if r is None:
+        d = self.__dict__
+        since, kept = d.get("_set"), d.get("_ref")
+        if kept is None or kept[0] is not since:
             p = ctypes.pointer(self.c())
-            r = self.__dict__["_ref"] = (p, int(_lib.moe_rows_alloc(p)))
-        return r
+            kept = d["_ref"] = (since, (p, int(_lib.moe_rows_alloc(p))))
+        return kept[1]
 
     def c(self) -> moe_config:
         el = self.E - self.e_first if self.E_local < 0 else self.E_local
