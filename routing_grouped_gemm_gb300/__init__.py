@@ -606,6 +606,8 @@ def moe_layer_forward_fp8(cfg: Config, x, wg, bias, w1_q, w1_scale, w3_q, w3_sca
 
 def _mx_tensor(t, name):
     """(rows, cols, dtype) of a tensor taken as rows of whole blocks."""
+    if t is None:
+        raise ValueError(f"{name} is required")
     if t.dtype not in (torch.bfloat16, torch.float32) or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous bf16 or fp32 CUDA tensor")
     if t.dim() == 0 or t.shape[-1] % 32:
@@ -641,7 +643,7 @@ def moe_dequantize_rows_mxfp4(codes, scale, dst, stream=None):
 def quantize_weights_mxfp4(w, stream=None):
     """(codes [..., cols / 2], scales [..., cols / 32]), uint8, of a weight such as
     w1 [E, H, D] or w2 [E, D, H] (bf16 or fp32; blocks along the last dimension)."""
-    cols = w.shape[-1]
+    _, cols, _ = _mx_tensor(w, "w")
     q = torch.empty((*w.shape[:-1], cols // 2), dtype=torch.uint8, device=w.device)
     sc = torch.empty((*w.shape[:-1], cols // 32), dtype=torch.uint8, device=w.device)
     moe_quantize_rows_mxfp4(w, q, sc, stream)
@@ -716,6 +718,8 @@ def moe_permute_backward(cfg: Config, dx_perm, row_of, dx, ws, stream=None):
     bf16 config)."""
     c, ra = cfg.ref()
     dt = cfg.torch_dtype
+    if dx_perm is None:
+        raise ValueError("dx_perm is required")
     if dx_perm.dtype not in (torch.float32, dt):
         raise ValueError(f"dx_perm: expected float32 or {dt}, got {dx_perm.dtype}")
     _check(_lib.moe_permute_backward(
