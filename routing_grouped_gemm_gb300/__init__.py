@@ -539,9 +539,11 @@ def moe_quantize_rows_fp8(src, dst, scale, stream=None):
 
 
 def quantize_weights_fp8(w, stream=None):
-    """(codes uint8, scales fp32 [..., rows]) of a bf16 weight [E, H, D] (one scale per row)."""
-    q = torch.empty(w.shape, dtype=torch.uint8, device=w.device)
-    sc = torch.empty(w.shape[:-1], dtype=torch.float32, device=w.device)
+    """(codes uint8, scales fp32 [..., rows]) of a bf16 weight [E, H, D] (one scale per row),
+    allocated on `stream`, which writes them."""
+    with torch.cuda.stream(stream):
+        q = torch.empty(w.shape, dtype=torch.uint8, device=w.device)
+        sc = torch.empty(w.shape[:-1], dtype=torch.float32, device=w.device)
     moe_quantize_rows_fp8(w, q, sc, stream)
     return q, sc
 
@@ -642,10 +644,13 @@ def moe_dequantize_rows_mxfp4(codes, scale, dst, stream=None):
 
 def quantize_weights_mxfp4(w, stream=None):
     """(codes [..., cols / 2], scales [..., cols / 32]), uint8, of a weight such as
-    w1 [E, H, D] or w2 [E, D, H] (bf16 or fp32; blocks along the last dimension)."""
+    w1 [E, H, D] or w2 [E, D, H] (bf16 or fp32; blocks along the last dimension).
+    They are allocated on `stream`, which writes them: their memory may have been
+    another tensor's that the current stream still works on."""
     _, cols, _ = _mx_tensor(w, "w")
-    q = torch.empty((*w.shape[:-1], cols // 2), dtype=torch.uint8, device=w.device)
-    sc = torch.empty((*w.shape[:-1], cols // 32), dtype=torch.uint8, device=w.device)
+    with torch.cuda.stream(stream):
+        q = torch.empty((*w.shape[:-1], cols // 2), dtype=torch.uint8, device=w.device)
+        sc = torch.empty((*w.shape[:-1], cols // 32), dtype=torch.uint8, device=w.device)
     moe_quantize_rows_mxfp4(w, q, sc, stream)
     return q, sc
 
