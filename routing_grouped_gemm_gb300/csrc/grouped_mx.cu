@@ -42,6 +42,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "common.cuh"
@@ -821,15 +822,16 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
     }
 }
 
-// Clusters of two that fit at once on the current device (0 if none).
+// Clusters of two that fit at once on the current device (0 if none).  The last
+// answer is kept together with what it was for, in one word: threads launch at once.
 template <bool kGemm1, int kBN>
 int max_mx_clusters(size_t smem) {
     constexpr int kMaxDev = 64;
-    static int cached[kMaxDev] = {0};
-    static size_t cached_smem[kMaxDev] = {0};
+    static std::atomic<uint64_t> last[kMaxDev];  // smem << 32 | clusters
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return 0;
-    if (cached[dev] > 0 && cached_smem[dev] == smem) return cached[dev];
+    const uint64_t kept = last[dev].load(std::memory_order_relaxed);
+    if (kept >> 32 == smem && (uint32_t)kept > 0) return (int)(uint32_t)kept;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * 256);
     cfg.blockDim = dim3(X_THREADS);
@@ -846,8 +848,7 @@ int max_mx_clusters(size_t smem) {
         cudaGetLastError();
         return 0;
     }
-    cached[dev] = n;
-    cached_smem[dev] = smem;
+    last[dev].store((uint64_t)smem << 32 | (uint32_t)n, std::memory_order_relaxed);
     return n;
 }
 
