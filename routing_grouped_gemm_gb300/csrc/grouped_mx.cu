@@ -831,20 +831,20 @@ grouped_mx_kernel(const __grid_constant__ CUtensorMap tmT8, const __grid_constan
     }
 }
 
-// Clusters of two that fit at once on the current device (0 if none).  The last
-// answer is kept together with what it was for, in one word: threads launch at once.
+// Clusters of two that fit at once on the current device (0 if none), asked once
+// for the largest launch: one CTA takes an SM whatever the number of experts, by its
+// ring in shared memory as by its 512 columns of tensor memory.
 template <bool kGemm1, int kBN>
-int max_mx_clusters(size_t smem) {
+int max_mx_clusters() {
     constexpr int kMaxDev = 64;
-    static std::atomic<uint64_t> last[kMaxDev];  // smem << 32 | clusters
+    static std::atomic<int> cached[kMaxDev];  // threads launch at once
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return 0;
-    const uint64_t kept = last[dev].load(std::memory_order_relaxed);
-    if (kept >> 32 == smem && (uint32_t)kept > 0) return (int)(uint32_t)kept;
+    if (const int n = cached[dev].load(std::memory_order_relaxed)) return n;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * 256);
     cfg.blockDim = dim3(X_THREADS);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = X_SMEM_MAX;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
@@ -857,7 +857,7 @@ int max_mx_clusters(size_t smem) {
         cudaGetLastError();
         return 0;
     }
-    last[dev].store((uint64_t)smem << 32 | (uint32_t)n, std::memory_order_relaxed);
+    cached[dev].store(n, std::memory_order_relaxed);
     return n;
 }
 
@@ -885,9 +885,9 @@ cudaError_t launch_mx(const MxMaps &m, MxParams p, long long token_tiles, cudaSt
     while (mx_smem_bytes<kGemm1, kBN>(stages, p.E_local) > X_SMEM_MAX) --stages;
     p.stages = stages;
     const size_t smem = mx_smem_bytes<kGemm1, kBN>(stages, p.E_local);
-    cudaError_t e = ensure_smem((const void *)grouped_mx_kernel<kGemm1, kBN>, smem);
+    cudaError_t e = ensure_smem((const void *)grouped_mx_kernel<kGemm1, kBN>, X_SMEM_MAX);
     if (e != cudaSuccess) return e;
-    const int clusters = max_mx_clusters<kGemm1, kBN>(smem);
+    const int clusters = max_mx_clusters<kGemm1, kBN>();
     if (clusters <= 0) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (unsigned)std::min<long long>(clusters, token_tiles * p.nt));
