@@ -10,12 +10,14 @@
 // operand), and y once to fp16, as the other bf16 layers store it.
 //
 // At 4 bits the tensor cores take a K = 64 step in the time of a bf16 K = 16
-// one, so everything around them counts: decode calls run at the weights' HBM
-// time (256 experts' 5.9 GB in 853 us), long ones at 45% tensor pipe
-// (4096 tokens x 6, 64 experts of 2048 x 1408: 115 us, 3.7 PFLOP/s), held by
-// operands and scales from L2, the epilogue's stores and the launches' ends, no
-// one of which is worth more than a few percent by itself.  So, few operand
-// rows per product:
+// one, so everything around them counts.  Decode calls run at the weights' HBM
+// time (256 experts' 5.9 GB in 854 us).  A prompt of a few hundred rows per expert
+// (4096 tokens x 6, 64 experts of 2048 x 1408: 113 us, 3.8 PFLOP/s) has the tensor
+// pipe busy 45% of GEMM1 and 37% of GEMM2: about 14 us are the launches'
+// beginnings, the epilogue took 22 of 122 us when it was left out, operands and
+// scales from L2 up to 2 us each.  A long Zipf-skewed one (16384 tokens x 8, 64
+// experts of 4096 x 1536) takes 826 us, 6.0 PFLOP/s: 80% of four times the bf16
+// rate measured on the GPU.  So, few operand rows per product:
 //   * the weights are the M operand, 256 rows on a pair of CTAs
 //     (cta_group::2), and the tokens the N operand, up to 32, 144 or 208 of an
 //     expert's rows (the launch says when which), split evenly over its tiles in
@@ -960,9 +962,9 @@ cudaError_t launch_grouped_swiglu_mxfp4(const uint8_t *x_perm_q, const uint8_t *
     // is worth it where it costs no further tile: the smallest of 32, 144 and 208
     // that takes an average expert's rows (and a standard deviation more) in as
     // few tiles as 208.  Grouped call on GB300, by tile: a decode batch (4 rows
-    // per expert) 850 us with 32, 886 with 208; 8192 tokens over 256 experts (256
-    // rows) 1260 us with 144, 1356 with 208; fine-grained (384 rows) 138 us with
-    // 144, 123 with 208.
+    // per expert) 855 us with 32, 874 with 208; 8192 tokens over 256 experts (256
+    // rows) 1282 us with 144, 1331 with 208; fine-grained (384 rows) 138 us with
+    // 144, 113 with 208.
     const double rows = avg_rows + sqrt((double)avg_rows);
     auto tiles = [&](int bn) { return std::max(1LL, (long long)std::ceil(rows / bn)); };
     const int bn = tiles(32) == tiles(208) ? 32 : tiles(144) == tiles(208) ? 144 : 208;

@@ -451,8 +451,9 @@ permute_count_scan_kernel(const int *__restrict__ topk_idx, int T, int k, int E,
 // the block) + popc(mask & lanes below), or -1 past the segment's end (the
 // masked layout's capacity, flagged by the count kernel).  Then x[t] is read
 // once in 16-byte vectors and written to every row found -- or, for the FP8
-// dispatch (kFp8), quantised to e4m3 once with one scale per row and the
-// codes and scale written to every row found.  Warp t also writes -1 into
+// dispatch (COPY_E4M3), quantised to e4m3 once with one scale per row and the
+// codes and scale written to every row found (COPY_MXFP4: to MXFP4, with one
+// scale per 32 values).  Warp t also writes -1 into
 // token_of_row for the padding rows of local segments i = t, t + T, ... and
 // for its 32-row share of the rows after the last segment.
 constexpr int IC_UNROLL = 8;
