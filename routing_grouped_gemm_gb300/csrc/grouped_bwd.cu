@@ -279,7 +279,7 @@ bwd_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             }
             tc_commit_pair(drain, 0x1);
             volatile int local_abort = 0;
-            mbar_wait_bounded(drain, 0u, &local_abort);
+            if (!mbar_wait_bounded(drain, 0u, &local_abort)) *abort_flag = 1;
         }
     } else {
         // ---------------- epilogue (warps 2..5, both CTAs) ----------------

@@ -225,7 +225,7 @@ grouped_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
             // every MMA issued by this thread completes before TMEM is freed
             tc_commit(drain);
             volatile int local_abort = 0;
-            mbar_wait_bounded(drain, 0u, &local_abort);
+            if (!mbar_wait_bounded(drain, 0u, &local_abort)) *abort_flag = 1;
         }
     } else {
         // ---------------- epilogue (warps 2..5) ----------------

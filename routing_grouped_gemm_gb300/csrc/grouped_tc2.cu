@@ -427,7 +427,7 @@ grouped_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_consta
             // every MMA issued here completes before either CTA frees TMEM
             tc_commit_pair(drain, 0x1);
             volatile int local_abort = 0;
-            mbar_wait_bounded(drain, 0u, &local_abort);
+            if (!mbar_wait_bounded(drain, 0u, &local_abort)) *abort_flag = 1;
         }
     } else if (warp < 2 + P_EPI_WARPS) {
         // ---------------- epilogue (warps 2..5, both CTAs) ----------------

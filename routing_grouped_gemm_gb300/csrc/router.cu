@@ -442,7 +442,7 @@ router_logits_tc_kernel(const __grid_constant__ CUtensorMap tmX,
             // every MMA issued here completes before TMEM is freed, even if
             // the epilogue gave up waiting
             volatile int local_abort = 0;
-            mbar_wait_bounded(done, 0u, &local_abort);
+            if (!mbar_wait_bounded(done, 0u, &local_abort)) *abort_flag = 1;
         }
     } else if (warp < 6) {
         const int q = warp & 3;

@@ -5,6 +5,8 @@ out, so the rules of that path are checked where they are written."""
 import os
 import re
 
+import pytest
+
 SRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "routing_grouped_gemm_gb300",
                    "csrc", "grouped_mx.cu")
 VOTE = re.compile(r"__all_sync|__shfl_sync|__any_sync")
@@ -44,3 +46,13 @@ def test_no_wait_is_left_without_a_look_at_its_result():
     text, waits = _waits()
     for start, call, _ in waits:
         assert text[start:call].strip(), f"line {text.count(chr(10), 0, call) + 1}"
+
+
+@pytest.mark.parametrize("name", ["grouped_mx", "grouped_tc", "grouped_tc2", "grouped_bwd", "router"])
+def test_a_drain_that_runs_out_is_reported(name):
+    """The wait for the MMAs in flight before a CTA frees tensor memory, in every tcgen05 kernel."""
+    text = open(os.path.join(os.path.dirname(SRC), name + ".cu")).read()
+    waits = re.findall(r"^.*(?:wait_drained\(|mbar_wait_bounded\((?:drain|done), 0u, &local_abort).*$", text, re.M)
+    assert waits
+    for w in waits:
+        assert "wait_drained(" in w or w.strip().startswith("if (!") and w.strip().endswith("*abort_flag = 1;"), w
