@@ -253,6 +253,22 @@ def _stream(stream) -> int:
     return stream.cuda_stream
 
 
+def _at(t, name, stream) -> int:
+    """_stream(stream) for a call on t's device, which has to be the current one: the
+    library launches there."""
+    dev = torch.cuda.current_device()
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}: a call is made on the current device, cuda:{dev}")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _ws(ws, stream):
+    """What a call ends with: its workspace's address and size, and the stream."""
+    if ws is None:
+        raise ValueError("ws is required")
+    return _ptr(ws), ws.numel(), _at(ws, "ws", stream)
+
+
 def _check(st: int, what: str):
     if st != MOE_OK:
         raise MoeError(st, what)
@@ -626,7 +642,7 @@ def moe_quantize_rows_mxfp4(src, dst, scale, stream=None):
     sc = _arg(scale, (*src.shape[:-1], cols // 32), torch.uint8, "scale")
     if rows == 0:
         return
-    _check(_lib.moe_quantize_rows_mxfp4(src.data_ptr(), dt, rows, cols, q, sc, _stream(stream)),
+    _check(_lib.moe_quantize_rows_mxfp4(src.data_ptr(), dt, rows, cols, q, sc, _at(src, "src", stream)),
            "moe_quantize_rows_mxfp4")
 
 
@@ -638,7 +654,7 @@ def moe_dequantize_rows_mxfp4(codes, scale, dst, stream=None):
     sc = _arg(scale, (*dst.shape[:-1], cols // 32), torch.uint8, "scale")
     if rows == 0:
         return
-    _check(_lib.moe_dequantize_rows_mxfp4(q, sc, rows, cols, dst.data_ptr(), dt, _stream(stream)),
+    _check(_lib.moe_dequantize_rows_mxfp4(q, sc, rows, cols, dst.data_ptr(), dt, _at(dst, "dst", stream)),
            "moe_dequantize_rows_mxfp4")
 
 
@@ -666,7 +682,7 @@ def moe_permute_mxfp4(cfg: Config, x, topk_idx, tokens_per_expert, seg_offsets, 
         _arg(seg_offsets, (cfg.e_local + 1,), i32, "seg_offsets"),
         _arg(row_of, (T, k), i32, "row_of"), _arg(token_of_row, (ra,), i32, "token_of_row"),
         _arg(x_perm_q, (ra, D // 2), u8, "x_perm_q"), _arg(x_scale, (ra, D // 32), u8, "x_scale"),
-        _ptr(ws), ws.numel(), _stream(stream)), "moe_permute_mxfp4")
+        *_ws(ws, stream)), "moe_permute_mxfp4")
 
 
 def _mx_weights(cfg: Config, w1_q, w1_scale, w3_q, w3_scale, w2_q, w2_scale):
@@ -689,7 +705,7 @@ def moe_grouped_swiglu_mxfp4(cfg: Config, x_perm_q, x_scale, seg_offsets, tokens
         _arg(tokens_per_expert, (cfg.E,), i32, "tokens_per_expert"),
         *_mx_weights(cfg, w1_q, w1_scale, w3_q, w3_scale, w2_q, w2_scale),
         _arg(h_q, (ra, H // 2), u8, "h_q"), _arg(h_scale, (ra, H // 32), u8, "h_scale"),
-        _arg(y_perm, (ra, D), torch.float16, "y_perm"), _ptr(ws), ws.numel(), _stream(stream)),
+        _arg(y_perm, (ra, D), torch.float16, "y_perm"), *_ws(ws, stream)),
         "moe_grouped_swiglu_mxfp4")
 
 
@@ -701,7 +717,7 @@ def moe_layer_forward_mxfp4(cfg: Config, x, wg, bias, w1_q, w1_scale, w3_q, w3_s
         cfg.ref()[0], _arg(x, (cfg.T, cfg.D), bf, "x"), _arg(wg, (cfg.E, cfg.D), bf, "wg"),
         0 if bias is None else _arg(bias, (cfg.E,), torch.float32, "bias"),
         *_mx_weights(cfg, w1_q, w1_scale, w3_q, w3_scale, w2_q, w2_scale),
-        _arg(out, (cfg.T, cfg.D), bf, "out"), _ptr(ws), ws.numel(), _stream(stream)),
+        _arg(out, (cfg.T, cfg.D), bf, "out"), *_ws(ws, stream)),
         "moe_layer_forward_mxfp4")
 
 
@@ -715,7 +731,7 @@ def moe_unpermute_combine_backward(cfg: Config, dout, y_perm, row_of, topk_w, dy
         c, _arg(dout, (T, D), dt, "dout"), _arg(y_perm, (ra, D), cfg.y_dtype, "y_perm"),
         _arg(row_of, (T, k), torch.int32, "row_of"), _arg(topk_w, (T, k), torch.float32, "topk_w"),
         _arg(dy_perm, (ra, D), dt, "dy_perm"), _arg(dtopk_w, (T, k), torch.float32, "dtopk_w"),
-        _ptr(ws), ws.numel(), _stream(stream)), "moe_unpermute_combine_backward")
+        *_ws(ws, stream)), "moe_unpermute_combine_backward")
 
 
 def moe_permute_backward(cfg: Config, dx_perm, row_of, dx, ws, stream=None):
@@ -731,7 +747,7 @@ def moe_permute_backward(cfg: Config, dx_perm, row_of, dx, ws, stream=None):
         c, _arg(dx_perm, (ra, cfg.D), dx_perm.dtype, "dx_perm"),
         MOE_BF16 if dx_perm.dtype == torch.bfloat16 else MOE_F32,
         _arg(row_of, (cfg.T, cfg.k), torch.int32, "row_of"), _arg(dx, (cfg.T, cfg.D), dt, "dx"),
-        _ptr(ws), ws.numel(), _stream(stream)), "moe_permute_backward")
+        *_ws(ws, stream)), "moe_permute_backward")
 
 
 def moe_grouped_swiglu_gather(cfg: Config, x, token_of_row, seg_offsets, tokens_per_expert, w1,
