@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "launch.h"
@@ -15,13 +16,18 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t
                                   const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-void *driver_fn(const char *name) {
-    void *ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    return cudaGetDriverEntryPointByVersion(name, &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-                   q == cudaDriverEntryPointSuccess
-               ? ptr
-               : nullptr;
+// A driver function, looked up until it is found (threads may look at once).
+template <typename Fn>
+Fn driver_fn(const char *name, std::atomic<Fn> &kept) {
+    Fn fn = kept.load(std::memory_order_relaxed);
+    if (!fn) {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion(name, &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            kept.store(fn = reinterpret_cast<Fn>(ptr), std::memory_order_relaxed);
+    }
+    return fn;
 }
 
 // The driver's encoder, with a context current on this thread, which it needs and
@@ -29,9 +35,11 @@ void *driver_fn(const char *name) {
 // then, as a runtime call would take it.  (cudaSetDevice, since it is allowed
 // while a stream is captured.)
 EncodeTiledFn encode_fn() {
-    static const EncodeTiledFn fn = reinterpret_cast<EncodeTiledFn>(driver_fn("cuTensorMapEncodeTiled"));
     typedef CUresult (*CtxGetCurrentFn)(CUcontext *);
-    static const CtxGetCurrentFn current = reinterpret_cast<CtxGetCurrentFn>(driver_fn("cuCtxGetCurrent"));
+    static std::atomic<EncodeTiledFn> kept_encode{nullptr};
+    static std::atomic<CtxGetCurrentFn> kept_current{nullptr};
+    const EncodeTiledFn fn = driver_fn("cuTensorMapEncodeTiled", kept_encode);
+    const CtxGetCurrentFn current = driver_fn("cuCtxGetCurrent", kept_current);
     CUcontext ctx = nullptr;
     int dev = 0;
     if (current && current(&ctx) == CUDA_SUCCESS && !ctx &&
