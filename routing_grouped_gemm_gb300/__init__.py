@@ -253,13 +253,17 @@ def _stream(stream) -> int:
     return stream.cuda_stream
 
 
+_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _at(t, name, stream) -> int:
     """_stream(stream) for a call on t's device, which has to be the current one: the
     library launches there."""
-    dev = torch.cuda.current_device()
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}: a call is made on the current device, cuda:{dev}")
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    dev = t.get_device()
+    if dev < 0 or dev != _device():
+        raise ValueError(f"{name} is on {t.device}: a call is made on the current device")
+    return _raw_stream(dev) if stream is None else stream.cuda_stream
 
 
 def _ws(ws, stream):

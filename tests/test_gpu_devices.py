@@ -42,7 +42,7 @@ def test_another_device(moe, monkeypatch):
     calls = _calls(moe, torch.zeros(n, dtype=torch.uint8, device="cuda"))
     torch.cuda.synchronize()
     before, real = moe.kernel_launches(), torch.cuda.current_device()
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: real + 1)
+    monkeypatch.setattr(moe, "_device", lambda: real + 1)
     for name, call in calls.items():
         with pytest.raises(ValueError, match="current device"):
             call()
