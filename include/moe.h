@@ -114,7 +114,7 @@ const char *moe_last_error_string(void);
 
 /* ABI version: major * 10000 + minor * 100 + patch.  2.0.0 made y_perm of
  * bf16 layers fp16 (it was fp32 in 1.x); 2.1.0 added the MXFP4 calls and the
- * gradients of the permute and combine steps. */
+ * gradients of the permute and combine steps; 2.2.0 the norms around a block. */
 int32_t moe_abi_version(void);
 
 /*
@@ -627,6 +627,107 @@ moe_status moe_permute_noalloc(const moe_config *cfg, const void *x, const int32
                                int32_t *tokens_per_expert, int32_t *seg_offsets,
                                int32_t *row_of, int32_t *token_of_row, void *x_perm,
                                int32_t *device_flags, moe_stream_t stream);
+
+/*
+ * The norms around a block, fused with its gate, its dropout and the residual
+ * sum (no counterpart in the pages: what a caller has between two blocks).
+ * Per row, in fp32:
+ *   v = y rsqrt(mean(y^2) + eps) post_gain      (y itself without post_gain)
+ *   s = res_scale resid + branch_scale gate keep v          -> resid_out
+ *   n = s rsqrt(mean(s^2) + eps) pre_gain                   -> norm_out
+ * s and n are rounded once each to dtype; n is the norm of the unrounded s.
+ * The mean squares are fp32: a row whose squares pass its range (values of
+ * about 1e19) is divided down to zeros.
+ *
+ *   T, D       rows and columns, T >= 0; D a multiple of 8 up to 32768 (wider:
+ *              MOE_ERR_UNSUPPORTED)
+ *   dtype      moe_dtype of resid, y, the gains, an element or channel gate and
+ *              the outputs
+ *   gate       moe_gate: MOE_GATE_CHANNEL gate [D], MOE_GATE_TOKEN gate [T]
+ *              fp32, MOE_GATE_ELEMENT gate [T, D]
+ *   eps        positive; res_scale, branch_scale: finite
+ *   p_drop     probability, in [0, 1), that an element of v is dropped, taken
+ *              to the nearest multiple of 2^-16 (at least 2^-16 below 1)
+ *
+ * Dropout.  keep is 0 or 1 / (1 - p_drop) and never stored: element c of row t
+ * is element i mod 8 of vector i / 8, i = t D + c, and takes half word i mod 8
+ * (the low half of a word first) of the four words that Philox4x32 with ten
+ * rounds (Salmon et al., "Parallel random numbers: as easy as 1, 2, 3", 2011)
+ * gives for the counter (i / 8, offset) under the key seed, each 64 bits, low
+ * word first; it stays when that half word is at least 65536 p_drop.  rng
+ * [2] int64 = {seed, offset} is device memory, 8-byte aligned, read when the
+ * kernel runs, so a captured graph takes what it holds at the replay; NULL
+ * allowed without dropout.  The caller moves offset on from call to call.
+ */
+typedef enum {
+    MOE_GATE_NONE = 0,
+    MOE_GATE_CHANNEL = 1,
+    MOE_GATE_TOKEN = 2,
+    MOE_GATE_ELEMENT = 3
+} moe_gate;
+
+typedef struct {
+    int32_t T, D, dtype, gate;
+    float eps, res_scale, branch_scale, p_drop;
+} moe_residual_config;
+
+/*
+ * resid [T, D]; y [T, D], or NULL: no branch -- s is resid, resid_out is NULL,
+ * and post_gain, gate and dropout are left out (the norm in front of the first
+ * block); post_gain [D] or NULL; pre_gain [D] with norm_out [T, D], or both
+ * NULL.  resid_out may be resid (in place) and norm_out may be y; otherwise
+ * inputs and outputs do not overlap.
+ */
+moe_status moe_residual_norm(const moe_residual_config *rc, const void *resid, const void *y,
+                             const void *post_gain, const void *gate, const void *pre_gain,
+                             const int64_t *rng, void *resid_out, void *norm_out,
+                             moe_stream_t stream);
+
+/*
+ * moe_unpermute_combine and moe_residual_norm in one pass: y is the weighted
+ * sum of a token's rows of y_perm (arguments and flags as moe_unpermute_combine,
+ * summed in fp32 in slot order), not rounded on the way to v.  y_out [T, D]
+ * (dtype): y rounded once, for the gradient; or NULL.  cfg and rc have the same
+ * T, D and dtype.  ws: moe_workspace_size(cfg).
+ */
+moe_status moe_combine_residual_norm(const moe_config *cfg, const moe_residual_config *rc,
+                                     const void *y_perm, const int32_t *row_of,
+                                     const float *topk_w, const void *resid,
+                                     const void *post_gain, const void *gate,
+                                     const void *pre_gain, const int64_t *rng, void *y_out,
+                                     void *resid_out, void *norm_out, void *ws, size_t ws_bytes,
+                                     moe_stream_t stream);
+
+/* Workspace bytes of moe_residual_norm_backward (-1: bad config).  It needs no
+ * zero-filling, and nothing in it lasts from one call to the next. */
+int64_t moe_residual_workspace_size(const moe_residual_config *rc);
+
+/*
+ * Gradient of moe_residual_norm.  s [T, D]: its resid_out (its resid, when y
+ * was NULL); y, post_gain, gate, pre_gain and rng as the forward had them (of
+ * moe_combine_residual_norm: its y_out as y).  dresid_out, dnorm_out [T, D]:
+ * the gradients of resid_out and norm_out; dresid_out may be NULL (zeros) when
+ * pre_gain is given, dnorm_out is NULL without pre_gain.  With r1, r2 the rows'
+ * rsqrt factors, g = dnorm_out pre_gain, means over the row and sums over rows:
+ *   ds = dresid_out + r2 (g - s r2^2 mean(g s)),   dpre_gain = sum dnorm_out s r2
+ *   dresid = res_scale ds                          (ds itself without y)
+ *   u = branch_scale keep ds,                      dgate = u v summed as gate is shared
+ *   dv = gate u,                                   dpost_gain = sum dv y r1
+ *   dy = r1 (dv post_gain - y r1^2 mean(dv post_gain y))   (dv without post_gain)
+ * dresid, dy [T, D] (dtype; dy NULL without y); dpost_gain, dpre_gain [D] fp32,
+ * given exactly with their gains; dgate: [D] fp32 (MOE_GATE_CHANNEL), [T] fp32
+ * (MOE_GATE_TOKEN), [T, D] dtype (MOE_GATE_ELEMENT), else NULL.  All are
+ * overwritten; with T = 0 the sums are zero.  dresid may be dresid_out or
+ * dnorm_out, and dy may be the other one; otherwise inputs and outputs do not
+ * overlap.  Sums run in a fixed order: results are bit-identical run to run.
+ */
+moe_status moe_residual_norm_backward(const moe_residual_config *rc, const void *s, const void *y,
+                                      const void *post_gain, const void *gate,
+                                      const void *pre_gain, const int64_t *rng,
+                                      const void *dresid_out, const void *dnorm_out, void *dresid,
+                                      void *dy, float *dpost_gain, void *dgate,
+                                      float *dpre_gain, void *ws, size_t ws_bytes,
+                                      moe_stream_t stream);
 
 /*
  * Synchronises `stream`, reads the workspace status word, clears it and

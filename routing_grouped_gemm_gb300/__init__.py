@@ -24,6 +24,7 @@ MOE_ERR_CUDA, MOE_ERR_TIMEOUT, MOE_ERR_BAD_ROUTING, MOE_ERR_WORKSPACE = 4, 5, 6,
 MOE_F32, MOE_BF16 = 0, 1
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_LAYOUT_CONTIGUOUS, MOE_LAYOUT_MASKED = 0, 1
+MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN, MOE_GATE_ELEMENT = 0, 1, 2, 3
 
 # every symbol include/moe.h declares
 ABI_SYMBOLS = (
@@ -41,6 +42,8 @@ ABI_SYMBOLS = (
     "moe_quantize_rows_mxfp4", "moe_dequantize_rows_mxfp4", "moe_permute_mxfp4",
     "moe_grouped_swiglu_mxfp4", "moe_layer_forward_mxfp4",
     "moe_unpermute_combine_backward", "moe_permute_backward",
+    "moe_residual_norm", "moe_combine_residual_norm", "moe_residual_workspace_size",
+    "moe_residual_norm_backward",
 )
 
 
@@ -56,6 +59,11 @@ class moe_config(ctypes.Structure):
         "layout", "align_m", "capacity", "n_group", "topk_group")]
 
 
+class moe_residual_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "D", "dtype", "gate")] + \
+        [(n, ctypes.c_float) for n in ("eps", "res_scale", "branch_scale", "p_drop")]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -64,6 +72,7 @@ def _load() -> ctypes.CDLL:
     lib = ctypes.CDLL(LIB_PATH)
     P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     C = ctypes.POINTER(moe_config)
+    R = ctypes.POINTER(moe_residual_config)
     sig = {
         "moe_status_string": (ctypes.c_char_p, [I32]),
         "moe_last_error_string": (ctypes.c_char_p, []),
@@ -106,6 +115,10 @@ def _load() -> ctypes.CDLL:
         "moe_layer_forward_mxfp4": (I32, [C, P, P, P, P, P, P, P, P, P, P, P, SZ, P]),
         "moe_unpermute_combine_backward": (I32, [C, P, P, P, P, P, P, P, SZ, P]),
         "moe_permute_backward": (I32, [C, P, I32, P, P, P, SZ, P]),
+        "moe_residual_norm": (I32, [R, P, P, P, P, P, P, P, P, P]),
+        "moe_combine_residual_norm": (I32, [C, R, P, P, P, P, P, P, P, P, P, P, P, P, SZ, P]),
+        "moe_residual_workspace_size": (I64, [R]),
+        "moe_residual_norm_backward": (I32, [R, P, P, P, P, P, P, P, P, P, P, P, P, P, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -175,6 +188,27 @@ class Config:
         return torch.float16 if self.dtype == MOE_BF16 else torch.float32
 
 
+@dataclass
+class ResidualConfig:
+    """The norms around a block, its gate, its dropout and the residual sum (moe_residual_norm)."""
+    T: int
+    D: int
+    dtype: int = MOE_BF16
+    gate: int = MOE_GATE_NONE
+    eps: float = 1e-6
+    res_scale: float = 1.0
+    branch_scale: float = 1.0
+    p_drop: float = 0.0
+
+    def c(self) -> moe_residual_config:
+        return moe_residual_config(self.T, self.D, self.dtype, self.gate, self.eps, self.res_scale,
+                                   self.branch_scale, self.p_drop)
+
+    @property
+    def torch_dtype(self) -> torch.dtype:
+        return torch.bfloat16 if self.dtype == MOE_BF16 else torch.float32
+
+
 def status_string(st: int) -> str:
     return _lib.moe_status_string(int(st)).decode()
 
@@ -235,6 +269,18 @@ def alloc_workspace(cfg: Config, layer: bool = False, device="cuda", host: bool 
     return torch.zeros(max(n, 256), dtype=torch.uint8, device=device)
 
 
+def residual_workspace_size(rc: ResidualConfig) -> int:
+    return int(_lib.moe_residual_workspace_size(ctypes.byref(rc.c())))
+
+
+def alloc_residual_workspace(rc: ResidualConfig, device="cuda") -> torch.Tensor:
+    """Workspace of moe_residual_norm_backward (torch-owned)."""
+    n = residual_workspace_size(rc)
+    if n < 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, "workspace size")
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
 # --------------------------------------------------------------------------
 # marshalling helpers
 # --------------------------------------------------------------------------
@@ -271,6 +317,11 @@ def _ws(ws, stream):
     if ws is None:
         raise ValueError("ws is required")
     return _ptr(ws), ws.numel(), _at(ws, "ws", stream)
+
+
+def _maybe(t, shape, dtype, name) -> int:
+    """_arg of a tensor that may be left out."""
+    return 0 if t is None else _arg(t, shape, dtype, name)
 
 
 def _check(st: int, what: str):
@@ -853,3 +904,77 @@ def layer_views(cfg: Config, ws: torch.Tensor) -> dict:
             out["x_perm_q"] = ws[off:off + ra * cfg.D].view(ra, cfg.D)
         off += up(region)
     return out
+
+
+# --------------------------------------------------------------------------
+# the norms around a block
+# --------------------------------------------------------------------------
+
+def _gate_form(rc):
+    """Shape and type of the gate, or None."""
+    return {MOE_GATE_CHANNEL: ((rc.D,), rc.torch_dtype), MOE_GATE_TOKEN: ((rc.T,), torch.float32),
+            MOE_GATE_ELEMENT: ((rc.T, rc.D), rc.torch_dtype)}.get(rc.gate)
+
+
+def _gate_arg(rc, gate) -> int:
+    form = _gate_form(rc)
+    if form is None:
+        if gate is not None:
+            raise ValueError("gate: the config names no kind of gate")
+        return 0
+    return _arg(gate, *form, "gate")
+
+
+def moe_residual_norm(rc: ResidualConfig, resid, y, post_gain, gate, pre_gain, rng, resid_out,
+                      norm_out, stream=None):
+    """Norm, dropout, gate and residual sum at the end of a block, and the norm in front of the next:
+    s = res_scale resid + branch_scale gate drop(norm(y) post_gain), n = norm(s) pre_gain.
+
+    post_gain, gate, pre_gain (with norm_out) and rng may be None; without y (and resid_out) it is
+    the norm of resid alone."""
+    td, dt = (rc.T, rc.D), rc.torch_dtype
+    _check(_lib.moe_residual_norm(
+        ctypes.byref(rc.c()), _arg(resid, td, dt, "resid"), _maybe(y, td, dt, "y"),
+        _maybe(post_gain, (rc.D,), dt, "post_gain"), _gate_arg(rc, gate),
+        _maybe(pre_gain, (rc.D,), dt, "pre_gain"), _maybe(rng, (2,), torch.int64, "rng"),
+        _maybe(resid_out, td, dt, "resid_out"), _maybe(norm_out, td, dt, "norm_out"),
+        _at(resid, "resid", stream)), "moe_residual_norm")
+
+
+def moe_combine_residual_norm(cfg: Config, rc: ResidualConfig, y_perm, row_of, topk_w, resid,
+                              post_gain, gate, pre_gain, rng, y_out, resid_out, norm_out, ws,
+                              stream=None):
+    """moe_unpermute_combine and moe_residual_norm in one pass; y_out (or None) takes the combined
+    rows, which the gradient needs."""
+    c, ra = cfg.ref()
+    td, tk, dt = (rc.T, rc.D), (cfg.T, cfg.k), rc.torch_dtype
+    p, n, s = _ws(ws, stream)
+    _check(_lib.moe_combine_residual_norm(
+        c, ctypes.byref(rc.c()), _arg(y_perm, (ra, cfg.D), cfg.y_dtype, "y_perm"),
+        _arg(row_of, tk, torch.int32, "row_of"), _arg(topk_w, tk, torch.float32, "topk_w"),
+        _arg(resid, td, dt, "resid"), _maybe(post_gain, (rc.D,), dt, "post_gain"),
+        _gate_arg(rc, gate), _maybe(pre_gain, (rc.D,), dt, "pre_gain"),
+        _maybe(rng, (2,), torch.int64, "rng"), _maybe(y_out, td, dt, "y_out"),
+        _arg(resid_out, td, dt, "resid_out"), _maybe(norm_out, td, dt, "norm_out"), p, n, s),
+        "moe_combine_residual_norm")
+
+
+def moe_residual_norm_backward(rc: ResidualConfig, s, y, post_gain, gate, pre_gain, rng, dresid_out,
+                               dnorm_out, dresid, dy, dpost_gain, dgate, dpre_gain, ws, stream=None):
+    """Gradient of moe_residual_norm: dresid and dy from dresid_out and dnorm_out, the gains' and a
+    shared gate's in fp32.  s is the forward's resid_out (its resid where it had no y)."""
+    td, dt, f32 = (rc.T, rc.D), rc.torch_dtype, torch.float32
+    form = _gate_form(rc)
+    if form is None and dgate is not None:
+        raise ValueError("dgate: the config names no kind of gate")
+    p, n, st = _ws(ws, stream)
+    _check(_lib.moe_residual_norm_backward(
+        ctypes.byref(rc.c()), _arg(s, td, dt, "s"), _maybe(y, td, dt, "y"),
+        _maybe(post_gain, (rc.D,), dt, "post_gain"), _gate_arg(rc, gate),
+        _maybe(pre_gain, (rc.D,), dt, "pre_gain"), _maybe(rng, (2,), torch.int64, "rng"),
+        _maybe(dresid_out, td, dt, "dresid_out"), _maybe(dnorm_out, td, dt, "dnorm_out"),
+        _arg(dresid, td, dt, "dresid"), _maybe(dy, td, dt, "dy"),
+        _maybe(dpost_gain, (rc.D,), f32, "dpost_gain"),
+        0 if form is None else _arg(dgate, form[0], form[1] if rc.gate == MOE_GATE_ELEMENT else f32,
+                                    "dgate"),
+        _maybe(dpre_gain, (rc.D,), f32, "dpre_gain"), p, n, st), "moe_residual_norm_backward")

@@ -255,4 +255,32 @@ cudaError_t launch_grouped_swiglu_bf16(const void *x_perm, const int *seg_offset
                                        int D, int H_local, int e_first, int E_local,
                                        int64_t rows_alloc, int *status, cudaStream_t stream);
 
+// The norms around a block with its gate, dropout and residual sum (rows of D
+// values, D a multiple of 8 up to kResidualMaxD).  gate_kind: 0 none, 1 [D],
+// 2 [T] fp32, 3 [T, D]; drop_cut: the dropout's probability in 1 / 65536, with
+// rng = {seed, offset} on the device.
+constexpr int kResidualMaxD = 32768;
+struct ResidualNorm {
+    int T, D, is_bf16, gate_kind, drop_cut;
+    float eps, res_scale, branch_scale;
+    const void *post, *gate, *pre;  // post, pre null: that norm is left out
+    const int64_t *rng;
+};
+cudaError_t launch_residual_norm(const ResidualNorm &r, const void *resid, const void *y,
+                                 void *resid_out, void *norm_out, cudaStream_t stream);
+// The same behind the combine of y_perm's rows (see launch_combine); y_out: the
+// combined rows too, or null.
+cudaError_t launch_combine_residual_norm(const ResidualNorm &r, const void *y_perm,
+                                         const int *row_of, const float *topk_w, int k,
+                                         int64_t rows_alloc, const void *resid, void *y_out,
+                                         void *resid_out, void *norm_out, int *status,
+                                         cudaStream_t stream);
+// Gradient; `part`: 3 * residual_parts(T, D) * D floats for the CTAs' sums of
+// the gains' and the gate's gradients.
+int residual_parts(int T, int D);
+cudaError_t launch_residual_norm_backward(const ResidualNorm &r, const void *s, const void *y,
+                                          const void *dresid_out, const void *dnorm_out,
+                                          void *dresid, void *dy, float *dpost, void *dgate,
+                                          float *dpre, float *part, cudaStream_t stream);
+
 }  // namespace moe

@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <math.h>
 #include <stdint.h>
 #include <stdio.h>
 #include <stdlib.h>
@@ -19,8 +20,9 @@
 namespace {
 
 // 2.0.0: y_perm of bf16 layers is fp16 (fp32 up to 1.5.0); 2.1.0 adds the
-// MXFP4 calls and the gradients of the permute and combine steps
-constexpr int32_t kAbiVersion = 20100;
+// MXFP4 calls and the gradients of the permute and combine steps; 2.2.0 adds
+// the norms around a block
+constexpr int32_t kAbiVersion = 20200;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 32;
 constexpr int64_t kAlign = 256;
@@ -1233,4 +1235,151 @@ MOE_EXPORT moe_status moe_get_device_status(const void *ws, size_t ws_bytes, moe
     if (host[0] & moe::FLAG_CAPACITY) return MOE_ERR_CAPACITY;
     if (host[0] & moe::FLAG_BAD_ROUTING) return MOE_ERR_BAD_ROUTING;
     return MOE_OK;
+}
+
+// ---------------------------------------------------------------------
+// The norms around a block
+// ---------------------------------------------------------------------
+static moe_status validate_residual(const moe_residual_config *r) {
+    if (!r) return arg_fail("residual config is NULL");
+    if (r->T < 0) return arg_fail("T < 0");
+    if (r->D < 8 || r->D % 8) return arg_fail("D must be a positive multiple of 8");
+    if (r->D > moe::kResidualMaxD)
+        return arg_fail("moe_residual_norm: D above 32768", MOE_ERR_UNSUPPORTED);
+    if (r->dtype != MOE_F32 && r->dtype != MOE_BF16) return arg_fail("unknown dtype");
+    if (r->gate < MOE_GATE_NONE || r->gate > MOE_GATE_ELEMENT) return arg_fail("unknown gate");
+    if (!(r->eps > 0.f) || !isfinite(r->eps)) return arg_fail("eps must be positive");
+    if (!isfinite(r->res_scale) || !isfinite(r->branch_scale))
+        return arg_fail("res_scale and branch_scale must be finite");
+    if (!(r->p_drop >= 0.f && r->p_drop < 1.f) || lrintf(r->p_drop * 65536.f) > 65535)
+        return arg_fail("p_drop must be in [0, 1), at least 2^-16 below 1");
+    return MOE_OK;
+}
+
+static moe::ResidualNorm residual_of(const moe_residual_config *r, const void *post,
+                                     const void *gate, const void *pre, const int64_t *rng) {
+    moe::ResidualNorm n;
+    n.T = r->T;
+    n.D = r->D;
+    n.is_bf16 = r->dtype == MOE_BF16;
+    n.gate_kind = r->gate;
+    n.drop_cut = (int)lrintf(r->p_drop * 65536.f);
+    n.eps = r->eps;
+    n.res_scale = r->res_scale;
+    n.branch_scale = r->branch_scale;
+    n.post = post;
+    n.gate = gate;
+    n.pre = pre;
+    n.rng = rng;
+    return n;
+}
+
+// The operands that say what the branch does; `y`: it has one.
+static moe_status check_branch(const moe_residual_config *r, const void *y, const void *post,
+                               const void *gate, const int64_t *rng) {
+    const bool drop = lrintf(r->p_drop * 65536.f) > 0;
+    if (!y && (post || gate || r->gate != MOE_GATE_NONE || drop))
+        return arg_fail("a post gain, a gate or dropout without y");
+    if (post && !need16(post)) return arg_fail("post_gain misaligned");
+    if ((r->gate != MOE_GATE_NONE) != (gate != nullptr))
+        return arg_fail("gate must be given exactly when the config names its kind");
+    if (gate && !need16(gate)) return arg_fail("gate misaligned");
+    if (drop && (!rng || !aligned(rng, 8))) return arg_fail("rng is NULL or misaligned");
+    return MOE_OK;
+}
+
+MOE_EXPORT moe_status moe_residual_norm(const moe_residual_config *rc, const void *resid,
+                                        const void *y, const void *post_gain, const void *gate,
+                                        const void *pre_gain, const int64_t *rng, void *resid_out,
+                                        void *norm_out, moe_stream_t stream) {
+    moe_status st = validate_residual(rc);
+    if (st != MOE_OK) return st;
+    if (rc->T == 0) return MOE_OK;
+    if (!need16(resid)) return arg_fail("resid is NULL or misaligned");
+    if (y && !need16(y)) return arg_fail("y misaligned");
+    st = check_branch(rc, y, post_gain, gate, rng);
+    if (st != MOE_OK) return st;
+    if (y ? !need16(resid_out) : resid_out != nullptr)
+        return arg_fail("resid_out must be given (16-byte aligned) with y and NULL without it");
+    if (pre_gain ? !need16(pre_gain) || !need16(norm_out) : norm_out != nullptr)
+        return arg_fail("pre_gain and norm_out go together, 16-byte aligned");
+    if (!y && !pre_gain) return arg_fail("neither y nor pre_gain: nothing to do");
+    const cudaError_t e = moe::launch_residual_norm(residual_of(rc, post_gain, gate, pre_gain, rng),
+                                                    resid, y, resid_out, norm_out, (cudaStream_t)stream);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_residual_norm");
+}
+
+MOE_EXPORT moe_status moe_combine_residual_norm(
+    const moe_config *cfg, const moe_residual_config *rc, const void *y_perm, const int32_t *row_of,
+    const float *topk_w, const void *resid, const void *post_gain, const void *gate,
+    const void *pre_gain, const int64_t *rng, void *y_out, void *resid_out, void *norm_out, void *ws,
+    size_t ws_bytes, moe_stream_t stream) {
+    moe_status st = validate(cfg);
+    if (st != MOE_OK) return st;
+    st = validate_residual(rc);
+    if (st != MOE_OK) return st;
+    if (rc->T != cfg->T || rc->D != cfg->D || rc->dtype != cfg->dtype)
+        return arg_fail("the two configs differ in T, D or dtype");
+    StepWs w;
+    st = carve_step(cfg, ws, ws_bytes, &w);
+    if (st != MOE_OK) return st;
+    if (cfg->T == 0) return MOE_OK;
+    if (!need16(row_of) || !need16(topk_w)) return arg_fail("row_of or topk_w is NULL or misaligned");
+    if (rows_alloc_of(cfg) > 0 && !need16(y_perm)) return arg_fail("y_perm is NULL or misaligned");
+    if (!need16(resid) || !need16(resid_out)) return arg_fail("resid or resid_out is NULL or misaligned");
+    if (y_out && !need16(y_out)) return arg_fail("y_out misaligned");
+    st = check_branch(rc, row_of, post_gain, gate, rng);
+    if (st != MOE_OK) return st;
+    if (pre_gain ? !need16(pre_gain) || !need16(norm_out) : norm_out != nullptr)
+        return arg_fail("pre_gain and norm_out go together, 16-byte aligned");
+    const cudaError_t e = moe::launch_combine_residual_norm(
+        residual_of(rc, post_gain, gate, pre_gain, rng), y_perm, row_of, topk_w, cfg->k,
+        rows_alloc_of(cfg), resid, y_out, resid_out, norm_out, &w.status->flags, (cudaStream_t)stream);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_combine_residual_norm");
+}
+
+MOE_EXPORT int64_t moe_residual_workspace_size(const moe_residual_config *rc) {
+    if (validate_residual(rc) != MOE_OK) return -1;
+    return align_up((int64_t)3 * 4 * moe::residual_parts(rc->T, rc->D) * rc->D);
+}
+
+MOE_EXPORT moe_status moe_residual_norm_backward(
+    const moe_residual_config *rc, const void *s, const void *y, const void *post_gain,
+    const void *gate, const void *pre_gain, const int64_t *rng, const void *dresid_out,
+    const void *dnorm_out, void *dresid, void *dy, float *dpost_gain, void *dgate, float *dpre_gain,
+    void *ws, size_t ws_bytes, moe_stream_t stream) {
+    moe_status st = validate_residual(rc);
+    if (st != MOE_OK) return st;
+    if (rc->T > 0) {
+        if (!need16(s)) return arg_fail("s is NULL or misaligned");
+        if (y && !need16(y)) return arg_fail("y misaligned");
+        st = check_branch(rc, y, post_gain, gate, rng);
+        if (st != MOE_OK) return st;
+        if (pre_gain ? !need16(pre_gain) || !need16(dnorm_out) : dnorm_out != nullptr)
+            return arg_fail("pre_gain and dnorm_out go together, 16-byte aligned");
+        if (dresid_out && !need16(dresid_out)) return arg_fail("dresid_out misaligned");
+        if (!dresid_out && !pre_gain) return arg_fail("neither dresid_out nor dnorm_out is given");
+        if (!y && !pre_gain) return arg_fail("neither y nor pre_gain: nothing to do");
+        if (!need16(dresid)) return arg_fail("dresid is NULL or misaligned");
+        if (y ? !need16(dy) : dy != nullptr)
+            return arg_fail("dy must be given (16-byte aligned) with y and NULL without it");
+    }
+    if (post_gain ? !need16(dpost_gain) : dpost_gain != nullptr)
+        return arg_fail("post_gain and dpost_gain go together, 16-byte aligned");
+    if (rc->gate != MOE_GATE_NONE ? !need16(dgate) && (rc->T > 0 || rc->gate == MOE_GATE_CHANNEL)
+                                  : dgate != nullptr)
+        return arg_fail("gate and dgate go together, 16-byte aligned");
+    if (pre_gain ? !need16(dpre_gain) : dpre_gain != nullptr)
+        return arg_fail("pre_gain and dpre_gain go together, 16-byte aligned");
+    if (rc->T > 0) {
+        if (!ws) return arg_fail("workspace is NULL", MOE_ERR_WORKSPACE);
+        if (!aligned(ws, kAlign))
+            return arg_fail("workspace must be 256-byte aligned", MOE_ERR_WORKSPACE);
+        if ((int64_t)ws_bytes < moe_residual_workspace_size(rc))
+            return arg_fail("workspace too small", MOE_ERR_WORKSPACE);
+    }
+    const cudaError_t e = moe::launch_residual_norm_backward(
+        residual_of(rc, post_gain, gate, pre_gain, rng), s, y, dresid_out, dnorm_out, dresid, dy,
+        dpost_gain, dgate, dpre_gain, static_cast<float *>(ws), (cudaStream_t)stream);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_residual_norm_backward");
 }
