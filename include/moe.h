@@ -114,7 +114,8 @@ const char *moe_last_error_string(void);
 
 /* ABI version: major * 10000 + minor * 100 + patch.  2.0.0 made y_perm of
  * bf16 layers fp16 (it was fp32 in 1.x); 2.1.0 added the MXFP4 calls and the
- * gradients of the permute and combine steps; 2.2.0 the norms around a block. */
+ * gradients of the permute and combine steps; 2.2.0 the norms around a block
+ * and the layer for a few tokens. */
 int32_t moe_abi_version(void);
 
 /*
@@ -627,6 +628,29 @@ moe_status moe_permute_noalloc(const moe_config *cfg, const void *x, const int32
                                int32_t *tokens_per_expert, int32_t *seg_offsets,
                                int32_t *row_of, int32_t *token_of_row, void *x_perm,
                                int32_t *device_flags, moe_stream_t stream);
+
+/*
+ * moe_layer_forward for 1 to 32 tokens (decode steps, drafted tokens) in one
+ * kernel launch (no counterpart in the pages): every step of the layer in one
+ * cooperative grid, and the chosen experts' weights read once.  More tokens:
+ * MOE_ERR_UNSUPPORTED (use moe_layer_forward).  Same arguments as
+ * moe_layer_forward, fp32 or bf16, any expert range and H shard; cfg's layout,
+ * align_m and capacity play no part.  out is rounded once from fp32 sums (no
+ * fp16 y_perm lies between, so its range does not bound y), h once to dtype; a
+ * NaN key is flagged as by moe_route_topk.  Differs from moe_layer_forward by
+ * rounding only, but a near tie of two keys may fall the other way.  Results
+ * are bit-identical run to run on one device.
+ *
+ * ws: moe_layer_few_workspace_size(cfg) (-1: bad config or T above 32),
+ * zero-filled once.  Its layout depends on cfg, so one workspace serves calls
+ * of one config; calls that share it must not run concurrently (two captured
+ * graphs included).  Capture into a graph once a first call has run outside.
+ */
+int64_t moe_layer_few_workspace_size(const moe_config *cfg);
+moe_status moe_layer_forward_few(const moe_config *cfg, const void *x, const void *wg,
+                                 const float *bias, const void *w1, const void *w3,
+                                 const void *w2, void *out, void *ws, size_t ws_bytes,
+                                 moe_stream_t stream);
 
 /*
  * The norms around a block, fused with its gate, its dropout and the residual

@@ -42,6 +42,7 @@ ABI_SYMBOLS = (
     "moe_quantize_rows_mxfp4", "moe_dequantize_rows_mxfp4", "moe_permute_mxfp4",
     "moe_grouped_swiglu_mxfp4", "moe_layer_forward_mxfp4",
     "moe_unpermute_combine_backward", "moe_permute_backward",
+    "moe_layer_few_workspace_size", "moe_layer_forward_few",
     "moe_residual_norm", "moe_combine_residual_norm", "moe_residual_workspace_size",
     "moe_residual_norm_backward",
 )
@@ -115,6 +116,8 @@ def _load() -> ctypes.CDLL:
         "moe_layer_forward_mxfp4": (I32, [C, P, P, P, P, P, P, P, P, P, P, P, SZ, P]),
         "moe_unpermute_combine_backward": (I32, [C, P, P, P, P, P, P, P, SZ, P]),
         "moe_permute_backward": (I32, [C, P, I32, P, P, P, SZ, P]),
+        "moe_layer_few_workspace_size": (I64, [C]),
+        "moe_layer_forward_few": (I32, [C, P, P, P, P, P, P, P, P, SZ, P]),
         "moe_residual_norm": (I32, [R, P, P, P, P, P, P, P, P, P]),
         "moe_combine_residual_norm": (I32, [C, R, P, P, P, P, P, P, P, P, P, P, P, P, SZ, P]),
         "moe_residual_workspace_size": (I64, [R]),
@@ -255,13 +258,19 @@ def layer_train_workspace_size(cfg: Config) -> int:
     return int(_lib.moe_layer_train_workspace_size(ctypes.byref(c)))
 
 
+def layer_few_workspace_size(cfg: Config) -> int:
+    c = cfg.c()
+    return int(_lib.moe_layer_few_workspace_size(ctypes.byref(c)))
+
+
 def alloc_workspace(cfg: Config, layer: bool = False, device="cuda", host: bool = False,
-                    train: bool = False) -> torch.Tensor:
+                    train: bool = False, few: bool = False) -> torch.Tensor:
     """Zero-filled workspace of the size the library asks for (torch-owned).
 
     layer: for moe_layer_forward; host: for moe_layer_forward_host; train: for
-    moe_layer_forward_train / moe_layer_backward."""
-    n = (layer_train_workspace_size(cfg) if train else
+    moe_layer_forward_train / moe_layer_backward; few: for moe_layer_forward_few."""
+    n = (layer_few_workspace_size(cfg) if few else
+         layer_train_workspace_size(cfg) if train else
          layer_host_workspace_size(cfg) if host else
          layer_workspace_size(cfg) if layer else workspace_size(cfg))
     if n < 0:
@@ -904,6 +913,17 @@ def layer_views(cfg: Config, ws: torch.Tensor) -> dict:
             out["x_perm_q"] = ws[off:off + ra * cfg.D].view(ra, cfg.D)
         off += up(region)
     return out
+
+
+def moe_layer_forward_few(cfg: Config, x, wg, bias, w1, w3, w2, out, ws, stream=None):
+    """moe_layer_forward for at most 32 tokens, in one launch; ws: alloc_workspace(cfg, few=True)."""
+    dt, td, hd = cfg.torch_dtype, (cfg.T, cfg.D), (cfg.e_local, cfg.H_local, cfg.D)
+    p, n, s = _ws(ws, stream)
+    _check(_lib.moe_layer_forward_few(
+        cfg.ref()[0], _arg(x, td, dt, "x"), _arg(wg, (cfg.E, cfg.D), dt, "wg"),
+        _maybe(bias, (cfg.E,), torch.float32, "bias"), _arg(w1, hd, dt, "w1"), _arg(w3, hd, dt, "w3"),
+        _arg(w2, (cfg.e_local, cfg.D, cfg.H_local), dt, "w2"), _arg(out, td, dt, "out"), p, n, s),
+        "moe_layer_forward_few")
 
 
 # --------------------------------------------------------------------------

@@ -922,6 +922,8 @@ cudaError_t launch_pair(const PairMaps &m, const PairParams &p, int clusters, si
 // 0: not known yet, 1: this device runs cooperative cluster launches, -1: it refused one
 int g_coop_ok[64] = {0};
 
+}  // namespace
+
 // A CUDA profiler attached to the process: Nsight Compute starts its target
 // with NV_NSIGHT_INJECTION_TRANSPORT_TYPE and NV_COMPUTE_PROFILER_PERFWORKS_DIR
 // in the environment, CUPTI-based tools name their injection library in
@@ -940,8 +942,6 @@ bool profiler_attached() {
     }();
     return attached;
 }
-
-}  // namespace
 
 int64_t grouped_pair_scratch_ints(int64_t rows_alloc, int E_local) {
     return 32 + (rows_alloc + P_PAIR_M - 1) / P_PAIR_M + E_local;

@@ -53,6 +53,8 @@ bool make_tmap_2d_f32(CUtensorMap *m, const void *base, uint64_t cols, uint64_t 
 // 32, 64 or 128 bytes (box_cols x element bytes must equal it).
 bool make_tmap_tile(CUtensorMap *m, const void *base, int elem_bytes, uint64_t cols, uint64_t rows,
                     uint64_t experts, uint32_t box_cols, uint32_t box_rows, int swizzle_bytes);
+// A CUDA profiler is attached to the process (cooperative launches are avoided).
+bool profiler_attached();
 int sm_count();  // SMs of the current device (0 on error)
 
 // Raises a kernel's dynamic shared-memory limit to at least `bytes` on the
@@ -254,6 +256,24 @@ cudaError_t launch_grouped_swiglu_bf16(const void *x_perm, const int *seg_offset
                                        const void *w3, const void *w2, void *h, void *y_perm,
                                        int D, int H_local, int e_first, int E_local,
                                        int64_t rows_alloc, int *status, cudaStream_t stream);
+
+// The whole layer for at most kFewMaxTokens tokens in one cooperative launch.
+// counters: few_scratch_ints(D) ints, zero before the first call and left zero;
+// h [T k, H_local] in the layer's type, logits [T, E] and part
+// (few_part_floats(T)) are scratch.
+constexpr int kFewMaxTokens = 32;
+constexpr int kFewMaxCtas = 160;
+struct FewLayer {
+    const void *x, *wg, *w1, *w3, *w2;
+    const float *bias;
+    void *out, *h;
+    float *logits, *part;
+    int *counters, *status;
+    int T, D, H_local, E, k, e_first, E_local, score, renorm, n_group, topk_group, is_bf16;
+};
+int64_t few_scratch_ints(int D);
+int64_t few_part_floats(int T);
+cudaError_t launch_few_layer(const FewLayer &f, cudaStream_t stream);
 
 // The norms around a block with its gate, dropout and residual sum (rows of D
 // values, D a multiple of 8 up to kResidualMaxD).  gate_kind: 0 none, 1 [D],

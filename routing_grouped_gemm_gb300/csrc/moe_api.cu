@@ -21,7 +21,7 @@ namespace {
 
 // 2.0.0: y_perm of bf16 layers is fp16 (fp32 up to 1.5.0); 2.1.0 adds the
 // MXFP4 calls and the gradients of the permute and combine steps; 2.2.0 adds
-// the norms around a block
+// the norms around a block and the layer for a few tokens
 constexpr int32_t kAbiVersion = 20200;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 32;
@@ -1235,6 +1235,83 @@ MOE_EXPORT moe_status moe_get_device_status(const void *ws, size_t ws_bytes, moe
     if (host[0] & moe::FLAG_CAPACITY) return MOE_ERR_CAPACITY;
     if (host[0] & moe::FLAG_BAD_ROUTING) return MOE_ERR_BAD_ROUTING;
     return MOE_OK;
+}
+
+// ---------------------------------------------------------------------
+// The layer for a few tokens: status | counters | logits | h | parts
+// ---------------------------------------------------------------------
+static moe_status few_supported(const moe_config *c) {
+    if (c->T > moe::kFewMaxTokens)
+        return arg_fail("moe_layer_forward_few: at most 32 tokens", MOE_ERR_UNSUPPORTED);
+    return MOE_OK;
+}
+
+static int64_t few_ws_layout(const moe_config *c, char *base, moe::FewLayer *f) {
+    int64_t off = sizeof(moe::StatusBlock);
+    auto take = [&](int64_t bytes) -> char * {
+        char *p = base ? base + off : nullptr;
+        off += align_up(bytes);
+        return p;
+    };
+    char *p_ctr = take(4 * moe::few_scratch_ints(c->D));
+    char *p_lg = take((int64_t)c->T * c->E * 4);
+    char *p_h = take((int64_t)c->T * c->k * c->H_local * elem_bytes(c));
+    char *p_part = take(4 * moe::few_part_floats(c->T));
+    if (f) {
+        f->status = &reinterpret_cast<moe::StatusBlock *>(base)->flags;
+        f->counters = reinterpret_cast<int *>(p_ctr);
+        f->logits = reinterpret_cast<float *>(p_lg);
+        f->h = p_h;
+        f->part = reinterpret_cast<float *>(p_part);
+    }
+    return off;
+}
+
+MOE_EXPORT int64_t moe_layer_few_workspace_size(const moe_config *cfg) {
+    if (validate(cfg) != MOE_OK || few_supported(cfg) != MOE_OK) return -1;
+    return few_ws_layout(cfg, nullptr, nullptr);
+}
+
+MOE_EXPORT moe_status moe_layer_forward_few(const moe_config *cfg, const void *x, const void *wg,
+                                            const float *bias, const void *w1, const void *w3,
+                                            const void *w2, void *out, void *ws, size_t ws_bytes,
+                                            moe_stream_t stream) {
+    moe_status st = validate(cfg);
+    if (st != MOE_OK) return st;
+    if ((st = few_supported(cfg)) != MOE_OK) return st;
+    if (!ws) return arg_fail("workspace is NULL", MOE_ERR_WORKSPACE);
+    if (!aligned(ws, kAlign)) return arg_fail("workspace must be 256-byte aligned", MOE_ERR_WORKSPACE);
+    if ((int64_t)ws_bytes < few_ws_layout(cfg, nullptr, nullptr))
+        return arg_fail("workspace too small for moe_layer_forward_few", MOE_ERR_WORKSPACE);
+    if (cfg->T == 0) return MOE_OK;
+    if (!need16(x) || !need16(wg) || !need16(out))
+        return arg_fail("x, wg or out is NULL or misaligned");
+    if (bias && !need16(bias)) return arg_fail("bias misaligned");
+    if (cfg->E_local > 0 && (!need16(w1) || !need16(w3) || !need16(w2)))
+        return arg_fail("expert weights are NULL or misaligned");
+    moe::FewLayer f = {};
+    few_ws_layout(cfg, static_cast<char *>(ws), &f);
+    f.x = x;
+    f.wg = wg;
+    f.bias = bias;
+    f.w1 = w1;
+    f.w3 = w3;
+    f.w2 = w2;
+    f.out = out;
+    f.T = cfg->T;
+    f.D = cfg->D;
+    f.H_local = cfg->H_local;
+    f.E = cfg->E;
+    f.k = cfg->k;
+    f.e_first = cfg->e_first;
+    f.E_local = cfg->E_local;
+    f.score = cfg->score;
+    f.renorm = cfg->renorm;
+    f.n_group = cfg->n_group > 1 ? cfg->n_group : 0;
+    f.topk_group = cfg->topk_group;
+    f.is_bf16 = cfg->dtype == MOE_BF16;
+    const cudaError_t e = moe::launch_few_layer(f, (cudaStream_t)stream);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_layer_forward_few");
 }
 
 // ---------------------------------------------------------------------

@@ -97,3 +97,31 @@ def test_missing_tensors_are_named(moe):
         moe.moe_residual_norm_backward(rc, *[None] * 13, ws)
     with pytest.raises(ValueError, match="no kind of gate"):
         moe.moe_residual_norm_backward(rc, *[None] * 11, torch.zeros(64), None, ws)
+
+
+# ---------------------------------------------------------------------------
+# the layer for a few tokens
+# ---------------------------------------------------------------------------
+
+def test_few_refusals(moe):
+    cfg = moe.Config(T=4, D=64, H_local=64, E=8, k=2)
+    n = moe.layer_few_workspace_size(cfg)
+    assert n % 256 == 0 and n > 256
+    base = dict(x=16, wg=16, bias=None, w1=16, w3=16, w2=16, out=16, ws=256, n=n)
+    before = moe.kernel_launches()
+
+    def call(c, **over):
+        return moe._lib.moe_layer_forward_few(c.ref()[0], *(base | over).values(), None)
+    for over, status in ((dict(x=None), 1), (dict(wg=8), 1), (dict(bias=8), 1), (dict(w1=None), 1), (dict(w3=8), 1),
+                         (dict(w2=None), 1), (dict(out=None), 1), (dict(ws=None), 7), (dict(ws=128), 7), (dict(n=n - 1), 7)):
+        assert call(cfg, **over) == status, over
+    many = moe.Config(T=33, D=64, H_local=64, E=8, k=2)
+    assert moe.layer_few_workspace_size(many) == -1
+    assert call(many) == moe.MOE_ERR_UNSUPPORTED
+    with pytest.raises(moe.MoeError):
+        moe.alloc_workspace(many, few=True)
+    assert call(moe.Config(T=4, D=12, H_local=64, E=8, k=2)) == moe.MOE_ERR_INVALID_ARG
+    assert call(moe.Config(T=0, D=64, H_local=64, E=8, k=2), x=None, out=None) == moe.MOE_OK
+    assert moe.kernel_launches() == before
+    with pytest.raises(ValueError, match="ws is required"):
+        moe.moe_layer_forward_few(cfg, *[None] * 7, None)
