@@ -23,11 +23,15 @@
 //
 // The 16 weight rows of a tile are the M side of mma.sync m16n8k16 and the
 // entry's rows the N = 8 side: at 8 rows per weight the tensor pipe idles either
-// way, and register accumulators need no TMEM round trip.  A producer warp
-// copies row pieces of 1 KB into a ring with bulk copies; a lane takes 16
-// consecutive bytes of a row (the sum over k does not care which k meet in one
-// instruction, as long as both operands agree), so fragments come straight from
-// 16-byte shared loads.  fp32 layers use the same tiles with fused multiply-adds.
+// way, and register accumulators need no TMEM round trip.  The CTA's 16 warps
+// split k: of every 1 KB of a row a warp takes 64 bytes, and a lane copies its
+// own 16 bytes of a row (the sum over k does not care which k meet in one
+// instruction, as long as both operands agree) with cp.async into a ring that it
+// alone reads back, so the stream needs no barrier but the sum over the warps at
+// a tile's end, and the copies of the next tiles run through it.  (Bulk copies by
+// a producer warp: each costs 55 ns to issue whatever its size, so 16 row pieces
+// of 1 KB per stage reached 39% of the copy rate, of 4 KB 97% in long rows.)
+// fp32 layers use the same tiles with fused multiply-adds.
 //
 // Rounding: keys, weights, both products' sums and the sum over experts are
 // fp32; h is rounded to the layer's type once (as in moe_grouped_swiglu), out
@@ -45,14 +49,13 @@
 namespace moe {
 namespace {
 
-constexpr int FW_WARPS = 8;  // consumer warps; one more produces
-constexpr int FW_THREADS = 32 * (FW_WARPS + 1);
-constexpr int FW_CHUNK = 1024;              // bytes of a row in one stage
-constexpr int FW_STRIDE = FW_CHUNK + 64;    // two rows' 64-byte pieces cover all banks
-constexpr int FW_M = 16;                    // weight rows per tile
-constexpr int FW_N = 8;                     // rows of an entry
-constexpr int FW_MAX_STAGES = 12;
-constexpr int FW_SMEM = 225 * 1024;
+constexpr int FW_WARPS = 16;
+constexpr int FW_THREADS = 32 * FW_WARPS;
+constexpr int FW_STEP = 64;                    // bytes of a row that a warp takes at once
+constexpr int FW_CHUNK = FW_STEP * FW_WARPS;   // and the CTA
+constexpr int FW_M = 16;                       // weight rows per tile
+constexpr int FW_N = 8;                        // rows of an entry
+constexpr int FW_SLOT = 3 * 512;               // a warp's step in the ring: 8 + 8 weight rows, 8 rows
 
 enum { FEW_ROUTE = 1, FEW_GEMM1 = 2, FEW_GEMM2 = 4, FEW_ALL = 7 };
 
@@ -66,7 +69,7 @@ struct FewParams {
     int *tile_count;   // [ceil(D / 16)] parts in; zero between calls
     int *status;
     int T, D, H, E, k, e_first, E_local, score, renorm, n_group, topk_group;
-    int phases, stages;
+    int phases;
 };
 
 template <typename T> struct Elem;
@@ -77,12 +80,15 @@ template <> struct Elem<__nv_bfloat16> {
     static __device__ __forceinline__ __nv_bfloat16 round(float v) { return __float2bfloat16_rn(v); }
 };
 
-__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-            smem_u32(dst)),
-        "l"(src), "r"(bytes), "r"(smem_u32(bar))
-        : "memory");
+// 16 bytes global -> shared, past L1; zeros when !in (src is not read then).
+__device__ __forceinline__ void copy16(void *dst, const void *src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+                 "r"(in ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -120,18 +126,12 @@ template <typename T> struct Acc;
 template <> struct Acc<__nv_bfloat16> {
     float c[4];
     __device__ __forceinline__ void clear() { c[0] = c[1] = c[2] = c[3] = 0.f; }
-    // one 64-byte step of the stage's rows, `off` bytes in; `in`: this lane's 16
-    // bytes lie inside the row (else they count as zeros)
-    __device__ __forceinline__ void step(const char *a, const char *b, int off, bool in, int cnt,
-                                         int lane) {
-        const int g = lane >> 2, o = off + (lane & 3) * 16;
-        uint4 lo = make_uint4(0, 0, 0, 0), hi = lo, bb = lo;
-        if (in) {
-            lo = *reinterpret_cast<const uint4 *>(a + g * FW_STRIDE + o);
-            hi = *reinterpret_cast<const uint4 *>(a + (g + 8) * FW_STRIDE + o);
-            // columns past the entry's rows: any row will do, they are not stored
-            bb = *reinterpret_cast<const uint4 *>(b + (g < cnt ? g : 0) * FW_STRIDE + o);
-        }
+    // one step: slot holds this lane's 16 bytes of rows g and g + 8 and of the entry's row g
+    __device__ __forceinline__ void step(const char *slot, int, int lane) {
+        const uint4 lo = *reinterpret_cast<const uint4 *>(slot + lane * 16);
+        const uint4 hi = *reinterpret_cast<const uint4 *>(slot + 512 + lane * 16);
+        // columns past the entry's rows hold anything; they are not stored
+        const uint4 bb = *reinterpret_cast<const uint4 *>(slot + 1024 + lane * 16);
         mma_bf16(c, lo.x, hi.x, lo.y, hi.y, bb.x, bb.y);
         mma_bf16(c, lo.z, hi.z, lo.w, hi.w, bb.z, bb.w);
     }
@@ -147,16 +147,13 @@ template <> struct Acc<float> {
 #pragma unroll
         for (int n = 0; n < FW_N; ++n) lo[n] = hi[n] = 0.f;
     }
-    __device__ __forceinline__ void step(const char *a, const char *b, int off, bool in, int cnt,
-                                         int lane) {
-        if (!in) return;
-        const int g = lane >> 2, o = off + (lane & 3) * 16;
-        const uint4 al = *reinterpret_cast<const uint4 *>(a + g * FW_STRIDE + o);
-        const uint4 ah = *reinterpret_cast<const uint4 *>(a + (g + 8) * FW_STRIDE + o);
+    __device__ __forceinline__ void step(const char *slot, int cnt, int lane) {
+        const uint4 al = *reinterpret_cast<const uint4 *>(slot + lane * 16);
+        const uint4 ah = *reinterpret_cast<const uint4 *>(slot + 512 + lane * 16);
 #pragma unroll
         for (int n = 0; n < FW_N; ++n) {
             if (n >= cnt) break;
-            const uint4 bb = *reinterpret_cast<const uint4 *>(b + n * FW_STRIDE + o);
+            const uint4 bb = *reinterpret_cast<const uint4 *>(slot + 1024 + n * 64 + (lane & 3) * 16);
             lo[n] = dot16<float>(al, bb, lo[n]);
             hi[n] = dot16<float>(ah, bb, hi[n]);
         }
@@ -182,15 +179,14 @@ template <> struct Acc<float> {
     }
 };
 
-// Shared memory behind the ring, in bytes (T k slots, T tokens).
-__host__ __device__ inline int few_table_bytes(int slots) { return (slots * 16 + 16 + 15) / 16 * 16; }
+// Shared memory, in bytes: the ring, the warps' sums, out's sums, the tables of
+// the T k (token, slot) pairs.
+__host__ __device__ inline int few_ring_bytes(int depth) { return FW_WARPS * depth * FW_SLOT; }
+constexpr int kFewRed = 2 * FW_WARPS * 32 * 16;
 __host__ __device__ inline int few_out_bytes(int T) { return FW_WARPS * FW_M * T * 4; }
-constexpr int kFewFixed = 2 * FW_WARPS * 32 * 16 /* s_red */ + 2 * FW_MAX_STAGES * 8 + 64;
-__host__ __device__ inline int few_stage_bytes(int T) {
-    return (FW_M + (T < FW_N ? T : FW_N)) * FW_STRIDE;
-}
+__host__ __device__ inline int few_table_bytes(int slots) { return slots * 16 + 16; }
 
-// Key of expert e for every token, by the CTA's consumer warps.
+// Key of expert e for every token, by the CTA's warps.
 template <typename T>
 __device__ __forceinline__ void few_route(const FewParams &p, float *s_part, int warp, int lane) {
     constexpr int EPV = 16 / (int)sizeof(T);
@@ -225,7 +221,7 @@ __device__ __forceinline__ void few_route(const FewParams &p, float *s_part, int
                 for (int o = 16; o > 0; o >>= 1) acc[n] += __shfl_xor_sync(0xffffffffu, acc[n], o);
                 if (lane == 0) s_part[warp * FW_N + n] = acc[n];
             }
-            bar_sync(1, 32 * FW_WARPS);
+            __syncthreads();
             const int at = warp * 32 + lane;  // (expert side by side, token)
             if (at < side * FW_N) {
                 const int j = at / FW_N, n = at % FW_N;
@@ -237,44 +233,36 @@ __device__ __forceinline__ void few_route(const FewParams &p, float *s_part, int
                     p.logits[(size_t)(t0 + n) * p.E + ej] = key;
                 }
             }
-            bar_sync(1, 32 * FW_WARPS);
+            __syncthreads();
         }
     }
 }
 
-template <typename T>
+// DEPTH: steps of a warp in flight.
+template <typename T, int DEPTH>
 __global__ void __launch_bounds__(FW_THREADS, 1)
 few_layer_kernel(const FewParams p) {
     extern __shared__ __align__(128) char smem[];
     __shared__ volatile int s_abort;
-    __shared__ int s_local, s_entries, s_last;
+    __shared__ int s_local, s_entries, s_last[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = gridDim.x;
-    const int slots = p.T * p.k, stage_bytes = few_stage_bytes(p.T);
-    char *ring = smem;
-    float4 *s_red = reinterpret_cast<float4 *>(ring + p.stages * stage_bytes);  // [2][warps][32]
-    uint64_t *full = reinterpret_cast<uint64_t *>(s_red + 2 * FW_WARPS * 32);
-    uint64_t *empty = full + FW_MAX_STAGES;
-    float *s_out = reinterpret_cast<float *>(empty + FW_MAX_STAGES + 8);  // [warps][T][16]
-    float *s_w = s_out + FW_WARPS * FW_M * p.T;                           // [slots]
-    int *s_idx = reinterpret_cast<int *>(s_w + slots);                    // [slots], then sorted pairs
-    int *s_sorted = s_idx + slots;        // [slots]: slot of the n-th pair in order of (expert, slot)
-    uint32_t *s_entry = reinterpret_cast<uint32_t *>(s_sorted + slots);   // [entries + 1]: expert << 16 | first pair
+    const int slots = p.T * p.k;
+    char *ring = smem + warp * DEPTH * FW_SLOT;  // this warp's
+    float4 *s_red = reinterpret_cast<float4 *>(smem + few_ring_bytes(DEPTH));  // [2][warps][32]
+    float *s_out = reinterpret_cast<float *>(s_red + 2 * FW_WARPS * 32);       // [warps][T][16]
+    float *s_w = s_out + FW_WARPS * FW_M * p.T;                                // [slots]
+    int *s_idx = reinterpret_cast<int *>(s_w + slots);                         // [slots]
+    int *s_sorted = s_idx + slots;  // [slots]: slot of the n-th pair in order of (expert, slot)
+    uint32_t *s_entry = reinterpret_cast<uint32_t *>(s_sorted + slots);  // [entries + 1]: expert << 16 | first pair
     constexpr int EB = (int)sizeof(T);
 
     griddep_wait();
-    if (tid == 0) {
-        s_abort = 0;
-        for (int i = 0; i < p.stages; ++i) {
-            mbar_init(&full[i], 2);  // the weights' and the rows' bytes are announced apart
-            mbar_init(&empty[i], FW_WARPS);
-        }
-        fence_mbarrier_init();
-    }
+    if (tid == 0) s_abort = 0;
     __syncthreads();
 
     // ---- route ----
     if (p.phases & FEW_ROUTE) {
-        if (warp < FW_WARPS) few_route<T>(p, reinterpret_cast<float *>(s_red), warp, lane);
+        few_route<T>(p, reinterpret_cast<float *>(s_red), warp, lane);
         __syncthreads();
         if (p.phases != FEW_ALL) return;
         if (tid == 0) {
@@ -284,10 +272,10 @@ few_layer_kernel(const FewParams p) {
         }
         __syncthreads();
     }
-    const bool dead = s_abort;  // the same for every thread: nothing sets it before the roles part
+    bool dead = s_abort;  // the same for every thread: set before the barrier only
     // ---- top-k and the entries, every CTA for itself ----
     if (!dead) {
-        for (int t = warp; t < p.T; t += FW_WARPS + 1)
+        for (int t = warp; t < p.T; t += FW_WARPS)
             warp_topk_weights<1024>(p.logits + (size_t)t * p.E, p.E, p.k, p.score, p.renorm,
                                     p.n_group, p.topk_group, t, s_idx, s_w,
                                     blockIdx.x == 0 ? p.status : nullptr, lane);
@@ -337,137 +325,90 @@ few_layer_kernel(const FewParams p) {
     __syncthreads();
 
     const int U = s_local ? s_entries : 0;
-    const int nt1 = p.H / 8, nc1 = (p.D * EB + FW_CHUNK - 1) / FW_CHUNK;
-    const int nt2 = (p.D + FW_M - 1) / FW_M, nc2 = (p.H * EB + FW_CHUNK - 1) / FW_CHUNK;
-    const bool do1 = p.phases & FEW_GEMM1, do2 = p.phases & FEW_GEMM2;
-    const int tiles1 = do1 ? U * nt1 : 0;
-    const long long per_tile = (long long)U * nc2, line = do2 ? per_tile * nt2 : 0;
-    // CTAs that take a part of the line: no more than it has chunks, so that none is empty
-    const int G2 = (int)min((long long)G, max(line, 1ll));
-    const bool part2 = (int)blockIdx.x < G2;
-    const long long lo = part2 ? line * blockIdx.x / G2 : 0, hi = part2 ? line * (blockIdx.x + 1) / G2 : 0;
     auto first_of = [&](int u) { return (int)(s_entry[u] & 0xffffu); };
+    // A warp's copies: its next step's row pieces (this lane's of rows g, g + 8
+    // and of the entry's row g) and how far the row goes on behind them.
+    const int g = lane >> 2, col = warp * FW_STEP + (lane & 3) * 16;
+    const char *lo = nullptr, *hi = nullptr, *row = nullptr;
+    bool has_lo = false, has_hi = false, has_row = false;  // this lane has such a row
+    int left = 0;     // bytes of the row from this lane's piece on; <= 0: past its end
+    int in_slot = 0;  // ring slot of the next copies, of the next step
+    int out_slot = 0;
+    const char *any = static_cast<const char *>(p.x);  // a valid address for copies of nothing
+    auto copy_weights = [&](int slot) {
+        char *d = ring + slot * FW_SLOT + lane * 16;
+        const bool in_lo = left > 0 && has_lo, in_hi = left > 0 && has_hi;
+        copy16(d, in_lo ? lo : any, in_lo);
+        copy16(d + 512, in_hi ? hi : any, in_hi);
+    };
+    auto copy_row = [&](int slot) {
+        if (has_row) copy16(ring + slot * FW_SLOT + 1024 + lane * 16, left > 0 ? row : any, left > 0);
+    };
+    auto advance = [&]() {
+        lo += FW_CHUNK;
+        hi += FW_CHUNK;
+        row += FW_CHUNK;
+        left -= FW_CHUNK;
+    };
+    auto bump = [&](int &slot) { slot = slot + 1 == DEPTH ? 0 : slot + 1; };
+    Acc<T> acc;
+    int turn = 0;
 
-    if (warp == FW_WARPS && !dead) {
-        // ---- producer ----
-        int stage = 0;
-        uint32_t phase = 0;
-        bool ok = true;
-        auto acquire = [&]() {
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[stage], phase ^ 1u, &s_abort));
-            return ok;
-        };
-        auto next = [&]() {
-            if (++stage == p.stages) { stage = 0; phase ^= 1u; }
-        };
-        auto row_piece = [&](char *dst, const void *base, size_t row, int row_bytes, int c, int bytes,
-                             uint64_t *bar) {
-            bulk_load(dst, static_cast<const char *>(base) + row * row_bytes + (size_t)c * FW_CHUNK,
-                      (uint32_t)bytes, bar);
-        };
-        for (int i = blockIdx.x; i < tiles1 && ok; i += G) {
-            const int u = i / nt1, j = i - u * nt1;
-            const int e = s_entry[u] >> 16, f = first_of(u), cnt = first_of(u + 1) - f;
-            const int n = lane - FW_M;  // lanes 16 ..: the entry's rows
-            const size_t token = n >= 0 && n < cnt ? (size_t)(s_sorted[f + n] / p.k) : 0;
-            const size_t row = ((size_t)e * p.H + (size_t)j * 8 + (lane & 7));
-            for (int c = 0; c < nc1 && acquire(); ++c, next()) {
-                const int bytes = min(FW_CHUNK, p.D * EB - c * FW_CHUNK);
-                char *st = ring + stage * stage_bytes;
-                if (lane == 0) mbar_arrive_expect_tx(&full[stage], FW_M * bytes);
-                if (lane == FW_M) mbar_arrive_expect_tx(&full[stage], cnt * bytes);
-                __syncwarp();
-                if (lane < FW_M)
-                    row_piece(st + lane * FW_STRIDE, lane < 8 ? p.w1 : p.w3, row, p.D * EB, c, bytes,
-                              &full[stage]);
-                else if (n < cnt)
-                    row_piece(st + lane * FW_STRIDE, p.x, token, p.D * EB, c, bytes, &full[stage]);
-            }
-        }
-        // GEMM2: the weights' part of the first stages goes out before the
-        // barrier, the rows' part (h) behind it
-        auto place = [&](long long i, int *dt, int *u, int *c) {
-            *dt = (int)(i / per_tile);
-            const int r = (int)(i - (long long)*dt * per_tile);
-            *u = r / nc2;
-            *c = r - *u * nc2;
-        };
-        auto load_w2 = [&](long long i) {
-            int dt, u, c;
-            place(i, &dt, &u, &c);
-            const int e = s_entry[u] >> 16, rows = min(FW_M, p.D - dt * FW_M);
-            const int bytes = min(FW_CHUNK, p.H * EB - c * FW_CHUNK);
-            if (lane == 0) mbar_arrive_expect_tx(&full[stage], rows * bytes);
-            __syncwarp();
-            if (lane < rows)
-                row_piece(ring + stage * stage_bytes + lane * FW_STRIDE, p.w2,
-                          (size_t)e * p.D + (size_t)dt * FW_M + lane, p.H * EB, c, bytes, &full[stage]);
-        };
-        auto load_h = [&](long long i) {
-            int dt, u, c;
-            place(i, &dt, &u, &c);
-            const int f = first_of(u), cnt = first_of(u + 1) - f;
-            const int bytes = min(FW_CHUNK, p.H * EB - c * FW_CHUNK);
-            if (lane == 0) mbar_arrive_expect_tx(&full[stage], cnt * bytes);
-            __syncwarp();
-            if (lane < cnt)
-                row_piece(ring + stage * stage_bytes + (FW_M + lane) * FW_STRIDE, p.h, (size_t)(f + lane),
-                          p.H * EB, c, bytes, &full[stage]);
-        };
-        if (ok && do2) {
-            const int stage0 = stage;
-            const uint32_t phase0 = phase;
-            const int ahead = (int)min((long long)p.stages, hi - lo);
-            for (int i = 0; i < ahead && acquire(); ++i, next()) load_w2(lo + i);
-            if (ok && p.phases == FEW_ALL) {
-                bool there = true;
-                if (lane == 0) there = wait_count_bounded(&p.bars[1], G, &s_abort);
-                ok = __all_sync(0xffffffffu, there);
-            }
-            if (ok) {
-                __syncwarp();
-                fence_proxy_async_global();  // h was written by ordinary stores
-                stage = stage0;
-                phase = phase0;
-                for (int i = 0; i < ahead; ++i, next()) load_h(lo + i);
-                for (long long i = lo + ahead; i < hi && acquire(); ++i, next()) {
-                    load_w2(i);
-                    load_h(i);
+    // ---- GEMM1: tiles of 8 hidden units of one entry ----
+    if ((p.phases & FEW_GEMM1) && !dead) {
+        const int nt = p.H / 8, row_bytes = p.D * EB, nc = (row_bytes + FW_CHUNK - 1) / FW_CHUNK;
+        const int tiles = U * nt;
+        int li = blockIdx.x, lc = nc;  // tile being copied, its chunks copied so far
+        bool begun = false;
+        auto copy_next = [&]() {
+            if (lc == nc) {
+                if (begun) li += G;
+                begun = true;
+                lc = 0;
+                if (li < tiles) {
+                    const int u = li / nt, j = li - u * nt;
+                    const int e = s_entry[u] >> 16, f = first_of(u), cnt = first_of(u + 1) - f;
+                    const size_t at = ((size_t)e * p.H + (size_t)j * 8 + g) * row_bytes + col;
+                    lo = static_cast<const char *>(p.w1) + at;
+                    hi = static_cast<const char *>(p.w3) + at;
+                    has_row = g < cnt;
+                    row = static_cast<const char *>(p.x) +
+                          (has_row ? (size_t)(s_sorted[f + g] / p.k) * row_bytes : 0) + col;
+                    left = row_bytes - col;
+                    has_lo = has_hi = true;
                 }
             }
-        }
-    } else if (!dead) {
-        // ---- consumers ----
-        int stage = 0, turn = 0;
-        uint32_t phase = 0;
-        Acc<T> acc;
-        // one stage: the row pieces' 64-byte steps, this warp's every eighth
-        auto consume = [&](int bytes, int cnt) {
-            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[stage], phase, &s_abort))) return false;
-            const char *a = ring + stage * stage_bytes, *b = a + FW_M * FW_STRIDE;
-#pragma unroll
-            for (int i = 0; i < FW_CHUNK / 64 / FW_WARPS; ++i) {
-                const int off = (warp + i * FW_WARPS) * 64;
-                if (off < bytes) acc.step(a, b, off, off + (lane & 3) * 16 < bytes, cnt, lane);
+            if (li < tiles) {
+                copy_weights(in_slot);
+                copy_row(in_slot);
+                bump(in_slot);
+                advance();
+                ++lc;
+            } else {
+                lc = 0;  // stay past the end
+                begun = false;
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[stage]);
-            if (++stage == p.stages) { stage = 0; phase ^= 1u; }
-            return true;
+            copy_commit();
         };
-        bool ok = true;
-        for (int i = blockIdx.x; i < tiles1 && ok; i += G) {
-            const int u = i / nt1, j = i - u * nt1;
+        for (int i = 0; i < DEPTH - 1; ++i) copy_next();
+        for (int i = blockIdx.x; i < tiles; i += G) {
+            const int u = i / nt, j = i - u * nt;
             const int f = first_of(u), cnt = first_of(u + 1) - f;
             acc.clear();
-            for (int c = 0; c < nc1 && ok; ++c) ok = consume(min(FW_CHUNK, p.D * EB - c * FW_CHUNK), cnt);
+            for (int c = 0; c < nc; ++c) {
+                copy_wait<DEPTH - 2>();
+                __syncwarp();
+                acc.step(ring + out_slot * FW_SLOT, cnt, lane);
+                bump(out_slot);
+                copy_next();  // into the slot read a step ago
+            }
             float v[4];
             acc.get(v, lane);
             float4 *red = s_red + turn * FW_WARPS * 32;
             turn ^= 1;  // the other buffer's readers are behind the barrier before this one
             red[warp * 32 + lane] = make_float4(v[0], v[1], v[2], v[3]);
-            ok = bar_and(1, 32 * FW_WARPS, ok);
-            if (ok && tid < 64) {
+            __syncthreads();
+            if (tid < 64) {
                 // thread (lane, half): gate and up of unit lane / 4 for row 2 (lane % 4) + half
                 const int half = tid >> 5, n = 2 * (lane & 3) + half;
                 float gate = 0.f, up = 0.f;
@@ -478,54 +419,154 @@ few_layer_kernel(const FewParams p) {
                     up += r[2 + half];
                 }
                 if (n < cnt)
-                    static_cast<T *>(p.h)[(size_t)(f + n) * p.H + j * 8 + (lane >> 2)] =
+                    static_cast<T *>(p.h)[(size_t)(f + n) * p.H + j * 8 + g] =
                         Elem<T>::round(gate / (1.f + expf(-gate)) * up);
             }
         }
-        if (do1 && p.phases == FEW_ALL) {
-            // h is read by the other CTAs' bulk copies
-            fence_proxy_async_global();
-            ok = bar_and(1, 32 * FW_WARPS, ok);
+        copy_wait<0>();
+        __syncwarp();
+        if (p.phases == FEW_ALL) {
+            __syncthreads();
             if (tid == 0) {
                 fence_acq_rel_gpu();
                 red_release_gpu_add(&p.bars[1], 1);
             }
             griddep_launch_dependents();
         }
-        if (do2 && ok) {
+    }
+
+    // ---- GEMM2: this CTA's part of the line of (tile, entry, chunk) ----
+    const int nt2 = (p.D + FW_M - 1) / FW_M;
+    if ((p.phases & FEW_GEMM2) && !dead && U == 0) {  // no token has an expert here
+        T *out = static_cast<T *>(p.out);
+        for (long long i = (long long)blockIdx.x * FW_THREADS + tid; i < (long long)p.T * p.D;
+             i += (long long)G * FW_THREADS)
+            out[i] = Elem<T>::round(0.f);
+    } else if ((p.phases & FEW_GEMM2) && !dead) {
+        const int row_bytes = p.H * EB, nc = (row_bytes + FW_CHUNK - 1) / FW_CHUNK;
+        const long long per_tile = (long long)U * nc, line = per_tile * nt2;
+        // CTAs that take a part: no more than there are chunks, so that none is empty
+        const int G2 = (int)min((long long)G, line);
+        const bool part_of = (int)blockIdx.x < G2;
+        const long long first = part_of ? line * blockIdx.x / G2 : 0;
+        const int total = part_of ? (int)(line * (blockIdx.x + 1) / G2 - first) : 0;
+        const int dt0 = (int)(first / per_tile);
+        const int u0 = (int)((first - dt0 * per_tile) / nc), c0 = (int)(first - dt0 * per_tile) - u0 * nc;
+        // copy cursor
+        int ln = 0, ldt = dt0, lu = u0, lc = c0;
+        auto set_weights = [&](int dt, int u, int c) {
+            const int e = s_entry[u] >> 16, d = dt * FW_M + g;
+            const size_t at = ((size_t)e * p.D + d) * row_bytes + (size_t)c * FW_CHUNK + col;
+            has_lo = d < p.D;  // D is a multiple of 8: rows g all are, rows g + 8 may not be
+            has_hi = d + 8 < p.D;
+            lo = static_cast<const char *>(p.w2) + (has_lo ? at : 0);
+            hi = static_cast<const char *>(p.w2) + (has_hi ? at + (size_t)8 * row_bytes : 0);
+            left = row_bytes - c * FW_CHUNK - col;
+        };
+        auto set_row = [&](int u, int c) {
+            const int f = first_of(u), cnt = first_of(u + 1) - f;
+            has_row = g < cnt;
+            row = static_cast<const char *>(p.h) + (size_t)(f + (has_row ? g : 0)) * row_bytes +
+                  (size_t)c * FW_CHUNK + col;
+            left = row_bytes - c * FW_CHUNK - col;
+        };
+        auto step_on = [&](int &dt, int &u, int &c) {  // true: another entry or tile begins
+            if (++c < nc) return false;
+            c = 0;
+            if (++u == U) {
+                u = 0;
+                ++dt;
+            }
+            return true;
+        };
+        // the weights of the first steps go out before the barrier, the rows (h) behind it
+        const int ahead = min(DEPTH - 1, total);
+        int dt = dt0, u = u0, c = c0;
+        for (int i = 0; i < ahead; ++i) {
+            if (i == 0 || c == 0) set_weights(dt, u, c);
+            copy_weights((in_slot + i) % DEPTH);
+            advance();
+            step_on(dt, u, c);
+        }
+        if (p.phases == FEW_ALL) {
+            if (tid == 0) wait_count_bounded(&p.bars[1], G, &s_abort);
+            __syncthreads();
+            dead = s_abort;
+        }
+        if (!dead) {
+            for (int i = 0; i < DEPTH - 1; ++i) {
+                if (i < ahead) {
+                    if (i == 0 || lc == 0) set_row(lu, lc);
+                    copy_row(in_slot);
+                    bump(in_slot);
+                    advance();
+                    step_on(ldt, lu, lc);
+                    ++ln;
+                }
+                copy_commit();
+            }
+            if (ln < total) {
+                set_weights(ldt, lu, lc);
+                set_row(lu, lc);
+            }
+            auto copy_next = [&]() {
+                if (ln < total) {
+                    copy_weights(in_slot);
+                    copy_row(in_slot);
+                    bump(in_slot);
+                    advance();
+                    ++ln;
+                    if (step_on(ldt, lu, lc) && ln < total) {
+                        set_weights(ldt, lu, lc);
+                        set_row(lu, lc);
+                    }
+                }
+                copy_commit();
+            };
             for (int i = lane; i < FW_M * p.T; i += 32) s_out[warp * FW_M * p.T + i] = 0.f;
             __syncwarp();
-            const int first_dt = per_tile ? (int)(lo / per_tile) : 0;
-            for (long long i = lo; i < hi && ok;) {
-                const int dt = (int)(i / per_tile);
-                const long long end = min(hi, (long long)(dt + 1) * per_tile);
-                const bool whole = i == (long long)dt * per_tile && end == i + per_tile;
-                while (i < end && ok) {  // this CTA's part of one entry
-                    const int r = (int)(i - (long long)dt * per_tile), u = r / nc2;
-                    int c = r - u * nc2;
+            T *out = static_cast<T *>(p.out);
+            dt = dt0, u = u0, c = c0;
+            int cut[2] = {-1, -1};  // tiles that others share: the first, the last
+            for (int n = 0; n < total;) {
+                const bool from_start = u == 0 && c == 0;
+                bool to_end = false;
+                while (n < total && !to_end) {  // this CTA's part of one entry
                     const int f = first_of(u), cnt = first_of(u + 1) - f;
                     acc.clear();
-                    for (; c < nc2 && i < end && ok; ++c, ++i)
-                        ok = consume(min(FW_CHUNK, p.H * EB - c * FW_CHUNK), cnt);
+                    bool more = true;
+                    while (more && n < total) {
+                        copy_wait<DEPTH - 2>();
+                        __syncwarp();
+                        acc.step(ring + out_slot * FW_SLOT, cnt, lane);
+                        bump(out_slot);
+                        copy_next();
+                        ++n;
+                        more = ++c < nc;
+                    }
+                    if (!more) {
+                        c = 0;
+                        to_end = ++u == U;
+                    }
                     float v[4];
                     acc.get(v, lane);
-                    const int g = lane >> 2;
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        const int n = 2 * (lane & 3) + half;
-                        if (n >= cnt) continue;
-                        const int slot = s_sorted[f + n];
+                        const int m = 2 * (lane & 3) + half;
+                        if (m >= cnt) continue;
+                        const int slot = s_sorted[f + m];
                         float *o = s_out + (warp * p.T + slot / p.k) * FW_M;
                         o[g] = fmaf(s_w[slot], v[half], o[g]);
                         o[g + 8] = fmaf(s_w[slot], v[2 + half], o[g + 8]);
                     }
+                    __syncwarp();
                 }
-                ok = bar_and(1, 32 * FW_WARPS, ok);
-                if (!ok) break;
                 // the warps' sums; a tile that others share goes through memory
-                float *part = p.part + ((size_t)blockIdx.x * 2 + (dt == first_dt ? 0 : 1)) * p.T * FW_M;
-                T *out = static_cast<T *>(p.out);
-                for (int o = tid; o < FW_M * p.T; o += 32 * FW_WARPS) {
+                const bool whole = from_start && to_end;
+                float *part = p.part + ((size_t)blockIdx.x * 2 + (dt == dt0 ? 0 : 1)) * p.T * FW_M;
+                if (!whole) cut[dt == dt0 ? 0 : 1] = dt;
+                __syncthreads();
+                for (int o = tid; o < FW_M * p.T; o += FW_THREADS) {
                     float sum = 0.f;
 #pragma unroll
                     for (int w = 0; w < FW_WARPS; ++w) {
@@ -538,58 +579,57 @@ few_layer_kernel(const FewParams p) {
                     else if (d < p.D)
                         out[(size_t)(o / FW_M) * p.D + d] = Elem<T>::round(sum);
                 }
-                bar_sync(1, 32 * FW_WARPS);
-                if (whole) continue;
-                // CTAs that share the tile: c0 .. c1
-                const long long a0 = (long long)dt * per_tile, a1 = a0 + per_tile;
-                int c0 = (int)(a0 * G2 / line), c1 = (int)min((long long)G2 - 1, (a1 - 1) * G2 / line);
-                while (line * (c0 + 1) / G2 <= a0) ++c0;
-                while (c0 > 0 && line * c0 / G2 > a0) --c0;
-                while (line * (c1 + 1) / G2 < a1) ++c1;
-                while (c1 > 0 && line * c1 / G2 >= a1) --c1;
-                if (tid == 0) {
-                    fence_acq_rel_gpu();
-                    const int before = atomicAdd(&p.tile_count[dt], 1);
-                    fence_acq_rel_gpu();
-                    s_last = before == c1 - c0;
-                    if (s_last) p.tile_count[dt] = 0;
-                }
-                bar_sync(1, 32 * FW_WARPS);
-                if (s_last)
-                    for (int o = tid; o < FW_M * p.T; o += 32 * FW_WARPS) {
-                        float sum = 0.f;
-                        for (int c = c0; c <= c1; ++c) {
-                            const int theirs = (int)(line * c / G2 / per_tile);
-                            sum += __ldcg(p.part + ((size_t)c * 2 + (dt == theirs ? 0 : 1)) * p.T * FW_M + o);
-                        }
-                        const int d = dt * FW_M + o % FW_M;
-                        if (d < p.D) out[(size_t)(o / FW_M) * p.D + d] = Elem<T>::round(sum);
-                    }
-                bar_sync(1, 32 * FW_WARPS);  // s_last is free again
+                __syncthreads();
+                u = 0;
+                ++dt;
             }
-            if (line == 0) {  // no token has an expert here
-                T *out = static_cast<T *>(p.out);
-                for (long long i = (long long)blockIdx.x * 32 * FW_WARPS + tid; i < (long long)p.T * p.D;
-                     i += (long long)G * 32 * FW_WARPS)
-                    out[i] = Elem<T>::round(0.f);
+            // shared tiles: the CTA that comes last adds the parts, in order
+            int ca[2], cb[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (cut[i] < 0) continue;
+                const long long a0 = cut[i] * per_tile, a1 = a0 + per_tile;
+                ca[i] = cb[i] = (int)blockIdx.x;
+                while (ca[i] > 0 && line * ca[i] / G2 > a0) --ca[i];
+                while (line * (cb[i] + 1) / G2 < a1) ++cb[i];
+            }
+            if (tid < 2) {
+                const int mine = tid == 0 ? cut[0] : cut[1];
+                if (mine >= 0) {
+                    fence_acq_rel_gpu();
+                    const int before = atomicAdd(&p.tile_count[mine], 1);
+                    fence_acq_rel_gpu();
+                    s_last[tid] = before == (tid == 0 ? cb[0] - ca[0] : cb[1] - ca[1]);
+                    if (s_last[tid]) p.tile_count[mine] = 0;
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (cut[i] < 0 || !s_last[i]) continue;
+                for (int o = tid; o < FW_M * p.T; o += FW_THREADS) {
+                    float sum = 0.f;
+                    for (int b = ca[i]; b <= cb[i]; ++b) {
+                        const int theirs = (int)(line * b / G2 / per_tile);
+                        sum += __ldcg(p.part + ((size_t)b * 2 + (cut[i] == theirs ? 0 : 1)) * p.T * FW_M + o);
+                    }
+                    const int d = cut[i] * FW_M + o % FW_M;
+                    if (d < p.D) out[(size_t)(o / FW_M) * p.D + d] = Elem<T>::round(sum);
+                }
             }
         }
+        copy_wait<0>();
     }
     __syncthreads();
-    const bool aborted = s_abort;
-    if (aborted) {
-        if (warp == 0) settle_inflight_copies();
-        __syncthreads();
-    }
     if (tid == 0) {
+        const bool aborted = s_abort;
         if (aborted) raise_flag(p.status, FLAG_TIMEOUT);
         if (p.phases == FEW_ALL) {
             // the last CTA to leave puts the counters back
             fence_acq_rel_gpu();
             if (atomicAdd(&p.bars[2], 1) == G - 1) {
                 fence_acq_rel_gpu();
-                const int late = atomicOr(p.status, 0) & FLAG_TIMEOUT;
-                if (late)  // some parts never came
+                if (atomicOr(p.status, 0) & FLAG_TIMEOUT)  // some parts never came
                     for (int i = 0; i < nt2; ++i) p.tile_count[i] = 0;
                 p.bars[0] = p.bars[1] = p.bars[2] = 0;
             }
@@ -628,16 +668,17 @@ cudaError_t launch_few_layer(const FewLayer &f, cudaStream_t stream) {
     p.renorm = f.renorm;
     p.n_group = f.n_group;
     p.topk_group = f.topk_group;
-    const int rest = kFewFixed + few_out_bytes(f.T) + few_table_bytes(f.T * f.k);
-    p.stages = std::min(FW_MAX_STAGES, (FW_SMEM - rest) / few_stage_bytes(f.T));
-    const size_t smem = (size_t)p.stages * few_stage_bytes(f.T) + rest;
-    const void *kernel = f.is_bf16 ? (const void *)few_layer_kernel<__nv_bfloat16>
-                                   : (const void *)few_layer_kernel<float>;
-    cudaError_t err = ensure_smem(kernel, smem);
+    // 8 steps of every warp in flight (128 KB of weights per SM), 6 where many
+    // tokens' sums take the shared memory
+    const bool deep = f.T <= 8;
+    const size_t smem = (size_t)few_ring_bytes(deep ? 8 : 6) + kFewRed + few_out_bytes(f.T) +
+                        few_table_bytes(f.T * f.k);
+    auto fn = f.is_bf16 ? (deep ? few_layer_kernel<__nv_bfloat16, 8> : few_layer_kernel<__nv_bfloat16, 6>)
+                        : (deep ? few_layer_kernel<float, 8> : few_layer_kernel<float, 6>);
+    cudaError_t err = ensure_smem((const void *)fn, smem);
     if (err != cudaSuccess) return err;
     const int ctas = std::min(sm_count(), kFewMaxCtas);
     if (ctas <= 0) return cudaErrorInvalidDevice;
-    auto fn = f.is_bf16 ? few_layer_kernel<__nv_bfloat16> : few_layer_kernel<float>;
     // A device (or a partition of one) that cannot hold the whole grid at once
     // refuses the cooperative launch, and under a profiler such launches have
     // failed: the three stages are then launched one by one.  MOE_FEW_LAUNCHES=3
