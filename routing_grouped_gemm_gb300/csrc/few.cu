@@ -55,6 +55,7 @@ constexpr int FW_STEP = 64;                    // bytes of a row that a warp tak
 constexpr int FW_CHUNK = FW_STEP * FW_WARPS;   // and the CTA
 constexpr int FW_M = 16;                       // weight rows per tile
 constexpr int FW_N = 8;                        // rows of an entry
+constexpr int FW_JOIN = 8;                     // chunks as long as joining a shared tile's parts takes
 constexpr int FW_SLOT = 3 * 512;               // a warp's step in the ring: 8 + 8 weight rows, 8 rows
 
 enum { FEW_ROUTE = 1, FEW_GEMM1 = 2, FEW_GEMM2 = 4, FEW_ALL = 7 };
@@ -184,123 +185,132 @@ template <> struct Acc<float> {
 __host__ __device__ inline int few_ring_bytes(int depth) { return FW_WARPS * depth * FW_SLOT; }
 constexpr int kFewRed = 2 * FW_WARPS * 32 * 16;
 __host__ __device__ inline int few_out_bytes(int T) { return FW_WARPS * FW_M * T * 4; }
-__host__ __device__ inline int few_table_bytes(int slots) { return slots * 16 + 16; }
+__host__ __device__ inline int few_table_bytes(int slots) { return slots * 20 + 16; }
 
-// Key of expert e for every token, by the CTA's warps.
-template <typename T>
-__device__ __forceinline__ void few_route(const FewParams &p, float *s_part, int warp, int lane) {
+// Keys of tokens t0 .. t0 + NT - 1 for one expert: this warp's share (v0, v0 +
+// stride, ...) of the dot products, summed over the lanes.
+template <typename T, int NT>
+__device__ __forceinline__ void few_dots(const FewParams &p, int e, int t0, int v0, int stride,
+                                         int lane, float *to) {
     constexpr int EPV = 16 / (int)sizeof(T);
-    const int G = gridDim.x, vecs = p.D / EPV;
-    const int mine = p.E > (int)blockIdx.x ? (p.E - (int)blockIdx.x + G - 1) / G : 0;
-    if (mine == 0) return;
-    int side = 1;  // experts side by side, 8 / side warps each
-    while (side < mine && side < FW_WARPS) side <<= 1;
-    const int wpe = FW_WARPS / side, sub = warp % wpe;
-    for (int i0 = 0; i0 < mine; i0 += side) {
-        const int i = i0 + warp / wpe;
-        const int e = blockIdx.x + i * G;
-        for (int t0 = 0; t0 < p.T; t0 += FW_N) {
-            float acc[FW_N];
+    const int vecs = p.D / EPV, n_here = min(NT, p.T - t0);
+    const uint4 *w = static_cast<const uint4 *>(p.wg) + (size_t)e * vecs;
+    const uint4 *x = static_cast<const uint4 *>(p.x) + (size_t)t0 * vecs;
+    float acc[NT];
 #pragma unroll
-            for (int n = 0; n < FW_N; ++n) acc[n] = 0.f;
-            if (i < mine) {
-                const uint4 *w = static_cast<const uint4 *>(p.wg) + (size_t)e * vecs;
-                const uint4 *x = static_cast<const uint4 *>(p.x) + (size_t)t0 * vecs;
-#pragma unroll 4
-                for (int v = sub * 32 + lane; v < vecs; v += wpe * 32) {
-                    const uint4 wv = w[v];
+    for (int n = 0; n < NT; ++n) acc[n] = 0.f;
+#pragma unroll 1
+    for (int v = v0 + lane; v < vecs; v += stride) {
+        const uint4 wv = w[v];
+        uint4 xv[NT];
 #pragma unroll
-                    for (int n = 0; n < FW_N; ++n)
-                        if (t0 + n < p.T) acc[n] = dot16<T>(wv, x[(size_t)n * vecs + v], acc[n]);
-                }
-            }
+        for (int n = 0; n < NT; ++n) xv[n] = x[(size_t)min(n, n_here - 1) * vecs + v];
 #pragma unroll
-            for (int n = 0; n < FW_N; ++n) {
-                if (t0 + n >= p.T) break;
+        for (int n = 0; n < NT; ++n) acc[n] = dot16<T>(wv, xv[n], acc[n]);
+    }
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) acc[n] += __shfl_xor_sync(0xffffffffu, acc[n], o);
-                if (lane == 0) s_part[warp * FW_N + n] = acc[n];
-            }
-            __syncthreads();
-            const int at = warp * 32 + lane;  // (expert side by side, token)
-            if (at < side * FW_N) {
-                const int j = at / FW_N, n = at % FW_N;
-                if (i0 + j < mine && t0 + n < p.T) {
-                    const int ej = blockIdx.x + (i0 + j) * G;
-                    float key = 0.f;
-                    for (int u = 0; u < wpe; ++u) key += s_part[(j * wpe + u) * FW_N + n];
-                    if (p.bias) key += p.bias[ej];
-                    p.logits[(size_t)(t0 + n) * p.E + ej] = key;
-                }
-            }
-            __syncthreads();
-        }
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) acc[n] += __shfl_xor_sync(0xffffffffu, acc[n], o);
+        if (lane == 0) to[n] = acc[n];
     }
 }
 
-// DEPTH: steps of a warp in flight.
-template <typename T, int DEPTH>
-__global__ void __launch_bounds__(FW_THREADS, 1)
-few_layer_kernel(const FewParams p) {
-    extern __shared__ __align__(128) char smem[];
-    __shared__ volatile int s_abort;
-    __shared__ int s_local, s_entries, s_last[2];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = gridDim.x;
-    const int slots = p.T * p.k;
-    char *ring = smem + warp * DEPTH * FW_SLOT;  // this warp's
-    float4 *s_red = reinterpret_cast<float4 *>(smem + few_ring_bytes(DEPTH));  // [2][warps][32]
-    float *s_out = reinterpret_cast<float *>(s_red + 2 * FW_WARPS * 32);       // [warps][T][16]
-    float *s_w = s_out + FW_WARPS * FW_M * p.T;                                // [slots]
-    int *s_idx = reinterpret_cast<int *>(s_w + slots);                         // [slots]
-    int *s_sorted = s_idx + slots;  // [slots]: slot of the n-th pair in order of (expert, slot)
-    uint32_t *s_entry = reinterpret_cast<uint32_t *>(s_sorted + slots);  // [entries + 1]: expert << 16 | first pair
-    constexpr int EB = (int)sizeof(T);
-
-    griddep_wait();
-    if (tid == 0) s_abort = 0;
-    __syncthreads();
-
-    // ---- route ----
-    if (p.phases & FEW_ROUTE) {
-        few_route<T>(p, reinterpret_cast<float *>(s_red), warp, lane);
+// The keys: (expert, group of 8 tokens) pairs over the CTAs, a CTA's own side by
+// side over its warps.
+template <typename T>
+__device__ __forceinline__ void few_route(const FewParams &p, float *s_part, int tid) {
+    const int warp = tid >> 5, lane = tid & 31, G = gridDim.x;
+    const int groups = (p.T + FW_N - 1) / FW_N, units = p.E * groups;
+    const int mine = units > (int)blockIdx.x ? (units - (int)blockIdx.x + G - 1) / G : 0;
+    if (mine == 0) return;
+    int side = 1;  // pairs side by side, FW_WARPS / side warps each
+    while (side < mine && side < FW_WARPS) side <<= 1;
+    const int wpe = FW_WARPS / side, sub = warp % wpe;
+    for (int i0 = 0; i0 < mine; i0 += side) {
+        const int i = i0 + warp / wpe, unit = blockIdx.x + i * G;
+        if (i < mine) {
+            const int e = unit / groups, t0 = (unit - e * groups) * FW_N;
+            if (p.T == 1)
+                few_dots<T, 1>(p, e, t0, sub * 32, wpe * 32, lane, s_part + warp * FW_N);
+            else
+                few_dots<T, FW_N>(p, e, t0, sub * 32, wpe * 32, lane, s_part + warp * FW_N);
+        }
         __syncthreads();
-        if (p.phases != FEW_ALL) return;
-        if (tid == 0) {
-            fence_acq_rel_gpu();
-            red_release_gpu_add(&p.bars[0], 1);
-            wait_count_bounded(&p.bars[0], G, &s_abort);
+        const int j = tid / FW_N, n = tid % FW_N;
+        if (j < side && i0 + j < mine) {
+            const int un = blockIdx.x + (i0 + j) * G, e = un / groups, t = (un - e * groups) * FW_N + n;
+            if (t < p.T) {
+                float key = 0.f;
+                for (int u = 0; u < wpe; ++u) key += s_part[(j * wpe + u) * FW_N + n];
+                if (p.bias) key += p.bias[e];
+                p.logits[(size_t)t * p.E + e] = key;
+            }
         }
         __syncthreads();
     }
-    bool dead = s_abort;  // the same for every thread: set before the barrier only
-    // ---- top-k and the entries, every CTA for itself ----
-    if (!dead) {
-        for (int t = warp; t < p.T; t += FW_WARPS)
-            warp_topk_weights<1024>(p.logits + (size_t)t * p.E, p.E, p.k, p.score, p.renorm,
-                                    p.n_group, p.topk_group, t, s_idx, s_w,
-                                    blockIdx.x == 0 ? p.status : nullptr, lane);
+}
+
+// The T k (token, slot) pairs whose expert is here, an expert's pairs together
+// and in order, cut into entries of at most 8.  s_sorted[n]: slot of the n-th
+// pair, s_token[n]: its token, s_entry[u]: expert << 16 | first pair of entry u,
+// with a last one that holds the number of pairs.  Returns the entries.
+__device__ __forceinline__ int few_entries(const FewParams &p, int slots, const int *s_idx,
+                                           int *s_sorted, int *s_token, uint32_t *s_entry,
+                                           int *s_count, int tid) {
+    const int lane = tid & 31;
+    if (slots <= 32) {  // one warp, a lane per pair: experts in the order of their first pairs
+        if (tid < 32) {
+            const int e = lane < slots ? s_idx[lane] - p.e_first : -1;
+            const bool here = e >= 0 && e < p.E_local;
+            const uint32_t mates = __match_any_sync(0xffffffffu, here ? e : -1 - lane);
+            const int lead = __ffs(mates) - 1, size = __popc(mates);
+            int packed = here && lead == lane ? (size << 16) | ((size + FW_N - 1) / FW_N) : 0;
+            const int own = packed;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {  // pairs and entries of the experts up to here
+                const int v = __shfl_up_sync(0xffffffffu, packed, o);
+                if (lane >= o) packed += v;
+            }
+            const int all = __shfl_sync(0xffffffffu, packed, 31);
+            const int before = __shfl_sync(0xffffffffu, packed - own, lead);
+            const int rank = __popc(mates & lanemask_lt()), place = (before >> 16) + rank;
+            if (here) {
+                s_sorted[place] = lane;
+                s_token[place] = lane / p.k;
+                if (rank % FW_N == 0)
+                    s_entry[(before & 0xffff) + rank / FW_N] = (uint32_t)e << 16 | (uint32_t)place;
+            }
+            if (lane == 0) {
+                s_entry[all & 0xffff] = (uint32_t)(all >> 16);
+                *s_count = all & 0xffff;
+            }
+        }
+        __syncthreads();
+        return *s_count;
     }
-    __syncthreads();
-    if (!dead) {
-        for (int i = tid; i < slots; i += FW_THREADS) {
-            const int e = s_idx[i] - p.e_first;
-            int place = 0, same = 0;
+    // a thread per pair: its place by counting
+    for (int i = tid; i < slots; i += FW_THREADS) {
+        const int e = s_idx[i] - p.e_first;
+        const bool here = e >= 0 && e < p.E_local;
+        int place = 0, same = 0;
+        if (here)
+#pragma unroll 4
             for (int j = 0; j < slots; ++j) {
                 const int ej = s_idx[j] - p.e_first;
-                if (ej < 0 || ej >= p.E_local) continue;
-                if (ej < e || (ej == e && j < i)) ++place;
-                if (ej == e && j < i) ++same;
+                const bool twin = ej == e && j < i;
+                place += (ej >= 0 && ej < e) || twin;
+                same += twin;
             }
-            if (e >= 0 && e < p.E_local) {
-                s_sorted[place] = i;
-                // the pair's expert, and whether it begins an entry; read by warp 0 below
-                s_entry[place] = (uint32_t)e << 16 | (same % FW_N == 0 ? 1u : 0u);
-            }
+        if (here) {
+            s_sorted[place] = i;
+            s_token[place] = i / p.k;
+            // the pair's expert, and whether it begins an entry: for the first warp
+            s_entry[place] = (uint32_t)e << 16 | (same % FW_N == 0 ? 1u : 0u);
         }
     }
-    if (tid == 0) s_local = 0;
     __syncthreads();
-    if (warp == 0 && !dead) {
+    if (tid < 32) {
         int local = 0;
         for (int i = lane; i < slots; i += 32) {
             const int e = s_idx[i] - p.e_first;
@@ -318,308 +328,343 @@ few_layer_kernel(const FewParams p) {
         }
         if (lane == 0) {
             s_entry[n] = (uint32_t)local;
-            s_local = local;
-            s_entries = n;
+            *s_count = n;
         }
     }
     __syncthreads();
+    return *s_count;
+}
 
-    const int U = s_local ? s_entries : 0;
+// A line of `n` cut into `parts`: first of part b, and the part that holds x.
+__device__ __forceinline__ int cut_first(int n, int parts, int b) {
+    const int q = n / parts, r = n - q * parts;
+    return q * b + min(b, r);
+}
+__device__ __forceinline__ int cut_holder(int n, int parts, int x) {
+    const int q = n / parts, r = n - q * parts;
+    return x < r * (q + 1) ? x / (q + 1) : r + (x - r * (q + 1)) / q;
+}
+
+// DEPTH: steps of a warp in flight.
+template <typename T, int DEPTH>
+__global__ void __launch_bounds__(FW_THREADS, 1)
+few_layer_kernel(const FewParams p) {
+    extern __shared__ __align__(128) char smem[];
+    __shared__ volatile int s_abort;
+    __shared__ int s_count, s_last[2];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = gridDim.x;
+    const int slots = p.T * p.k;
+    char *ring = smem + warp * DEPTH * FW_SLOT;  // this warp's
+    float4 *s_red = reinterpret_cast<float4 *>(smem + few_ring_bytes(DEPTH));  // [2][warps][32]
+    float *s_out = reinterpret_cast<float *>(s_red + 2 * FW_WARPS * 32);       // [warps][T][16]
+    float *s_w = s_out + FW_WARPS * FW_M * p.T;                                // [slots]
+    int *s_idx = reinterpret_cast<int *>(s_w + slots);                         // [slots]
+    int *s_sorted = s_idx + slots;                                             // [slots]
+    int *s_token = s_sorted + slots;                                           // [slots]
+    uint32_t *s_entry = reinterpret_cast<uint32_t *>(s_token + slots);         // [slots + 1]
+    constexpr int EB = (int)sizeof(T);
+
+    griddep_wait();
+    if (tid == 0) s_abort = 0;
+    __syncthreads();
+
+    // ---- route ----
+    if (p.phases & FEW_ROUTE) {
+        few_route<T>(p, reinterpret_cast<float *>(s_red), tid);
+        if (p.phases != FEW_ALL) return;
+        if (tid == 0) {
+            fence_acq_rel_gpu();
+            red_release_gpu_add(&p.bars[0], 1);
+            wait_count_bounded(&p.bars[0], G, &s_abort);
+        }
+        __syncthreads();
+    }
+    bool dead = s_abort;  // the same for every thread: set before the barrier only
+    int U = 0;
+    if (!dead) {  // top-k and the entries, every CTA for itself
+        for (int t = warp; t < p.T; t += FW_WARPS)
+            warp_topk_weights<1024>(p.logits + (size_t)t * p.E, p.E, p.k, p.score, p.renorm,
+                                    p.n_group, p.topk_group, t, s_idx, s_w,
+                                    blockIdx.x == 0 ? p.status : nullptr, lane);
+        __syncthreads();
+        U = few_entries(p, slots, s_idx, s_sorted, s_token, s_entry, &s_count, tid);
+    }
     auto first_of = [&](int u) { return (int)(s_entry[u] & 0xffffu); };
-    // A warp's copies: its next step's row pieces (this lane's of rows g, g + 8
-    // and of the entry's row g) and how far the row goes on behind them.
-    const int g = lane >> 2, col = warp * FW_STEP + (lane & 3) * 16;
-    const char *lo = nullptr, *hi = nullptr, *row = nullptr;
-    bool has_lo = false, has_hi = false, has_row = false;  // this lane has such a row
-    int left = 0;     // bytes of the row from this lane's piece on; <= 0: past its end
-    int in_slot = 0;  // ring slot of the next copies, of the next step
-    int out_slot = 0;
-    const char *any = static_cast<const char *>(p.x);  // a valid address for copies of nothing
-    auto copy_weights = [&](int slot) {
-        char *d = ring + slot * FW_SLOT + lane * 16;
-        const bool in_lo = left > 0 && has_lo, in_hi = left > 0 && has_hi;
-        copy16(d, in_lo ? lo : any, in_lo);
-        copy16(d + 512, in_hi ? hi : any, in_hi);
-    };
-    auto copy_row = [&](int slot) {
-        if (has_row) copy16(ring + slot * FW_SLOT + 1024 + lane * 16, left > 0 ? row : any, left > 0);
-    };
-    auto advance = [&]() {
-        lo += FW_CHUNK;
-        hi += FW_CHUNK;
-        row += FW_CHUNK;
-        left -= FW_CHUNK;
-    };
-    auto bump = [&](int &slot) { slot = slot + 1 == DEPTH ? 0 : slot + 1; };
-    Acc<T> acc;
-    int turn = 0;
 
-    // ---- GEMM1: tiles of 8 hidden units of one entry ----
-    if ((p.phases & FEW_GEMM1) && !dead) {
-        const int nt = p.H / 8, row_bytes = p.D * EB, nc = (row_bytes + FW_CHUNK - 1) / FW_CHUNK;
-        const int tiles = U * nt;
-        int li = blockIdx.x, lc = nc;  // tile being copied, its chunks copied so far
-        bool begun = false;
-        auto copy_next = [&]() {
-            if (lc == nc) {
-                if (begun) li += G;
-                begun = true;
-                lc = 0;
-                if (li < tiles) {
-                    const int u = li / nt, j = li - u * nt;
-                    const int e = s_entry[u] >> 16, f = first_of(u), cnt = first_of(u + 1) - f;
-                    const size_t at = ((size_t)e * p.H + (size_t)j * 8 + g) * row_bytes + col;
-                    lo = static_cast<const char *>(p.w1) + at;
-                    hi = static_cast<const char *>(p.w3) + at;
-                    has_row = g < cnt;
-                    row = static_cast<const char *>(p.x) +
-                          (has_row ? (size_t)(s_sorted[f + g] / p.k) * row_bytes : 0) + col;
-                    left = row_bytes - col;
-                    has_lo = has_hi = true;
+    const int g = lane >> 2, col = warp * FW_STEP + (lane & 3) * 16;
+    const char *any = static_cast<const char *>(p.x);  // a valid address for copies of nothing
+    const int nt2 = (p.D + FW_M - 1) / FW_M;
+    int in_slot = 0, out_slot = 0;  // ring slot of the next copies, of the next step
+    Acc<T> acc;
+
+    // Both products run the same loops (the second finds them in the instruction
+    // cache): a SEGMENT is a tile's rows against one entry, nc chunks long.
+    //   GEMM1: tile = 8 hidden units, whole tiles i = blockIdx.x, + G, ... of the
+    //          U nt of them, tiles of an entry running fastest
+    //   GEMM2: tile = 16 rows of out, entries running fastest, this CTA's part of
+    //          the line of chunks
+#pragma unroll 1
+    for (int second = 0; second < 2; ++second) {
+        if (!(p.phases & (second ? FEW_GEMM2 : FEW_GEMM1)) || dead || U == 0) continue;
+        const int row_bytes = (second ? p.H : p.D) * EB, nc = (row_bytes + FW_CHUNK - 1) / FW_CHUNK;
+        const int nt = second ? nt2 : p.H / 8;
+        int total, tile0, u0, c0 = 0;  // chunks of this CTA, and where they begin
+        int G2 = G, per_tile = 0, line = 0;
+        if (!second) {
+            const int tiles = U * nt, b = blockIdx.x;
+            total = b < tiles ? ((tiles - b + G - 1) / G) * nc : 0;
+            u0 = b / nt;
+            tile0 = b - u0 * nt;
+        } else {
+            per_tile = U * nc;
+            line = per_tile * nt;
+            // Cut anywhere, the parts are equal to a chunk, but tiles cut in two
+            // cost a handshake at the end, as long as FW_JOIN chunks take; whole
+            // tiles where that is no longer.
+            const bool whole_tiles = (nt + G - 1) / G * per_tile <= line / G + FW_JOIN;
+            const int unit = whole_tiles ? per_tile : 1, units = line / unit;
+            G2 = min(G, units);
+            const bool part_of = (int)blockIdx.x < G2;
+            const int first = part_of ? cut_first(units, G2, blockIdx.x) * unit : 0;
+            total = part_of ? cut_first(units, G2, blockIdx.x + 1) * unit - first : 0;
+            tile0 = first / per_tile;
+            const int r = first - tile0 * per_tile;
+            u0 = r / nc;
+            c0 = r - u0 * nc;
+            if (whole_tiles) line = 0;  // no tile is shared
+        }
+        const char *wlo = static_cast<const char *>(second ? p.w2 : p.w1);
+        const char *whi = second ? wlo + (size_t)8 * row_bytes : static_cast<const char *>(p.w3);
+        const char *rows = static_cast<const char *>(second ? p.h : p.x);
+        auto next_segment = [&](int &tile, int &u) {
+            if (second) {
+                if (++u == U) {
+                    u = 0;
+                    ++tile;
+                }
+            } else {
+                tile += G;
+                while (tile >= nt) {
+                    tile -= nt;
+                    ++u;
                 }
             }
-            if (li < tiles) {
-                copy_weights(in_slot);
+        };
+        // the copies' cursor: a segment, its next chunk, and this lane's 16 bytes
+        // there of rows g and g + 8 and of the entry's row g
+        int ltile = tile0, lu = u0, lc = c0, lleft = total, left = 0;
+        bool fresh = true, has_lo = false, has_hi = false, has_row = false;
+        const char *lo = any, *hi = any, *row = any;
+        auto open = [&]() {
+            const int e = s_entry[lu] >> 16, f = first_of(lu), cnt = first_of(lu + 1) - f;
+            const int r = second ? ltile * FW_M + g : ltile * 8 + g, R = second ? p.D : p.H;
+            const size_t at = ((size_t)e * R + r) * row_bytes + (size_t)lc * FW_CHUNK + col;
+            has_lo = r < R;
+            has_hi = !second || r + 8 < R;
+            has_row = g < cnt;
+            lo = wlo + at;
+            hi = whi + at;
+            const int n = f + (has_row ? g : 0);
+            row = rows + (size_t)(second ? n : s_token[n]) * row_bytes + (size_t)lc * FW_CHUNK + col;
+            left = row_bytes - lc * FW_CHUNK - col;
+            fresh = false;
+        };
+        auto copy_weights = [&](int slot) {
+            char *d = ring + slot * FW_SLOT + lane * 16;
+            const bool in_lo = left > 0 && has_lo, in_hi = left > 0 && has_hi;
+            copy16(d, in_lo ? lo : any, in_lo);
+            copy16(d + 512, in_hi ? hi : any, in_hi);
+        };
+        auto copy_row = [&](int slot) {
+            if (has_row)
+                copy16(ring + slot * FW_SLOT + 1024 + lane * 16, left > 0 ? row : any, left > 0);
+        };
+        auto bump = [&](int &slot) { slot = slot + 1 == DEPTH ? 0 : slot + 1; };
+        auto advance = [&]() {
+            lo += FW_CHUNK;
+            hi += FW_CHUNK;
+            row += FW_CHUNK;
+            left -= FW_CHUNK;
+            --lleft;
+            if (++lc == nc) {
+                lc = 0;
+                next_segment(ltile, lu);
+                fresh = true;
+            }
+        };
+        // first the weights' part of the first steps; the second product's go out
+        // before the barrier, its rows (h) behind it
+        int slot = in_slot;
+#pragma unroll 1
+        for (int i = 0; i < DEPTH - 1 && lleft > 0; ++i) {
+            if (fresh) open();
+            copy_weights(slot);
+            bump(slot);
+            advance();
+        }
+        if (second && p.phases == FEW_ALL) {
+            if (tid == 0) wait_count_bounded(&p.bars[1], G, &s_abort);
+            __syncthreads();
+            dead = s_abort;
+            if (dead) break;
+        }
+        ltile = tile0, lu = u0, lc = c0, lleft = total, fresh = true;
+#pragma unroll 1
+        for (int i = 0; i < DEPTH - 1; ++i) {
+            if (lleft > 0) {
+                if (fresh) open();
                 copy_row(in_slot);
                 bump(in_slot);
                 advance();
-                ++lc;
-            } else {
-                lc = 0;  // stay past the end
-                begun = false;
             }
-            copy_commit();
-        };
-        for (int i = 0; i < DEPTH - 1; ++i) copy_next();
-        for (int i = blockIdx.x; i < tiles; i += G) {
-            const int u = i / nt, j = i - u * nt;
+            copy_commit();  // the first group holds all the weights so far
+        }
+        if (second) {
+            for (int i = lane; i < FW_M * p.T; i += 32) s_out[warp * FW_M * p.T + i] = 0.f;
+            __syncwarp();
+        }
+        T *out = static_cast<T *>(p.out);
+        int tile = tile0, u = u0, c = c0, turn = 0;
+        bool from_start = u0 == 0 && c0 == 0;
+        int cut[2] = {-1, -1};  // tiles that others share: the first, the last
+#pragma unroll 1
+        for (int n = 0; n < total;) {
             const int f = first_of(u), cnt = first_of(u + 1) - f;
             acc.clear();
-            for (int c = 0; c < nc; ++c) {
+#pragma unroll 1
+            do {
                 copy_wait<DEPTH - 2>();
                 __syncwarp();
                 acc.step(ring + out_slot * FW_SLOT, cnt, lane);
                 bump(out_slot);
-                copy_next();  // into the slot read a step ago
-            }
-            float v[4];
-            acc.get(v, lane);
-            float4 *red = s_red + turn * FW_WARPS * 32;
-            turn ^= 1;  // the other buffer's readers are behind the barrier before this one
-            red[warp * 32 + lane] = make_float4(v[0], v[1], v[2], v[3]);
-            __syncthreads();
-            if (tid < 64) {
-                // thread (lane, half): gate and up of unit lane / 4 for row 2 (lane % 4) + half
-                const int half = tid >> 5, n = 2 * (lane & 3) + half;
-                float gate = 0.f, up = 0.f;
-#pragma unroll
-                for (int w = 0; w < FW_WARPS; ++w) {
-                    const float *r = reinterpret_cast<const float *>(&red[w * 32 + lane]);
-                    gate += r[half];
-                    up += r[2 + half];
-                }
-                if (n < cnt)
-                    static_cast<T *>(p.h)[(size_t)(f + n) * p.H + j * 8 + g] =
-                        Elem<T>::round(gate / (1.f + expf(-gate)) * up);
-            }
-        }
-        copy_wait<0>();
-        __syncwarp();
-        if (p.phases == FEW_ALL) {
-            __syncthreads();
-            if (tid == 0) {
-                fence_acq_rel_gpu();
-                red_release_gpu_add(&p.bars[1], 1);
-            }
-            griddep_launch_dependents();
-        }
-    }
-
-    // ---- GEMM2: this CTA's part of the line of (tile, entry, chunk) ----
-    const int nt2 = (p.D + FW_M - 1) / FW_M;
-    if ((p.phases & FEW_GEMM2) && !dead && U == 0) {  // no token has an expert here
-        T *out = static_cast<T *>(p.out);
-        for (long long i = (long long)blockIdx.x * FW_THREADS + tid; i < (long long)p.T * p.D;
-             i += (long long)G * FW_THREADS)
-            out[i] = Elem<T>::round(0.f);
-    } else if ((p.phases & FEW_GEMM2) && !dead) {
-        const int row_bytes = p.H * EB, nc = (row_bytes + FW_CHUNK - 1) / FW_CHUNK;
-        const long long per_tile = (long long)U * nc, line = per_tile * nt2;
-        // CTAs that take a part: no more than there are chunks, so that none is empty
-        const int G2 = (int)min((long long)G, line);
-        const bool part_of = (int)blockIdx.x < G2;
-        const long long first = part_of ? line * blockIdx.x / G2 : 0;
-        const int total = part_of ? (int)(line * (blockIdx.x + 1) / G2 - first) : 0;
-        const int dt0 = (int)(first / per_tile);
-        const int u0 = (int)((first - dt0 * per_tile) / nc), c0 = (int)(first - dt0 * per_tile) - u0 * nc;
-        // copy cursor
-        int ln = 0, ldt = dt0, lu = u0, lc = c0;
-        auto set_weights = [&](int dt, int u, int c) {
-            const int e = s_entry[u] >> 16, d = dt * FW_M + g;
-            const size_t at = ((size_t)e * p.D + d) * row_bytes + (size_t)c * FW_CHUNK + col;
-            has_lo = d < p.D;  // D is a multiple of 8: rows g all are, rows g + 8 may not be
-            has_hi = d + 8 < p.D;
-            lo = static_cast<const char *>(p.w2) + (has_lo ? at : 0);
-            hi = static_cast<const char *>(p.w2) + (has_hi ? at + (size_t)8 * row_bytes : 0);
-            left = row_bytes - c * FW_CHUNK - col;
-        };
-        auto set_row = [&](int u, int c) {
-            const int f = first_of(u), cnt = first_of(u + 1) - f;
-            has_row = g < cnt;
-            row = static_cast<const char *>(p.h) + (size_t)(f + (has_row ? g : 0)) * row_bytes +
-                  (size_t)c * FW_CHUNK + col;
-            left = row_bytes - c * FW_CHUNK - col;
-        };
-        auto step_on = [&](int &dt, int &u, int &c) {  // true: another entry or tile begins
-            if (++c < nc) return false;
-            c = 0;
-            if (++u == U) {
-                u = 0;
-                ++dt;
-            }
-            return true;
-        };
-        // the weights of the first steps go out before the barrier, the rows (h) behind it
-        const int ahead = min(DEPTH - 1, total);
-        int dt = dt0, u = u0, c = c0;
-        for (int i = 0; i < ahead; ++i) {
-            if (i == 0 || c == 0) set_weights(dt, u, c);
-            copy_weights((in_slot + i) % DEPTH);
-            advance();
-            step_on(dt, u, c);
-        }
-        if (p.phases == FEW_ALL) {
-            if (tid == 0) wait_count_bounded(&p.bars[1], G, &s_abort);
-            __syncthreads();
-            dead = s_abort;
-        }
-        if (!dead) {
-            for (int i = 0; i < DEPTH - 1; ++i) {
-                if (i < ahead) {
-                    if (i == 0 || lc == 0) set_row(lu, lc);
-                    copy_row(in_slot);
-                    bump(in_slot);
-                    advance();
-                    step_on(ldt, lu, lc);
-                    ++ln;
-                }
-                copy_commit();
-            }
-            if (ln < total) {
-                set_weights(ldt, lu, lc);
-                set_row(lu, lc);
-            }
-            auto copy_next = [&]() {
-                if (ln < total) {
+                if (lleft > 0) {  // into the slot read a step ago
+                    if (fresh) open();
                     copy_weights(in_slot);
                     copy_row(in_slot);
                     bump(in_slot);
                     advance();
-                    ++ln;
-                    if (step_on(ldt, lu, lc) && ln < total) {
-                        set_weights(ldt, lu, lc);
-                        set_row(lu, lc);
-                    }
                 }
                 copy_commit();
-            };
-            for (int i = lane; i < FW_M * p.T; i += 32) s_out[warp * FW_M * p.T + i] = 0.f;
-            __syncwarp();
-            T *out = static_cast<T *>(p.out);
-            dt = dt0, u = u0, c = c0;
-            int cut[2] = {-1, -1};  // tiles that others share: the first, the last
-            for (int n = 0; n < total;) {
-                const bool from_start = u == 0 && c == 0;
-                bool to_end = false;
-                while (n < total && !to_end) {  // this CTA's part of one entry
-                    const int f = first_of(u), cnt = first_of(u + 1) - f;
-                    acc.clear();
-                    bool more = true;
-                    while (more && n < total) {
-                        copy_wait<DEPTH - 2>();
-                        __syncwarp();
-                        acc.step(ring + out_slot * FW_SLOT, cnt, lane);
-                        bump(out_slot);
-                        copy_next();
-                        ++n;
-                        more = ++c < nc;
-                    }
-                    if (!more) {
-                        c = 0;
-                        to_end = ++u == U;
-                    }
-                    float v[4];
-                    acc.get(v, lane);
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int m = 2 * (lane & 3) + half;
-                        if (m >= cnt) continue;
-                        const int slot = s_sorted[f + m];
-                        float *o = s_out + (warp * p.T + slot / p.k) * FW_M;
-                        o[g] = fmaf(s_w[slot], v[half], o[g]);
-                        o[g + 8] = fmaf(s_w[slot], v[2 + half], o[g + 8]);
-                    }
-                    __syncwarp();
-                }
-                // the warps' sums; a tile that others share goes through memory
-                const bool whole = from_start && to_end;
-                float *part = p.part + ((size_t)blockIdx.x * 2 + (dt == dt0 ? 0 : 1)) * p.T * FW_M;
-                if (!whole) cut[dt == dt0 ? 0 : 1] = dt;
+                ++n;
+            } while (++c < nc && n < total);
+            float v[4];
+            acc.get(v, lane);
+            if (!second) {
+                float4 *red = s_red + turn * FW_WARPS * 32;
+                turn ^= 1;  // the other buffer's readers are behind the barrier before this one
+                red[warp * 32 + lane] = make_float4(v[0], v[1], v[2], v[3]);
                 __syncthreads();
-                for (int o = tid; o < FW_M * p.T; o += FW_THREADS) {
-                    float sum = 0.f;
+                if (tid < 64) {
+                    // thread (lane, half): gate and up of unit lane / 4 for row 2 (lane % 4) + half
+                    const int half = tid >> 5, m = 2 * (lane & 3) + half;
+                    float gate = 0.f, up = 0.f;
 #pragma unroll
                     for (int w = 0; w < FW_WARPS; ++w) {
-                        sum += s_out[w * FW_M * p.T + o];
-                        s_out[w * FW_M * p.T + o] = 0.f;
+                        const float *r = reinterpret_cast<const float *>(&red[w * 32 + lane]);
+                        gate += r[half];
+                        up += r[2 + half];
                     }
-                    const int d = dt * FW_M + o % FW_M;
-                    if (!whole)
-                        part[o] = sum;
-                    else if (d < p.D)
-                        out[(size_t)(o / FW_M) * p.D + d] = Elem<T>::round(sum);
+                    if (m < cnt)
+                        static_cast<T *>(p.h)[(size_t)(f + m) * p.H + tile * 8 + g] =
+                            Elem<T>::round(gate / (1.f + expf(-gate)) * up);
                 }
-                __syncthreads();
-                u = 0;
-                ++dt;
+                c = 0;
+                next_segment(tile, u);
+                continue;
             }
-            // shared tiles: the CTA that comes last adds the parts, in order
-            int ca[2], cb[2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if (cut[i] < 0) continue;
-                const long long a0 = cut[i] * per_tile, a1 = a0 + per_tile;
-                ca[i] = cb[i] = (int)blockIdx.x;
-                while (ca[i] > 0 && line * ca[i] / G2 > a0) --ca[i];
-                while (line * (cb[i] + 1) / G2 < a1) ++cb[i];
+            for (int half = 0; half < 2; ++half) {
+                const int m = 2 * (lane & 3) + half;
+                if (m >= cnt) continue;
+                float *o = s_out + (warp * p.T + s_token[f + m]) * FW_M;
+                const float w = s_w[s_sorted[f + m]];
+                o[g] = fmaf(w, v[half], o[g]);
+                o[g + 8] = fmaf(w, v[2 + half], o[g + 8]);
             }
-            if (tid < 2) {
-                const int mine = tid == 0 ? cut[0] : cut[1];
-                if (mine >= 0) {
-                    fence_acq_rel_gpu();
-                    const int before = atomicAdd(&p.tile_count[mine], 1);
-                    fence_acq_rel_gpu();
-                    s_last[tid] = before == (tid == 0 ? cb[0] - ca[0] : cb[1] - ca[1]);
-                    if (s_last[tid]) p.tile_count[mine] = 0;
+            __syncwarp();
+            bool to_end = false;
+            if (c == nc) {
+                c = 0;
+                to_end = ++u == U;
+            }
+            if (!to_end && n < total) continue;
+            // the warps' sums; a tile that others share goes through memory
+            const bool whole = from_start && to_end;
+            const int side = tile == tile0 ? 0 : 1;
+            float *part = p.part + ((size_t)blockIdx.x * 2 + side) * p.T * FW_M;
+            if (!whole) cut[side] = tile;
+            __syncthreads();
+            for (int o = tid; o < FW_M * p.T; o += FW_THREADS) {
+                float sum = 0.f;
+#pragma unroll
+                for (int w = 0; w < FW_WARPS; ++w) {
+                    sum += s_out[w * FW_M * p.T + o];
+                    s_out[w * FW_M * p.T + o] = 0.f;
                 }
+                const int d = tile * FW_M + o % FW_M;
+                if (!whole)
+                    part[o] = sum;
+                else if (d < p.D)
+                    out[(size_t)(o / FW_M) * p.D + d] = Elem<T>::round(sum);
             }
             __syncthreads();
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if (cut[i] < 0 || !s_last[i]) continue;
-                for (int o = tid; o < FW_M * p.T; o += FW_THREADS) {
-                    float sum = 0.f;
-                    for (int b = ca[i]; b <= cb[i]; ++b) {
-                        const int theirs = (int)(line * b / G2 / per_tile);
-                        sum += __ldcg(p.part + ((size_t)b * 2 + (cut[i] == theirs ? 0 : 1)) * p.T * FW_M + o);
-                    }
-                    const int d = cut[i] * FW_M + o % FW_M;
-                    if (d < p.D) out[(size_t)(o / FW_M) * p.D + d] = Elem<T>::round(sum);
-                }
-            }
+            from_start = true;
+            u = 0;
+            ++tile;
         }
         copy_wait<0>();
+        __syncthreads();
+        if (!second) {
+            if (p.phases == FEW_ALL) {
+                if (tid == 0) {
+                    fence_acq_rel_gpu();
+                    red_release_gpu_add(&p.bars[1], 1);
+                }
+                griddep_launch_dependents();
+            }
+            continue;
+        }
+        if (line == 0 || (cut[0] < 0 && cut[1] < 0)) continue;
+        // shared tiles: the CTA that comes last adds the parts, in order
+        int ca[2], cb[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (cut[i] < 0) continue;
+            ca[i] = cut_holder(line, G2, cut[i] * per_tile);
+            cb[i] = cut_holder(line, G2, (cut[i] + 1) * per_tile - 1);
+        }
+        if (tid < 2) {
+            const int mine = tid == 0 ? cut[0] : cut[1];
+            if (mine >= 0) {
+                fence_acq_rel_gpu();
+                const int before = atomicAdd(&p.tile_count[mine], 1);
+                fence_acq_rel_gpu();
+                s_last[tid] = before == (tid == 0 ? cb[0] - ca[0] : cb[1] - ca[1]);
+                if (s_last[tid]) p.tile_count[mine] = 0;
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (cut[i] < 0 || !s_last[i]) continue;
+            for (int o = tid; o < FW_M * p.T; o += FW_THREADS) {
+                float sum = 0.f;
+                for (int b = ca[i]; b <= cb[i]; ++b) {
+                    const int theirs = cut_first(line, G2, b) / per_tile;
+                    sum += __ldcg(p.part + ((size_t)b * 2 + (cut[i] == theirs ? 0 : 1)) * p.T * FW_M + o);
+                }
+                const int d = cut[i] * FW_M + o % FW_M;
+                if (d < p.D) out[(size_t)(o / FW_M) * p.D + d] = Elem<T>::round(sum);
+            }
+        }
     }
+    if (U == 0 && !dead && (p.phases & FEW_GEMM2)) {  // no token has an expert here
+        T *out = static_cast<T *>(p.out);
+        for (long long i = (long long)blockIdx.x * FW_THREADS + tid; i < (long long)p.T * p.D;
+             i += (long long)G * FW_THREADS)
+            out[i] = Elem<T>::round(0.f);
+    }
+    copy_wait<0>();
     __syncthreads();
     if (tid == 0) {
         const bool aborted = s_abort;
