@@ -136,7 +136,7 @@ template <> struct Acc<__nv_bfloat16> {
         mma_bf16(c, lo.x, hi.x, lo.y, hi.y, bb.x, bb.y);
         mma_bf16(c, lo.z, hi.z, lo.w, hi.w, bb.z, bb.w);
     }
-    __device__ __forceinline__ void get(float (&v)[4], int) const {
+    __device__ __forceinline__ void get(float (&v)[4], int, int) const {
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = c[i];
     }
@@ -160,10 +160,11 @@ template <> struct Acc<float> {
         }
     }
     // the four lanes of a row hold every fourth 16 bytes of it
-    __device__ __forceinline__ void get(float (&v)[4], int lane) {
+    __device__ __forceinline__ void get(float (&v)[4], int cnt, int lane) {
         const int q = lane & 3;
 #pragma unroll
         for (int n = 0; n < FW_N; ++n) {
+            if (n >= cnt) break;
 #pragma unroll
             for (int o = 1; o < 4; o <<= 1) {
                 lo[n] += __shfl_xor_sync(0xffffffffu, lo[n], o);
@@ -352,6 +353,7 @@ few_layer_kernel(const FewParams p) {
     extern __shared__ __align__(128) char smem[];
     __shared__ volatile int s_abort;
     __shared__ int s_count, s_last[2];
+    __shared__ uint64_t s_full[2], s_free[2];  // the buffers of the warps' sums
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = gridDim.x;
     const int slots = p.T * p.k;
     char *ring = smem + warp * DEPTH * FW_SLOT;  // this warp's
@@ -365,7 +367,14 @@ few_layer_kernel(const FewParams p) {
     constexpr int EB = (int)sizeof(T);
 
     griddep_wait();
-    if (tid == 0) s_abort = 0;
+    if (tid == 0) {
+        s_abort = 0;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], FW_WARPS);
+            mbar_init(&s_free[i], 1);
+        }
+        fence_mbarrier_init();
+    }
     __syncthreads();
 
     // ---- route ----
@@ -548,26 +557,37 @@ few_layer_kernel(const FewParams p) {
                 ++n;
             } while (++c < nc && n < total);
             float v[4];
-            acc.get(v, lane);
+            acc.get(v, cnt, lane);
             if (!second) {
-                float4 *red = s_red + turn * FW_WARPS * 32;
-                turn ^= 1;  // the other buffer's readers are behind the barrier before this one
+                // The warps' sums meet in one of two buffers; one warp, another for
+                // every tile, adds them up while the rest go on with the next tile.
+                const int buf = turn & 1;
+                const uint32_t round = (uint32_t)(turn >> 1) & 1u;
+                float4 *red = s_red + buf * FW_WARPS * 32;
+                mbar_wait_bounded(&s_free[buf], round ^ 1u, &s_abort);
                 red[warp * 32 + lane] = make_float4(v[0], v[1], v[2], v[3]);
-                __syncthreads();
-                if (tid < 64) {
-                    // thread (lane, half): gate and up of unit lane / 4 for row 2 (lane % 4) + half
-                    const int half = tid >> 5, m = 2 * (lane & 3) + half;
-                    float gate = 0.f, up = 0.f;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_full[buf]);
+                if (turn % FW_WARPS == warp) {
+                    mbar_wait_bounded(&s_full[buf], round, &s_abort);
+                    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                     for (int w = 0; w < FW_WARPS; ++w) {
-                        const float *r = reinterpret_cast<const float *>(&red[w * 32 + lane]);
-                        gate += r[half];
-                        up += r[2 + half];
+                        const float4 r = red[w * 32 + lane];
+                        sum.x += r.x;
+                        sum.y += r.y;
+                        sum.z += r.z;
+                        sum.w += r.w;
                     }
-                    if (m < cnt)
-                        static_cast<T *>(p.h)[(size_t)(f + m) * p.H + tile * 8 + g] =
-                            Elem<T>::round(gate / (1.f + expf(-gate)) * up);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s_free[buf]);
+                    // gate (x, y) and up (z, w) of unit g for the entry's rows 2 q, 2 q + 1
+                    const int m = 2 * (lane & 3);
+                    T *h = static_cast<T *>(p.h) + (size_t)(f + m) * p.H + tile * 8 + g;
+                    if (m < cnt) h[0] = Elem<T>::round(sum.x / (1.f + expf(-sum.x)) * sum.z);
+                    if (m + 1 < cnt) h[p.H] = Elem<T>::round(sum.y / (1.f + expf(-sum.y)) * sum.w);
                 }
+                ++turn;
                 c = 0;
                 next_segment(tile, u);
                 continue;
