@@ -24,11 +24,11 @@
 // The 16 weight rows of a tile are the M side of mma.sync m16n8k16 and the
 // entry's rows the N = 8 side: at 8 rows per weight the tensor pipe idles either
 // way, and register accumulators need no TMEM round trip.  The CTA's 16 warps
-// split k: of every 1 KB of a row a warp takes 64 bytes, and a lane copies its
-// own 16 bytes of a row (the sum over k does not care which k meet in one
-// instruction, as long as both operands agree) with cp.async into a ring that it
-// alone reads back, so the stream needs no barrier but the sum over the warps at
-// a tile's end, and the copies of the next tiles run through it.  (Bulk copies by
+// split k: of every 2 KB of a row a warp takes 128 bytes, copied with cp.async
+// into a ring of its own and read back as 16-byte pieces (the sum over k does not
+// care which k meet in one instruction, as long as both operands agree), so the
+// stream needs no barrier but the sum over the warps at a tile's end, and the
+// copies of the next tiles run through it.  (Bulk copies by
 // a producer warp: each costs 55 ns to issue whatever its size, so 16 row pieces
 // of 1 KB per stage reached 39% of the copy rate, of 4 KB 97% in long rows.)
 // fp32 layers use the same tiles with fused multiply-adds.
@@ -51,12 +51,11 @@ namespace {
 
 constexpr int FW_WARPS = 16;
 constexpr int FW_THREADS = 32 * FW_WARPS;
-constexpr int FW_STEP = 64;                    // bytes of a row that a warp takes at once
+constexpr int FW_STEP = 128;                   // bytes of a row that a warp takes at once
 constexpr int FW_CHUNK = FW_STEP * FW_WARPS;   // and the CTA
 constexpr int FW_M = 16;                       // weight rows per tile
 constexpr int FW_N = 8;                        // rows of an entry
-constexpr int FW_JOIN = 8;                     // chunks as long as joining a shared tile's parts takes
-constexpr int FW_SLOT = 3 * 512;               // a warp's step in the ring: 8 + 8 weight rows, 8 rows
+constexpr int FW_JOIN = 4;                     // chunks as long as joining a shared tile's parts takes
 
 enum { FEW_ROUTE = 1, FEW_GEMM1 = 2, FEW_GEMM2 = 4, FEW_ALL = 7 };
 
@@ -119,22 +118,32 @@ template <> __device__ __forceinline__ float dot16<float>(uint4 a, uint4 b, floa
     return fmaf(__uint_as_float(a.w), __uint_as_float(b.w), c);
 }
 
-// What a lane of a consumer warp has summed of a 16 x 8 tile: in the layout of
-// the mma's accumulator, rows g and g + 8, columns 2 q and 2 q + 1 (g = lane / 4,
-// q = lane % 4).
+// A step in the ring: 16 weight rows, then the entry's rows, 128 bytes of each in
+// 16-byte pieces.  Odd rows have the halves exchanged: lanes 8 i .. 8 i + 7 read
+// 64 bytes of two rows at once, which so lie in different banks.
+__device__ __forceinline__ int piece_at(int row, int piece) {
+    return row * FW_STEP + (piece ^ ((row & 1) << 2)) * 16;
+}
+
+// What a lane of a warp has summed of a 16 x 8 tile: in the layout of the mma's
+// accumulator, rows g and g + 8, columns 2 q and 2 q + 1 (g = lane / 4, q = lane % 4).
 template <typename T> struct Acc;
 
 template <> struct Acc<__nv_bfloat16> {
     float c[4];
     __device__ __forceinline__ void clear() { c[0] = c[1] = c[2] = c[3] = 0.f; }
-    // one step: slot holds this lane's 16 bytes of rows g and g + 8 and of the entry's row g
-    __device__ __forceinline__ void step(const char *slot, int, int lane) {
-        const uint4 lo = *reinterpret_cast<const uint4 *>(slot + lane * 16);
-        const uint4 hi = *reinterpret_cast<const uint4 *>(slot + 512 + lane * 16);
-        // columns past the entry's rows hold anything; they are not stored
-        const uint4 bb = *reinterpret_cast<const uint4 *>(slot + 1024 + lane * 16);
-        mma_bf16(c, lo.x, hi.x, lo.y, hi.y, bb.x, bb.y);
-        mma_bf16(c, lo.z, hi.z, lo.w, hi.w, bb.z, bb.w);
+    __device__ __forceinline__ void step(const char *slot, int cnt, int lane) {
+        const int g = lane >> 2;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int at = piece_at(g, (lane & 3) + 4 * half);
+            const uint4 lo = *reinterpret_cast<const uint4 *>(slot + at);
+            const uint4 hi = *reinterpret_cast<const uint4 *>(slot + 8 * FW_STEP + at);
+            uint4 bb = make_uint4(0, 0, 0, 0);
+            if (g < cnt) bb = *reinterpret_cast<const uint4 *>(slot + FW_M * FW_STEP + at);
+            mma_bf16(c, lo.x, hi.x, lo.y, hi.y, bb.x, bb.y);
+            mma_bf16(c, lo.z, hi.z, lo.w, hi.w, bb.z, bb.w);
+        }
     }
     __device__ __forceinline__ void get(float (&v)[4], int, int) const {
 #pragma unroll
@@ -149,14 +158,19 @@ template <> struct Acc<float> {
         for (int n = 0; n < FW_N; ++n) lo[n] = hi[n] = 0.f;
     }
     __device__ __forceinline__ void step(const char *slot, int cnt, int lane) {
-        const uint4 al = *reinterpret_cast<const uint4 *>(slot + lane * 16);
-        const uint4 ah = *reinterpret_cast<const uint4 *>(slot + 512 + lane * 16);
 #pragma unroll
-        for (int n = 0; n < FW_N; ++n) {
-            if (n >= cnt) break;
-            const uint4 bb = *reinterpret_cast<const uint4 *>(slot + 1024 + n * 64 + (lane & 3) * 16);
-            lo[n] = dot16<float>(al, bb, lo[n]);
-            hi[n] = dot16<float>(ah, bb, hi[n]);
+        for (int half = 0; half < 2; ++half) {
+            const int piece = (lane & 3) + 4 * half, at = piece_at(lane >> 2, piece);
+            const uint4 al = *reinterpret_cast<const uint4 *>(slot + at);
+            const uint4 ah = *reinterpret_cast<const uint4 *>(slot + 8 * FW_STEP + at);
+#pragma unroll
+            for (int n = 0; n < FW_N; ++n) {
+                if (n >= cnt) break;
+                const uint4 bb =
+                    *reinterpret_cast<const uint4 *>(slot + FW_M * FW_STEP + piece_at(n, piece));
+                lo[n] = dot16<float>(al, bb, lo[n]);
+                hi[n] = dot16<float>(ah, bb, hi[n]);
+            }
         }
     }
     // the four lanes of a row hold every fourth 16 bytes of it
@@ -181,11 +195,14 @@ template <> struct Acc<float> {
     }
 };
 
-// Shared memory, in bytes: the ring, the warps' sums, out's sums, the tables of
-// the T k (token, slot) pairs.
-__host__ __device__ inline int few_ring_bytes(int depth) { return FW_WARPS * depth * FW_SLOT; }
-constexpr int kFewRed = 2 * FW_WARPS * 32 * 16;
-__host__ __device__ inline int few_out_bytes(int T) { return FW_WARPS * FW_M * T * 4; }
+// Shared memory, in bytes: the ring, the warps' sums (GEMM1's two buffers of a
+// tile, then GEMM2's of out), the tables of the T k (token, slot) pairs.
+__host__ __device__ inline int few_slot_bytes(int T) {
+    return (FW_M + (T < FW_N ? T : FW_N)) * FW_STEP;
+}
+__host__ __device__ inline int few_sum_bytes(int T) {
+    return FW_WARPS * FW_M * 4 * (T > 16 ? T : 16);
+}
 __host__ __device__ inline int few_table_bytes(int slots) { return slots * 20 + 16; }
 
 // Keys of tokens t0 .. t0 + NT - 1 for one expert: this warp's share (v0, v0 +
@@ -356,10 +373,11 @@ few_layer_kernel(const FewParams p) {
     __shared__ uint64_t s_full[2], s_free[2];  // the buffers of the warps' sums
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = gridDim.x;
     const int slots = p.T * p.k;
-    char *ring = smem + warp * DEPTH * FW_SLOT;  // this warp's
-    float4 *s_red = reinterpret_cast<float4 *>(smem + few_ring_bytes(DEPTH));  // [2][warps][32]
-    float *s_out = reinterpret_cast<float *>(s_red + 2 * FW_WARPS * 32);       // [warps][T][16]
-    float *s_w = s_out + FW_WARPS * FW_M * p.T;                                // [slots]
+    const int slot_bytes = few_slot_bytes(p.T);
+    char *ring = smem + warp * DEPTH * slot_bytes;  // this warp's
+    float4 *s_red = reinterpret_cast<float4 *>(smem + FW_WARPS * DEPTH * slot_bytes);  // [2][warps][32]
+    float *s_out = reinterpret_cast<float *>(s_red);                                   // [warps][T][16]
+    float *s_w = s_out + few_sum_bytes(p.T) / 4;                                       // [slots]
     int *s_idx = reinterpret_cast<int *>(s_w + slots);                         // [slots]
     int *s_sorted = s_idx + slots;                                             // [slots]
     int *s_token = s_sorted + slots;                                           // [slots]
@@ -400,7 +418,8 @@ few_layer_kernel(const FewParams p) {
     }
     auto first_of = [&](int u) { return (int)(s_entry[u] & 0xffffu); };
 
-    const int g = lane >> 2, col = warp * FW_STEP + (lane & 3) * 16;
+    const int g = lane >> 2;
+    const int r4 = lane >> 3, c16 = lane & 7;  // a copy takes 4 rows' 128 bytes
     const char *any = static_cast<const char *>(p.x);  // a valid address for copies of nothing
     const int nt2 = (p.D + FW_M - 1) / FW_M;
     int in_slot = 0, out_slot = 0;  // ring slot of the next copies, of the next step
@@ -442,9 +461,14 @@ few_layer_kernel(const FewParams p) {
             c0 = r - u0 * nc;
             if (whole_tiles) line = 0;  // no tile is shared
         }
-        const char *wlo = static_cast<const char *>(second ? p.w2 : p.w1);
-        const char *whi = second ? wlo + (size_t)8 * row_bytes : static_cast<const char *>(p.w3);
+        const char *weights = static_cast<const char *>(second ? p.w2 : p.w1);
         const char *rows = static_cast<const char *>(second ? p.h : p.x);
+        // from rows g of a tile to its rows g + 8: the up weights, or eight rows on
+        const ptrdiff_t to_hi = second ? (ptrdiff_t)8 * row_bytes
+                                       : static_cast<const char *>(p.w3) - weights;
+        const ptrdiff_t to_4 = (ptrdiff_t)4 * row_bytes;
+        const int tile_rows = second ? FW_M : 8, R = second ? p.D : p.H;
+        const int steps = (row_bytes + FW_STEP - 1) / FW_STEP;
         auto next_segment = [&](int &tile, int &u) {
             if (second) {
                 if (++u == U) {
@@ -459,44 +483,51 @@ few_layer_kernel(const FewParams p) {
                 }
             }
         };
-        // the copies' cursor: a segment, its next chunk, and this lane's 16 bytes
-        // there of rows g and g + 8 and of the entry's row g
-        int ltile = tile0, lu = u0, lc = c0, lleft = total, left = 0;
-        bool fresh = true, has_lo = false, has_hi = false, has_row = false;
-        const char *lo = any, *hi = any, *row = any;
+        // The copies' cursor: a segment, its next chunk, and this lane's pieces
+        // there of rows r4, r4 + 4 (and 8 on) and of the entry's rows r4, r4 + 4.
+        // The warps take turns at a segment's first step: where a row is no whole
+        // number of chunks, each gets as many steps as the others.
+        int ltile = tile0, lu = u0, lc = c0, lleft = total, left = 0, turn0 = 0;
+        bool fresh = true, has_hi = false;
+        int has_rows = 0;
+        const char *lo = any, *row = any, *row_4 = any;
         auto open = [&]() {
             const int e = s_entry[lu] >> 16, f = first_of(lu), cnt = first_of(lu + 1) - f;
-            const int r = second ? ltile * FW_M + g : ltile * 8 + g, R = second ? p.D : p.H;
-            const size_t at = ((size_t)e * R + r) * row_bytes + (size_t)lc * FW_CHUNK + col;
-            has_lo = r < R;
-            has_hi = !second || r + 8 < R;
-            has_row = g < cnt;
-            lo = wlo + at;
-            hi = whi + at;
-            const int n = f + (has_row ? g : 0);
-            row = rows + (size_t)(second ? n : s_token[n]) * row_bytes + (size_t)lc * FW_CHUNK + col;
-            left = row_bytes - lc * FW_CHUNK - col;
+            const int first_row = ltile * tile_rows;
+            const int col = lc * FW_CHUNK + ((warp + turn0) & (FW_WARPS - 1)) * FW_STEP + c16 * 16;
+            lo = weights + ((size_t)e * R + first_row + r4) * row_bytes + col;
+            has_hi = !second || first_row + 8 < R;  // R is a multiple of 8
+            has_rows = cnt - r4;  // > 0: row r4 is there, > 4: row r4 + 4 too
+            const int n = f + (has_rows > 0 ? r4 : 0), n4 = f + (has_rows > 4 ? r4 + 4 : 0);
+            row = rows + (size_t)(second ? n : s_token[n]) * row_bytes + col;
+            row_4 = rows + (size_t)(second ? n4 : s_token[n4]) * row_bytes + col;
+            left = row_bytes - col;
             fresh = false;
         };
+        auto put = [&](int slot, int r, const char *src, bool in) {
+            copy16(ring + slot * slot_bytes + piece_at(r, c16), in ? src : any, in);
+        };
         auto copy_weights = [&](int slot) {
-            char *d = ring + slot * FW_SLOT + lane * 16;
-            const bool in_lo = left > 0 && has_lo, in_hi = left > 0 && has_hi;
-            copy16(d, in_lo ? lo : any, in_lo);
-            copy16(d + 512, in_hi ? hi : any, in_hi);
+            const bool in = left > 0;
+            put(slot, r4, lo, in);
+            put(slot, r4 + 4, lo + to_4, in);
+            put(slot, r4 + 8, lo + to_hi, in && has_hi);
+            put(slot, r4 + 12, lo + to_hi + to_4, in && has_hi);
         };
         auto copy_row = [&](int slot) {
-            if (has_row)
-                copy16(ring + slot * FW_SLOT + 1024 + lane * 16, left > 0 ? row : any, left > 0);
+            if (has_rows > 0) put(slot, FW_M + r4, row, left > 0);
+            if (has_rows > 4) put(slot, FW_M + r4 + 4, row_4, left > 0);
         };
         auto bump = [&](int &slot) { slot = slot + 1 == DEPTH ? 0 : slot + 1; };
         auto advance = [&]() {
             lo += FW_CHUNK;
-            hi += FW_CHUNK;
             row += FW_CHUNK;
+            row_4 += FW_CHUNK;
             left -= FW_CHUNK;
             --lleft;
             if (++lc == nc) {
                 lc = 0;
+                turn0 += steps;
                 next_segment(ltile, lu);
                 fresh = true;
             }
@@ -517,7 +548,7 @@ few_layer_kernel(const FewParams p) {
             dead = s_abort;
             if (dead) break;
         }
-        ltile = tile0, lu = u0, lc = c0, lleft = total, fresh = true;
+        ltile = tile0, lu = u0, lc = c0, lleft = total, turn0 = 0, fresh = true;
 #pragma unroll 1
         for (int i = 0; i < DEPTH - 1; ++i) {
             if (lleft > 0) {
@@ -544,7 +575,7 @@ few_layer_kernel(const FewParams p) {
             do {
                 copy_wait<DEPTH - 2>();
                 __syncwarp();
-                acc.step(ring + out_slot * FW_SLOT, cnt, lane);
+                acc.step(ring + out_slot * slot_bytes, cnt, lane);
                 bump(out_slot);
                 if (lleft > 0) {  // into the slot read a step ago
                     if (fresh) open();
@@ -733,13 +764,20 @@ cudaError_t launch_few_layer(const FewLayer &f, cudaStream_t stream) {
     p.renorm = f.renorm;
     p.n_group = f.n_group;
     p.topk_group = f.topk_group;
-    // 8 steps of every warp in flight (128 KB of weights per SM), 6 where many
-    // tokens' sums take the shared memory
-    const bool deep = f.T <= 8;
-    const size_t smem = (size_t)few_ring_bytes(deep ? 8 : 6) + kFewRed + few_out_bytes(f.T) +
+    // As many steps of every warp in flight as the shared memory takes: 5 of them
+    // (160 KB of weights per SM) for one token, 4 up to 4 tokens, 3 up to 16, 2
+    // above, where the sums of out for all the tokens take their place.
+    const int depth = f.T == 1 ? 6 : f.T <= 4 ? 5 : f.T <= 16 ? 4 : 3;
+    const size_t smem = (size_t)FW_WARPS * depth * few_slot_bytes(f.T) + few_sum_bytes(f.T) +
                         few_table_bytes(f.T * f.k);
-    auto fn = f.is_bf16 ? (deep ? few_layer_kernel<__nv_bfloat16, 8> : few_layer_kernel<__nv_bfloat16, 6>)
-                        : (deep ? few_layer_kernel<float, 8> : few_layer_kernel<float, 6>);
+    auto fn = f.is_bf16 ? (depth == 6   ? few_layer_kernel<__nv_bfloat16, 6>
+                           : depth == 5 ? few_layer_kernel<__nv_bfloat16, 5>
+                           : depth == 4 ? few_layer_kernel<__nv_bfloat16, 4>
+                                        : few_layer_kernel<__nv_bfloat16, 3>)
+                        : (depth == 6   ? few_layer_kernel<float, 6>
+                           : depth == 5 ? few_layer_kernel<float, 5>
+                           : depth == 4 ? few_layer_kernel<float, 4>
+                                        : few_layer_kernel<float, 3>);
     cudaError_t err = ensure_smem((const void *)fn, smem);
     if (err != cudaSuccess) return err;
     const int ctas = std::min(sm_count(), kFewMaxCtas);
