@@ -23,8 +23,8 @@
 //
 // The 16 weight rows of a tile are the M side of mma.sync m16n8k16 and the
 // entry's rows the N = 8 side: at 8 rows per weight the tensor pipe idles either
-// way, and register accumulators need no TMEM round trip.  The CTA's 16 warps
-// split k: of every 2 KB of a row a warp takes 128 bytes, copied with cp.async
+// way, and register accumulators need no TMEM round trip.  The CTA's 8 warps
+// split k: of every 2 KB of a row a warp takes 256 bytes, copied with cp.async
 // into a ring of its own and read back as 16-byte pieces (the sum over k does not
 // care which k meet in one instruction, as long as both operands agree), so the
 // stream needs no barrier but the sum over the warps at a tile's end, and the
@@ -49,12 +49,13 @@
 namespace moe {
 namespace {
 
-constexpr int FW_WARPS = 16;
+constexpr int FW_WARPS = 8;
 constexpr int FW_THREADS = 32 * FW_WARPS;
-constexpr int FW_STEP = 128;                   // bytes of a row that a warp takes at once
+constexpr int FW_STEP = 256;                   // bytes of a row that a warp takes at once
 constexpr int FW_CHUNK = FW_STEP * FW_WARPS;   // and the CTA
 constexpr int FW_M = 16;                       // weight rows per tile
 constexpr int FW_N = 8;                        // rows of an entry
+constexpr int FW_SMEM = 226 * 1024;            // of the 227 KB a CTA may have
 constexpr int FW_JOIN = 4;                     // chunks as long as joining a shared tile's parts takes
 
 enum { FEW_ROUTE = 1, FEW_GEMM1 = 2, FEW_GEMM2 = 4, FEW_ALL = 7 };
@@ -80,9 +81,10 @@ template <> struct Elem<__nv_bfloat16> {
     static __device__ __forceinline__ __nv_bfloat16 round(float v) { return __float2bfloat16_rn(v); }
 };
 
-// 16 bytes global -> shared, past L1; zeros when !in (src is not read then).
-__device__ __forceinline__ void copy16(void *dst, const void *src, bool in) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+// 16 bytes global -> shared, past L1; zeros when !in (nothing is read then,
+// wherever src points).
+__device__ __forceinline__ void copy16(uint32_t dst, const char *src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                  "r"(in ? 16 : 0)
                  : "memory");
 }
@@ -118,11 +120,13 @@ template <> __device__ __forceinline__ float dot16<float>(uint4 a, uint4 b, floa
     return fmaf(__uint_as_float(a.w), __uint_as_float(b.w), c);
 }
 
-// A step in the ring: 16 weight rows, then the entry's rows, 128 bytes of each in
-// 16-byte pieces.  Odd rows have the halves exchanged: lanes 8 i .. 8 i + 7 read
-// 64 bytes of two rows at once, which so lie in different banks.
+// A step in the ring: two halves of 128 bytes of a row; in each, 16 weight rows,
+// then the entry's rows, 128 bytes of each in 16-byte pieces.  Odd rows have
+// their 64 bytes exchanged: lanes 8 i .. 8 i + 7 read 64 bytes of two rows at
+// once, which so lie in different banks.
+constexpr int FW_LINE = 128;
 __device__ __forceinline__ int piece_at(int row, int piece) {
-    return row * FW_STEP + (piece ^ ((row & 1) << 2)) * 16;
+    return row * FW_LINE + (piece ^ ((row & 1) << 2)) * 16;
 }
 
 // What a lane of a warp has summed of a 16 x 8 tile: in the layout of the mma's
@@ -130,24 +134,31 @@ __device__ __forceinline__ int piece_at(int row, int piece) {
 template <typename T> struct Acc;
 
 template <> struct Acc<__nv_bfloat16> {
-    float c[4];
-    __device__ __forceinline__ void clear() { c[0] = c[1] = c[2] = c[3] = 0.f; }
-    __device__ __forceinline__ void step(const char *slot, int cnt, int lane) {
-        const int g = lane >> 2;
+    float c[2][4];  // two chains of products
+    __device__ __forceinline__ void clear() {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int at = piece_at(g, (lane & 3) + 4 * half);
-            const uint4 lo = *reinterpret_cast<const uint4 *>(slot + at);
-            const uint4 hi = *reinterpret_cast<const uint4 *>(slot + 8 * FW_STEP + at);
-            uint4 bb = make_uint4(0, 0, 0, 0);
-            if (g < cnt) bb = *reinterpret_cast<const uint4 *>(slot + FW_M * FW_STEP + at);
-            mma_bf16(c, lo.x, hi.x, lo.y, hi.y, bb.x, bb.y);
-            mma_bf16(c, lo.z, hi.z, lo.w, hi.w, bb.z, bb.w);
-        }
+        for (int i = 0; i < 4; ++i) c[0][i] = c[1][i] = 0.f;
+    }
+    __device__ __forceinline__ void step(const char *slot, int half_bytes, int cnt, int lane) {
+        const int g = lane >> 2;
+        const char *at = slot + piece_at(g, lane & 3);
+        const int other = piece_at(g, (lane & 3) + 4) - piece_at(g, lane & 3);
+#pragma unroll
+        for (int half = 0; half < 2; ++half, at += half_bytes)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const char *a = at + k * other;
+                const uint4 lo = *reinterpret_cast<const uint4 *>(a);
+                const uint4 hi = *reinterpret_cast<const uint4 *>(a + 8 * FW_LINE);
+                uint4 bb = make_uint4(0, 0, 0, 0);
+                if (g < cnt) bb = *reinterpret_cast<const uint4 *>(a + FW_M * FW_LINE);
+                mma_bf16(c[0], lo.x, hi.x, lo.y, hi.y, bb.x, bb.y);
+                mma_bf16(c[1], lo.z, hi.z, lo.w, hi.w, bb.z, bb.w);
+            }
     }
     __device__ __forceinline__ void get(float (&v)[4], int, int) const {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = c[i];
+        for (int i = 0; i < 4; ++i) v[i] = c[0][i] + c[1][i];
     }
 };
 
@@ -157,21 +168,23 @@ template <> struct Acc<float> {
 #pragma unroll
         for (int n = 0; n < FW_N; ++n) lo[n] = hi[n] = 0.f;
     }
-    __device__ __forceinline__ void step(const char *slot, int cnt, int lane) {
+    __device__ __forceinline__ void step(const char *slot, int half_bytes, int cnt, int lane) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int piece = (lane & 3) + 4 * half, at = piece_at(lane >> 2, piece);
-            const uint4 al = *reinterpret_cast<const uint4 *>(slot + at);
-            const uint4 ah = *reinterpret_cast<const uint4 *>(slot + 8 * FW_STEP + at);
+        for (int half = 0; half < 2; ++half, slot += half_bytes)
 #pragma unroll
-            for (int n = 0; n < FW_N; ++n) {
-                if (n >= cnt) break;
-                const uint4 bb =
-                    *reinterpret_cast<const uint4 *>(slot + FW_M * FW_STEP + piece_at(n, piece));
-                lo[n] = dot16<float>(al, bb, lo[n]);
-                hi[n] = dot16<float>(ah, bb, hi[n]);
+            for (int k = 0; k < 2; ++k) {
+                const int piece = (lane & 3) + 4 * k, at = piece_at(lane >> 2, piece);
+                const uint4 al = *reinterpret_cast<const uint4 *>(slot + at);
+                const uint4 ah = *reinterpret_cast<const uint4 *>(slot + 8 * FW_LINE + at);
+#pragma unroll
+                for (int n = 0; n < FW_N; ++n) {
+                    if (n >= cnt) break;
+                    const uint4 bb =
+                        *reinterpret_cast<const uint4 *>(slot + FW_M * FW_LINE + piece_at(n, piece));
+                    lo[n] = dot16<float>(al, bb, lo[n]);
+                    hi[n] = dot16<float>(ah, bb, hi[n]);
+                }
             }
-        }
     }
     // the four lanes of a row hold every fourth 16 bytes of it
     __device__ __forceinline__ void get(float (&v)[4], int cnt, int lane) {
@@ -201,7 +214,7 @@ __host__ __device__ inline int few_slot_bytes(int T) {
     return (FW_M + (T < FW_N ? T : FW_N)) * FW_STEP;
 }
 __host__ __device__ inline int few_sum_bytes(int T) {
-    return FW_WARPS * FW_M * 4 * (T > 16 ? T : 16);
+    return FW_WARPS * FW_M * 4 * (T > 16 ? T : 16);  // GEMM1: 2 x 32 lanes x 16 bytes a warp
 }
 __host__ __device__ inline int few_table_bytes(int slots) { return slots * 20 + 16; }
 
@@ -375,6 +388,7 @@ few_layer_kernel(const FewParams p) {
     const int slots = p.T * p.k;
     const int slot_bytes = few_slot_bytes(p.T);
     char *ring = smem + warp * DEPTH * slot_bytes;  // this warp's
+    const int half_bytes = slot_bytes / 2;
     float4 *s_red = reinterpret_cast<float4 *>(smem + FW_WARPS * DEPTH * slot_bytes);  // [2][warps][32]
     float *s_out = reinterpret_cast<float *>(s_red);                                   // [warps][T][16]
     float *s_w = s_out + few_sum_bytes(p.T) / 4;                                       // [slots]
@@ -420,7 +434,7 @@ few_layer_kernel(const FewParams p) {
 
     const int g = lane >> 2;
     const int r4 = lane >> 3, c16 = lane & 7;  // a copy takes 4 rows' 128 bytes
-    const char *any = static_cast<const char *>(p.x);  // a valid address for copies of nothing
+    const uint32_t to_piece = smem_u32(ring) + piece_at(r4, c16);
     const int nt2 = (p.D + FW_M - 1) / FW_M;
     int in_slot = 0, out_slot = 0;  // ring slot of the next copies, of the next step
     Acc<T> acc;
@@ -490,12 +504,14 @@ few_layer_kernel(const FewParams p) {
         int ltile = tile0, lu = u0, lc = c0, lleft = total, left = 0, turn0 = 0;
         bool fresh = true, has_hi = false;
         int has_rows = 0;
-        const char *lo = any, *row = any, *row_4 = any;
+        const char *lo = nullptr, *hi = nullptr, *row = nullptr, *row_4 = nullptr;
         auto open = [&]() {
-            const int e = s_entry[lu] >> 16, f = first_of(lu), cnt = first_of(lu + 1) - f;
+            const uint32_t entry = s_entry[lu];
+            const int e = entry >> 16, f = entry & 0xffff, cnt = first_of(lu + 1) - f;
             const int first_row = ltile * tile_rows;
             const int col = lc * FW_CHUNK + ((warp + turn0) & (FW_WARPS - 1)) * FW_STEP + c16 * 16;
-            lo = weights + ((size_t)e * R + first_row + r4) * row_bytes + col;
+            lo = weights + (size_t)(e * R + first_row + r4) * row_bytes + col;
+            hi = lo + to_hi;
             has_hi = !second || first_row + 8 < R;  // R is a multiple of 8
             has_rows = cnt - r4;  // > 0: row r4 is there, > 4: row r4 + 4 too
             const int n = f + (has_rows > 0 ? r4 : 0), n4 = f + (has_rows > 4 ? r4 + 4 : 0);
@@ -504,23 +520,33 @@ few_layer_kernel(const FewParams p) {
             left = row_bytes - col;
             fresh = false;
         };
-        auto put = [&](int slot, int r, const char *src, bool in) {
-            copy16(ring + slot * slot_bytes + piece_at(r, c16), in ? src : any, in);
-        };
         auto copy_weights = [&](int slot) {
-            const bool in = left > 0;
-            put(slot, r4, lo, in);
-            put(slot, r4 + 4, lo + to_4, in);
-            put(slot, r4 + 8, lo + to_hi, in && has_hi);
-            put(slot, r4 + 12, lo + to_hi + to_4, in && has_hi);
+            const uint32_t d = to_piece + slot * slot_bytes;
+            const bool in[2] = {left > 0, left > FW_LINE};
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const uint32_t dh = d + half * half_bytes;
+                copy16(dh, lo + half * FW_LINE, in[half]);
+                copy16(dh + 4 * FW_LINE, lo + to_4 + half * FW_LINE, in[half]);
+                copy16(dh + 8 * FW_LINE, hi + half * FW_LINE, in[half] && has_hi);
+                copy16(dh + 12 * FW_LINE, hi + to_4 + half * FW_LINE, in[half] && has_hi);
+            }
         };
         auto copy_row = [&](int slot) {
-            if (has_rows > 0) put(slot, FW_M + r4, row, left > 0);
-            if (has_rows > 4) put(slot, FW_M + r4 + 4, row_4, left > 0);
+            const uint32_t d = to_piece + slot * slot_bytes + FW_M * FW_LINE;
+            if (has_rows > 0) {
+                copy16(d, row, left > 0);
+                copy16(d + half_bytes, row + FW_LINE, left > FW_LINE);
+            }
+            if (has_rows > 4) {
+                copy16(d + 4 * FW_LINE, row_4, left > 0);
+                copy16(d + half_bytes + 4 * FW_LINE, row_4 + FW_LINE, left > FW_LINE);
+            }
         };
         auto bump = [&](int &slot) { slot = slot + 1 == DEPTH ? 0 : slot + 1; };
         auto advance = [&]() {
             lo += FW_CHUNK;
+            hi += FW_CHUNK;
             row += FW_CHUNK;
             row_4 += FW_CHUNK;
             left -= FW_CHUNK;
@@ -575,7 +601,7 @@ few_layer_kernel(const FewParams p) {
             do {
                 copy_wait<DEPTH - 2>();
                 __syncwarp();
-                acc.step(ring + out_slot * slot_bytes, cnt, lane);
+                acc.step(ring + out_slot * slot_bytes, half_bytes, cnt, lane);
                 bump(out_slot);
                 if (lleft > 0) {  // into the slot read a step ago
                     if (fresh) open();
@@ -764,12 +790,12 @@ cudaError_t launch_few_layer(const FewLayer &f, cudaStream_t stream) {
     p.renorm = f.renorm;
     p.n_group = f.n_group;
     p.topk_group = f.topk_group;
-    // As many steps of every warp in flight as the shared memory takes: 5 of them
-    // (160 KB of weights per SM) for one token, 4 up to 4 tokens, 3 up to 16, 2
-    // above, where the sums of out for all the tokens take their place.
-    const int depth = f.T == 1 ? 6 : f.T <= 4 ? 5 : f.T <= 16 ? 4 : 3;
-    const size_t smem = (size_t)FW_WARPS * depth * few_slot_bytes(f.T) + few_sum_bytes(f.T) +
-                        few_table_bytes(f.T * f.k);
+    // As many steps of every warp as the shared memory takes, one of them being
+    // read: 6 for one token (160 KB of weights in flight per SM), 5 up to 4
+    // tokens, else 4, or 3 with many pairs.
+    const int rest = few_sum_bytes(f.T) + few_table_bytes(f.T * f.k);
+    const int depth = std::min(6, (FW_SMEM - rest) / (FW_WARPS * few_slot_bytes(f.T)));
+    const size_t smem = (size_t)FW_WARPS * depth * few_slot_bytes(f.T) + rest;
     auto fn = f.is_bf16 ? (depth == 6   ? few_layer_kernel<__nv_bfloat16, 6>
                            : depth == 5 ? few_layer_kernel<__nv_bfloat16, 5>
                            : depth == 4 ? few_layer_kernel<__nv_bfloat16, 4>

@@ -1243,11 +1243,13 @@ MOE_EXPORT moe_status moe_get_device_status(const void *ws, size_t ws_bytes, moe
 static moe_status few_supported(const moe_config *c) {
     if (c->T > moe::kFewMaxTokens)
         return arg_fail("moe_layer_forward_few: at most 32 tokens", MOE_ERR_UNSUPPORTED);
-    // the kernel numbers (16 rows of out, pair, 2 KB of a row of w2) with int32
+    // the kernel numbers (16 rows of out, pair, 2 KB of a row of w2), tiles and weight
+    // rows with int32
     const int64_t chunks = ((int64_t)c->H_local * elem_bytes(c) + 2047) / 2048;
     if ((int64_t)c->T * c->k * chunks * ((c->D + 15) / 16) >= (int64_t)1 << 31 ||
-        (int64_t)c->T * c->k * (c->H_local / 8) >= (int64_t)1 << 31)
-        return arg_fail("moe_layer_forward_few: w2 too large", MOE_ERR_UNSUPPORTED);
+        (int64_t)c->T * c->k * (c->H_local / 8) >= (int64_t)1 << 31 ||
+        (int64_t)c->E_local * std::max(c->D, c->H_local) >= (int64_t)1 << 31)
+        return arg_fail("moe_layer_forward_few: D, H_local or E_local too large", MOE_ERR_UNSUPPORTED);
     return MOE_OK;
 }
 
