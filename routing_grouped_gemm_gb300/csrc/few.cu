@@ -15,7 +15,7 @@
 //            (token, slot) pairs by expert; at most 8 pairs of an expert form an
 //            ENTRY, one pass over that expert's weights
 //   GEMM1    tiles of 8 gate and 8 up rows of one entry over the CTAs -> h
-//   -- barrier -- the loads of w2 begin before it: they do not depend on h
+//   -- barrier --
 //   GEMM2    tiles of 16 rows of out; all (tile, entry, chunk of H) triples in
 //            one line, cut into equal parts over the CTAs, so that the stream
 //            ends everywhere at once.  A tile cut by that gets its parts' fp32
@@ -558,33 +558,26 @@ few_layer_kernel(const FewParams p) {
                 fresh = true;
             }
         };
-        // first the weights' part of the first steps; the second product's go out
-        // before the barrier, its rows (h) behind it
-        int slot = in_slot;
-#pragma unroll 1
-        for (int i = 0; i < DEPTH - 1 && lleft > 0; ++i) {
-            if (fresh) open();
-            copy_weights(slot);
-            bump(slot);
-            advance();
-        }
+        // h of every CTA.  (The first steps' weights do not need it, but copying
+        // them ahead of the barrier measured the same: its loads then queue behind.)
         if (second && p.phases == FEW_ALL) {
             if (tid == 0) wait_count_bounded(&p.bars[1], G, &s_abort);
             __syncthreads();
             dead = s_abort;
             if (dead) break;
         }
-        ltile = tile0, lu = u0, lc = c0, lleft = total, turn0 = 0, fresh = true;
-#pragma unroll 1
-        for (int i = 0; i < DEPTH - 1; ++i) {
+        auto copy_next = [&]() {
             if (lleft > 0) {
                 if (fresh) open();
+                copy_weights(in_slot);
                 copy_row(in_slot);
                 bump(in_slot);
                 advance();
             }
-            copy_commit();  // the first group holds all the weights so far
-        }
+            copy_commit();
+        };
+#pragma unroll 1
+        for (int i = 0; i < DEPTH - 1; ++i) copy_next();
         if (second) {
             for (int i = lane; i < FW_M * p.T; i += 32) s_out[warp * FW_M * p.T + i] = 0.f;
             __syncwarp();
@@ -603,14 +596,7 @@ few_layer_kernel(const FewParams p) {
                 __syncwarp();
                 acc.step(ring + out_slot * slot_bytes, half_bytes, cnt, lane);
                 bump(out_slot);
-                if (lleft > 0) {  // into the slot read a step ago
-                    if (fresh) open();
-                    copy_weights(in_slot);
-                    copy_row(in_slot);
-                    bump(in_slot);
-                    advance();
-                }
-                copy_commit();
+                copy_next();  // into the slot read a step ago
                 ++n;
             } while (++c < nc && n < total);
             float v[4];
