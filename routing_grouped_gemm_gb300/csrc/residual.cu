@@ -293,13 +293,114 @@ residual_norm_kernel(const ForwardArgs a) {
 // ---------------------------------------------------------------------
 // gradient
 // ---------------------------------------------------------------------
+// Pairs of fp32, added and multiplied two at a time.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pair(float x, float y) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 parts(f2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f2 both(float x) { return pair(x, x); }
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float sum2(f2 v) {
+    const float2 p = parts(v);
+    return p.x + p.y;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void unpack8(const Pack<BF16> &p, f2 (&f)[4]) {
+    float v[8];
+    unpack8<BF16>(p, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = pair(v[2 * i], v[2 * i + 1]);
+}
+template <bool BF16>
+__device__ __forceinline__ void store8(void *p, size_t vec, const f2 (&f)[4]) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 q = parts(f[i]);
+        v[2 * i] = q.x;
+        v[2 * i + 1] = q.y;
+    }
+    store8<BF16>(p, vec, v);
+}
+
+// Bit e: element e of a vector stays.
+__device__ __forceinline__ uint32_t keep_bits(uint64_t vec, uint32_t cut, uint64_t seed,
+                                              uint64_t offset) {
+    const uint4 w = philox(vec, offset, seed);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    uint32_t bits = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        bits |= ((u[i] & 0xffffu) >= cut ? 1u : 0u) << (2 * i);
+        bits |= ((u[i] >> 16) >= cut ? 1u : 0u) << (2 * i + 1);
+    }
+    return bits;
+}
+__device__ __forceinline__ f2 kept(f2 v, uint32_t bits, int i) {
+    const float2 p = parts(v);
+    return pair(bits >> (2 * i) & 1u ? p.x : 0.f, bits >> (2 * i + 1) & 1u ? p.y : 0.f);
+}
+
+// Eight sums over a warp in nine exchanges: lanes trade halves of what they have
+// until each holds one sum, lane 4 i .. 4 i + 3 the i-th.
+__device__ __forceinline__ float warp_sums(float (&v)[8]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int half = 4, bit = 16; half > 0; half >>= 1, bit >>= 1) {
+        const bool high = lane & bit;
+#pragma unroll
+        for (int i = 0; i < half; ++i) {
+            const float give = high ? v[i] : v[i + half], take = high ? v[i + half] : v[i];
+            v[i] = take + __shfl_xor_sync(0xffffffffu, give, bit);
+        }
+    }
+    v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
+    return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
+}
+
+// The same over the CTA (at most 32 warps; one barrier, `slot` as in block_sum);
+// every thread gets the sums.
+template <bool WARP>
+__device__ __forceinline__ void row_sums(float (&v)[8], float *slot) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
+    float sum = warp_sums(v);
+    if (!WARP) {
+        if ((lane & 3) == 0) slot[(lane >> 2) * 32 + warp] = sum;
+        __syncthreads();
+        sum = 0.f;
+        for (int w = lane & 3; w < nwarps; w += 4) sum += slot[(lane >> 2) * 32 + w];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __shfl_sync(0xffffffffu, sum, 4 * i);
+}
+
 struct BackwardArgs {
     const void *s, *y, *post, *gate, *pre, *ds_out, *dn;
     void *dresid, *dy, *dgate;
-    float *part;  // [3][gridDim.x][D]: this CTA's sums for dpre, dpost, dgate (channel)
+    float *part;  // [2][gridDim.x][D]: this CTA's column sums P and G
     Drop drop;
     float eps, res_scale, branch_scale;
-    int T, D, gate_kind;
+    int T, D, gate_kind, depth;
+    int in_ring;  // arrays there: 4, or 5 with a gate for every element
 };
 
 // With r1, r2 the rows' rsqrt factors and gp = dn pre:
@@ -307,128 +408,246 @@ struct BackwardArgs {
 //   u = branch_scale keep ds;  dgate = u v;  dv = gate u
 //   dy = r1 (dv post - y r1^2 mean(dv post y))
 // ds is linear in two row sums that are not known yet, so with
-// q = branch_scale keep post y,
+// q = branch_scale keep post gate y,
 //   sum(ds q) = sum(ds_out q) + r2 sum(gp q) - c sum(s q)
-// and every sum of the row comes out of ONE reduction.  (mean(dv post y) is
-// that sum with the gate inside q, or times the token's gate.)
-template <bool BF16, int NV>
-__global__ void __launch_bounds__(1024)
+// and every sum of the row comes out of ONE reduction.  (A token's gate is left
+// out of q and multiplied in behind.)  The column sums are two:
+//   P = sum dn s r2 = dpre,   G = sum keep ds y r1 (times a gate that is not the
+//   channel's);  dpost = branch_scale gate G and dgate = branch_scale post G.
+//
+// A row per CTA (WARP: per warp, narrow rows), rows over the grid.  Each thread
+// copies its own columns of the next rows into shared memory with cp.async, so
+// that depth - 1 rows are in flight while one is worked on and no barrier but the
+// reduction's is needed; it reads them from there twice, before and behind the
+// reduction.  Rows too wide for two in shared memory are read from global memory
+// instead, the second time from L2 (RING false).
+template <bool BF16, int NV, bool WARP, bool DROP, bool RING>
+__global__ void __launch_bounds__(WARP ? 256 : NV == 1 ? 256 : 512, NV == 1 ? 2 : 1)
 residual_norm_backward_kernel(const BackwardArgs a) {
+    extern __shared__ __align__(16) char smem[];
+    __shared__ float s_sum[2][8 * 32];
     griddep_launch_dependents();
     griddep_wait();
-    __shared__ float s_sum[2][6 * 32];
-    const int V = a.D / 8, tid = threadIdx.x;
+    constexpr int EB = BF16 ? 16 : 32;  // bytes of a vector
+    const int V = a.D / 8, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int mine = WARP ? lane : tid, across = WARP ? 32 : blockDim.x;
+    const int unit = WARP ? blockIdx.x * (blockDim.x >> 5) + warp : blockIdx.x;
+    const int units = WARP ? gridDim.x * (blockDim.x >> 5) : gridDim.x;
     const float inv_d = 1.f / (float)a.D;
-    const bool branch = a.y;
-    const bool elem_gate = a.gate_kind == GATE_CHANNEL || a.gate_kind == GATE_ELEMENT;
+    const bool branch = a.y, elem = a.gate_kind == GATE_ELEMENT;
+    const float dscale = DROP ? a.drop.scale : 1.f;
     uint64_t seed = 0, offset = 0;
-    if (a.drop.cut) {
+    if (DROP) {
         seed = (uint64_t)a.drop.rng[0];
         offset = (uint64_t)a.drop.rng[1];
     }
-    float dpre[NV][8], dpost[NV][8], dgate[NV][8];
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) dpre[i][e] = dpost[i][e] = dgate[i][e] = 0.f;
-
-    int turn = 0;
-    for (int t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
-        const size_t base = (size_t)t * V;
-        const float gt = a.gate_kind == GATE_TOKEN ? static_cast<const float *>(a.gate)[t] : 1.f;
-        // what is read of element e of vector v, and what follows from it
-        auto read = [&](int v, float (&s)[8], float (&dso)[8], float (&dn)[8], float (&gp)[8],
-                        float (&y)[8], float (&post)[8], float (&gate)[8], float (&keep)[8]) {
-            unpack8<BF16>(load8<BF16>(a.s, base + v), s);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                dso[e] = dn[e] = gp[e] = y[e] = 0.f;
-                post[e] = gate[e] = 1.f;
-                keep[e] = a.branch_scale;
-            }
-            if (a.ds_out) unpack8<BF16>(load8<BF16>(a.ds_out, base + v), dso);
-            if (a.pre) {
-                unpack8<BF16>(load8<BF16>(a.dn, base + v), dn);
-                unpack8<BF16>(load8<BF16>(a.pre, v), gp);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) gp[e] *= dn[e];
-            }
-            if (branch) {
-                unpack8<BF16>(load8<BF16>(a.y, base + v), y);
-                if (a.post) unpack8<BF16>(load8<BF16>(a.post, v), post);
-                if (elem_gate)
-                    unpack8<BF16>(load8<BF16>(a.gate, a.gate_kind == GATE_CHANNEL ? v : base + v),
-                                  gate);
-                if (a.drop.cut) drop8(keep, base + v, a.drop, seed, offset);
-            }
-        };
-        float m[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int v = tid + i * blockDim.x;
-            if (v >= V) continue;
-            float s[8], dso[8], dn[8], gp[8], y[8], post[8], gate[8], keep[8];
-            read(v, s, dso, dn, gp, y, post, gate, keep);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float q = keep[e] * gate[e] * post[e] * y[e];
-                m[0] = fmaf(s[e], s[e], m[0]);
-                m[1] = fmaf(gp[e], s[e], m[1]);
-                m[2] = fmaf(y[e], y[e], m[2]);
-                m[3] = fmaf(dso[e], q, m[3]);
-                m[4] = fmaf(gp[e], q, m[4]);
-                m[5] = fmaf(s[e], q, m[5]);
-            }
-        }
-        block_sum<6>(m, s_sum[turn]);
-        const float r2 = a.pre ? rsqrtf(fmaf(m[0], inv_d, a.eps)) : 0.f;
-        const float c = r2 * r2 * r2 * (m[1] * inv_d);
-        const float r1 = a.post ? rsqrtf(fmaf(m[2], inv_d, a.eps)) : 1.f;
-        const float dot = m[3] + r2 * m[4] - c * m[5];  // sum(ds q)
-        const float c1 = a.post ? r1 * r1 * (gt * dot * inv_d) : 0.f;
-        if (a.gate_kind == GATE_TOKEN && tid == 0) static_cast<float *>(a.dgate)[t] = r1 * dot;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int v = tid + i * blockDim.x;
-            if (v >= V) continue;
-            float s[8], dso[8], dn[8], gp[8], y[8], post[8], gate[8], keep[8], o[8];
-            read(v, s, dso, dn, gp, y, post, gate, keep);
-            float dg[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float ds = dso[e] + (r2 * gp[e] - c * s[e]);
-                dpre[i][e] = fmaf(dn[e], s[e] * r2, dpre[i][e]);
-                const float u = keep[e] * ds, yr = y[e] * r1;
-                dg[e] = u * (yr * post[e]);
-                dgate[i][e] += dg[e];
-                const float dv = u * gate[e] * gt;
-                dpost[i][e] = fmaf(dv, yr, dpost[i][e]);
-                s[e] = branch ? a.res_scale * ds : ds;
-                o[e] = r1 * (dv * post[e] - y[e] * c1);
-            }
-            store8<BF16>(a.dresid, base + v, s);
-            if (branch) store8<BF16>(a.dy, base + v, o);
-            if (a.gate_kind == GATE_ELEMENT) store8<BF16>(a.dgate, base + v, dg);
-        }
-    }
+    // what a column multiplies by: coef = branch_scale keep post gate (of a channel)
+    Pack<BF16> pre[NV];
+    f2 coef[NV][4], P[NV][4], G[NV][4];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int v = tid + i * blockDim.x;
+        const int v = mine + i * across;
+        pre[i] = Pack<BF16>{};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            coef[i][e] = both(a.branch_scale * dscale);
+            P[i][e] = G[i][e] = both(0.f);
+        }
         if (v >= V) continue;
-        float *p = a.part + (size_t)blockIdx.x * a.D;
-        const size_t plane = (size_t)gridDim.x * a.D;
-        if (a.pre) store8<false>(p, v, dpre[i]);
-        if (a.post) store8<false>(p + plane, v, dpost[i]);
-        if (a.gate_kind == GATE_CHANNEL) store8<false>(p + 2 * plane, v, dgate[i]);
+        f2 f[4];
+        if (a.pre) pre[i] = load8<BF16>(a.pre, v);
+        if (a.post) {
+            unpack8<BF16>(load8<BF16>(a.post, v), f);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) coef[i][e] = mul2(coef[i][e], f[e]);
+        }
+        if (a.gate_kind == GATE_CHANNEL) {
+            unpack8<BF16>(load8<BF16>(a.gate, v), f);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) coef[i][e] = mul2(coef[i][e], f[e]);
+        }
+    }
+
+    // the thread's ring: [depth][array][NV] vectors, a plane of 16-byte pieces per
+    // (array, vector, half) over the CTA's threads
+    const void *arrays[5] = {a.s, a.ds_out, a.dn, a.y, elem ? a.gate : nullptr};
+    const uint32_t plane = blockDim.x * 16, ring = smem_u32(smem) + tid * 16;
+    const uint32_t stage_bytes = a.in_ring * NV * (EB / 16) * plane;
+    auto copy_row = [&](long long t, int stage) {
+        if (!RING) return;
+        if (t < a.T) {
+#pragma unroll
+            for (int k = 0; k < 5; ++k) {
+                if (!arrays[k]) continue;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int v = mine + i * across;
+                    if (v >= V) continue;
+                    const char *src = static_cast<const char *>(arrays[k]) + ((size_t)t * V + v) * EB;
+                    const uint32_t dst = ring + stage * stage_bytes + (k * NV + i) * (EB / 16) * plane;
+#pragma unroll
+                    for (int h = 0; h < EB / 16; ++h)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + h * plane),
+                                     "l"(src + 16 * h)
+                                     : "memory");
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto take = [&](int k, int i, int stage, size_t base) {
+        Pack<BF16> r = {};
+        if (!arrays[k] || mine + i * across >= V) return r;
+        if (!RING) return load8<BF16>(arrays[k], base + mine + i * across);
+        const char *p = smem + tid * 16 + stage * stage_bytes + (k * NV + i) * (EB / 16) * plane;
+        r.a = *reinterpret_cast<const uint4 *>(p);
+        if constexpr (!BF16) r.b = *reinterpret_cast<const uint4 *>(p + plane);
+        return r;
+    };
+    for (int i = 0; i < a.depth - 1; ++i) copy_row(unit + (long long)i * units, i);
+
+    int turn = 0, stage = 0;
+    for (long long row = unit; row < a.T; row += units, turn ^= 1) {
+        const int t = (int)row;
+        const int last = stage == 0 ? a.depth - 1 : stage - 1;  // read a row ago
+        copy_row(t + (long long)(a.depth - 1) * units, last);
+        if (RING) switch (a.depth) {  // the row's own copies are the depth-th last group
+        case 2: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+        case 3: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+        default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+        }
+        const size_t base = (size_t)t * V;
+        const float gt = a.gate_kind == GATE_TOKEN ? static_cast<const float *>(a.gate)[t] : 1.f;
+        uint32_t bits[NV];
+        f2 m[6];
+#pragma unroll
+        for (int n = 0; n < 6; ++n) m[n] = both(0.f);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            bits[i] = 0xffu;
+            if (DROP) bits[i] = keep_bits(base + mine + i * across, a.drop.cut, seed, offset);
+            f2 s[4], d[4], n[4], y[4], w[4];
+            unpack8<BF16>(take(0, i, stage, base), s);
+            unpack8<BF16>(take(1, i, stage, base), d);
+            unpack8<BF16>(take(2, i, stage, base), n);
+            unpack8<BF16>(take(3, i, stage, base), y);
+            unpack8<BF16>(pre[i], w);
+            if (elem) {
+                f2 ge[4];
+                unpack8<BF16>(take(4, i, stage, base), ge);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const f2 y2 = y[e];
+                    m[2] = fma2(y2, y2, m[2]);
+                    y[e] = mul2(y2, ge[e]);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const f2 gp = mul2(n[e], w[e]);
+                f2 q = mul2(y[e], coef[i][e]);
+                if (DROP) q = kept(q, bits[i], e);
+                m[0] = fma2(s[e], s[e], m[0]);
+                m[1] = fma2(gp, s[e], m[1]);
+                if (!elem) m[2] = fma2(y[e], y[e], m[2]);
+                m[3] = fma2(d[e], q, m[3]);
+                m[4] = fma2(gp, q, m[4]);
+                m[5] = fma2(s[e], q, m[5]);
+            }
+        }
+        float sum[8] = {sum2(m[0]), sum2(m[1]), sum2(m[2]), sum2(m[3]), sum2(m[4]), sum2(m[5]), 0.f, 0.f};
+        row_sums<WARP>(sum, s_sum[turn]);
+        const float r2 = a.pre ? rsqrtf(fmaf(sum[0], inv_d, a.eps)) : 0.f;
+        const float c = r2 * r2 * r2 * (sum[1] * inv_d);
+        const float r1 = a.post ? rsqrtf(fmaf(sum[2], inv_d, a.eps)) : 1.f;
+        const float dot = sum[3] + r2 * sum[4] - c * sum[5];  // sum(ds q)
+        const float c1 = a.post ? r1 * r1 * (gt * dot * inv_d) : 0.f;
+        if (a.gate_kind == GATE_TOKEN && mine == 0) static_cast<float *>(a.dgate)[t] = r1 * dot;
+        asm volatile("" ::: "memory");  // the row is read again, not kept: registers are short
+        const f2 r2_2 = both(r2), c_2 = both(-c), res_2 = both(branch ? a.res_scale : 1.f);
+        const f2 r1_2 = both(r1), g_2 = both(r1 * gt), c1_2 = both(-r1 * c1);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int v = mine + i * across;
+            if (v >= V) continue;
+            f2 s[4], d[4], n[4], y[4], w[4], ge[4];
+            unpack8<BF16>(take(0, i, stage, base), s);
+            unpack8<BF16>(take(1, i, stage, base), d);
+            unpack8<BF16>(take(2, i, stage, base), n);
+            unpack8<BF16>(take(3, i, stage, base), y);
+            unpack8<BF16>(pre[i], w);
+            if (elem) unpack8<BF16>(take(4, i, stage, base), ge);
+            f2 dg[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const f2 ds = fma2(s[e], c_2, fma2(mul2(n[e], w[e]), r2_2, d[e]));
+                P[i][e] = fma2(n[e], mul2(s[e], r2_2), P[i][e]);
+                f2 k = DROP ? kept(ds, bits[i], e) : ds;
+                if (elem) {
+                    dg[e] = mul2(mul2(k, coef[i][e]), mul2(y[e], r1_2));
+                    k = mul2(k, ge[e]);
+                }
+                G[i][e] = fma2(k, mul2(y[e], g_2), G[i][e]);
+                d[e] = mul2(ds, res_2);
+                y[e] = fma2(mul2(k, coef[i][e]), g_2, mul2(y[e], c1_2));
+            }
+            store8<BF16>(a.dresid, base + v, d);
+            if (branch) store8<BF16>(a.dy, base + v, y);
+            if (elem) store8<BF16>(a.dgate, base + v, dg);
+        }
+        if (++stage == a.depth) stage = 0;
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+
+    // The CTA's column sums.  A channel's gate takes the token's gate for one:
+    // G holds neither.
+    if (!a.pre && !a.post && a.gate_kind != GATE_CHANNEL) return;
+    float *part = a.part + (size_t)blockIdx.x * a.D;
+    const size_t to_G = (size_t)gridDim.x * a.D;
+    if (!WARP) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int v = mine + i * across;
+            if (v >= V) continue;
+            store8<false>(part, v, P[i]);
+            store8<false>(part + to_G, v, G[i]);
+        }
+        return;
+    }
+    // the warps' sums through the ring, P then G
+    const int nwarps = blockDim.x >> 5;
+    float *sums = reinterpret_cast<float *>(smem);
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (mine + i * across < V)
+                store8<false>(sums + (size_t)warp * a.D, mine + i * across, which ? G[i] : P[i]);
+        __syncthreads();
+        for (int d = tid; d < a.D; d += blockDim.x) {
+            float x = 0.f;
+            for (int w = 0; w < nwarps; ++w) x += sums[(size_t)w * a.D + d];
+            part[which * to_G + d] = x;
+        }
     }
 }
 
-// out[c] = sum over the CTAs' parts, in a fixed order.  blockIdx.y: which sum.
+// dpre, dpost and a channel gate's gradient from the CTAs' parts, added in a
+// fixed order.  blockIdx.y: P or G.
 struct FinishArgs {
     const float *part;
-    float *out[3];
-    int parts, D;
+    const void *post, *gate;  // the other factor of dgate and dpost, or null
+    float *dpre, *dpost, *dgate;
+    float scale;  // branch_scale and the dropout's factor
+    int parts, D, is_bf16;
 };
+
+__device__ __forceinline__ float factor_at(const void *p, int c, int is_bf16) {
+    if (!p) return 1.f;
+    return is_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[c])
+                   : static_cast<const float *>(p)[c];
+}
 
 constexpr int FIN_COLS = 32, FIN_ROWS = 16;
 __global__ void __launch_bounds__(FIN_COLS *FIN_ROWS)
@@ -436,10 +655,10 @@ residual_finish_kernel(const FinishArgs a) {
     griddep_launch_dependents();
     griddep_wait();
     __shared__ float s[FIN_ROWS][FIN_COLS];
-    float *out = blockIdx.y == 0 ? a.out[0] : blockIdx.y == 1 ? a.out[1] : a.out[2];
-    if (!out) return;
+    const bool is_G = blockIdx.y;
+    if (is_G ? !a.dpost && !a.dgate : !a.dpre) return;
     const int c = blockIdx.x * FIN_COLS + threadIdx.x, r = threadIdx.y;
-    const float *p = a.part + (size_t)blockIdx.y * a.parts * a.D;
+    const float *p = a.part + (is_G ? (size_t)a.parts * a.D : 0);
     float sum = 0.f;
     if (c < a.D)
         for (int i = r; i < a.parts; i += FIN_ROWS) sum += p[(size_t)i * a.D + c];
@@ -448,7 +667,13 @@ residual_finish_kernel(const FinishArgs a) {
     if (r == 0 && c < a.D) {
 #pragma unroll
         for (int i = 1; i < FIN_ROWS; ++i) sum += s[i][threadIdx.x];
-        out[c] = sum;
+        if (!is_G) {
+            a.dpre[c] = sum;
+        } else {
+            sum *= a.scale;
+            if (a.dpost) a.dpost[c] = sum * factor_at(a.gate, c, a.is_bf16);
+            if (a.dgate) a.dgate[c] = sum * factor_at(a.post, c, a.is_bf16);
+        }
     }
 }
 
@@ -528,15 +753,50 @@ cudaError_t launch_combine_residual_norm(const ResidualNorm &r, const void *y_pe
     return forward<true>(r, a, stream);
 }
 
-int residual_parts(int T, int D) { return std::min(T, D <= 1024 ? 1216 : D <= 4096 ? 608 : 304); }
+// Shape of a gradient launch.
+struct GradientShape {
+    int nv, threads, depth, ctas, in_ring;
+    bool warp, ring;
+    size_t smem;
+};
+
+namespace {
+
+GradientShape gradient_shape(int T, int D, int is_bf16, int gate_kind) {
+    GradientShape g = {};
+    const int V = D / 8;
+    // a row per warp while its columns' sums fit a lane's registers, and two rows of
+    // every warp shared memory
+    g.warp = V <= (is_bf16 ? 128 : 64);
+    g.nv = g.warp ? (V <= 32 ? 1 : V <= 64 ? 2 : 4) : (V <= 256 ? 1 : 2);
+    g.threads = g.warp ? 256 : ((V + g.nv - 1) / g.nv + 31) / 32 * 32;
+    g.in_ring = gate_kind == GATE_ELEMENT ? 5 : 4;
+    const int per_sm = g.nv == 1 ? 2 : 1;
+    const size_t stage = (size_t)g.in_ring * g.nv * (is_bf16 ? 1 : 2) * g.threads * 16;
+    g.depth = (int)std::min<size_t>(4, (size_t)(220 * 1024 / per_sm) / stage);
+    g.ring = g.warp || (V <= 1024 && g.depth >= 2);
+    g.smem = g.warp ? std::max(stage * g.depth, (size_t)8 * D * 4) : stage * g.depth;
+    if (!g.ring) {
+        g.nv = V <= 2048 ? 4 : 8;
+        g.threads = ((V + g.nv - 1) / g.nv + 31) / 32 * 32;
+        g.depth = 1;
+        g.smem = 0;
+    }
+    const int rows = g.warp ? 8 : 1;  // at a time in a CTA
+    g.ctas = std::min((T + rows - 1) / rows, 152 * per_sm);
+    return g;
+}
+
+}  // namespace
+
+int residual_parts(int T, int D) { return std::min(T, 304); }
 
 cudaError_t launch_residual_norm_backward(const ResidualNorm &r, const void *s, const void *y,
                                           const void *dresid_out, const void *dnorm_out,
                                           void *dresid, void *dy, float *dpost, void *dgate,
                                           float *dpre, float *part, cudaStream_t stream) {
     cudaError_t err;
-    float *sums[3] = {dpre, dpost, r.gate_kind == GATE_CHANNEL ? (float *)dgate : nullptr};
-    const int parts = residual_parts(r.T, r.D);
+    const GradientShape g = gradient_shape(r.T, r.D, r.is_bf16, r.gate_kind);
     if (r.T > 0) {
         BackwardArgs a = {};
         a.s = s;
@@ -557,25 +817,43 @@ cudaError_t launch_residual_norm_backward(const ResidualNorm &r, const void *s, 
         a.T = r.T;
         a.D = r.D;
         a.gate_kind = r.gate_kind;
-        int threads, nv;
-        row_shape(r.D / 8, &threads, &nv);
-        auto kernel = r.is_bf16 ? (nv == 1   ? residual_norm_backward_kernel<true, 1>
-                                   : nv == 2 ? residual_norm_backward_kernel<true, 2>
-                                             : residual_norm_backward_kernel<true, 4>)
-                                : (nv == 1   ? residual_norm_backward_kernel<false, 1>
-                                   : nv == 2 ? residual_norm_backward_kernel<false, 2>
-                                             : residual_norm_backward_kernel<false, 4>);
-        err = launch_pdl(kernel, dim3(parts), dim3(threads), 0, stream, a);
+        a.depth = g.depth;
+        a.in_ring = g.in_ring;
+        using Kernel = void (*)(BackwardArgs);
+        static const Kernel kernels[2][2][7] = {
+#define MOE_GRADIENT(BF16, DROP)                                                                  \
+    {residual_norm_backward_kernel<BF16, 1, true, DROP, true>,                                    \
+     residual_norm_backward_kernel<BF16, 2, true, DROP, true>,                                    \
+     residual_norm_backward_kernel<BF16, 4, true, DROP, true>,                                    \
+     residual_norm_backward_kernel<BF16, 1, false, DROP, true>,                                   \
+     residual_norm_backward_kernel<BF16, 2, false, DROP, true>,                                   \
+     residual_norm_backward_kernel<BF16, 4, false, DROP, false>,                                  \
+     residual_norm_backward_kernel<BF16, 8, false, DROP, false>}
+            {MOE_GRADIENT(false, false), MOE_GRADIENT(false, true)},
+            {MOE_GRADIENT(true, false), MOE_GRADIENT(true, true)}};
+#undef MOE_GRADIENT
+        const int which = g.warp ? (g.nv == 4 ? 2 : g.nv - 1) : g.ring ? 2 + g.nv : g.nv == 4 ? 5 : 6;
+        const Kernel kernel = kernels[r.is_bf16 ? 1 : 0][r.drop_cut > 0 ? 1 : 0][which];
+        if ((err = ensure_smem((const void *)kernel, g.smem)) != cudaSuccess) return err;
+        err = launch_pdl(kernel, dim3(g.ctas), dim3(g.threads), g.smem, stream, a);
         if (err != cudaSuccess) return err;
         count_launch();
     }
-    if (!sums[0] && !sums[1] && !sums[2]) return cudaSuccess;
     FinishArgs f = {};
     f.part = part;
-    for (int i = 0; i < 3; ++i) f.out[i] = sums[i];
-    f.parts = parts;  // none without rows: the sums are zero
+    f.dpre = dpre;
+    f.dpost = dpost;
+    if (r.gate_kind == GATE_CHANNEL) {
+        f.dgate = (float *)dgate;
+        f.gate = r.gate;
+    }
+    f.post = r.post;
+    if (!f.dpre && !f.dpost && !f.dgate) return cudaSuccess;
+    f.scale = r.branch_scale * make_drop(r).scale;
+    f.parts = g.ctas;  // none without rows: the sums are zero
     f.D = r.D;
-    err = launch_pdl(residual_finish_kernel, dim3((r.D + FIN_COLS - 1) / FIN_COLS, 3),
+    f.is_bf16 = r.is_bf16;
+    err = launch_pdl(residual_finish_kernel, dim3((r.D + FIN_COLS - 1) / FIN_COLS, 2),
                      dim3(FIN_COLS, FIN_ROWS), 0, stream, f);
     if (err == cudaSuccess) count_launch();
     return err;

@@ -37,7 +37,7 @@ def test_workspace_size(moe):
     assert moe.residual_workspace_size(_rc(moe, T=0)) == 0
     for T, D in ((1, 8), (4096, 2048), (16384, 32768)):
         n = moe.residual_workspace_size(_rc(moe, T=T, D=D))
-        assert n % 256 == 0 and n >= 12 * D
+        assert n % 256 == 0 and n >= 8 * D
 
 
 # resid, y, post, gate, pre, rng, resid_out, norm_out
