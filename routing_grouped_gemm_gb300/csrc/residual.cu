@@ -421,7 +421,13 @@ struct BackwardArgs {
 // reduction's is needed; it reads them from there twice, before and behind the
 // reduction.  Rows too wide for two in shared memory are read from global memory
 // instead, the second time from L2 (RING false).
-template <bool BF16, int NV, bool WARP, bool DROP, bool RING>
+//
+// The kernel is as much bound by instructions as by bytes (per vector of 8 about
+// 100 to unpack five operands twice, 80 of arithmetic two values at a time), so
+// what is usual is known when it is compiled: FULL has both gradients, both norms'
+// operands and no gate of its own for every element; DROP is dropout.  The rest
+// asks as it goes.
+template <bool BF16, int NV, bool WARP, bool FULL, bool DROP, bool RING>
 __global__ void __launch_bounds__(WARP ? 256 : NV == 1 ? 256 : 512, NV == 1 ? 2 : 1)
 residual_norm_backward_kernel(const BackwardArgs a) {
     extern __shared__ __align__(16) char smem[];
@@ -434,10 +440,11 @@ residual_norm_backward_kernel(const BackwardArgs a) {
     const int unit = WARP ? blockIdx.x * (blockDim.x >> 5) + warp : blockIdx.x;
     const int units = WARP ? gridDim.x * (blockDim.x >> 5) : gridDim.x;
     const float inv_d = 1.f / (float)a.D;
-    const bool branch = a.y, elem = a.gate_kind == GATE_ELEMENT;
-    const float dscale = DROP ? a.drop.scale : 1.f;
+    const bool branch = FULL || a.y, elem = !FULL && a.gate_kind == GATE_ELEMENT;
+    const bool drops = FULL ? DROP : a.drop.cut > 0, has_pre = FULL || a.pre;
+    const float dscale = drops ? a.drop.scale : 1.f;
     uint64_t seed = 0, offset = 0;
-    if (DROP) {
+    if (drops) {
         seed = (uint64_t)a.drop.rng[0];
         offset = (uint64_t)a.drop.rng[1];
     }
@@ -455,7 +462,7 @@ residual_norm_backward_kernel(const BackwardArgs a) {
         }
         if (v >= V) continue;
         f2 f[4];
-        if (a.pre) pre[i] = load8<BF16>(a.pre, v);
+        if (has_pre) pre[i] = load8<BF16>(a.pre, v);
         if (a.post) {
             unpack8<BF16>(load8<BF16>(a.post, v), f);
 #pragma unroll
@@ -473,12 +480,23 @@ residual_norm_backward_kernel(const BackwardArgs a) {
     const void *arrays[5] = {a.s, a.ds_out, a.dn, a.y, elem ? a.gate : nullptr};
     const uint32_t plane = blockDim.x * 16, ring = smem_u32(smem) + tid * 16;
     const uint32_t stage_bytes = a.in_ring * NV * (EB / 16) * plane;
+    auto has = [&](int k) { return FULL ? k < 4 : arrays[k] != nullptr; };
+    if (RING) {  // columns past the row's end read zeros
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (mine + i * across >= V)
+                for (int k = 0; k < a.depth * a.in_ring; ++k)
+#pragma unroll
+                    for (int h = 0; h < EB / 16; ++h)
+                        *reinterpret_cast<uint4 *>(smem + tid * 16 + ((k * NV + i) * (EB / 16) + h) * plane) =
+                            make_uint4(0, 0, 0, 0);
+    }
     auto copy_row = [&](long long t, int stage) {
         if (!RING) return;
         if (t < a.T) {
 #pragma unroll
             for (int k = 0; k < 5; ++k) {
-                if (!arrays[k]) continue;
+                if (!has(k)) continue;
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     const int v = mine + i * across;
@@ -497,8 +515,8 @@ residual_norm_backward_kernel(const BackwardArgs a) {
     };
     auto take = [&](int k, int i, int stage, size_t base) {
         Pack<BF16> r = {};
-        if (!arrays[k] || mine + i * across >= V) return r;
-        if (!RING) return load8<BF16>(arrays[k], base + mine + i * across);
+        if (!has(k)) return r;
+        if (!RING) return mine + i * across < V ? load8<BF16>(arrays[k], base + mine + i * across) : r;
         const char *p = smem + tid * 16 + stage * stage_bytes + (k * NV + i) * (EB / 16) * plane;
         r.a = *reinterpret_cast<const uint4 *>(p);
         if constexpr (!BF16) r.b = *reinterpret_cast<const uint4 *>(p + plane);
@@ -525,7 +543,7 @@ residual_norm_backward_kernel(const BackwardArgs a) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             bits[i] = 0xffu;
-            if (DROP) bits[i] = keep_bits(base + mine + i * across, a.drop.cut, seed, offset);
+            if (drops) bits[i] = keep_bits(base + mine + i * across, a.drop.cut, seed, offset);
             f2 s[4], d[4], n[4], y[4], w[4];
             unpack8<BF16>(take(0, i, stage, base), s);
             unpack8<BF16>(take(1, i, stage, base), d);
@@ -546,7 +564,7 @@ residual_norm_backward_kernel(const BackwardArgs a) {
             for (int e = 0; e < 4; ++e) {
                 const f2 gp = mul2(n[e], w[e]);
                 f2 q = mul2(y[e], coef[i][e]);
-                if (DROP) q = kept(q, bits[i], e);
+                if (drops) q = kept(q, bits[i], e);
                 m[0] = fma2(s[e], s[e], m[0]);
                 m[1] = fma2(gp, s[e], m[1]);
                 if (!elem) m[2] = fma2(y[e], y[e], m[2]);
@@ -557,7 +575,7 @@ residual_norm_backward_kernel(const BackwardArgs a) {
         }
         float sum[8] = {sum2(m[0]), sum2(m[1]), sum2(m[2]), sum2(m[3]), sum2(m[4]), sum2(m[5]), 0.f, 0.f};
         row_sums<WARP>(sum, s_sum[turn]);
-        const float r2 = a.pre ? rsqrtf(fmaf(sum[0], inv_d, a.eps)) : 0.f;
+        const float r2 = has_pre ? rsqrtf(fmaf(sum[0], inv_d, a.eps)) : 0.f;
         const float c = r2 * r2 * r2 * (sum[1] * inv_d);
         const float r1 = a.post ? rsqrtf(fmaf(sum[2], inv_d, a.eps)) : 1.f;
         const float dot = sum[3] + r2 * sum[4] - c * sum[5];  // sum(ds q)
@@ -582,7 +600,7 @@ residual_norm_backward_kernel(const BackwardArgs a) {
             for (int e = 0; e < 4; ++e) {
                 const f2 ds = fma2(s[e], c_2, fma2(mul2(n[e], w[e]), r2_2, d[e]));
                 P[i][e] = fma2(n[e], mul2(s[e], r2_2), P[i][e]);
-                f2 k = DROP ? kept(ds, bits[i], e) : ds;
+                f2 k = drops ? kept(ds, bits[i], e) : ds;
                 if (elem) {
                     dg[e] = mul2(mul2(k, coef[i][e]), mul2(y[e], r1_2));
                     k = mul2(k, ge[e]);
@@ -649,7 +667,7 @@ __device__ __forceinline__ float factor_at(const void *p, int c, int is_bf16) {
                    : static_cast<const float *>(p)[c];
 }
 
-constexpr int FIN_COLS = 32, FIN_ROWS = 16;
+constexpr int FIN_COLS = 32, FIN_ROWS = 32;
 __global__ void __launch_bounds__(FIN_COLS *FIN_ROWS)
 residual_finish_kernel(const FinishArgs a) {
     griddep_launch_dependents();
@@ -661,6 +679,7 @@ residual_finish_kernel(const FinishArgs a) {
     const float *p = a.part + (is_G ? (size_t)a.parts * a.D : 0);
     float sum = 0.f;
     if (c < a.D)
+#pragma unroll 5
         for (int i = r; i < a.parts; i += FIN_ROWS) sum += p[(size_t)i * a.D + c];
     s[r][threadIdx.x] = sum;
     __syncthreads();
@@ -820,20 +839,25 @@ cudaError_t launch_residual_norm_backward(const ResidualNorm &r, const void *s, 
         a.depth = g.depth;
         a.in_ring = g.in_ring;
         using Kernel = void (*)(BackwardArgs);
-        static const Kernel kernels[2][2][7] = {
-#define MOE_GRADIENT(BF16, DROP)                                                                  \
-    {residual_norm_backward_kernel<BF16, 1, true, DROP, true>,                                    \
-     residual_norm_backward_kernel<BF16, 2, true, DROP, true>,                                    \
-     residual_norm_backward_kernel<BF16, 4, true, DROP, true>,                                    \
-     residual_norm_backward_kernel<BF16, 1, false, DROP, true>,                                   \
-     residual_norm_backward_kernel<BF16, 2, false, DROP, true>,                                   \
-     residual_norm_backward_kernel<BF16, 4, false, DROP, false>,                                  \
-     residual_norm_backward_kernel<BF16, 8, false, DROP, false>}
-            {MOE_GRADIENT(false, false), MOE_GRADIENT(false, true)},
-            {MOE_GRADIENT(true, false), MOE_GRADIENT(true, true)}};
-#undef MOE_GRADIENT
+        // [type][rows in a warp: 1, 2, 4 vectors a lane; in a CTA: 1, 2; without a ring: 4, 8]
+#define MOE_RINGS(BF16, FULL, DROP)                                                             \
+    residual_norm_backward_kernel<BF16, 1, true, FULL, DROP, true>,                               \
+        residual_norm_backward_kernel<BF16, 2, true, FULL, DROP, true>,                           \
+        residual_norm_backward_kernel<BF16, 4, true, FULL, DROP, true>,                           \
+        residual_norm_backward_kernel<BF16, 1, false, FULL, DROP, true>,                          \
+        residual_norm_backward_kernel<BF16, 2, false, FULL, DROP, true>
+#define MOE_ANY(BF16)                                                                           \
+    MOE_RINGS(BF16, false, false), residual_norm_backward_kernel<BF16, 4, false, false, false, false>, \
+        residual_norm_backward_kernel<BF16, 8, false, false, false, false>
+        static const Kernel any[2][7] = {{MOE_ANY(false)}, {MOE_ANY(true)}};
+        static const Kernel full[2][2][5] = {{{MOE_RINGS(false, true, false)}, {MOE_RINGS(false, true, true)}},
+                                             {{MOE_RINGS(true, true, false)}, {MOE_RINGS(true, true, true)}}};
+#undef MOE_RINGS
+#undef MOE_ANY
         const int which = g.warp ? (g.nv == 4 ? 2 : g.nv - 1) : g.ring ? 2 + g.nv : g.nv == 4 ? 5 : 6;
-        const Kernel kernel = kernels[r.is_bf16 ? 1 : 0][r.drop_cut > 0 ? 1 : 0][which];
+        const bool is_full = g.ring && y && dresid_out && r.pre && r.gate_kind != GATE_ELEMENT;
+        const Kernel kernel = is_full ? full[r.is_bf16 ? 1 : 0][r.drop_cut > 0 ? 1 : 0][which]
+                                      : any[r.is_bf16 ? 1 : 0][which];
         if ((err = ensure_smem((const void *)kernel, g.smem)) != cudaSuccess) return err;
         err = launch_pdl(kernel, dim3(g.ctas), dim3(g.threads), g.smem, stream, a);
         if (err != cudaSuccess) return err;
