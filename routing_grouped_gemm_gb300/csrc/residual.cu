@@ -72,8 +72,15 @@ __device__ __forceinline__ void store8(void *p, size_t vec, const float (&f)[8])
         for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
         static_cast<uint4 *>(p)[vec] = o;
     } else {
-        static_cast<float4 *>(p)[2 * vec] = make_float4(f[0], f[1], f[2], f[3]);
-        static_cast<float4 *>(p)[2 * vec + 1] = make_float4(f[4], f[5], f[6], f[7]);
+        float *q = static_cast<float *>(p) + 8 * vec;
+        if ((reinterpret_cast<uintptr_t>(q) & 31) == 0) {  // a whole sector at once
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(q), "f"(f[0]),
+                         "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
+                         : "memory");
+        } else {
+            reinterpret_cast<float4 *>(q)[0] = make_float4(f[0], f[1], f[2], f[3]);
+            reinterpret_cast<float4 *>(q)[1] = make_float4(f[4], f[5], f[6], f[7]);
+        }
     }
 }
 
@@ -121,6 +128,79 @@ __device__ __forceinline__ void drop8(float (&f)[8], uint64_t vec, const Drop &d
 }
 
 // ---------------------------------------------------------------------
+// arithmetic on pairs
+// ---------------------------------------------------------------------
+// Pairs of fp32, added and multiplied two at a time.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pair(float x, float y) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 parts(f2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f2 both(float x) { return pair(x, x); }
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float sum2(f2 v) {
+    const float2 p = parts(v);
+    return p.x + p.y;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void unpack8(const Pack<BF16> &p, f2 (&f)[4]) {
+    float v[8];
+    unpack8<BF16>(p, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = pair(v[2 * i], v[2 * i + 1]);
+}
+template <bool BF16>
+__device__ __forceinline__ void store8(void *p, size_t vec, const f2 (&f)[4]) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 q = parts(f[i]);
+        v[2 * i] = q.x;
+        v[2 * i + 1] = q.y;
+    }
+    store8<BF16>(p, vec, v);
+}
+
+__device__ __forceinline__ void put8(float *shared, const f2 (&f)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) reinterpret_cast<float2 *>(shared)[i] = parts(f[i]);
+}
+
+// Bit e: element e of a vector stays.
+__device__ __forceinline__ uint32_t keep_bits(uint64_t vec, uint32_t cut, uint64_t seed,
+                                              uint64_t offset) {
+    const uint4 w = philox(vec, offset, seed);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    uint32_t bits = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        bits |= ((u[i] & 0xffffu) >= cut ? 1u : 0u) << (2 * i);
+        bits |= ((u[i] >> 16) >= cut ? 1u : 0u) << (2 * i + 1);
+    }
+    return bits;
+}
+__device__ __forceinline__ f2 kept(f2 v, uint32_t bits, int i) {
+    const float2 p = parts(v);
+    return pair(bits >> (2 * i) & 1u ? p.x : 0.f, bits >> (2 * i + 1) & 1u ? p.y : 0.f);
+}
+
+// ---------------------------------------------------------------------
 // row sums over a CTA
 // ---------------------------------------------------------------------
 // Sums v[0..N) over the CTA's threads; every thread gets them.  One barrier:
@@ -148,6 +228,82 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float *slot) {
 }
 
 // ---------------------------------------------------------------------
+// a thread's own columns of the next rows, in shared memory
+// ---------------------------------------------------------------------
+// Thread `mine` of the `across` that share a row copies vectors mine + i across
+// (i < NV) of up to 5 arrays with cp.async and alone reads them back (fp32: a warp
+// copies for its lanes), so that the next rows are in flight while one is worked
+// on and nothing has to be waited for but one's own copies.  [depth][array][NV] vectors, a plane of 16-byte pieces
+// over the CTA's threads for each (and each half of an fp32 vector).
+template <bool BF16, int NV> struct Ring {
+    static constexpr int EB = BF16 ? 16 : 32;  // bytes of a vector
+    char *own;
+    uint32_t plane, stage_bytes;
+    int V, mine, across, depth;
+
+    __device__ __forceinline__ Ring(char *smem, int V_, int mine_, int across_, int depth_, int arrays)
+        : own(smem + threadIdx.x * 16), plane(blockDim.x * 16),
+          stage_bytes(arrays * NV * (EB / 16) * plane), V(V_), mine(mine_), across(across_), depth(depth_) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)  // columns past the row's end read zeros
+            if (mine + i * across >= V)
+                for (int k = 0; k < depth * arrays; ++k)
+#pragma unroll
+                    for (int h = 0; h < EB / 16; ++h)
+                        *reinterpret_cast<uint4 *>(own + ((k * NV + i) * (EB / 16) + h) * plane) =
+                            make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void copy(const void *array, int k, size_t base, int stage) {
+        const uint32_t at = smem_u32(own) + stage * stage_bytes + k * NV * (EB / 16) * plane;
+        const char *src = static_cast<const char *>(array) + base * EB;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if constexpr (BF16) {
+                const int v = mine + i * across;
+                if (v < V) copy_piece(at + i * plane, src + (size_t)v * 16);
+            } else {
+                // A warp's 32 vectors are 64 pieces in a row: a lane takes pieces
+                // lane and lane + 32, so that each copy reads 512 bytes on end,
+                // and puts them where the vector's own lane looks.
+                const int lane = threadIdx.x & 31;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int q = 32 * h + lane, v = mine - lane + i * across + (q >> 1);
+                    if (v < V)
+                        copy_piece(at + (2 * i + (q & 1)) * plane + ((q >> 1) - lane) * 16,
+                                   src + (size_t)v * 32 + 16 * (q & 1));
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ static void copy_piece(uint32_t dst, const char *src) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    }
+    __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    // the oldest of `depth` committed rows is there
+    __device__ __forceinline__ void wait() {
+        switch (depth) {
+        case 2: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+        case 3: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+        default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+        }
+        if (!BF16) __syncwarp();
+    }
+    // before a slot that the warp has read is copied into again
+    __device__ __forceinline__ void reuse() {
+        if (!BF16) __syncwarp();
+    }
+    __device__ __forceinline__ void drain() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+    __device__ __forceinline__ Pack<BF16> take(int k, int i, int stage) const {
+        const char *p = own + stage * stage_bytes + (k * NV + i) * (EB / 16) * plane;
+        Pack<BF16> r;
+        r.a = *reinterpret_cast<const uint4 *>(p);
+        if constexpr (!BF16) r.b = *reinterpret_cast<const uint4 *>(p + plane);
+        return r;
+    }
+};
+
+// ---------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------
 struct ForwardArgs {
@@ -156,6 +312,7 @@ struct ForwardArgs {
     Drop drop;
     float eps, res_scale, branch_scale;
     int T, D, gate_kind;
+    int depth, in_ring;  // rows and arrays of the ring kernel's
     // the combine in front (COMBINE): y[t] = sum_j topk_w[t, j] y_perm[row_of[t, j]]
     const int *row_of;
     const float *topk_w;
@@ -164,11 +321,20 @@ struct ForwardArgs {
     int *status;
 };
 
+// 8 values of an expert's row: fp16 with bf16 layers, else fp32.
+template <bool BF16> using ExpertPack = Pack<BF16>;
 template <bool BF16>
-__device__ __forceinline__ void expert_row8(const void *y_perm, size_t vec, float (&f)[8]) {
-    if constexpr (BF16) {  // fp16 rows
-        const uint4 q = __ldcs(static_cast<const uint4 *>(y_perm) + vec);
-        const __half2 *h = reinterpret_cast<const __half2 *>(&q);
+__device__ __forceinline__ ExpertPack<BF16> expert_load8(const void *y_perm, size_t vec) {
+    ExpertPack<BF16> r;
+    const uint4 *p = static_cast<const uint4 *>(y_perm) + (BF16 ? vec : 2 * vec);
+    r.a = __ldcs(p);
+    if constexpr (!BF16) r.b = __ldcs(p + 1);
+    return r;
+}
+template <bool BF16>
+__device__ __forceinline__ void expert_unpack8(const ExpertPack<BF16> &q, float (&f)[8]) {
+    if constexpr (BF16) {
+        const __half2 *h = reinterpret_cast<const __half2 *>(&q.a);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float2 p = __half22float2(h[i]);
@@ -176,17 +342,20 @@ __device__ __forceinline__ void expert_row8(const void *y_perm, size_t vec, floa
             f[2 * i + 1] = p.y;
         }
     } else {
-        unpack8<false>(load8<false>(y_perm, vec), f);
+        unpack8<false>(q, f);
     }
 }
 
+// One row per CTA at a time, straight from global memory: few rows, the widest
+// ones, and behind the combine.
 // NV vectors of 8 per thread: vector tid + i blockDim of the row.
 template <bool BF16, int NV, bool COMBINE>
 __global__ void __launch_bounds__(1024)
-residual_norm_kernel(const ForwardArgs a) {
+residual_norm_row_kernel(const ForwardArgs a) {
     griddep_launch_dependents();
     griddep_wait();
     __shared__ float s_sum[2][32];
+    constexpr int SLOTS = NV == 1 ? 2 : 1;
     __shared__ int s_row[32];
     __shared__ float s_w[32];
     const int V = a.D / 8, tid = threadIdx.x;
@@ -222,21 +391,46 @@ residual_norm_kernel(const ForwardArgs a) {
             for (int e = 0; e < 8; ++e) s[i][e] = y[i][e] = 0.f;
             if (v >= V) continue;
             unpack8<BF16>(load8<BF16>(a.resid, base + v), s[i]);
-            if constexpr (COMBINE) {
-                for (int j = 0; j < a.k; ++j) {
-                    if (s_row[j] < 0) continue;
-                    float f[8];
-                    expert_row8<BF16>(a.y, (size_t)s_row[j] * V + v, f);
+            if (!COMBINE && branch) unpack8<BF16>(load8<BF16>(a.y, base + v), y[i]);
+        }
+        if constexpr (COMBINE) {
+            for (int j0 = 0; j0 < a.k; j0 += SLOTS) {  // SLOTS rows' loads in flight
+                Pack<BF16> q[SLOTS][NV];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) y[i][e] = fmaf(s_w[j], f[e], y[i][e]);
+                for (int u = 0; u < SLOTS; ++u) {
+                    const int j = j0 + u;
+                    if (j >= a.k || s_row[j] < 0) continue;
+                    const size_t at = (size_t)s_row[j] * V + tid;
+#pragma unroll
+                    for (int i = 0; i < NV; ++i)
+                        if (tid + i * blockDim.x < V)
+                            q[u][i] = expert_load8<BF16>(a.y, at + i * blockDim.x);
                 }
-                if (a.y_out) store8<BF16>(a.y_out, base + v, y[i]);
-            } else if (branch) {
-                unpack8<BF16>(load8<BF16>(a.y, base + v), y[i]);
+#pragma unroll
+                for (int u = 0; u < SLOTS; ++u) {
+                    const int j = j0 + u;
+                    if (j >= a.k || s_row[j] < 0) continue;
+                    const float w = s_w[j];
+#pragma unroll
+                    for (int i = 0; i < NV; ++i) {
+                        if (tid + i * blockDim.x >= V) continue;
+                        float f[8];
+                        expert_unpack8<BF16>(q[u][i], f);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) y[i][e] = fmaf(w, f[e], y[i][e]);
+                    }
+                }
             }
+            if (a.y_out) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if (tid + i * blockDim.x < V) store8<BF16>(a.y_out, base + tid + i * blockDim.x, y[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int e = 0; e < 8; ++e) sum[0] = fmaf(y[i][e], y[i][e], sum[0]);
-        }
         if (branch) {
             float r1 = 1.f;
             if (a.post) {
@@ -290,74 +484,137 @@ residual_norm_kernel(const ForwardArgs a) {
     }
 }
 
+// Many rows: a row per CTA (WARP: per warp, narrow rows) at a time, the next ones
+// in a Ring.  FULL: a branch and the next norm, no gate for every element.
+template <bool BF16, int NV, bool WARP, bool FULL>
+__global__ void __launch_bounds__(256, NV == 4 && WARP ? 1 : 2)
+residual_norm_ring_kernel(const ForwardArgs a) {
+    extern __shared__ __align__(16) char smem[];
+    __shared__ float s_sum[2][32];
+    griddep_launch_dependents();
+    griddep_wait();
+    const int V = a.D / 8, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int mine = WARP ? lane : tid, across = WARP ? 32 : blockDim.x;
+    const int unit = WARP ? blockIdx.x * (blockDim.x >> 5) + warp : blockIdx.x;
+    const int units = WARP ? gridDim.x * (blockDim.x >> 5) : gridDim.x;
+    const float inv_d = 1.f / (float)a.D;
+    const bool branch = FULL || a.y, elem = !FULL && a.gate_kind == GATE_ELEMENT;
+    const bool has_pre = FULL || a.pre, drops = a.drop.cut > 0;
+    uint64_t seed = 0, offset = 0;
+    if (drops) {
+        seed = (uint64_t)a.drop.rng[0];
+        offset = (uint64_t)a.drop.rng[1];
+    }
+    Pack<BF16> pre[NV];
+    f2 coef[NV][4];  // branch_scale, the dropout's factor, post, a channel's gate
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int v = mine + i * across;
+        pre[i] = Pack<BF16>{};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) coef[i][e] = both(a.branch_scale * (drops ? a.drop.scale : 1.f));
+        if (v >= V) continue;
+        f2 f[4];
+        if (has_pre) pre[i] = load8<BF16>(a.pre, v);
+        if (a.post) {
+            unpack8<BF16>(load8<BF16>(a.post, v), f);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) coef[i][e] = mul2(coef[i][e], f[e]);
+        }
+        if (a.gate_kind == GATE_CHANNEL) {
+            unpack8<BF16>(load8<BF16>(a.gate, v), f);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) coef[i][e] = mul2(coef[i][e], f[e]);
+        }
+    }
+    Ring<BF16, NV> ring(smem, V, mine, across, a.depth, a.in_ring);
+    auto copy_row = [&](long long t, int stage) {
+        if (t < a.T) {
+            const size_t base = (size_t)t * V;
+            ring.copy(a.resid, 0, base, stage);
+            if (branch) ring.copy(a.y, 1, base, stage);
+            if (elem) ring.copy(a.gate, 2, base, stage);
+        }
+        ring.commit();
+    };
+    int turn = 0, stage = 0;
+    auto row_sum = [&](float x) {
+        float v[1] = {x};
+        if (WARP) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+        } else {
+            block_sum<1>(v, s_sum[turn]);
+            turn ^= 1;
+        }
+        return v[0];
+    };
+    for (int i = 0; i < a.depth - 1; ++i) copy_row(unit + (long long)i * units, i);
+    for (long long t = unit; t < a.T; t += units) {
+        ring.reuse();
+        copy_row(t + (long long)(a.depth - 1) * units, stage == 0 ? a.depth - 1 : stage - 1);
+        ring.wait();
+        const size_t base = (size_t)t * V;
+        f2 s[NV][4];
+        f2 sum;
+        if (branch) {
+            float r1 = a.gate_kind == GATE_TOKEN ? static_cast<const float *>(a.gate)[t] : 1.f;
+            f2 y[NV][4];
+#pragma unroll
+            for (int i = 0; i < NV; ++i) unpack8<BF16>(ring.take(1, i, stage), y[i]);
+            if (a.post) {
+                sum = both(0.f);
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sum = fma2(y[i][e], y[i][e], sum);
+                r1 *= rsqrtf(fmaf(row_sum(sum2(sum)), inv_d, a.eps));
+            }
+            const f2 r1_2 = both(r1), res_2 = both(a.res_scale);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                unpack8<BF16>(ring.take(0, i, stage), s[i]);
+                uint32_t bits = 0xffu;
+                if (drops) bits = keep_bits(base + mine + i * across, a.drop.cut, seed, offset);
+                f2 ge[4];
+                if (elem) unpack8<BF16>(ring.take(2, i, stage), ge);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    f2 v = mul2(mul2(y[i][e], r1_2), coef[i][e]);
+                    if (elem) v = mul2(v, ge[e]);
+                    if (drops) v = kept(v, bits, e);
+                    s[i][e] = fma2(s[i][e], res_2, v);
+                }
+                if (mine + i * across < V) store8<BF16>(a.resid_out, base + mine + i * across, s[i]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) unpack8<BF16>(ring.take(0, i, stage), s[i]);
+        }
+        if (has_pre) {
+            sum = both(0.f);
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum = fma2(s[i][e], s[i][e], sum);
+            const f2 r2_2 = both(rsqrtf(fmaf(row_sum(sum2(sum)), inv_d, a.eps)));
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                f2 w[4];
+                unpack8<BF16>(pre[i], w);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = mul2(mul2(s[i][e], r2_2), w[e]);
+                if (mine + i * across < V) store8<BF16>(a.norm_out, base + mine + i * across, w);
+            }
+        }
+        if (++stage == a.depth) stage = 0;
+    }
+    ring.drain();
+}
+
 // ---------------------------------------------------------------------
 // gradient
 // ---------------------------------------------------------------------
-// Pairs of fp32, added and multiplied two at a time.
-using f2 = unsigned long long;
-__device__ __forceinline__ f2 pair(float x, float y) {
-    f2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-    return r;
-}
-__device__ __forceinline__ float2 parts(f2 v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ f2 both(float x) { return pair(x, x); }
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ float sum2(f2 v) {
-    const float2 p = parts(v);
-    return p.x + p.y;
-}
-
-template <bool BF16>
-__device__ __forceinline__ void unpack8(const Pack<BF16> &p, f2 (&f)[4]) {
-    float v[8];
-    unpack8<BF16>(p, v);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = pair(v[2 * i], v[2 * i + 1]);
-}
-template <bool BF16>
-__device__ __forceinline__ void store8(void *p, size_t vec, const f2 (&f)[4]) {
-    float v[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 q = parts(f[i]);
-        v[2 * i] = q.x;
-        v[2 * i + 1] = q.y;
-    }
-    store8<BF16>(p, vec, v);
-}
-
-// Bit e: element e of a vector stays.
-__device__ __forceinline__ uint32_t keep_bits(uint64_t vec, uint32_t cut, uint64_t seed,
-                                              uint64_t offset) {
-    const uint4 w = philox(vec, offset, seed);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-    uint32_t bits = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        bits |= ((u[i] & 0xffffu) >= cut ? 1u : 0u) << (2 * i);
-        bits |= ((u[i] >> 16) >= cut ? 1u : 0u) << (2 * i + 1);
-    }
-    return bits;
-}
-__device__ __forceinline__ f2 kept(f2 v, uint32_t bits, int i) {
-    const float2 p = parts(v);
-    return pair(bits >> (2 * i) & 1u ? p.x : 0.f, bits >> (2 * i + 1) & 1u ? p.y : 0.f);
-}
-
 // Eight sums over a warp in nine exchanges: lanes trade halves of what they have
 // until each holds one sum, lane 4 i .. 4 i + 3 the i-th.
 __device__ __forceinline__ float warp_sums(float (&v)[8]) {
@@ -415,11 +672,9 @@ struct BackwardArgs {
 //   P = sum dn s r2 = dpre,   G = sum keep ds y r1 (times a gate that is not the
 //   channel's);  dpost = branch_scale gate G and dgate = branch_scale post G.
 //
-// A row per CTA (WARP: per warp, narrow rows), rows over the grid.  Each thread
-// copies its own columns of the next rows into shared memory with cp.async, so
-// that depth - 1 rows are in flight while one is worked on and no barrier but the
-// reduction's is needed; it reads them from there twice, before and behind the
-// reduction.  Rows too wide for two in shared memory are read from global memory
+// A row per CTA (WARP: per warp, narrow rows), rows over the grid, in a Ring from
+// which each thread reads its columns twice, before and behind the reduction
+// (registers are short).  Rows too wide for two in shared memory are read from global memory
 // instead, the second time from L2 (RING false).
 //
 // The kernel is as much bound by instructions as by bytes (per vector of 8 about
@@ -434,7 +689,6 @@ residual_norm_backward_kernel(const BackwardArgs a) {
     __shared__ float s_sum[2][8 * 32];
     griddep_launch_dependents();
     griddep_wait();
-    constexpr int EB = BF16 ? 16 : 32;  // bytes of a vector
     const int V = a.D / 8, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int mine = WARP ? lane : tid, across = WARP ? 32 : blockDim.x;
     const int unit = WARP ? blockIdx.x * (blockDim.x >> 5) + warp : blockIdx.x;
@@ -475,52 +729,23 @@ residual_norm_backward_kernel(const BackwardArgs a) {
         }
     }
 
-    // the thread's ring: [depth][array][NV] vectors, a plane of 16-byte pieces per
-    // (array, vector, half) over the CTA's threads
     const void *arrays[5] = {a.s, a.ds_out, a.dn, a.y, elem ? a.gate : nullptr};
-    const uint32_t plane = blockDim.x * 16, ring = smem_u32(smem) + tid * 16;
-    const uint32_t stage_bytes = a.in_ring * NV * (EB / 16) * plane;
     auto has = [&](int k) { return FULL ? k < 4 : arrays[k] != nullptr; };
-    if (RING) {  // columns past the row's end read zeros
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (mine + i * across >= V)
-                for (int k = 0; k < a.depth * a.in_ring; ++k)
-#pragma unroll
-                    for (int h = 0; h < EB / 16; ++h)
-                        *reinterpret_cast<uint4 *>(smem + tid * 16 + ((k * NV + i) * (EB / 16) + h) * plane) =
-                            make_uint4(0, 0, 0, 0);
-    }
+    Ring<BF16, NV> ring(smem, V, mine, across, RING ? a.depth : 0, a.in_ring);
     auto copy_row = [&](long long t, int stage) {
         if (!RING) return;
         if (t < a.T) {
 #pragma unroll
-            for (int k = 0; k < 5; ++k) {
-                if (!has(k)) continue;
-#pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const int v = mine + i * across;
-                    if (v >= V) continue;
-                    const char *src = static_cast<const char *>(arrays[k]) + ((size_t)t * V + v) * EB;
-                    const uint32_t dst = ring + stage * stage_bytes + (k * NV + i) * (EB / 16) * plane;
-#pragma unroll
-                    for (int h = 0; h < EB / 16; ++h)
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + h * plane),
-                                     "l"(src + 16 * h)
-                                     : "memory");
-                }
-            }
+            for (int k = 0; k < 5; ++k)
+                if (has(k)) ring.copy(arrays[k], k, (size_t)t * V, stage);
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
+        ring.commit();
     };
     auto take = [&](int k, int i, int stage, size_t base) {
-        Pack<BF16> r = {};
-        if (!has(k)) return r;
-        if (!RING) return mine + i * across < V ? load8<BF16>(arrays[k], base + mine + i * across) : r;
-        const char *p = smem + tid * 16 + stage * stage_bytes + (k * NV + i) * (EB / 16) * plane;
-        r.a = *reinterpret_cast<const uint4 *>(p);
-        if constexpr (!BF16) r.b = *reinterpret_cast<const uint4 *>(p + plane);
-        return r;
+        const Pack<BF16> none = {};
+        if (!has(k)) return none;
+        if (RING) return ring.take(k, i, stage);
+        return mine + i * across < V ? load8<BF16>(arrays[k], base + mine + i * across) : none;
     };
     for (int i = 0; i < a.depth - 1; ++i) copy_row(unit + (long long)i * units, i);
 
@@ -528,12 +753,9 @@ residual_norm_backward_kernel(const BackwardArgs a) {
     for (long long row = unit; row < a.T; row += units, turn ^= 1) {
         const int t = (int)row;
         const int last = stage == 0 ? a.depth - 1 : stage - 1;  // read a row ago
+        if (RING) ring.reuse();
         copy_row(t + (long long)(a.depth - 1) * units, last);
-        if (RING) switch (a.depth) {  // the row's own copies are the depth-th last group
-        case 2: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-        case 3: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-        default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-        }
+        if (RING) ring.wait();
         const size_t base = (size_t)t * V;
         const float gt = a.gate_kind == GATE_TOKEN ? static_cast<const float *>(a.gate)[t] : 1.f;
         uint32_t bits[NV];
@@ -615,7 +837,7 @@ residual_norm_backward_kernel(const BackwardArgs a) {
         }
         if (++stage == a.depth) stage = 0;
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    ring.drain();
 
     // The CTA's column sums.  A channel's gate takes the token's gate for one:
     // G holds neither.
@@ -641,7 +863,7 @@ residual_norm_backward_kernel(const BackwardArgs a) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (mine + i * across < V)
-                store8<false>(sums + (size_t)warp * a.D, mine + i * across, which ? G[i] : P[i]);
+                put8(sums + (size_t)warp * a.D + 8 * (mine + i * across), which ? G[i] : P[i]);
         __syncthreads();
         for (int d = tid; d < a.D; d += blockDim.x) {
             float x = 0.f;
@@ -712,17 +934,54 @@ Drop make_drop(const ResidualNorm &r) {
 }
 
 template <bool COMBINE>
-cudaError_t forward(const ResidualNorm &r, const ForwardArgs &a, cudaStream_t stream) {
+cudaError_t forward_rows(const ResidualNorm &r, const ForwardArgs &a, cudaStream_t stream) {
     int threads, nv;
-    row_shape(r.D / 8, &threads, &nv);
-    auto kernel = r.is_bf16 ? (nv == 1   ? residual_norm_kernel<true, 1, COMBINE>
-                               : nv == 2 ? residual_norm_kernel<true, 2, COMBINE>
-                                         : residual_norm_kernel<true, 4, COMBINE>)
-                            : (nv == 1   ? residual_norm_kernel<false, 1, COMBINE>
-                               : nv == 2 ? residual_norm_kernel<false, 2, COMBINE>
-                                         : residual_norm_kernel<false, 4, COMBINE>);
+    const int V = r.D / 8;
+    row_shape(V, &threads, &nv);
+    auto kernel = r.is_bf16 ? (nv == 1   ? residual_norm_row_kernel<true, 1, COMBINE>
+                               : nv == 2 ? residual_norm_row_kernel<true, 2, COMBINE>
+                                         : residual_norm_row_kernel<true, 4, COMBINE>)
+                            : (nv == 1   ? residual_norm_row_kernel<false, 1, COMBINE>
+                               : nv == 2 ? residual_norm_row_kernel<false, 2, COMBINE>
+                                         : residual_norm_row_kernel<false, 4, COMBINE>);
     const int grid = std::min(r.T, std::max(1, sm_count()) * std::max(1, 2048 / threads));
     const cudaError_t err = launch_pdl(kernel, dim3(grid), dim3(threads), 0, stream, a);
+    if (err == cudaSuccess) count_launch();
+    return err;
+}
+
+cudaError_t forward(const ResidualNorm &r, ForwardArgs &a, cudaStream_t stream) {
+    const int V = r.D / 8, vec = r.is_bf16 ? 16 : 32;
+    const bool warp = V <= 128;
+    // What a row costs besides its vectors (two reductions, its copies' addresses)
+    // is paid by every warp, so few warps take several vectors each (16384 x 4096:
+    // one vector 95.8 us, two 86.5), and two rows in the ring are in flight enough
+    // (two 86.5, three 89.9, four 93.0).
+    const int nv = warp ? (V <= 32 ? 1 : V <= 64 ? 2 : 4) : V <= 512 ? 2 : 4;
+    const int threads = warp ? 256 : ((V + nv - 1) / nv + 31) / 32 * 32;
+    a.in_ring = r.gate_kind == GATE_ELEMENT ? 3 : 2;
+    const size_t stage = (size_t)a.in_ring * nv * vec * threads;
+    int per_sm = warp ? (nv == 4 ? 1 : 2) : std::min(8, 512 / threads);
+    while (per_sm > 1 && 2 * stage * per_sm > 220 * 1024) --per_sm;
+    a.depth = 2 * stage * per_sm > 220 * 1024 ? 1 : 2;
+    const int at_once = sm_count() * per_sm * (warp ? 8 : 1);
+    // one row a CTA leaves nothing to copy ahead: then, and for the widest rows,
+    // straight from global memory
+    if (V > 1024 || a.depth < 2 || r.T <= at_once) return forward_rows<false>(r, a, stream);
+    using Kernel = void (*)(ForwardArgs);
+#define MOE_RINGS(BF16, FULL)                                                                   \
+    {residual_norm_ring_kernel<BF16, 1, true, FULL>, residual_norm_ring_kernel<BF16, 2, true, FULL>, \
+     residual_norm_ring_kernel<BF16, 4, true, FULL>, residual_norm_ring_kernel<BF16, 2, false, FULL>, \
+     residual_norm_ring_kernel<BF16, 4, false, FULL>}
+    static const Kernel kernels[2][2][5] = {{MOE_RINGS(false, false), MOE_RINGS(false, true)},
+                                            {MOE_RINGS(true, false), MOE_RINGS(true, true)}};
+#undef MOE_RINGS
+    const bool is_full = a.y && a.pre && r.gate_kind != GATE_ELEMENT;
+    const int which = warp ? (nv == 4 ? 2 : nv - 1) : (nv == 4 ? 4 : 3);
+    const Kernel kernel = kernels[r.is_bf16 ? 1 : 0][is_full ? 1 : 0][which];
+    cudaError_t err = ensure_smem((const void *)kernel, stage * a.depth);
+    if (err != cudaSuccess) return err;
+    err = launch_pdl(kernel, dim3(sm_count() * per_sm), dim3(threads), stage * a.depth, stream, a);
     if (err == cudaSuccess) count_launch();
     return err;
 }
@@ -752,7 +1011,7 @@ cudaError_t launch_residual_norm(const ResidualNorm &r, const void *resid, const
     if (r.T == 0) return cudaSuccess;
     ForwardArgs a = forward_args(r, resid, resid_out, norm_out);
     a.y = y;
-    return forward<false>(r, a, stream);
+    return forward(r, a, stream);
 }
 
 cudaError_t launch_combine_residual_norm(const ResidualNorm &r, const void *y_perm,
@@ -769,7 +1028,7 @@ cudaError_t launch_combine_residual_norm(const ResidualNorm &r, const void *y_pe
     a.k = k;
     a.rows_alloc = rows_alloc;
     a.status = status;
-    return forward<true>(r, a, stream);
+    return forward_rows<true>(r, a, stream);
 }
 
 // Shape of a gradient launch.
@@ -781,25 +1040,31 @@ struct GradientShape {
 
 namespace {
 
+// A row per warp up to 512 columns, else per CTA, with as few vectors a thread as
+// 256 threads allow (4096 x 2048: one 22.9 us, two 25.0).  Two rows in the ring
+// where a thread has two vectors, else three (16384 x 4096: 133 us with two, 145
+// with three; 16384 x 2048: 70.9 and 67.3): more in flight than DRAM needs costs.
 GradientShape gradient_shape(int T, int D, int is_bf16, int gate_kind) {
     GradientShape g = {};
     const int V = D / 8;
-    // a row per warp while its columns' sums fit a lane's registers, and two rows of
-    // every warp shared memory
-    g.warp = V <= (is_bf16 ? 128 : 64);
-    g.nv = g.warp ? (V <= 32 ? 1 : V <= 64 ? 2 : 4) : (V <= 256 ? 1 : 2);
+    g.warp = V <= 64;
+    g.nv = (g.warp ? V <= 32 : V <= 256) ? 1 : 2;
     g.threads = g.warp ? 256 : ((V + g.nv - 1) / g.nv + 31) / 32 * 32;
     g.in_ring = gate_kind == GATE_ELEMENT ? 5 : 4;
-    const int per_sm = g.nv == 1 ? 2 : 1;
     const size_t stage = (size_t)g.in_ring * g.nv * (is_bf16 ? 1 : 2) * g.threads * 16;
-    g.depth = (int)std::min<size_t>(4, (size_t)(220 * 1024 / per_sm) / stage);
-    g.ring = g.warp || (V <= 1024 && g.depth >= 2);
+    // CTAs per SM by their registers, fewer where two rows each are too much
+    int per_sm = g.warp ? 3 - g.nv : std::max(1, std::min(4, 512 / g.threads));
+    auto fit = [&] { return (int)std::min<size_t>(g.nv == 1 ? 3 : 2, (size_t)(220 * 1024 / per_sm) / stage); };
+    while (per_sm > 1 && fit() < 2) --per_sm;
+    g.depth = fit();
+    g.ring = V <= 1024 && g.depth >= 2;
     g.smem = g.warp ? std::max(stage * g.depth, (size_t)8 * D * 4) : stage * g.depth;
     if (!g.ring) {
         g.nv = V <= 2048 ? 4 : 8;
         g.threads = ((V + g.nv - 1) / g.nv + 31) / 32 * 32;
         g.depth = 1;
         g.smem = 0;
+        per_sm = 1;
     }
     const int rows = g.warp ? 8 : 1;  // at a time in a CTA
     g.ctas = std::min((T + rows - 1) / rows, 152 * per_sm);
@@ -808,7 +1073,7 @@ GradientShape gradient_shape(int T, int D, int is_bf16, int gate_kind) {
 
 }  // namespace
 
-int residual_parts(int T, int D) { return std::min(T, 304); }
+int residual_parts(int T, int D) { return std::min(T, 4 * 152); }
 
 cudaError_t launch_residual_norm_backward(const ResidualNorm &r, const void *s, const void *y,
                                           const void *dresid_out, const void *dnorm_out,
@@ -839,22 +1104,21 @@ cudaError_t launch_residual_norm_backward(const ResidualNorm &r, const void *s, 
         a.depth = g.depth;
         a.in_ring = g.in_ring;
         using Kernel = void (*)(BackwardArgs);
-        // [type][rows in a warp: 1, 2, 4 vectors a lane; in a CTA: 1, 2; without a ring: 4, 8]
+        // [type][a row per warp: 1, 2 vectors a lane; per CTA: 1, 2; without a ring: 4, 8]
 #define MOE_RINGS(BF16, FULL, DROP)                                                             \
     residual_norm_backward_kernel<BF16, 1, true, FULL, DROP, true>,                               \
         residual_norm_backward_kernel<BF16, 2, true, FULL, DROP, true>,                           \
-        residual_norm_backward_kernel<BF16, 4, true, FULL, DROP, true>,                           \
         residual_norm_backward_kernel<BF16, 1, false, FULL, DROP, true>,                          \
         residual_norm_backward_kernel<BF16, 2, false, FULL, DROP, true>
 #define MOE_ANY(BF16)                                                                           \
     MOE_RINGS(BF16, false, false), residual_norm_backward_kernel<BF16, 4, false, false, false, false>, \
         residual_norm_backward_kernel<BF16, 8, false, false, false, false>
-        static const Kernel any[2][7] = {{MOE_ANY(false)}, {MOE_ANY(true)}};
-        static const Kernel full[2][2][5] = {{{MOE_RINGS(false, true, false)}, {MOE_RINGS(false, true, true)}},
+        static const Kernel any[2][6] = {{MOE_ANY(false)}, {MOE_ANY(true)}};
+        static const Kernel full[2][2][4] = {{{MOE_RINGS(false, true, false)}, {MOE_RINGS(false, true, true)}},
                                              {{MOE_RINGS(true, true, false)}, {MOE_RINGS(true, true, true)}}};
 #undef MOE_RINGS
 #undef MOE_ANY
-        const int which = g.warp ? (g.nv == 4 ? 2 : g.nv - 1) : g.ring ? 2 + g.nv : g.nv == 4 ? 5 : 6;
+        const int which = g.warp ? g.nv - 1 : g.ring ? 1 + g.nv : g.nv == 4 ? 4 : 5;
         const bool is_full = g.ring && y && dresid_out && r.pre && r.gate_kind != GATE_ELEMENT;
         const Kernel kernel = is_full ? full[r.is_bf16 ? 1 : 0][r.drop_cut > 0 ? 1 : 0][which]
                                       : any[r.is_bf16 ? 1 : 0][which];

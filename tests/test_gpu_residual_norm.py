@@ -363,3 +363,15 @@ def test_side_stream(moe):
     side.synchronize()
     assert torch.equal(got[0][0], want[0][0]) and torch.equal(got[0][1], want[0][1])
     assert all(want[1][k] is None or torch.equal(got[1][k], want[1][k]) for k in want[1])
+
+
+# rows enough for several a CTA (or a warp), in every shape of the kernels, with the last rows ragged
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,D", [(11003, 72), (7001, 264), (5003, 520), (4999, 1000), (2003, 1032), (1501, 2056), (1301, 4104),
+                                 (701, 8192), (331, 12296), (309, 16400)])
+def test_many_rows(moe, T, D, dtype):
+    for gate, p in (("channel", 0.1), ("element", 0.0)):
+        rc, t, n = _case(moe, T, D, dtype, gate, p=p)
+        _check_forward(rc, t, gate, *_forward(moe, rc, t, in_place=gate == "element"))
+        dso, dn = n(T, D), n(T, D)
+        _check_gradient(rc, t, gate, dso, dn, _gradient(moe, rc, t, gate, dso, dn))
