@@ -203,6 +203,21 @@ class ResidualConfig:
     branch_scale: float = 1.0
     p_drop: float = 0.0
 
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        self.__dict__["_set"] = object()  # as in Config
+
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k not in ("_set", "_ref")}
+
+    def ref(self):
+        """Pointer to the C struct, built once for these values."""
+        d = self.__dict__
+        since, kept = d.get("_set"), d.get("_ref")
+        if kept is None or kept[0] is not since:
+            kept = d["_ref"] = (since, ctypes.pointer(self.c()))
+        return kept[1]
+
     def c(self) -> moe_residual_config:
         return moe_residual_config(self.T, self.D, self.dtype, self.gate, self.eps, self.res_scale,
                                    self.branch_scale, self.p_drop)
@@ -279,7 +294,7 @@ def alloc_workspace(cfg: Config, layer: bool = False, device="cuda", host: bool 
 
 
 def residual_workspace_size(rc: ResidualConfig) -> int:
-    return int(_lib.moe_residual_workspace_size(ctypes.byref(rc.c())))
+    return int(_lib.moe_residual_workspace_size(rc.ref()))
 
 
 def alloc_residual_workspace(rc: ResidualConfig, device="cuda") -> torch.Tensor:
@@ -954,7 +969,7 @@ def moe_residual_norm(rc: ResidualConfig, resid, y, post_gain, gate, pre_gain, r
     the norm of resid alone."""
     td, dt = (rc.T, rc.D), rc.torch_dtype
     _check(_lib.moe_residual_norm(
-        ctypes.byref(rc.c()), _arg(resid, td, dt, "resid"), _maybe(y, td, dt, "y"),
+        rc.ref(), _arg(resid, td, dt, "resid"), _maybe(y, td, dt, "y"),
         _maybe(post_gain, (rc.D,), dt, "post_gain"), _gate_arg(rc, gate),
         _maybe(pre_gain, (rc.D,), dt, "pre_gain"), _maybe(rng, (2,), torch.int64, "rng"),
         _maybe(resid_out, td, dt, "resid_out"), _maybe(norm_out, td, dt, "norm_out"),
@@ -970,7 +985,7 @@ def moe_combine_residual_norm(cfg: Config, rc: ResidualConfig, y_perm, row_of, t
     td, tk, dt = (rc.T, rc.D), (cfg.T, cfg.k), rc.torch_dtype
     p, n, s = _ws(ws, stream)
     _check(_lib.moe_combine_residual_norm(
-        c, ctypes.byref(rc.c()), _arg(y_perm, (ra, cfg.D), cfg.y_dtype, "y_perm"),
+        c, rc.ref(), _arg(y_perm, (ra, cfg.D), cfg.y_dtype, "y_perm"),
         _arg(row_of, tk, torch.int32, "row_of"), _arg(topk_w, tk, torch.float32, "topk_w"),
         _arg(resid, td, dt, "resid"), _maybe(post_gain, (rc.D,), dt, "post_gain"),
         _gate_arg(rc, gate), _maybe(pre_gain, (rc.D,), dt, "pre_gain"),
@@ -989,7 +1004,7 @@ def moe_residual_norm_backward(rc: ResidualConfig, s, y, post_gain, gate, pre_ga
         raise ValueError("dgate: the config names no kind of gate")
     p, n, st = _ws(ws, stream)
     _check(_lib.moe_residual_norm_backward(
-        ctypes.byref(rc.c()), _arg(s, td, dt, "s"), _maybe(y, td, dt, "y"),
+        rc.ref(), _arg(s, td, dt, "s"), _maybe(y, td, dt, "y"),
         _maybe(post_gain, (rc.D,), dt, "post_gain"), _gate_arg(rc, gate),
         _maybe(pre_gain, (rc.D,), dt, "pre_gain"), _maybe(rng, (2,), torch.int64, "rng"),
         _maybe(dresid_out, td, dt, "dresid_out"), _maybe(dnorm_out, td, dt, "dnorm_out"),

@@ -322,17 +322,16 @@ struct ForwardArgs {
 };
 
 // 8 values of an expert's row: fp16 with bf16 layers, else fp32.
-template <bool BF16> using ExpertPack = Pack<BF16>;
 template <bool BF16>
-__device__ __forceinline__ ExpertPack<BF16> expert_load8(const void *y_perm, size_t vec) {
-    ExpertPack<BF16> r;
+__device__ __forceinline__ Pack<BF16> expert_load8(const void *y_perm, size_t vec) {
+    Pack<BF16> r;
     const uint4 *p = static_cast<const uint4 *>(y_perm) + (BF16 ? vec : 2 * vec);
     r.a = __ldcs(p);
     if constexpr (!BF16) r.b = __ldcs(p + 1);
     return r;
 }
 template <bool BF16>
-__device__ __forceinline__ void expert_unpack8(const ExpertPack<BF16> &q, float (&f)[8]) {
+__device__ __forceinline__ void expert_unpack8(const Pack<BF16> &q, float (&f)[8]) {
     if constexpr (BF16) {
         const __half2 *h = reinterpret_cast<const __half2 *>(&q.a);
 #pragma unroll
@@ -355,7 +354,6 @@ residual_norm_row_kernel(const ForwardArgs a) {
     griddep_launch_dependents();
     griddep_wait();
     __shared__ float s_sum[2][32];
-    constexpr int SLOTS = NV == 1 ? 2 : 1;
     __shared__ int s_row[32];
     __shared__ float s_w[32];
     const int V = a.D / 8, tid = threadIdx.x;
@@ -366,19 +364,27 @@ residual_norm_row_kernel(const ForwardArgs a) {
         seed = (uint64_t)a.drop.rng[0];
         offset = (uint64_t)a.drop.rng[1];
     }
+    int row = -1;
+    float w = 0.f;
+    auto read_places = [&](long long t) {
+        if (t >= a.T) return;
+        row = a.row_of[t * a.k + tid];
+        w = a.topk_w[t * a.k + tid];
+    };
+    if (COMBINE && tid < a.k) read_places(blockIdx.x);
     int turn = 0;
-    for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+    for (long long t = blockIdx.x; t < a.T; t += gridDim.x) {
         const size_t base = (size_t)t * V;
         if constexpr (COMBINE) {
             __syncthreads();  // the row before is done with s_row
             if (tid < a.k) {
-                int r = a.row_of[(size_t)t * a.k + tid];
-                if (r < -1 || (long long)r >= a.rows_alloc) {
+                if (row < -1 || (long long)row >= a.rows_alloc) {
                     raise_flag(a.status, FLAG_BAD_ROUTING);
-                    r = -1;
+                    row = -1;
                 }
-                s_row[tid] = r;
-                s_w[tid] = a.topk_w[(size_t)t * a.k + tid];
+                s_row[tid] = row;
+                s_w[tid] = w;
+                read_places(t + gridDim.x);  // of the next row: there when this one is done
             }
             __syncthreads();
         }
@@ -394,31 +400,17 @@ residual_norm_row_kernel(const ForwardArgs a) {
             if (!COMBINE && branch) unpack8<BF16>(load8<BF16>(a.y, base + v), y[i]);
         }
         if constexpr (COMBINE) {
-            for (int j0 = 0; j0 < a.k; j0 += SLOTS) {  // SLOTS rows' loads in flight
-                Pack<BF16> q[SLOTS][NV];
+            for (int j = 0; j < a.k; ++j) {
+                if (s_row[j] < 0) continue;
+                const float wj = s_w[j];
 #pragma unroll
-                for (int u = 0; u < SLOTS; ++u) {
-                    const int j = j0 + u;
-                    if (j >= a.k || s_row[j] < 0) continue;
-                    const size_t at = (size_t)s_row[j] * V + tid;
+                for (int i = 0; i < NV; ++i) {
+                    const int v = tid + i * blockDim.x;
+                    if (v >= V) continue;
+                    float f[8];
+                    expert_unpack8<BF16>(expert_load8<BF16>(a.y, (size_t)s_row[j] * V + v), f);
 #pragma unroll
-                    for (int i = 0; i < NV; ++i)
-                        if (tid + i * blockDim.x < V)
-                            q[u][i] = expert_load8<BF16>(a.y, at + i * blockDim.x);
-                }
-#pragma unroll
-                for (int u = 0; u < SLOTS; ++u) {
-                    const int j = j0 + u;
-                    if (j >= a.k || s_row[j] < 0) continue;
-                    const float w = s_w[j];
-#pragma unroll
-                    for (int i = 0; i < NV; ++i) {
-                        if (tid + i * blockDim.x >= V) continue;
-                        float f[8];
-                        expert_unpack8<BF16>(q[u][i], f);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) y[i][e] = fmaf(w, f[e], y[i][e]);
-                    }
+                    for (int e = 0; e < 8; ++e) y[i][e] = fmaf(wj, f[e], y[i][e]);
                 }
             }
             if (a.y_out) {

@@ -375,3 +375,29 @@ def test_many_rows(moe, T, D, dtype):
         _check_forward(rc, t, gate, *_forward(moe, rc, t, in_place=gate == "element"))
         dso, dn = n(T, D), n(T, D)
         _check_gradient(rc, t, gate, dso, dn, _gradient(moe, rc, t, gate, dso, dn))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,D,E,k,gate,pre", [(3001, 520, 8, 2, "channel", True), (1999, 2048, 16, 6, "token", True),
+                                              (1400, 4104, 12, 3, "element", True), (2500, 1032, 8, 4, "none", False),
+                                              (1203, 1048, 40, 32, "channel", True)])
+def test_combine_many_rows(moe, dtype, T, D, E, k, gate, pre):
+    rc, t, n = _case(moe, T, D, dtype, gate, p=0.1 if k < 4 else 0.0, pre=pre)
+    cfg, yp, row, w = _rows(moe, T, D, dtype, E, k, n)
+    t["y"] = None
+    row[T // 2, 0], row[T - 1, k - 1] = moe.rows_alloc(cfg), -7  # flagged, and left out
+    ws = moe.alloc_workspace(cfg)
+    y, r, o = (torch.full_like(t["resid"], float("nan")) for _ in range(3))
+    o = o if pre else None
+    moe.moe_combine_residual_norm(cfg, rc, yp, row, w, t["resid"], t["post"], t["gate"], t["pre"], t["rng"], y, r, o, ws)
+    assert moe.moe_get_device_status(ws) == moe.MOE_ERR_BAD_ROUTING
+    row[T // 2, 0] = row[T - 1, k - 1] = -1
+    at = row.long().clamp(min=0)
+    want, size = torch.zeros(T, D, dtype=torch.float64, device="cuda"), torch.zeros(T, D, dtype=torch.float64, device="cuda")
+    for j in range(k):
+        part = torch.where((row[:, j] >= 0)[:, None], w[:, j, None].double() * yp[at[:, j]].double(), 0.0)
+        want += part
+        size += part.abs()
+    y_err = 2 * k * ref.U * size.cpu()
+    _close(y, want, y_err, "y_out")
+    _check_forward(rc, t, gate, r, o, want.cpu(), y_err)
