@@ -24,7 +24,7 @@
 // The 16 weight rows of a tile are the M side of mma.sync m16n8k16 and the
 // entry's rows the N = 8 side: at 8 rows per weight the tensor pipe idles either
 // way, and register accumulators need no TMEM round trip.  The CTA's 8 warps
-// split k: of every 2 KB of a row a warp takes 256 bytes, copied with cp.async
+// split k: of every 2 KB of a row a warp takes 256 bytes (short rows: see below), copied with cp.async
 // into a ring of its own and read back as 16-byte pieces (the sum over k does not
 // care which k meet in one instruction, as long as both operands agree), so the
 // stream needs no barrier but the sum over the warps at a tile's end, and the
@@ -52,11 +52,10 @@ namespace {
 constexpr int FW_WARPS = 8;
 constexpr int FW_THREADS = 32 * FW_WARPS;
 constexpr int FW_STEP = 256;                   // bytes of a row that a warp takes at once
-constexpr int FW_CHUNK = FW_STEP * FW_WARPS;   // and the CTA
 constexpr int FW_M = 16;                       // weight rows per tile
 constexpr int FW_N = 8;                        // rows of an entry
 constexpr int FW_SMEM = 226 * 1024;            // of the 227 KB a CTA may have
-constexpr int FW_JOIN = 4;                     // chunks as long as joining a shared tile's parts takes
+constexpr int FW_JOIN = 8192;                  // bytes of a row as long as joining a shared tile's parts takes
 
 enum { FEW_ROUTE = 1, FEW_GEMM1 = 2, FEW_GEMM2 = 4, FEW_ALL = 7 };
 
@@ -366,6 +365,12 @@ __device__ __forceinline__ int few_entries(const FewParams &p, int slots, const 
     return *s_count;
 }
 
+// Log2 of the warps that share a row of `steps` steps: as many as it has steps for.
+__device__ __forceinline__ int few_sharing(int steps) {
+    return (steps > 1) + (steps > 2) + (steps > 4);
+}
+static_assert(FW_WARPS == 8, "few_sharing counts up to it");
+
 // A line of `n` cut into `parts`: first of part b, and the part that holds x.
 __device__ __forceinline__ int cut_first(int n, int parts, int b) {
     const int q = n / parts, r = n - q * parts;
@@ -383,7 +388,7 @@ few_layer_kernel(const FewParams p) {
     extern __shared__ __align__(128) char smem[];
     __shared__ volatile int s_abort;
     __shared__ int s_count, s_last[2];
-    __shared__ uint64_t s_full[2], s_free[2];  // the buffers of the warps' sums
+    __shared__ uint64_t s_full[FW_WARPS][2], s_free[FW_WARPS][2];  // the groups' buffers of their sums
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = gridDim.x;
     const int slots = p.T * p.k;
     const int slot_bytes = few_slot_bytes(p.T);
@@ -401,9 +406,10 @@ few_layer_kernel(const FewParams p) {
     griddep_wait();
     if (tid == 0) {
         s_abort = 0;
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&s_full[i], FW_WARPS);
-            mbar_init(&s_free[i], 1);
+        const int ks = 1 << few_sharing((p.D * EB + FW_STEP - 1) / FW_STEP);
+        for (int i = 0; i < 2 * FW_WARPS; ++i) {
+            mbar_init(&s_full[i >> 1][i & 1], ks);
+            mbar_init(&s_free[i >> 1][i & 1], 1);
         }
         fence_mbarrier_init();
     }
@@ -440,40 +446,60 @@ few_layer_kernel(const FewParams p) {
     Acc<T> acc;
 
     // Both products run the same loops (the second finds them in the instruction
-    // cache): a SEGMENT is a tile's rows against one entry, nc chunks long.
-    //   GEMM1: tile = 8 hidden units, whole tiles i = blockIdx.x, + G, ... of the
-    //          U nt of them, tiles of an entry running fastest
-    //   GEMM2: tile = 16 rows of out, entries running fastest, this CTA's part of
-    //          the line of chunks
+    // cache): a SEGMENT is a tile's rows against one entry, nc chunks long.  Where a
+    // row is short, fewer than all warps share it and the groups of `ks` warps take
+    // different segments (24 tokens, D = 160, H = 880: 47 us with all 8 on a row).
+    //   GEMM1: tile = 8 hidden units; the U nt tiles over all CTAs' groups, tiles of
+    //          an entry running fastest
+    //   GEMM2: tile = 16 rows of out; this CTA's part of the line of chunks, entries
+    //          running fastest, a tile's entries over the groups
 #pragma unroll 1
     for (int second = 0; second < 2; ++second) {
         if (!(p.phases & (second ? FEW_GEMM2 : FEW_GEMM1)) || dead || U == 0) continue;
-        const int row_bytes = (second ? p.H : p.D) * EB, nc = (row_bytes + FW_CHUNK - 1) / FW_CHUNK;
+        const int row_bytes = (second ? p.H : p.D) * EB;
+        const int steps = (row_bytes + FW_STEP - 1) / FW_STEP;
+        const int lg = few_sharing(steps), ks = 1 << lg;
+        const int groups = FW_WARPS >> lg, group = warp >> lg, chunk = ks * FW_STEP;
+        const int nc = (steps + ks - 1) >> lg;
         const int nt = second ? nt2 : p.H / 8;
-        int total, tile0, u0, c0 = 0;  // chunks of this CTA, and where they begin
-        int G2 = G, per_tile = 0, line = 0;
+        int tile0, u0, c0 = 0;  // where this warp begins
+        int G2 = G, per_tile = 0, line = 0, first = 0, end = 0;
         if (!second) {
-            const int tiles = U * nt, b = blockIdx.x;
-            total = b < tiles ? ((tiles - b + G - 1) / G) * nc : 0;
+            const int b = blockIdx.x * groups + group;
             u0 = b / nt;
             tile0 = b - u0 * nt;
         } else {
             per_tile = U * nc;
             line = per_tile * nt;
             // Cut anywhere, the parts are equal to a chunk, but tiles cut in two
-            // cost a handshake at the end, as long as FW_JOIN chunks take; whole
-            // tiles where that is no longer.
-            const bool whole_tiles = (nt + G - 1) / G * per_tile <= line / G + FW_JOIN;
+            // cost a handshake at the end, as long as FW_JOIN bytes of a row take;
+            // whole tiles where that is no longer.
+            const bool whole_tiles =
+                (long long)((nt + G - 1) / G * per_tile - line / G) * min(chunk, row_bytes) <= FW_JOIN;
             const int unit = whole_tiles ? per_tile : 1, units = line / unit;
             G2 = min(G, units);
-            const bool part_of = (int)blockIdx.x < G2;
-            const int first = part_of ? cut_first(units, G2, blockIdx.x) * unit : 0;
-            total = part_of ? cut_first(units, G2, blockIdx.x + 1) * unit - first : 0;
+            if ((int)blockIdx.x < G2) {
+                first = cut_first(units, G2, blockIdx.x) * unit;
+                end = cut_first(units, G2, blockIdx.x + 1) * unit;
+            }
             tile0 = first / per_tile;
             const int r = first - tile0 * per_tile;
             u0 = r / nc;
             c0 = r - u0 * nc;
             if (whole_tiles) line = 0;  // no tile is shared
+        }
+        const int first_tile = tile0;
+        const bool from_start = u0 == 0 && c0 == 0;
+        if (second) {  // this group's first segment
+            const int skip = (group - u0) & (groups - 1);
+            if (skip) c0 = 0;
+            u0 += skip;
+            if (u0 >= U) {
+                u0 = group;
+                ++tile0;
+                c0 = 0;
+            }
+            if (group >= U) tile0 = nt;  // none
         }
         const char *weights = static_cast<const char *>(second ? p.w2 : p.w1);
         const char *rows = static_cast<const char *>(second ? p.h : p.x);
@@ -482,34 +508,38 @@ few_layer_kernel(const FewParams p) {
                                        : static_cast<const char *>(p.w3) - weights;
         const ptrdiff_t to_4 = (ptrdiff_t)4 * row_bytes;
         const int tile_rows = second ? FW_M : 8, R = second ? p.D : p.H;
-        const int steps = (row_bytes + FW_STEP - 1) / FW_STEP;
         auto next_segment = [&](int &tile, int &u) {
             if (second) {
-                if (++u == U) {
-                    u = 0;
+                u += groups;
+                if (u >= U) {
+                    u = group;
                     ++tile;
                 }
             } else {
-                tile += G;
+                tile += G * groups;
                 while (tile >= nt) {
                     tile -= nt;
                     ++u;
                 }
             }
         };
+        // chunks of the line in front of a segment's chunk c; GEMM1 has no line
+        auto position = [&](int tile, int u, int c) { return (tile * U + u) * nc + c; };
         // The copies' cursor: a segment, its next chunk, and this lane's pieces
         // there of rows r4, r4 + 4 (and 8 on) and of the entry's rows r4, r4 + 4.
         // The warps take turns at a segment's first step: where a row is no whole
         // number of chunks, each gets as many steps as the others.
-        int ltile = tile0, lu = u0, lc = c0, lleft = total, left = 0, turn0 = 0;
+        int ltile = tile0, lu = u0, lc = c0, left = 0, turn0 = 0;
         bool fresh = true, has_hi = false;
+        int lpos = position(ltile, lu, lc);
+        bool ahead = second ? lpos < end : lu < U;
         int has_rows = 0;
         const char *lo = nullptr, *hi = nullptr, *row = nullptr, *row_4 = nullptr;
         auto open = [&]() {
             const uint32_t entry = s_entry[lu];
             const int e = entry >> 16, f = entry & 0xffff, cnt = first_of(lu + 1) - f;
             const int first_row = ltile * tile_rows;
-            const int col = lc * FW_CHUNK + ((warp + turn0) & (FW_WARPS - 1)) * FW_STEP + c16 * 16;
+            const int col = lc * chunk + ((warp + turn0) & (ks - 1)) * FW_STEP + c16 * 16;
             lo = weights + (size_t)(e * R + first_row + r4) * row_bytes + col;
             hi = lo + to_hi;
             has_hi = !second || first_row + 8 < R;  // R is a multiple of 8
@@ -544,19 +574,34 @@ few_layer_kernel(const FewParams p) {
             }
         };
         auto bump = [&](int &slot) { slot = slot + 1 == DEPTH ? 0 : slot + 1; };
-        auto advance = [&]() {
-            lo += FW_CHUNK;
-            hi += FW_CHUNK;
-            row += FW_CHUNK;
-            row_4 += FW_CHUNK;
-            left -= FW_CHUNK;
-            --lleft;
-            if (++lc == nc) {
-                lc = 0;
-                turn0 += steps;
-                next_segment(ltile, lu);
-                fresh = true;
+        auto copy_next = [&]() {
+            if (ahead) {
+                if (fresh) open();
+                copy_weights(in_slot);
+                copy_row(in_slot);
+                bump(in_slot);
+                lo += chunk;
+                hi += chunk;
+                row += chunk;
+                row_4 += chunk;
+                left -= chunk;
+                if (++lc == nc) {
+                    lc = 0;
+                    turn0 += steps;
+                    next_segment(ltile, lu);
+                    if (groups > 1) lpos = position(ltile, lu, 0) - 1;
+                    fresh = true;
+                }
+                ahead = second ? ++lpos < end : lu < U;
             }
+            copy_commit();
+        };
+        auto step = [&](int cnt) {  // the oldest copies, and the next into the slot read a step ago
+            copy_wait<DEPTH - 2>();
+            __syncwarp();
+            acc.step(ring + out_slot * slot_bytes, half_bytes, cnt, lane);
+            bump(out_slot);
+            copy_next();
         };
         // h of every CTA.  (The first steps' weights do not need it, but copying
         // them ahead of the barrier measured the same: its loads then queue behind.)
@@ -566,96 +611,87 @@ few_layer_kernel(const FewParams p) {
             dead = s_abort;
             if (dead) break;
         }
-        auto copy_next = [&]() {
-            if (lleft > 0) {
-                if (fresh) open();
-                copy_weights(in_slot);
-                copy_row(in_slot);
-                bump(in_slot);
-                advance();
-            }
-            copy_commit();
-        };
 #pragma unroll 1
         for (int i = 0; i < DEPTH - 1; ++i) copy_next();
+        T *out = static_cast<T *>(p.out);
+        int tile = tile0, u = u0, c = c0, turn = 0;
+        int cut[2] = {-1, -1};  // tiles that others share: the first, the last
         if (second) {
             for (int i = lane; i < FW_M * p.T; i += 32) s_out[warp * FW_M * p.T + i] = 0.f;
             __syncwarp();
         }
-        T *out = static_cast<T *>(p.out);
-        int tile = tile0, u = u0, c = c0, turn = 0;
-        bool from_start = u0 == 0 && c0 == 0;
-        int cut[2] = {-1, -1};  // tiles that others share: the first, the last
+        // GEMM1: all of the warp's segments.  GEMM2: tile by tile of the CTA's part,
+        // with the CTA's sums at the end of each.
 #pragma unroll 1
-        for (int n = 0; n < total;) {
-            const int f = first_of(u), cnt = first_of(u + 1) - f;
-            acc.clear();
+        for (int at = first_tile; second ? at * per_tile < end : at == first_tile; ++at) {
+            while (second ? tile == at && position(tile, u, c) < end : u < U) {
+                const int f = first_of(u), cnt = first_of(u + 1) - f;
+                const int last = second ? min(nc, c + end - position(tile, u, c)) : nc;
+                acc.clear();
 #pragma unroll 1
-            do {
-                copy_wait<DEPTH - 2>();
-                __syncwarp();
-                acc.step(ring + out_slot * slot_bytes, half_bytes, cnt, lane);
-                bump(out_slot);
-                copy_next();  // into the slot read a step ago
-                ++n;
-            } while (++c < nc && n < total);
-            float v[4];
-            acc.get(v, cnt, lane);
-            if (!second) {
-                // The warps' sums meet in one of two buffers; one warp, another for
-                // every tile, adds them up while the rest go on with the next tile.
-                const int buf = turn & 1;
-                const uint32_t round = (uint32_t)(turn >> 1) & 1u;
-                float4 *red = s_red + buf * FW_WARPS * 32;
-                mbar_wait_bounded(&s_free[buf], round ^ 1u, &s_abort);
-                red[warp * 32 + lane] = make_float4(v[0], v[1], v[2], v[3]);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s_full[buf]);
-                if (turn % FW_WARPS == warp) {
-                    mbar_wait_bounded(&s_full[buf], round, &s_abort);
-                    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (; c < last; ++c) step(cnt);
+                float v[4];
+                acc.get(v, cnt, lane);
+                if (!second) {
+                    // The warps' sums meet in one of two buffers; one warp, another for
+                    // every tile, adds them up while the rest go on with the next tile.
+                    float4 sum = make_float4(v[0], v[1], v[2], v[3]);
+                    bool mine = true;
+                    if (ks > 1) {
+                        const int buf = turn & 1;
+                        const uint32_t round = (uint32_t)(turn >> 1) & 1u;
+                        float4 *red = s_red + (buf * FW_WARPS + group * ks) * 32 + lane;
+                        mbar_wait_bounded(&s_free[group][buf], round ^ 1u, &s_abort);
+                        red[(warp & (ks - 1)) * 32] = sum;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&s_full[group][buf]);
+                        mine = (turn & (ks - 1)) == (warp & (ks - 1));
+                        if (mine) {
+                            mbar_wait_bounded(&s_full[group][buf], round, &s_abort);
+                            sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                    for (int w = 0; w < FW_WARPS; ++w) {
-                        const float4 r = red[w * 32 + lane];
-                        sum.x += r.x;
-                        sum.y += r.y;
-                        sum.z += r.z;
-                        sum.w += r.w;
+                            for (int w = 0; w < FW_WARPS; ++w) {
+                                if (w >= ks) break;
+                                const float4 r = red[w * 32];
+                                sum.x += r.x;
+                                sum.y += r.y;
+                                sum.z += r.z;
+                                sum.w += r.w;
+                            }
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&s_free[group][buf]);
+                        }
+                        ++turn;
+                    }
+                    if (mine) {
+                        // gate (x, y) and up (z, w) of unit g for the entry's rows 2 q, 2 q + 1
+                        const int m = 2 * (lane & 3);
+                        T *h = static_cast<T *>(p.h) + (size_t)(f + m) * p.H + tile * 8 + g;
+                        if (m < cnt) h[0] = Elem<T>::round(sum.x / (1.f + expf(-sum.x)) * sum.z);
+                        if (m + 1 < cnt) h[p.H] = Elem<T>::round(sum.y / (1.f + expf(-sum.y)) * sum.w);
+                    }
+                } else {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int m = 2 * (lane & 3) + half;
+                        if (m >= cnt) continue;
+                        float *o = s_out + (warp * p.T + s_token[f + m]) * FW_M;
+                        const float w = s_w[s_sorted[f + m]];
+                        o[g] = fmaf(w, v[half], o[g]);
+                        o[g + 8] = fmaf(w, v[2 + half], o[g + 8]);
                     }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&s_free[buf]);
-                    // gate (x, y) and up (z, w) of unit g for the entry's rows 2 q, 2 q + 1
-                    const int m = 2 * (lane & 3);
-                    T *h = static_cast<T *>(p.h) + (size_t)(f + m) * p.H + tile * 8 + g;
-                    if (m < cnt) h[0] = Elem<T>::round(sum.x / (1.f + expf(-sum.x)) * sum.z);
-                    if (m + 1 < cnt) h[p.H] = Elem<T>::round(sum.y / (1.f + expf(-sum.y)) * sum.w);
+                    if (c < nc) break;  // the part ends here
                 }
-                ++turn;
                 c = 0;
                 next_segment(tile, u);
-                continue;
             }
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int m = 2 * (lane & 3) + half;
-                if (m >= cnt) continue;
-                float *o = s_out + (warp * p.T + s_token[f + m]) * FW_M;
-                const float w = s_w[s_sorted[f + m]];
-                o[g] = fmaf(w, v[half], o[g]);
-                o[g + 8] = fmaf(w, v[2 + half], o[g + 8]);
-            }
-            __syncwarp();
-            bool to_end = false;
-            if (c == nc) {
-                c = 0;
-                to_end = ++u == U;
-            }
-            if (!to_end && n < total) continue;
+            if (!second) continue;
             // the warps' sums; a tile that others share goes through memory
-            const bool whole = from_start && to_end;
-            const int side = tile == tile0 ? 0 : 1;
+            const bool whole = (at > first_tile || from_start) && (at + 1) * per_tile <= end;
+            const int side = at == first_tile ? 0 : 1;
             float *part = p.part + ((size_t)blockIdx.x * 2 + side) * p.T * FW_M;
-            if (!whole) cut[side] = tile;
+            if (!whole) cut[side] = at;
             __syncthreads();
             for (int o = tid; o < FW_M * p.T; o += FW_THREADS) {
                 float sum = 0.f;
@@ -664,16 +700,13 @@ few_layer_kernel(const FewParams p) {
                     sum += s_out[w * FW_M * p.T + o];
                     s_out[w * FW_M * p.T + o] = 0.f;
                 }
-                const int d = tile * FW_M + o % FW_M;
+                const int d = at * FW_M + o % FW_M;
                 if (!whole)
                     part[o] = sum;
                 else if (d < p.D)
                     out[(size_t)(o / FW_M) * p.D + d] = Elem<T>::round(sum);
             }
             __syncthreads();
-            from_start = true;
-            u = 0;
-            ++tile;
         }
         copy_wait<0>();
         __syncthreads();

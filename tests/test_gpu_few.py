@@ -318,3 +318,14 @@ def test_a_decode_step_between_its_norms(moe):
     s = resid.double() + 0.5 * rms(y, post)
     assert ((r.double() - s).abs() <= 2 ** -8 * s.abs() + 2 ** -18 * (resid.double().abs() + 1)).all()
     assert ((n.double() - rms(s, after)).abs() <= 2 ** -8 * rms(s, after).abs() + 2 ** -16).all()
+
+
+# rows of 1, 2, 3, 4, 5, 8 and 9 steps of 256 bytes: fewer than all warps share the short ones
+@pytest.mark.parametrize("dtype", [1, 0], ids=["bf16", "f32"])
+@pytest.mark.parametrize("D,H", [(128, 1152), (136, 1032), (264, 1024), (392, 640), (520, 512), (640, 264), (1024, 136), (1160, 120)])
+def test_rows_of_every_length(moe, D, H, dtype):
+    f = 1 if dtype else 2  # the same bytes in fp32
+    for T, E, k in ((1, 9, 7), (13, 6, 3), (30, 3, 2)):
+        c = moe.Config(T=T, D=D // f // 8 * 8, H_local=H // f // 8 * 8, E=E, k=k, dtype=dtype, renorm=1)
+        t = _inputs(moe, c)
+        _check(moe, c, t, _call(moe, c, t)[0])
