@@ -639,12 +639,13 @@ moe_status moe_permute_noalloc(const moe_config *cfg, const void *x, const int32
  * fp16 y_perm lies between, so its range does not bound y), h once to dtype; a
  * NaN key is flagged as by moe_route_topk.  Differs from moe_layer_forward by
  * rounding only, but a near tie of two keys may fall the other way.  Results
- * are bit-identical run to run on one device.
+ * are bit-identical run to run on one device.  out may be x.
  *
- * ws: moe_layer_few_workspace_size(cfg) (-1: bad config or T above 32),
- * zero-filled once.  Its layout depends on cfg, so one workspace serves calls
- * of one config; calls that share it must not run concurrently (two captured
- * graphs included).  Capture into a graph once a first call has run outside.
+ * ws: moe_layer_few_workspace_size(cfg) bytes (-1: bad config, T above 32, or
+ * sizes whose tiles pass int32), zero-filled once and used by this call alone: it
+ * then serves every config with the same D that it is large enough for.  Calls
+ * that share it must not run concurrently (two captured graphs included).
+ * Capture into a graph once a first call has run outside.
  */
 int64_t moe_layer_few_workspace_size(const moe_config *cfg);
 moe_status moe_layer_forward_few(const moe_config *cfg, const void *x, const void *wg,

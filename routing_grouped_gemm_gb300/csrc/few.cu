@@ -33,6 +33,14 @@
 // of 1 KB per stage reached 39% of the copy rate, of 4 KB 97% in long rows.)
 // fp32 layers use the same tiles with fused multiply-adds.
 //
+// Measured (GB300, bf16): 16 tokens over 256 experts of 7168 x 2048, 9.0 GB of
+// weights, 1.22-1.28 ms (7.0-7.4 TB/s, the copy rate is 6.8); 8 tokens of the
+// fine-grained layer, 0.60 GB, 103-108 us (5.6-5.9 TB/s); one token of it, 104 MB,
+// 31.7 us, of which the stream's floor is 15.3.  The rest is latency: keys 2 us,
+// barrier 1.3, top-k 2.4, entries 1.2, 4-6 until the first weights are there
+// (address translation and DRAM), the second barrier 2, and all of it run once, so
+// that its instructions come from L2.
+//
 // Rounding: keys, weights, both products' sums and the sum over experts are
 // fp32; h is rounded to the layer's type once (as in moe_grouped_swiglu), out
 // once.  Every sum has a fixed order for a given grid, so results do not change
@@ -448,7 +456,7 @@ few_layer_kernel(const FewParams p) {
     // Both products run the same loops (the second finds them in the instruction
     // cache): a SEGMENT is a tile's rows against one entry, nc chunks long.  Where a
     // row is short, fewer than all warps share it and the groups of `ks` warps take
-    // different segments (24 tokens, D = 160, H = 880: 47 us with all 8 on a row).
+    // different segments (24 tokens, D = 160, H = 880: 39 us, with all 8 on a row 47).
     //   GEMM1: tile = 8 hidden units; the U nt tiles over all CTAs' groups, tiles of
     //          an entry running fastest
     //   GEMM2: tile = 16 rows of out; this CTA's part of the line of chunks, entries

@@ -12,8 +12,14 @@
 //
 // Every element is touched a fixed few times, so the passes are bound by HBM:
 // forward 4 T D elements (r, y in; s, n out), gradient 6 (s, y, ds, dn in; dr,
-// dy out).  One CTA owns a row at a time and keeps it in registers between the
-// row sums, so nothing is read twice.
+// dy out), and close behind by instructions: at 2 bytes an element the copy rate
+// leaves about 20 per element and warp lane.  A row's values stay on the SM
+// between its sums, and the next row is on its way meanwhile.  Measured on GB300
+// (bf16, of the copy rate): 16384 x 4096 forward 86.5 us (92%), its gradient 132
+// (90%), gradient of 8192 x 7168 113.6 (92%); dropout's generator adds 13 us to
+// 44 at 16384 x 2048.  Behind the combine (16384 x 2048, 6 rows a token) 118 us
+// (84%): a row's loads wait for its places, and more of them in flight per thread
+// or in a shared ring measured slower (8192 x 4096, 4 rows: 101 us, a ring 134).
 #include <algorithm>
 
 #include "common.cuh"

@@ -216,6 +216,70 @@ def test_workspace_reused_for_fewer_tokens_and_left_dirty(moe):
         ws[head:] = 255
 
 
+def test_workspace_shared_by_configs_of_the_same_width(moe):
+    cfgs = [moe.Config(T=T, D=264, H_local=H, E=E, k=k, renorm=1, dtype=dt)
+            for T, H, E, k, dt in ((32, 264, 64, 8, 0), (5, 72, 3, 3, 1), (16, 520, 100, 2, 1), (1, 8, 8, 8, 0))]
+    n = max(moe.layer_few_workspace_size(c) for c in cfgs)
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    for c in cfgs + cfgs[::-1]:
+        t = _inputs(moe, c)
+        assert torch.equal(_call(moe, c, t, ws)[0], _call(moe, c, t)[0])
+
+
+def test_in_place(moe):
+    """out may be x: every CTA has read x before any writes."""
+    c = moe.Config(T=7, D=520, H_local=136, E=8, k=2, renorm=1)
+    t = _inputs(moe, c)
+    want, ws = _call(moe, c, t)[0], moe.alloc_workspace(c, few=True)
+    moe.moe_layer_forward_few(c, t["x"], t["wg"], t["bias"], t["w1"], t["w3"], t["w2"], t["x"], ws)
+    assert torch.equal(t["x"], want)
+
+
+def test_two_streams_with_a_workspace_each(moe):
+    """Two calls at once: each grid needs the whole device, so they take turns."""
+    c = moe.Config(T=8, D=1032, H_local=520, E=16, k=4, renorm=1)
+    t = [_inputs(moe, c, seed=i) for i in range(2)]
+    want = [_call(moe, c, v)[0] for v in t]
+    ws, out = [moe.alloc_workspace(c, few=True) for _ in t], [torch.empty_like(w) for w in want]
+    streams = [torch.cuda.Stream() for _ in t]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for v, w, o, s in zip(t, ws, out, streams):
+            moe.moe_layer_forward_few(c, v["x"], v["wg"], v["bias"], v["w1"], v["w3"], v["w2"], o, w, stream=s)
+    torch.cuda.synchronize()
+    for w, o, e in zip(ws, out, want):
+        assert moe.moe_get_device_status(w) == moe.MOE_OK and torch.equal(o, e)
+
+
+def test_another_device_or_the_host(moe, monkeypatch):
+    """A workspace that is not on the current device is refused before any launch (the current device is made
+    to look like another one)."""
+    c = moe.Config(T=4, D=64, H_local=64, E=8, k=2)
+    t = _inputs(moe, c)
+    rc = moe.ResidualConfig(T=4, D=64)
+    ws, rws = moe.alloc_workspace(c, few=True), moe.alloc_residual_workspace(rc)
+    x, g = t["x"], t["x"][0].contiguous()
+    y = torch.zeros(moe.rows_alloc(c), 64, dtype=torch.float16, device="cuda")
+    row, w, f = (torch.zeros(4, 2, dtype=d, device="cuda") for d in (torch.int32, torch.float32, torch.float32))
+    sw, f = moe.alloc_workspace(c), torch.empty(64, device="cuda")
+
+    def calls(ws, rws, sw, x):
+        return (lambda: moe.moe_layer_forward_few(c, t["x"], t["wg"], t["bias"], t["w1"], t["w3"], t["w2"], t["x"], ws),
+                lambda: moe.moe_residual_norm(rc, x, None, None, None, g, None, None, x),
+                lambda: moe.moe_combine_residual_norm(c, rc, y, row, w, t["x"], None, None, g, None, None, t["x"], t["x"], sw),
+                lambda: moe.moe_residual_norm_backward(rc, t["x"], None, None, None, g, None, None, t["x"], t["x"], None,
+                                                       None, None, f, rws))
+    before, real = moe.kernel_launches(), torch.cuda.current_device()
+    for call in calls(ws.cpu(), rws.cpu(), sw.cpu(), x.cpu()):
+        with pytest.raises(ValueError, match="on cpu|CUDA tensor"):
+            call()
+    monkeypatch.setattr(moe, "_device", lambda: real + 1)
+    for call in calls(ws, rws, sw, x):
+        with pytest.raises(ValueError, match="current device"):
+            call()
+    assert moe.kernel_launches() == before
+
+
 def test_bitwise_reproducible(moe):
     c = moe.Config(T=12, D=2056, H_local=512, E=32, k=4, renorm=1)
     t, ws = _inputs(moe, c), None
