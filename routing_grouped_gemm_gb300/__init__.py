@@ -211,11 +211,15 @@ class ResidualConfig:
         return {k: v for k, v in self.__dict__.items() if k not in ("_set", "_ref")}
 
     def ref(self):
-        """Pointer to the C struct, built once for these values."""
+        """(pointer to the C struct, shape of the rows, of a gain, their type, the gate's shape and
+        type or None), built once for these values."""
         d = self.__dict__
         since, kept = d.get("_set"), d.get("_ref")
         if kept is None or kept[0] is not since:
-            kept = d["_ref"] = (since, ctypes.pointer(self.c()))
+            rows, gain, dt = (self.T, self.D), (self.D,), self.torch_dtype
+            gate = {MOE_GATE_CHANNEL: (gain, dt), MOE_GATE_TOKEN: ((self.T,), torch.float32),
+                    MOE_GATE_ELEMENT: (rows, dt)}.get(self.gate)
+            kept = d["_ref"] = (since, (ctypes.pointer(self.c()), rows, gain, dt, gate))
         return kept[1]
 
     def c(self) -> moe_residual_config:
@@ -294,7 +298,7 @@ def alloc_workspace(cfg: Config, layer: bool = False, device="cuda", host: bool 
 
 
 def residual_workspace_size(rc: ResidualConfig) -> int:
-    return int(_lib.moe_residual_workspace_size(rc.ref()))
+    return int(_lib.moe_residual_workspace_size(rc.ref()[0]))
 
 
 def alloc_residual_workspace(rc: ResidualConfig, device="cuda") -> torch.Tensor:
@@ -945,14 +949,7 @@ def moe_layer_forward_few(cfg: Config, x, wg, bias, w1, w3, w2, out, ws, stream=
 # the norms around a block
 # --------------------------------------------------------------------------
 
-def _gate_form(rc):
-    """Shape and type of the gate, or None."""
-    return {MOE_GATE_CHANNEL: ((rc.D,), rc.torch_dtype), MOE_GATE_TOKEN: ((rc.T,), torch.float32),
-            MOE_GATE_ELEMENT: ((rc.T, rc.D), rc.torch_dtype)}.get(rc.gate)
-
-
-def _gate_arg(rc, gate) -> int:
-    form = _gate_form(rc)
+def _gate_arg(form, gate) -> int:
     if form is None:
         if gate is not None:
             raise ValueError("gate: the config names no kind of gate")
@@ -967,13 +964,12 @@ def moe_residual_norm(rc: ResidualConfig, resid, y, post_gain, gate, pre_gain, r
 
     post_gain, gate, pre_gain (with norm_out) and rng may be None; without y (and resid_out) it is
     the norm of resid alone."""
-    td, dt = (rc.T, rc.D), rc.torch_dtype
+    c, td, d, dt, form = rc.ref()
     _check(_lib.moe_residual_norm(
-        rc.ref(), _arg(resid, td, dt, "resid"), _maybe(y, td, dt, "y"),
-        _maybe(post_gain, (rc.D,), dt, "post_gain"), _gate_arg(rc, gate),
-        _maybe(pre_gain, (rc.D,), dt, "pre_gain"), _maybe(rng, (2,), torch.int64, "rng"),
-        _maybe(resid_out, td, dt, "resid_out"), _maybe(norm_out, td, dt, "norm_out"),
-        _at(resid, "resid", stream)), "moe_residual_norm")
+        c, _arg(resid, td, dt, "resid"), _maybe(y, td, dt, "y"), _maybe(post_gain, d, dt, "post_gain"),
+        _gate_arg(form, gate), _maybe(pre_gain, d, dt, "pre_gain"),
+        _maybe(rng, (2,), torch.int64, "rng"), _maybe(resid_out, td, dt, "resid_out"),
+        _maybe(norm_out, td, dt, "norm_out"), _at(resid, "resid", stream)), "moe_residual_norm")
 
 
 def moe_combine_residual_norm(cfg: Config, rc: ResidualConfig, y_perm, row_of, topk_w, resid,
@@ -981,35 +977,32 @@ def moe_combine_residual_norm(cfg: Config, rc: ResidualConfig, y_perm, row_of, t
                               stream=None):
     """moe_unpermute_combine and moe_residual_norm in one pass; y_out (or None) takes the combined
     rows, which the gradient needs."""
-    c, ra = cfg.ref()
-    td, tk, dt = (rc.T, rc.D), (cfg.T, cfg.k), rc.torch_dtype
+    (cc, ra), (c, td, d, dt, form) = cfg.ref(), rc.ref()
+    tk = (cfg.T, cfg.k)
     p, n, s = _ws(ws, stream)
     _check(_lib.moe_combine_residual_norm(
-        c, rc.ref(), _arg(y_perm, (ra, cfg.D), cfg.y_dtype, "y_perm"),
+        cc, c, _arg(y_perm, (ra, cfg.D), cfg.y_dtype, "y_perm"),
         _arg(row_of, tk, torch.int32, "row_of"), _arg(topk_w, tk, torch.float32, "topk_w"),
-        _arg(resid, td, dt, "resid"), _maybe(post_gain, (rc.D,), dt, "post_gain"),
-        _gate_arg(rc, gate), _maybe(pre_gain, (rc.D,), dt, "pre_gain"),
-        _maybe(rng, (2,), torch.int64, "rng"), _maybe(y_out, td, dt, "y_out"),
-        _arg(resid_out, td, dt, "resid_out"), _maybe(norm_out, td, dt, "norm_out"), p, n, s),
-        "moe_combine_residual_norm")
+        _arg(resid, td, dt, "resid"), _maybe(post_gain, d, dt, "post_gain"), _gate_arg(form, gate),
+        _maybe(pre_gain, d, dt, "pre_gain"), _maybe(rng, (2,), torch.int64, "rng"),
+        _maybe(y_out, td, dt, "y_out"), _arg(resid_out, td, dt, "resid_out"),
+        _maybe(norm_out, td, dt, "norm_out"), p, n, s), "moe_combine_residual_norm")
 
 
 def moe_residual_norm_backward(rc: ResidualConfig, s, y, post_gain, gate, pre_gain, rng, dresid_out,
                                dnorm_out, dresid, dy, dpost_gain, dgate, dpre_gain, ws, stream=None):
     """Gradient of moe_residual_norm: dresid and dy from dresid_out and dnorm_out, the gains' and a
     shared gate's in fp32.  s is the forward's resid_out (its resid where it had no y)."""
-    td, dt, f32 = (rc.T, rc.D), rc.torch_dtype, torch.float32
-    form = _gate_form(rc)
+    c, td, d, dt, form = rc.ref()
+    f32 = torch.float32
     if form is None and dgate is not None:
         raise ValueError("dgate: the config names no kind of gate")
     p, n, st = _ws(ws, stream)
     _check(_lib.moe_residual_norm_backward(
-        rc.ref(), _arg(s, td, dt, "s"), _maybe(y, td, dt, "y"),
-        _maybe(post_gain, (rc.D,), dt, "post_gain"), _gate_arg(rc, gate),
-        _maybe(pre_gain, (rc.D,), dt, "pre_gain"), _maybe(rng, (2,), torch.int64, "rng"),
-        _maybe(dresid_out, td, dt, "dresid_out"), _maybe(dnorm_out, td, dt, "dnorm_out"),
-        _arg(dresid, td, dt, "dresid"), _maybe(dy, td, dt, "dy"),
-        _maybe(dpost_gain, (rc.D,), f32, "dpost_gain"),
-        0 if form is None else _arg(dgate, form[0], form[1] if rc.gate == MOE_GATE_ELEMENT else f32,
-                                    "dgate"),
-        _maybe(dpre_gain, (rc.D,), f32, "dpre_gain"), p, n, st), "moe_residual_norm_backward")
+        c, _arg(s, td, dt, "s"), _maybe(y, td, dt, "y"), _maybe(post_gain, d, dt, "post_gain"),
+        _gate_arg(form, gate), _maybe(pre_gain, d, dt, "pre_gain"),
+        _maybe(rng, (2,), torch.int64, "rng"), _maybe(dresid_out, td, dt, "dresid_out"),
+        _maybe(dnorm_out, td, dt, "dnorm_out"), _arg(dresid, td, dt, "dresid"),
+        _maybe(dy, td, dt, "dy"), _maybe(dpost_gain, d, f32, "dpost_gain"),
+        0 if form is None else _arg(dgate, form[0], dt if rc.gate == MOE_GATE_ELEMENT else f32, "dgate"),
+        _maybe(dpre_gain, d, f32, "dpre_gain"), p, n, st), "moe_residual_norm_backward")

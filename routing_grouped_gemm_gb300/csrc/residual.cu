@@ -243,12 +243,14 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float *slot) {
 // over the CTA's threads for each (and each half of an fp32 vector).
 template <bool BF16, int NV> struct Ring {
     static constexpr int EB = BF16 ? 16 : 32;  // bytes of a vector
+    // fp32: a copy writes to two planes at once, which so begin in different banks
+    static constexpr int PAD = BF16 ? 0 : 64;
     char *own;
     uint32_t plane, stage_bytes;
     int V, mine, across, depth;
 
     __device__ __forceinline__ Ring(char *smem, int V_, int mine_, int across_, int depth_, int arrays)
-        : own(smem + threadIdx.x * 16), plane(blockDim.x * 16),
+        : own(smem + threadIdx.x * 16), plane(blockDim.x * 16 + PAD),
           stage_bytes(arrays * NV * (EB / 16) * plane), V(V_), mine(mine_), across(across_), depth(depth_) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)  // columns past the row's end read zeros
@@ -916,6 +918,11 @@ residual_finish_kernel(const FinishArgs a) {
     }
 }
 
+// Bytes of one row's slot of a Ring.
+size_t ring_bytes(int arrays, int nv, int is_bf16, int threads) {
+    return (size_t)arrays * nv * (is_bf16 ? threads * 16 : 2 * (threads * 16 + 64));
+}
+
 // Threads and vectors per thread for rows of V vectors.
 void row_shape(int V, int *threads, int *nv) {
     *nv = V <= 1024 ? 1 : V <= 2048 ? 2 : 4;
@@ -949,7 +956,7 @@ cudaError_t forward_rows(const ResidualNorm &r, const ForwardArgs &a, cudaStream
 }
 
 cudaError_t forward(const ResidualNorm &r, ForwardArgs &a, cudaStream_t stream) {
-    const int V = r.D / 8, vec = r.is_bf16 ? 16 : 32;
+    const int V = r.D / 8;
     const bool warp = V <= 128;
     // What a row costs besides its vectors (two reductions, its copies' addresses)
     // is paid by every warp, so few warps take several vectors each (16384 x 4096:
@@ -958,7 +965,7 @@ cudaError_t forward(const ResidualNorm &r, ForwardArgs &a, cudaStream_t stream) 
     const int nv = warp ? (V <= 32 ? 1 : V <= 64 ? 2 : 4) : V <= 512 ? 2 : 4;
     const int threads = warp ? 256 : ((V + nv - 1) / nv + 31) / 32 * 32;
     a.in_ring = r.gate_kind == GATE_ELEMENT ? 3 : 2;
-    const size_t stage = (size_t)a.in_ring * nv * vec * threads;
+    const size_t stage = ring_bytes(a.in_ring, nv, r.is_bf16, threads);
     int per_sm = warp ? (nv == 4 ? 1 : 2) : std::min(8, 512 / threads);
     while (per_sm > 1 && 2 * stage * per_sm > 220 * 1024) --per_sm;
     a.depth = 2 * stage * per_sm > 220 * 1024 ? 1 : 2;
@@ -1049,7 +1056,7 @@ GradientShape gradient_shape(int T, int D, int is_bf16, int gate_kind) {
     g.nv = (g.warp ? V <= 32 : V <= 256) ? 1 : 2;
     g.threads = g.warp ? 256 : ((V + g.nv - 1) / g.nv + 31) / 32 * 32;
     g.in_ring = gate_kind == GATE_ELEMENT ? 5 : 4;
-    const size_t stage = (size_t)g.in_ring * g.nv * (is_bf16 ? 1 : 2) * g.threads * 16;
+    const size_t stage = ring_bytes(g.in_ring, g.nv, is_bf16, g.threads);
     // CTAs per SM by their registers, fewer where two rows each are too much
     int per_sm = g.warp ? 3 - g.nv : std::max(1, std::min(4, 512 / g.threads));
     auto fit = [&] { return (int)std::min<size_t>(g.nv == 1 ? 3 : 2, (size_t)(220 * 1024 / per_sm) / stage); };

@@ -125,3 +125,12 @@ def test_few_refusals(moe):
     assert moe.kernel_launches() == before
     with pytest.raises(ValueError, match="ws is required"):
         moe.moe_layer_forward_few(cfg, *[None] * 7, None)
+
+
+def test_a_changed_config_is_taken(moe):
+    rc = moe.ResidualConfig(T=4, D=64)
+    assert rc.ref()[0].contents.eps == pytest.approx(1e-6) and rc.ref()[4] is None and rc.ref() is rc.ref()
+    rc.eps, rc.gate, rc.T = 0.5, moe.MOE_GATE_TOKEN, 7
+    c, rows, gain, dt, gate = rc.ref()
+    assert (c.contents.eps, c.contents.gate, c.contents.T, rows) == (0.5, moe.MOE_GATE_TOKEN, 7, (7, 64))
+    assert gate == ((7,), torch.float32) and gain == (64,) and dt is torch.bfloat16
