@@ -711,7 +711,8 @@ moe_status moe_residual_norm(const moe_residual_config *rc, const void *resid, c
 /*
  * moe_unpermute_combine and moe_residual_norm in one pass: y is the weighted
  * sum of a token's rows of y_perm (arguments and flags as moe_unpermute_combine,
- * summed in fp32 in slot order), not rounded on the way to v.  y_out [T, D]
+ * summed in fp32 in slot order), not rounded on the way to v; resid_out may be
+ * resid.  y_out [T, D]
  * (dtype): y rounded once, for the gradient; or NULL.  cfg and rc have the same
  * T, D and dtype.  ws: moe_workspace_size(cfg).
  */

@@ -5,8 +5,8 @@
 //   v = y rsqrt(mean(y^2) + eps) post        with one;
 //   s = res_scale r + branch_scale gate keep v          (the new residual)
 //   n = s rsqrt(mean(s^2) + eps) pre                    (the next block's input)
-// keep is 0 or 1 / (1 - p) from a counter-based generator (keep_word below),
-// so no mask is stored: forward and gradient derive it from (seed, offset).
+// keep is 0 or 1 / (1 - p) from a counter-based generator (philox below), so
+// no mask is stored: forward and gradient derive it from (seed, offset).
 // All arithmetic is fp32; s and n are rounded once each, and n is the norm of
 // the unrounded s.
 //

@@ -196,7 +196,10 @@ def test_combine(moe, dtype, T, D, E, k, gate):
     y_err = 2 * k * ref.U * part.abs().sum(1)  # k products and k sums
     _close(outs[0], y, y_err, "y_out")
     _check_forward(rc, t, gate, outs[1], outs[2], y, y_err)
-    # y_out left out, and the unfused combine's rows
+    # in place; y_out left out, and the unfused combine's rows
+    r3, n3 = t["resid"].clone(), torch.empty_like(outs[0])
+    moe.moe_combine_residual_norm(cfg, rc, yp, row, w, r3, t["post"], t["gate"], t["pre"], t["rng"], None, r3, n3, ws)
+    assert torch.equal(r3, outs[1]) and torch.equal(n3, outs[2])
     y2, r2, n2 = (torch.empty_like(outs[0]) for _ in range(3))
     moe.moe_combine_residual_norm(cfg, rc, yp, row, w, t["resid"], t["post"], t["gate"], t["pre"], t["rng"], None, r2, n2, ws)
     assert torch.equal(r2, outs[1]) and torch.equal(n2, outs[2])
