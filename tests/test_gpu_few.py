@@ -135,6 +135,8 @@ CASES = [
     dict(T=31, D=136, H_local=264, E=2, k=2, renorm=1),
     dict(T=32, D=264, H_local=40, E=1024, k=32, renorm=1),
     dict(T=32, D=8, H_local=2048, E=4, k=1),
+    dict(T=32, D=520, H_local=264, E=32, k=32),
+    dict(T=3, D=4608, H_local=4104, E=3, k=1, score=1),
     dict(T=32, D=1048, H_local=424, E=20, k=3, e_first=3, E_local=13, score=1, renorm=1),
 ]
 
