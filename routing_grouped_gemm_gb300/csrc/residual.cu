@@ -239,30 +239,33 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float *slot) {
 // Thread `mine` of the `across` that share a row copies vectors mine + i across
 // (i < NV) of up to 5 arrays with cp.async and alone reads them back (fp32: a warp
 // copies for its lanes), so that the next rows are in flight while one is worked
-// on and nothing has to be waited for but one's own copies.  [depth][array][NV] vectors, a plane of 16-byte pieces
-// over the CTA's threads for each (and each half of an fp32 vector).
+// on and nothing has to be waited for but one's own copies.  [depth][array][NV]
+// planes, in each a vector of 16 or 32 bytes for every thread of the CTA.  Of an
+// fp32 vector's two 16-byte pieces every other four threads have the second one
+// first, so that eight threads' reads lie in different banks; both stay within
+// the vector's 32 bytes, or a copy would fetch its sector twice.
 template <bool BF16, int NV> struct Ring {
     static constexpr int EB = BF16 ? 16 : 32;  // bytes of a vector
-    // fp32: a copy writes to two planes at once, which so begin in different banks
-    static constexpr int PAD = BF16 ? 0 : 64;
     char *own;
     uint32_t plane, stage_bytes;
     int V, mine, across, depth;
 
     __device__ __forceinline__ Ring(char *smem, int V_, int mine_, int across_, int depth_, int arrays)
-        : own(smem + threadIdx.x * 16), plane(blockDim.x * 16 + PAD),
-          stage_bytes(arrays * NV * (EB / 16) * plane), V(V_), mine(mine_), across(across_), depth(depth_) {
+        : own(smem + threadIdx.x * EB), plane(blockDim.x * EB), stage_bytes(arrays * NV * plane), V(V_),
+          mine(mine_), across(across_), depth(depth_) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)  // columns past the row's end read zeros
             if (mine + i * across >= V)
                 for (int k = 0; k < depth * arrays; ++k)
 #pragma unroll
                     for (int h = 0; h < EB / 16; ++h)
-                        *reinterpret_cast<uint4 *>(own + ((k * NV + i) * (EB / 16) + h) * plane) =
+                        *reinterpret_cast<uint4 *>(own + (k * NV + i) * plane + 16 * h) =
                             make_uint4(0, 0, 0, 0);
     }
+    // where thread `t` has piece h of its fp32 vector, within the vector
+    __device__ __forceinline__ static int swapped(int t, int h) { return (h ^ (t >> 2 & 1)) * 16; }
     __device__ __forceinline__ void copy(const void *array, int k, size_t base, int stage) {
-        const uint32_t at = smem_u32(own) + stage * stage_bytes + k * NV * (EB / 16) * plane;
+        const uint32_t at = smem_u32(own) + stage * stage_bytes + k * NV * plane;
         const char *src = static_cast<const char *>(array) + base * EB;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -276,9 +279,9 @@ template <bool BF16, int NV> struct Ring {
                 const int lane = threadIdx.x & 31;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int q = 32 * h + lane, v = mine - lane + i * across + (q >> 1);
+                    const int q = 32 * h + lane, to = q >> 1, v = mine - lane + i * across + to;
                     if (v < V)
-                        copy_piece(at + (2 * i + (q & 1)) * plane + ((q >> 1) - lane) * 16,
+                        copy_piece(at + i * plane + (to - lane) * 32 + swapped(to, q & 1),
                                    src + (size_t)v * 32 + 16 * (q & 1));
                 }
             }
@@ -303,10 +306,14 @@ template <bool BF16, int NV> struct Ring {
     }
     __device__ __forceinline__ void drain() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
     __device__ __forceinline__ Pack<BF16> take(int k, int i, int stage) const {
-        const char *p = own + stage * stage_bytes + (k * NV + i) * (EB / 16) * plane;
+        const char *p = own + stage * stage_bytes + (k * NV + i) * plane;
         Pack<BF16> r;
-        r.a = *reinterpret_cast<const uint4 *>(p);
-        if constexpr (!BF16) r.b = *reinterpret_cast<const uint4 *>(p + plane);
+        if constexpr (BF16) {
+            r.a = *reinterpret_cast<const uint4 *>(p);
+        } else {
+            r.a = *reinterpret_cast<const uint4 *>(p + swapped(threadIdx.x, 0));
+            r.b = *reinterpret_cast<const uint4 *>(p + swapped(threadIdx.x, 1));
+        }
         return r;
     }
 };
@@ -920,7 +927,7 @@ residual_finish_kernel(const FinishArgs a) {
 
 // Bytes of one row's slot of a Ring.
 size_t ring_bytes(int arrays, int nv, int is_bf16, int threads) {
-    return (size_t)arrays * nv * (is_bf16 ? threads * 16 : 2 * (threads * 16 + 64));
+    return (size_t)arrays * nv * threads * (is_bf16 ? 16 : 32);
 }
 
 // Threads and vectors per thread for rows of V vectors.
