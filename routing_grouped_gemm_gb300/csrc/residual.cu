@@ -17,7 +17,7 @@
 // between its sums, and the next row is on its way meanwhile.  Measured on GB300
 // (bf16, of the copy rate): 16384 x 4096 forward 86.5 us (92%), its gradient 132
 // (90%), gradient of 8192 x 7168 113.6 (92%); dropout's generator adds 13 us to
-// 44 at 16384 x 2048.  Behind the combine (16384 x 2048, 6 rows a token) 118 us
+// 44 at 16384 x 2048; fp32 8192 x 2048 forward 45.9 (86%), gradient 70.5 (84%).  Behind the combine (16384 x 2048, 6 rows a token) 118 us
 // (84%): a row's loads wait for its places, and more of them in flight per thread
 // or in a shared ring measured slower (8192 x 4096, 4 rows: 101 us, a ring 134).
 #include <algorithm>
@@ -1056,11 +1056,13 @@ namespace {
 // 256 threads allow (4096 x 2048: one 22.9 us, two 25.0).  Two rows in the ring
 // where a thread has two vectors, else three (16384 x 4096: 133 us with two, 145
 // with three; 16384 x 2048: 70.9 and 67.3): more in flight than DRAM needs costs.
-GradientShape gradient_shape(int T, int D, int is_bf16, int gate_kind) {
+// With dropout a row's instructions bound it, and over many rows two vectors a
+// thread share them (16384 x 2048: 84.6 us, one 97.1; 4096 rows: 32.6 and 31.1).
+GradientShape gradient_shape(int T, int D, int is_bf16, int gate_kind, bool drops) {
     GradientShape g = {};
     const int V = D / 8;
     g.warp = V <= 64;
-    g.nv = (g.warp ? V <= 32 : V <= 256) ? 1 : 2;
+    g.nv = (g.warp ? V <= 32 : V <= (drops && T >= 8192 ? 192 : 256)) ? 1 : 2;
     g.threads = g.warp ? 256 : ((V + g.nv - 1) / g.nv + 31) / 32 * 32;
     g.in_ring = gate_kind == GATE_ELEMENT ? 5 : 4;
     const size_t stage = ring_bytes(g.in_ring, g.nv, is_bf16, g.threads);
@@ -1092,7 +1094,7 @@ cudaError_t launch_residual_norm_backward(const ResidualNorm &r, const void *s, 
                                           void *dresid, void *dy, float *dpost, void *dgate,
                                           float *dpre, float *part, cudaStream_t stream) {
     cudaError_t err;
-    const GradientShape g = gradient_shape(r.T, r.D, r.is_bf16, r.gate_kind);
+    const GradientShape g = gradient_shape(r.T, r.D, r.is_bf16, r.gate_kind, r.drop_cut > 0);
     if (r.T > 0) {
         BackwardArgs a = {};
         a.s = s;

@@ -371,7 +371,7 @@ def test_side_stream(moe):
 # rows enough for several a CTA (or a warp), in every shape of the kernels, with the last rows ragged
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("T,D", [(11003, 72), (7001, 264), (5003, 520), (4999, 1000), (2003, 1032), (1501, 2056), (1301, 4104),
-                                 (701, 8192), (331, 12296), (309, 16400)])
+                                 (701, 8192), (331, 12296), (309, 16400), (8195, 1608)])
 def test_many_rows(moe, T, D, dtype):
     for gate, p in (("channel", 0.1), ("element", 0.0)):
         rc, t, n = _case(moe, T, D, dtype, gate, p=p)
