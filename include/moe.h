@@ -636,7 +636,8 @@ moe_status moe_permute_noalloc(const moe_config *cfg, const void *x, const int32
  * MOE_ERR_UNSUPPORTED (use moe_layer_forward).  Same arguments as
  * moe_layer_forward, fp32 or bf16, any expert range and H shard; cfg's layout,
  * align_m and capacity play no part.  out is rounded once from fp32 sums (no
- * fp16 y_perm lies between, so its range does not bound y), h once to dtype; a
+ * fp16 y_perm lies between, so its range does not bound y); h of a bf16 layer is
+ * kept to 16 significant bits (two bf16); a
  * NaN key is flagged as by moe_route_topk.  Differs from moe_layer_forward by
  * rounding only, but a near tie of two keys may fall the other way.  Results
  * are bit-identical run to run on one device.  out may be x.

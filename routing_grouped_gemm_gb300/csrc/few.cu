@@ -12,8 +12,8 @@
 //
 //   route    expert rows of Wg over the CTAs, one dot product per token
 //   -- barrier -- every CTA selects all tokens' experts for itself and sorts the
-//            (token, slot) pairs by expert; at most 8 pairs of an expert form an
-//            ENTRY, one pass over that expert's weights
+//            (token, slot) pairs by expert; at most 4 pairs of an expert (fp32:
+//            8) form an ENTRY, one pass over that expert's weights
 //   GEMM1    tiles of 8 gate and 8 up rows of one entry over the CTAs -> h
 //   -- barrier --
 //   GEMM2    tiles of 16 rows of out; all (tile, entry, chunk of H) triples in
@@ -38,14 +38,17 @@
 // Measured (GB300, bf16): 16 tokens over 256 experts of 7168 x 2048, 9.0 GB of
 // weights, 1.22-1.28 ms (7.0-7.4 TB/s, the copy rate is 6.8); 8 tokens of the
 // fine-grained layer, 0.60 GB, 103-108 us (5.6-5.9 TB/s); one token of it, 104 MB,
-// 31.7 us, of which the stream's floor is 15.3.  The rest is latency: keys 2 us,
+// 32.9 us, of which the stream's floor is 15.3.  The rest is latency: keys 2 us,
 // barrier 1.3, top-k 2.4, entries 1.2, 4-6 until the first weights are there
 // (address translation and DRAM), the second barrier 2, and all of it run once, so
 // that its instructions come from L2.  (The layer's own calls take 63 us.)
 //
 // Rounding: keys, weights, both products' sums and the sum over experts are
-// fp32; h is rounded to the layer's type once (as in moe_grouped_swiglu), out
-// once.  Every sum has a fixed order for a given grid, so results do not change
+// fp32; out is rounded once.  h of a bf16 layer goes to the second product as the
+// sum of two bf16 (16 significant bits): four pairs' second parts take the columns
+// that an entry of four leaves free, so they cost no instruction of the product,
+// and out is off by its own rounding alone (h in one bf16: 0.0023-0.0027 of the
+// RMS against 64 bits, in two 0.0017).  Every sum has a fixed order for a given grid, so results do not change
 // from run to run.
 #include <algorithm>
 
@@ -72,22 +75,30 @@ enum { FEW_ROUTE = 1, FEW_GEMM1 = 2, FEW_GEMM2 = 4, FEW_ALL = 7 };
 struct FewParams {
     const void *x, *wg, *w1, *w3, *w2;
     const float *bias;
-    void *out, *h;     // h: [T k][H] by the pair's place in the sorted order
+    void *out, *h;     // h: [T k][H] by the pair's place in the sorted order (bf16: [2][T k][H])
     float *logits;     // [T][E]
     float *part;       // [gridDim.x][2][T][16]
     int *bars;         // [0], [1] the grid barriers, [2] CTAs done; zero between calls
     int *tile_count;   // [ceil(D / 16)] parts in; zero between calls
     int *status;
     int T, D, H, E, k, e_first, E_local, score, renorm, n_group, topk_group;
+    int rows;  // pairs of an entry, at most
     int phases;
 };
 
 template <typename T> struct Elem;
 template <> struct Elem<float> {
     static __device__ __forceinline__ float round(float v) { return v; }
+    static __device__ __forceinline__ void put(float v, float *h, float *) { *h = v; }
 };
 template <> struct Elem<__nv_bfloat16> {
     static __device__ __forceinline__ __nv_bfloat16 round(float v) { return __float2bfloat16_rn(v); }
+    // v as the sum of two bf16; what is not finite has no second part
+    static __device__ __forceinline__ void put(float v, __nv_bfloat16 *h, __nv_bfloat16 *low) {
+        *h = round(v);
+        const float first = __bfloat162float(*h);
+        *low = round(fabsf(first) <= 3.0e38f ? v - first : 0.f);
+    }
 };
 
 // 16 bytes global -> shared, past L1; zeros when !in (nothing is read then,
@@ -148,19 +159,22 @@ template <> struct Acc<__nv_bfloat16> {
 #pragma unroll
         for (int i = 0; i < 4; ++i) c[0][i] = c[1][i] = 0.f;
     }
-    __device__ __forceinline__ void step(const char *slot, int half_bytes, int cnt, int lane) {
-        const int g = lane >> 2;
-        const char *at = slot + piece_at(g, lane & 3);
+    // lows: 0, or where the second parts of the entry's rows (columns 4 ..) begin
+    __device__ __forceinline__ void step(const char *slot, int half_bytes, int cnt, int lows, int lane) {
+        const int g = lane >> 2, row = FW_M + (lows && g >= 4 ? lows + g - 4 : g);
+        const bool there = (lows ? g & 3 : g) < cnt;
+        const char *at = slot + piece_at(g, lane & 3), *bt = slot + piece_at(row, lane & 3);
         const int other = piece_at(g, (lane & 3) + 4) - piece_at(g, lane & 3);
+        const int other_b = piece_at(row, (lane & 3) + 4) - piece_at(row, lane & 3);
 #pragma unroll
-        for (int half = 0; half < 2; ++half, at += half_bytes)
+        for (int half = 0; half < 2; ++half, at += half_bytes, bt += half_bytes)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const char *a = at + k * other;
                 const uint4 lo = *reinterpret_cast<const uint4 *>(a);
                 const uint4 hi = *reinterpret_cast<const uint4 *>(a + 8 * FW_LINE);
                 uint4 bb = make_uint4(0, 0, 0, 0);
-                if (g < cnt) bb = *reinterpret_cast<const uint4 *>(a + FW_M * FW_LINE);
+                if (there) bb = *reinterpret_cast<const uint4 *>(bt + k * other_b);
                 mma_bf16(c[0], lo.x, hi.x, lo.y, hi.y, bb.x, bb.y);
                 mma_bf16(c[1], lo.z, hi.z, lo.w, hi.w, bb.z, bb.w);
             }
@@ -177,7 +191,7 @@ template <> struct Acc<float> {
 #pragma unroll
         for (int n = 0; n < FW_N; ++n) lo[n] = hi[n] = 0.f;
     }
-    __device__ __forceinline__ void step(const char *slot, int half_bytes, int cnt, int lane) {
+    __device__ __forceinline__ void step(const char *slot, int half_bytes, int cnt, int, int lane) {
 #pragma unroll
         for (int half = 0; half < 2; ++half, slot += half_bytes)
 #pragma unroll
@@ -219,8 +233,10 @@ template <> struct Acc<float> {
 
 // Shared memory, in bytes: the ring, the warps' sums (GEMM1's two buffers of a
 // tile, then GEMM2's of out), the tables of the T k (token, slot) pairs.
-__host__ __device__ inline int few_slot_bytes(int T) {
-    return (FW_M + (T < FW_N ? T : FW_N)) * FW_STEP;
+template <typename T> constexpr bool kFewSplit = sizeof(T) == 2;  // h in two parts
+// Rows of an entry's pairs in the ring: fp32 `rows`, bf16 twice that (the parts of h).
+__host__ __device__ inline int few_slot_bytes(int rows, bool split) {
+    return (FW_M + (split ? 2 * rows : rows)) * FW_STEP;
 }
 __host__ __device__ inline int few_sum_bytes(int T) {
     return FW_WARPS * FW_M * 4 * (T > 16 ? T : 16);  // GEMM1: 2 x 32 lanes x 16 bytes a warp
@@ -292,7 +308,7 @@ __device__ __forceinline__ void few_route(const FewParams &p, float *s_part, int
 }
 
 // The T k (token, slot) pairs whose expert is here, an expert's pairs together
-// and in order, cut into entries of at most 8.  s_sorted[n]: slot of the n-th
+// and in order, cut into entries of at most p.rows.  s_sorted[n]: slot of the n-th
 // pair, s_token[n]: its token, s_entry[u]: expert << 16 | first pair of entry u,
 // with a last one that holds the number of pairs.  Returns the entries.
 __device__ __forceinline__ int few_entries(const FewParams &p, int slots, const int *s_idx,
@@ -305,7 +321,7 @@ __device__ __forceinline__ int few_entries(const FewParams &p, int slots, const 
             const bool here = e >= 0 && e < p.E_local;
             const uint32_t mates = __match_any_sync(0xffffffffu, here ? e : -1 - lane);
             const int lead = __ffs(mates) - 1, size = __popc(mates);
-            int packed = here && lead == lane ? (size << 16) | ((size + FW_N - 1) / FW_N) : 0;
+            int packed = here && lead == lane ? (size << 16) | ((size + p.rows - 1) / p.rows) : 0;
             const int own = packed;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {  // pairs and entries of the experts up to here
@@ -318,8 +334,8 @@ __device__ __forceinline__ int few_entries(const FewParams &p, int slots, const 
             if (here) {
                 s_sorted[place] = lane;
                 s_token[place] = lane / p.k;
-                if (rank % FW_N == 0)
-                    s_entry[(before & 0xffff) + rank / FW_N] = (uint32_t)e << 16 | (uint32_t)place;
+                if (rank % p.rows == 0)
+                    s_entry[(before & 0xffff) + rank / p.rows] = (uint32_t)e << 16 | (uint32_t)place;
             }
             if (lane == 0) {
                 s_entry[all & 0xffff] = (uint32_t)(all >> 16);
@@ -346,7 +362,7 @@ __device__ __forceinline__ int few_entries(const FewParams &p, int slots, const 
             s_sorted[place] = i;
             s_token[place] = i / p.k;
             // the pair's expert, and whether it begins an entry: for the first warp
-            s_entry[place] = (uint32_t)e << 16 | (same % FW_N == 0 ? 1u : 0u);
+            s_entry[place] = (uint32_t)e << 16 | (same % p.rows == 0 ? 1u : 0u);
         }
     }
     __syncthreads();
@@ -401,7 +417,8 @@ few_layer_kernel(const FewParams p) {
     __shared__ uint64_t s_full[FW_WARPS][2], s_free[FW_WARPS][2];  // the groups' buffers of their sums
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = gridDim.x;
     const int slots = p.T * p.k;
-    const int slot_bytes = few_slot_bytes(p.T);
+    constexpr bool SPLIT = kFewSplit<T>;
+    const int slot_bytes = few_slot_bytes(p.rows, SPLIT);
     char *ring = smem + warp * DEPTH * slot_bytes;  // this warp's
     const int half_bytes = slot_bytes / 2;
     float4 *s_red = reinterpret_cast<float4 *>(smem + FW_WARPS * DEPTH * slot_bytes);  // [2][warps][32]
@@ -451,6 +468,8 @@ few_layer_kernel(const FewParams p) {
     const int g = lane >> 2;
     const int r4 = lane >> 3, c16 = lane & 7;  // a copy takes 4 rows' 128 bytes
     const uint32_t to_piece = smem_u32(ring) + piece_at(r4, c16);
+    // where a copy's second row goes: four on, or its first row's second part
+    const uint32_t to_second = smem_u32(ring) + piece_at(FW_M + (SPLIT ? p.rows : 4) + r4, c16);
     const int nt2 = (p.D + FW_M - 1) / FW_M;
     int in_slot = 0, out_slot = 0;  // ring slot of the next copies, of the next step
     Acc<T> acc;
@@ -518,6 +537,7 @@ few_layer_kernel(const FewParams p) {
                                        : static_cast<const char *>(p.w3) - weights;
         const ptrdiff_t to_4 = (ptrdiff_t)4 * row_bytes;
         const int tile_rows = second ? FW_M : 8, R = second ? p.D : p.H;
+        const bool two = SPLIT && second;  // the rows are h's two parts
         auto next_segment = [&](int &tile, int &u) {
             if (second) {
                 u += groups;
@@ -543,7 +563,7 @@ few_layer_kernel(const FewParams p) {
         bool fresh = true, has_hi = false;
         int lpos = position(ltile, lu, lc);
         bool ahead = second ? lpos < end : lu < U;
-        int has_rows = 0;
+        bool has_row = false, has_second = false;
         const char *lo = nullptr, *hi = nullptr, *row = nullptr, *row_4 = nullptr;
         auto open = [&]() {
             const uint32_t entry = s_entry[lu];
@@ -553,8 +573,9 @@ few_layer_kernel(const FewParams p) {
             lo = weights + (size_t)(e * R + first_row + r4) * row_bytes + col;
             hi = lo + to_hi;
             has_hi = !second || first_row + 8 < R;  // R is a multiple of 8
-            has_rows = cnt - r4;  // > 0: row r4 is there, > 4: row r4 + 4 too
-            const int n = f + (has_rows > 0 ? r4 : 0), n4 = f + (has_rows > 4 ? r4 + 4 : 0);
+            has_row = r4 < cnt;
+            has_second = two ? has_row : r4 + 4 < cnt;
+            const int n = f + (has_row ? r4 : 0), n4 = two ? slots + n : f + (has_second ? r4 + 4 : 0);
             row = rows + (size_t)(second ? n : s_token[n]) * row_bytes + col;
             row_4 = rows + (size_t)(second ? n4 : s_token[n4]) * row_bytes + col;
             left = row_bytes - col;
@@ -573,14 +594,15 @@ few_layer_kernel(const FewParams p) {
             }
         };
         auto copy_row = [&](int slot) {
-            const uint32_t d = to_piece + slot * slot_bytes + FW_M * FW_LINE;
-            if (has_rows > 0) {
+            if (has_row) {
+                const uint32_t d = to_piece + slot * slot_bytes + FW_M * FW_LINE;
                 copy16(d, row, left > 0);
                 copy16(d + half_bytes, row + FW_LINE, left > FW_LINE);
             }
-            if (has_rows > 4) {
-                copy16(d + 4 * FW_LINE, row_4, left > 0);
-                copy16(d + half_bytes + 4 * FW_LINE, row_4 + FW_LINE, left > FW_LINE);
+            if (has_second) {
+                const uint32_t d = to_second + slot * slot_bytes;
+                copy16(d, row_4, left > 0);
+                copy16(d + half_bytes, row_4 + FW_LINE, left > FW_LINE);
             }
         };
         auto bump = [&](int &slot) { slot = slot + 1 == DEPTH ? 0 : slot + 1; };
@@ -609,7 +631,7 @@ few_layer_kernel(const FewParams p) {
         auto step = [&](int cnt) {  // the oldest copies, and the next into the slot read a step ago
             copy_wait<DEPTH - 2>();
             __syncwarp();
-            acc.step(ring + out_slot * slot_bytes, half_bytes, cnt, lane);
+            acc.step(ring + out_slot * slot_bytes, half_bytes, cnt, two ? p.rows : 0, lane);
             bump(out_slot);
             copy_next();
         };
@@ -677,10 +699,16 @@ few_layer_kernel(const FewParams p) {
                         // gate (x, y) and up (z, w) of unit g for the entry's rows 2 q, 2 q + 1
                         const int m = 2 * (lane & 3);
                         T *h = static_cast<T *>(p.h) + (size_t)(f + m) * p.H + tile * 8 + g;
-                        if (m < cnt) h[0] = Elem<T>::round(sum.x / (1.f + expf(-sum.x)) * sum.z);
-                        if (m + 1 < cnt) h[p.H] = Elem<T>::round(sum.y / (1.f + expf(-sum.y)) * sum.w);
+                        T *low = h + (size_t)slots * p.H;
+                        if (m < cnt) Elem<T>::put(sum.x / (1.f + expf(-sum.x)) * sum.z, h, low);
+                        if (m + 1 < cnt)
+                            Elem<T>::put(sum.y / (1.f + expf(-sum.y)) * sum.w, h + p.H, low + p.H);
                     }
                 } else {
+                    if (SPLIT) {  // columns 4 .. are the second parts' sums
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 2);
+                    }
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         const int m = 2 * (lane & 3) + half;
@@ -823,8 +851,10 @@ cudaError_t launch_few_layer(const FewLayer &f, cudaStream_t stream) {
     // read: 6 for one token (160 KB of weights in flight per SM), 5 up to 4
     // tokens, else 4, or 3 with many pairs.
     const int rest = few_sum_bytes(f.T) + few_table_bytes(f.T * f.k);
-    const int depth = std::min(6, (FW_SMEM - rest) / (FW_WARPS * few_slot_bytes(f.T)));
-    const size_t smem = (size_t)FW_WARPS * depth * few_slot_bytes(f.T) + rest;
+    p.rows = std::min(f.T, f.is_bf16 ? FW_N / 2 : FW_N);
+    const int slot = few_slot_bytes(p.rows, f.is_bf16);
+    const int depth = std::min(6, (FW_SMEM - rest) / (FW_WARPS * slot));
+    const size_t smem = (size_t)FW_WARPS * depth * slot + rest;
     auto fn = f.is_bf16 ? (depth == 6   ? few_layer_kernel<__nv_bfloat16, 6>
                            : depth == 5 ? few_layer_kernel<__nv_bfloat16, 5>
                            : depth == 4 ? few_layer_kernel<__nv_bfloat16, 4>

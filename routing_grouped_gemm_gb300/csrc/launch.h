@@ -259,7 +259,7 @@ cudaError_t launch_grouped_swiglu_bf16(const void *x_perm, const int *seg_offset
 
 // The whole layer for at most kFewMaxTokens tokens in one cooperative launch.
 // counters: few_scratch_ints(D) ints, zero before the first call and left zero;
-// h [T k, H_local] in the layer's type, logits [T, E] and part
+// h [T k, H_local] (fp32, or two bf16 for each), logits [T, E] and part
 // (few_part_floats(T)) are scratch.
 constexpr int kFewMaxTokens = 32;
 constexpr int kFewMaxCtas = 160;

@@ -201,7 +201,10 @@ def test_agrees_with_the_layer(moe):
     ws = moe.alloc_workspace(c, layer=True)
     moe.moe_layer_forward(c, t["x"], t["wg"], t["bias"], t["w1"], t["w3"], t["w2"], out, ws)
     got, _ = _call(moe, c, t)
-    assert (got.float() - out.float()).abs().max() <= 2e-2 * out.float().square().mean().sqrt()
+    # each side rounds out once, at most 2^-8 of the value: together a whole step, 2^-7; the layer's h and y_perm,
+    # rounded where this call's are not, add less than 1e-2 of the RMS (see _check)
+    a, b = got.float(), out.float()
+    assert ((a - b).abs() <= 2.0 ** -7 * torch.maximum(a.abs(), b.abs()) + 1e-2 * b.square().mean().sqrt()).all()
 
 
 def test_workspace_reused_for_fewer_tokens_and_left_dirty(moe):
