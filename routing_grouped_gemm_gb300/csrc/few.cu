@@ -66,7 +66,7 @@ constexpr int FW_WARPS = 8;
 constexpr int FW_THREADS = 32 * FW_WARPS;
 constexpr int FW_STEP = 256;                   // bytes of a row that a warp takes at once
 constexpr int FW_M = 16;                       // weight rows per tile
-constexpr int FW_N = 8;                        // rows of an entry
+constexpr int FW_N = 8;                        // the most rows of an entry (bf16: half as many)
 constexpr int FW_SMEM = 226 * 1024;            // of the 227 KB a CTA may have
 constexpr int FW_JOIN = 8192;                  // bytes of a row as long as joining a shared tile's parts takes
 
@@ -848,8 +848,8 @@ cudaError_t launch_few_layer(const FewLayer &f, cudaStream_t stream) {
     p.n_group = f.n_group;
     p.topk_group = f.topk_group;
     // As many steps of every warp as the shared memory takes, one of them being
-    // read: 6 for one token (160 KB of weights in flight per SM), 5 up to 4
-    // tokens, else 4, or 3 with many pairs.
+    // read: 6 for one token (160 KB of weights in flight per SM), 5 for two, else
+    // 4 (fp32: 6 to 4), or 3 with many pairs.
     const int rest = few_sum_bytes(f.T) + few_table_bytes(f.T * f.k);
     p.rows = std::min(f.T, f.is_bf16 ? FW_N / 2 : FW_N);
     const int slot = few_slot_bytes(p.rows, f.is_bf16);
