@@ -668,12 +668,12 @@ struct BackwardArgs {
 };
 
 // With r1, r2 the rows' rsqrt factors and gp = dn pre:
-//   ds = ds_out + r2 gp - c s,  c = r2^3 mean(gp s)
+//   ds = ds_out + r2 gp - c s r2,  c = r2^2 mean(gp s)
 //   u = branch_scale keep ds;  dgate = u v;  dv = gate u
 //   dy = r1 (dv post - y r1^2 mean(dv post y))
 // ds is linear in two row sums that are not known yet, so with
 // q = branch_scale keep post gate y,
-//   sum(ds q) = sum(ds_out q) + r2 sum(gp q) - c sum(s q)
+//   sum(ds q) = sum(ds_out q) + r2 sum(gp q) - c r2 sum(s q)
 // and every sum of the row comes out of ONE reduction.  (A token's gate is left
 // out of q and multiplied in behind.)  The column sums are two:
 //   P = sum dn s r2 = dpre,   G = sum keep ds y r1 (times a gate that is not the
@@ -805,14 +805,16 @@ residual_norm_backward_kernel(const BackwardArgs a) {
         float sum[8] = {sum2(m[0]), sum2(m[1]), sum2(m[2]), sum2(m[3]), sum2(m[4]), sum2(m[5]), 0.f, 0.f};
         row_sums<WARP>(sum, s_sum[turn]);
         const float r2 = has_pre ? rsqrtf(fmaf(sum[0], inv_d, a.eps)) : 0.f;
-        const float c = r2 * r2 * r2 * (sum[1] * inv_d);
+        // r1 and r2 multiply what they bring near one, a step at a time: their squares
+        // and cubes leave the range of fp32 long before a row does
+        const float c = r2 * (r2 * (sum[1] * inv_d));  // of s r2
         const float r1 = a.post ? rsqrtf(fmaf(sum[2], inv_d, a.eps)) : 1.f;
-        const float dot = sum[3] + r2 * sum[4] - c * sum[5];  // sum(ds q)
-        const float c1 = a.post ? r1 * r1 * (gt * dot * inv_d) : 0.f;
+        const float dot = sum[3] + r2 * sum[4] - c * (r2 * sum[5]);  // sum(ds q)
+        const float c1 = a.post ? r1 * (r1 * (dot * inv_d)) : 0.f;   // of gate y r1
         if (a.gate_kind == GATE_TOKEN && mine == 0) static_cast<float *>(a.dgate)[t] = r1 * dot;
         asm volatile("" ::: "memory");  // the row is read again, not kept: registers are short
         const f2 r2_2 = both(r2), c_2 = both(-c), res_2 = both(branch ? a.res_scale : 1.f);
-        const f2 r1_2 = both(r1), g_2 = both(r1 * gt), c1_2 = both(-r1 * c1);
+        const f2 r1_2 = both(r1), g_2 = both(r1 * gt), c1_2 = both(-c1);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int v = mine + i * across;
@@ -827,16 +829,17 @@ residual_norm_backward_kernel(const BackwardArgs a) {
             f2 dg[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const f2 ds = fma2(s[e], c_2, fma2(mul2(n[e], w[e]), r2_2, d[e]));
-                P[i][e] = fma2(n[e], mul2(s[e], r2_2), P[i][e]);
+                const f2 sr = mul2(s[e], r2_2), yr = mul2(y[e], g_2);
+                const f2 ds = fma2(sr, c_2, fma2(mul2(n[e], w[e]), r2_2, d[e]));
+                P[i][e] = fma2(n[e], sr, P[i][e]);
                 f2 k = drops ? kept(ds, bits[i], e) : ds;
                 if (elem) {
                     dg[e] = mul2(mul2(k, coef[i][e]), mul2(y[e], r1_2));
                     k = mul2(k, ge[e]);
                 }
-                G[i][e] = fma2(k, mul2(y[e], g_2), G[i][e]);
+                G[i][e] = fma2(k, yr, G[i][e]);
                 d[e] = mul2(ds, res_2);
-                y[e] = fma2(mul2(k, coef[i][e]), g_2, mul2(y[e], c1_2));
+                y[e] = fma2(mul2(k, coef[i][e]), g_2, mul2(yr, c1_2));
             }
             store8<BF16>(a.dresid, base + v, d);
             if (branch) store8<BF16>(a.dy, base + v, y);

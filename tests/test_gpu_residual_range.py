@@ -1,0 +1,43 @@
+"""The norms around a block where fp32 could spoil a result: rows far from one, rows of zeros at a tiny eps.
+
+Bounds as in test_gpu_residual_norm: what fp32 may add (residual_reference derives it, relative to the terms, so it
+holds at any scale) plus half a step of the output's type.
+"""
+import pytest
+import torch
+
+from test_gpu_residual_norm import _case, _check_gradient, _gradient, moe  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+# a row per warp with one and with two vectors a lane, per CTA with one and with two, without a ring
+SHAPES = [(37, 136), (21, 392), (9, 1048), (5, 4104), (3, 8200)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("gate", ["channel", "token", "element"])
+@pytest.mark.parametrize("scale", [1e13, 1e15, 1e17])
+@pytest.mark.parametrize("T,D", SHAPES)
+def test_gradient_of_large_rows(moe, T, D, scale, gate, dtype):
+    """Rows of `scale`, whose squares' sum (at most 8200 e34) fp32 holds.  dnorm_out has the same scale and leans
+    towards s, so that every term of ds is about one."""
+    rc, t, n = _case(moe, T, D, dtype, gate, res_scale=0.7)
+    s = n(T, D, to=torch.float32)
+    t["pre"] = t["pre"].abs()
+    t["resid"], t["y"] = (scale * s).to(rc.torch_dtype), n(T, D, scale=scale)
+    dn = (scale * (n(T, D, to=torch.float32) + s)).to(rc.torch_dtype)
+    for dso in (n(T, D), None):
+        _check_gradient(rc, t, gate, dso, dn, _gradient(moe, rc, t, gate, dso, dn))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("gate", ["channel", "token", "element"])
+@pytest.mark.parametrize("T,D", SHAPES)
+def test_gradient_of_rows_of_zeros_and_small_rows_at_a_tiny_eps(moe, T, D, gate, dtype):
+    rc, t, n = _case(moe, T, D, dtype, gate, eps=1e-30)
+    t["resid"][0] = t["y"][0] = 0
+    t["resid"][1] *= 1e-14
+    t["y"][1] *= 1e-14
+    dn = n(T, D)
+    for dso in (n(T, D), None):
+        _check_gradient(rc, t, gate, dso, dn, _gradient(moe, rc, t, gate, dso, dn))
