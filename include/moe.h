@@ -731,8 +731,9 @@ int64_t moe_residual_workspace_size(const moe_residual_config *rc);
 
 /*
  * Gradient of moe_residual_norm.  s [T, D]: its resid_out (its resid, when y
- * was NULL); y, post_gain, gate, pre_gain and rng as the forward had them (of
- * moe_combine_residual_norm: its y_out as y).  dresid_out, dnorm_out [T, D]:
+ * was NULL), not looked at without pre_gain; y, post_gain, gate, pre_gain and
+ * rng as the forward had them (of moe_combine_residual_norm: its y_out as y).
+ * dresid_out, dnorm_out [T, D]:
  * the gradients of resid_out and norm_out; dresid_out may be NULL (zeros) when
  * pre_gain is given, dnorm_out is NULL without pre_gain.  With r1, r2 the rows'
  * rsqrt factors, g = dnorm_out pre_gain, means over the row and sums over rows:

@@ -736,7 +736,8 @@ residual_norm_backward_kernel(const BackwardArgs a) {
         }
     }
 
-    const void *arrays[5] = {a.s, a.ds_out, a.dn, a.y, elem ? a.gate : nullptr};
+    // without the next norm ds is ds_out: s is left out, whatever it holds
+    const void *arrays[5] = {has_pre ? a.s : nullptr, a.ds_out, a.dn, a.y, elem ? a.gate : nullptr};
     auto has = [&](int k) { return FULL ? k < 4 : arrays[k] != nullptr; };
     Ring<BF16, NV> ring(smem, V, mine, across, RING ? a.depth : 0, a.in_ring);
     auto copy_row = [&](long long t, int stage) {

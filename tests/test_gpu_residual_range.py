@@ -1,4 +1,5 @@
-"""The norms around a block where fp32 could spoil a result: rows far from one, rows of zeros at a tiny eps.
+"""The norms around a block where fp32 could spoil a result: rows far from one, rows of zeros at a tiny eps,
+infinities where a form does not look.
 
 Bounds as in test_gpu_residual_norm: what fp32 may add (residual_reference derives it, relative to the terms, so it
 holds at any scale) plus half a step of the output's type.
@@ -6,7 +7,7 @@ holds at any scale) plus half a step of the output's type.
 import pytest
 import torch
 
-from test_gpu_residual_norm import _case, _check_gradient, _gradient, moe  # noqa: F401
+from test_gpu_residual_norm import GATES, _case, _check_gradient, _gradient, moe  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -41,3 +42,17 @@ def test_gradient_of_rows_of_zeros_and_small_rows_at_a_tiny_eps(moe, T, D, gate,
     dn = n(T, D)
     for dso in (n(T, D), None):
         _check_gradient(rc, t, gate, dso, dn, _gradient(moe, rc, t, gate, dso, dn))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("gate", list(GATES))
+@pytest.mark.parametrize("T,D", SHAPES)
+def test_gradient_without_the_next_norm_does_not_look_at_s(moe, T, D, gate, dtype):
+    """Without pre_gain ds is dresid_out, whatever s holds (a residual that overflowed, say)."""
+    rc, t, n = _case(moe, T, D, dtype, gate, pre=False, p=0.2)
+    dso = n(T, D)
+    want = _gradient(moe, rc, t, gate, dso, None)
+    _check_gradient(rc, t, gate, dso, None, want)
+    t["resid"][0, 3], t["resid"][1, D - 1], t["resid"][2] = float("inf"), float("nan"), 3e38
+    got = _gradient(moe, rc, t, gate, dso, None)
+    assert all(want[k] is None or torch.equal(got[k], want[k]) for k in want)
