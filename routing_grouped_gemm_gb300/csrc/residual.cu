@@ -840,7 +840,8 @@ residual_norm_backward_kernel(const BackwardArgs a) {
                 }
                 G[i][e] = fma2(k, yr, G[i][e]);
                 d[e] = mul2(ds, res_2);
-                y[e] = fma2(mul2(k, coef[i][e]), g_2, mul2(yr, c1_2));
+                const f2 dv = mul2(mul2(k, coef[i][e]), g_2);
+                y[e] = a.post ? fma2(yr, c1_2, dv) : dv;  // no mean without a norm, whatever y holds
             }
             store8<BF16>(a.dresid, base + v, d);
             if (branch) store8<BF16>(a.dy, base + v, y);

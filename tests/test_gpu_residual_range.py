@@ -56,3 +56,25 @@ def test_gradient_without_the_next_norm_does_not_look_at_s(moe, T, D, gate, dtyp
     t["resid"][0, 3], t["resid"][1, D - 1], t["resid"][2] = float("inf"), float("nan"), 3e38
     got = _gradient(moe, rc, t, gate, dso, None)
     assert all(want[k] is None or torch.equal(got[k], want[k]) for k in want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("pre", [True, False])
+@pytest.mark.parametrize("gate", list(GATES))
+@pytest.mark.parametrize("T,D", SHAPES)
+def test_gradient_without_the_branch_norm_keeps_y_out_of_dy(moe, T, D, gate, pre, dtype):
+    """Without post_gain dy = gate u does not depend on y: an infinity there reaches the gate's gradient alone."""
+    rc, t, n = _case(moe, T, D, dtype, gate, post=False, pre=pre)
+    dso, dn = n(T, D), n(T, D) if pre else None
+    want = _gradient(moe, rc, t, gate, dso, dn)
+    _check_gradient(rc, t, gate, dso, dn, want)
+    t["y"][1, 5], t["y"][2, D - 2] = float("inf"), float("nan")
+    got = _gradient(moe, rc, t, gate, dso, dn)
+    for k in want:
+        if want[k] is None:
+            continue
+        same = torch.ones_like(want[k], dtype=torch.bool)
+        if k == "dgate":
+            same[(..., [5, D - 2]) if gate == "channel" else [1, 2] if gate == "token" else ([1, 2], [5, D - 2])] = False
+            assert not got[k][~same].isfinite().any()
+        assert torch.equal(got[k][same], want[k][same]), k
