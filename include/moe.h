@@ -675,15 +675,18 @@ moe_status moe_layer_forward_few(const moe_config *cfg, const void *x, const voi
  *   p_drop     probability, in [0, 1), that an element of v is dropped, taken
  *              to the nearest multiple of 2^-16 (at least 2^-16 below 1)
  *
- * Dropout.  keep is 0 or 1 / (1 - p_drop) and never stored: element c of row t
- * is element i mod 8 of vector i / 8, i = t D + c, and takes half word i mod 8
- * (the low half of a word first) of the four words that Philox4x32 with ten
- * rounds (Salmon et al., "Parallel random numbers: as easy as 1, 2, 3", 2011)
- * gives for the counter (i / 8, offset) under the key seed, each 64 bits, low
- * word first; it stays when that half word is at least 65536 p_drop.  rng
- * [2] int64 = {seed, offset} is device memory, 8-byte aligned, read when the
- * kernel runs, so a captured graph takes what it holds at the replay; NULL
- * allowed without dropout.  The caller moves offset on from call to call.
+ * Dropout.  keep is 0 or 1 / (1 - p_drop) and never stored.  A dropped element
+ * adds nothing to s, whatever v and the gate hold there (infinities and NaN too;
+ * y's own norm takes all of y), and the gradient looks at neither its y, where
+ * there is no such norm, nor its own gate.  Element c of row t is element i mod 8
+ * of vector i / 8, i = t D + c, and takes half word i mod 8 (the low half of a
+ * word first) of the four words that Philox4x32 with ten rounds (Salmon et al.,
+ * "Parallel random numbers: as easy as 1, 2, 3", 2011) gives for the counter
+ * (i / 8, offset) under the key seed, each 64 bits, low word first; it stays when
+ * that half word is at least 65536 p_drop.  rng [2] int64 = {seed, offset} is
+ * device memory, 8-byte aligned, read when the kernel runs, so a captured graph
+ * takes what it holds at the replay; NULL allowed without dropout.  The caller
+ * moves offset on from call to call.
  */
 typedef enum {
     MOE_GATE_NONE = 0,

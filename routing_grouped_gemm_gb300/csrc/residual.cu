@@ -121,18 +121,6 @@ struct Drop {
     float scale;
 };
 
-// f[e] *= keep factor: half words of the vector's four words, low half first.
-__device__ __forceinline__ void drop8(float (&f)[8], uint64_t vec, const Drop &d, uint64_t seed,
-                                      uint64_t offset) {
-    const uint4 w = philox(vec, offset, seed);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = (u[i] & 0xffffu) >= d.cut ? f[2 * i] * d.scale : 0.f;
-        f[2 * i + 1] = (u[i] >> 16) >= d.cut ? f[2 * i + 1] * d.scale : 0.f;
-    }
-}
-
 // ---------------------------------------------------------------------
 // arithmetic on pairs
 // ---------------------------------------------------------------------
@@ -188,7 +176,7 @@ __device__ __forceinline__ void put8(float *shared, const f2 (&f)[4]) {
     for (int i = 0; i < 4; ++i) reinterpret_cast<float2 *>(shared)[i] = parts(f[i]);
 }
 
-// Bit e: element e of a vector stays.
+// Bit e: element e of a vector stays: half word e of the vector's four words, low half first.
 __device__ __forceinline__ uint32_t keep_bits(uint64_t vec, uint32_t cut, uint64_t seed,
                                               uint64_t offset) {
     const uint4 w = philox(vec, offset, seed);
@@ -457,15 +445,21 @@ residual_norm_row_kernel(const ForwardArgs a) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) y[i][e] = y[i][e] * r1 * g[e];
                 }
-                if (a.drop.cut) drop8(y[i], base + v, a.drop, seed, offset);
+                uint32_t bits = 0xffu;
+                if (a.drop.cut) {
+                    bits = keep_bits(base + v, a.drop.cut, seed, offset);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[i][e] *= a.drop.scale;
+                }
                 if (a.gate_kind == GATE_CHANNEL || a.gate_kind == GATE_ELEMENT) {
                     unpack8<BF16>(load8<BF16>(a.gate, a.gate_kind == GATE_CHANNEL ? v : base + v), g);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) y[i][e] *= g[e];
                 }
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    s[i][e] = fmaf(a.res_scale, s[i][e], a.branch_scale * (gt * y[i][e]));
+                for (int e = 0; e < 8; ++e)  // nothing of a dropped element, be it infinite
+                    s[i][e] = fmaf(a.res_scale, s[i][e],
+                                   bits >> e & 1u ? a.branch_scale * (gt * y[i][e]) : 0.f);
                 store8<BF16>(a.resid_out, base + v, s[i]);
             }
         }
@@ -827,6 +821,14 @@ residual_norm_backward_kernel(const BackwardArgs a) {
             unpack8<BF16>(take(3, i, stage, base), y);
             unpack8<BF16>(pre[i], w);
             if (elem) unpack8<BF16>(take(4, i, stage, base), ge);
+            if (drops && !a.post) {  // a dropped y may be infinite (under a norm the row is lost then)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = kept(y[e], bits[i], e);
+            }
+            if (elem && drops) {  // and so may its gate
+#pragma unroll
+                for (int e = 0; e < 4; ++e) ge[e] = kept(ge[e], bits[i], e);
+            }
             f2 dg[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {

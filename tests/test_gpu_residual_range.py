@@ -7,7 +7,7 @@ holds at any scale) plus half a step of the output's type.
 import pytest
 import torch
 
-from test_gpu_residual_norm import GATES, _case, _check_gradient, _gradient, moe  # noqa: F401
+from test_gpu_residual_norm import GATES, _case, _check_gradient, _forward, _gradient, _keep, moe  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -78,3 +78,51 @@ def test_gradient_without_the_branch_norm_keeps_y_out_of_dy(moe, T, D, gate, pre
             same[(..., [5, D - 2]) if gate == "channel" else [1, 2] if gate == "token" else ([1, 2], [5, D - 2])] = False
             assert not got[k][~same].isfinite().any()
         assert torch.equal(got[k][same], want[k][same]), k
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("post", [True, False])
+@pytest.mark.parametrize("T,D", [(5, 72), (2500, 72), (5, 1048), (1300, 1048), (3, 8200)])
+def test_a_dropped_element_adds_nothing(moe, T, D, post, dtype):
+    """Infinities and NaN in dropped places -- of a gate for every element, and of y where it has no norm -- change
+    nothing, forward (few rows and many take different kernels) and gradient."""
+    rc, t, n = _case(moe, T, D, dtype, "element", post=post, p=0.5)
+    dso, dn = n(T, D), n(T, D)
+    want, dwant = _forward(moe, rc, t), _gradient(moe, rc, t, "element", dso, dn)
+    gone = (_keep(rc, t) == 0).cuda()
+    for name, bad in (("gate", float("inf")), ("gate", float("nan")), ("y", float("inf")), ("y", float("nan"))):
+        if name == "y" and post:
+            continue
+        u = dict(t, **{name: t[name].masked_fill(gone, bad)})
+        got, dgot = _forward(moe, rc, u), _gradient(moe, rc, u, "element", dso, dn)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert all(dwant[k] is None or torch.equal(dgot[k], dwant[k]) for k in dwant)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("gate", ["channel", "token"])
+@pytest.mark.parametrize("T,D", [(5, 72), (2500, 72), (5, 1048), (1300, 1048), (3, 8200)])
+def test_a_dropped_element_under_an_infinite_shared_gate(moe, T, D, gate, dtype):
+    rc, t, n = _case(moe, T, D, dtype, gate, p=0.5, pre=False)
+    gone = (_keep(rc, t) == 0).cuda()
+    t["gate"][2] = float("inf")
+    r, _ = _forward(moe, rc, t)
+    assert torch.equal(r[gone], t["resid"][gone])
+    there = ~gone[:, 2] if gate == "channel" else ~gone[2]
+    assert not (r[:, 2] if gate == "channel" else r[2])[there].isfinite().any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_combine_dropped_element(moe, dtype):
+    rc, t, n = _case(moe, 9, 264, dtype, "element", p=0.5)
+    cfg = moe.Config(T=9, D=264, H_local=64, E=1, k=1, align_m=1, dtype=rc.dtype)
+    yp = n(9, 264, to=torch.float16 if dtype == "bf16" else torch.float32)
+    row, w = torch.arange(9, device="cuda").int()[:, None].contiguous(), torch.ones(9, 1, device="cuda")
+    ws = moe.alloc_workspace(cfg)
+
+    def call(gate):
+        out = [torch.empty_like(t["resid"]) for _ in range(3)]
+        moe.moe_combine_residual_norm(cfg, rc, yp, row, w, t["resid"], t["post"], gate, t["pre"], t["rng"], *out, ws)
+        return out
+    got = call(t["gate"].masked_fill((_keep(rc, t) == 0).cuda(), float("inf")))
+    assert all(torch.equal(a, b) for a, b in zip(got, call(t["gate"])))
