@@ -707,7 +707,12 @@ few_layer_kernel(const FewParams p) {
                 } else {
                     if (SPLIT) {  // columns 4 .. are the second parts' sums
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 2);
+                        for (int i = 0; i < 4; ++i) {
+                            const float low = __shfl_xor_sync(0xffffffffu, v[i], 2);
+                            // an infinite weight is infinite by the first part alone: the
+                            // second, zero or of the other sign, would make it NaN
+                            v[i] = fabsf(v[i]) < INFINITY ? v[i] + low : v[i];
+                        }
                     }
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
