@@ -97,7 +97,7 @@ template <> struct Elem<__nv_bfloat16> {
     static __device__ __forceinline__ void put(float v, __nv_bfloat16 *h, __nv_bfloat16 *low) {
         *h = round(v);
         const float first = __bfloat162float(*h);
-        *low = round(fabsf(first) <= 3.0e38f ? v - first : 0.f);
+        *low = round(fabsf(first) < INFINITY ? v - first : 0.f);
     }
 };
 

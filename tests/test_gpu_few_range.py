@@ -28,3 +28,25 @@ def test_infinite_weights_of_the_second_product(moe, T, dtype):
         assert (got[here, d].double() == h[here, u].sign() * float("inf")).all()
         same[here, d] = False
     assert torch.equal(got[same], want[same])
+
+
+def test_h_next_to_the_largest_bf16(moe):
+    """h = 3.2e38 (bf16 ends at 3.39e38) keeps its second part: unit 0's h takes 16 bits, unit 1's is the bf16 next
+    to it, and w2 takes their difference.  Every product here is exact but silu(1.8e19) = 1.8e19."""
+    c = moe.Config(T=1, D=8, H_local=8, E=1, k=1)
+    z = torch.zeros(1, 8, 8, dtype=torch.bfloat16, device="cuda")
+    x = z[0, :1].clone()
+    x[0, 0] = 1
+    gate = 249 * 2.0 ** 56   # eight bits
+    up = 251 * 2.0 ** 56
+    h = gate * up            # 62499 2^112 = 3.2e38: sixteen
+    first = torch.tensor(h, dtype=torch.float64).to(torch.bfloat16).double().item()
+    assert 3.0e38 < first < 3.39e38 and first != h
+    # unit 1: 2^63 times first 2^-63
+    w1, w3, w2 = z.clone(), z.clone(), z.clone()
+    w1[0, 0, 0], w3[0, 0, 0] = gate, up
+    w1[0, 1, 0], w3[0, 1, 0] = 2.0 ** 63, first / 2.0 ** 63
+    w2[0, 0, 0], w2[0, 0, 1] = 2.0 ** -112, -(2.0 ** -112)
+    out, _ = _call(moe, c, dict(x=x, wg=z[0, :1].clone(), bias=None, w1=w1, w3=w3, w2=w2))
+    assert out[0, 0].item() == (h - first) * 2.0 ** -112
+    assert (out[0, 1:] == 0).all()
