@@ -644,8 +644,8 @@ moe_status moe_permute_noalloc(const moe_config *cfg, const void *x, const int32
  *
  * ws: moe_layer_few_workspace_size(cfg) bytes (-1: bad config, T above 32, or
  * sizes whose tiles pass int32), zero-filled once and used by this call alone: it
- * then serves every config with the same D that it is large enough for.  Calls
- * that share it must not run concurrently (two captured graphs included).
+ * then serves every config that it is large enough for.  Calls that share it must
+ * not run concurrently (two captured graphs included).
  * Capture into a graph once a first call has run outside.
  */
 int64_t moe_layer_few_workspace_size(const moe_config *cfg);

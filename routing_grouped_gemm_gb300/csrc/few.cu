@@ -79,7 +79,9 @@ struct FewParams {
     float *logits;     // [T][E]
     float *part;       // [gridDim.x][2][T][16]
     int *bars;         // [0], [1] the grid barriers, [2] CTAs done; zero between calls
-    int *tile_count;   // [ceil(D / 16)] parts in; zero between calls
+    // Parts in of the shared tile that CTA b holds the first part of: half word b
+    // (one tile at most goes on behind b's part); zero between calls.
+    unsigned *tile_count;
     int *status;
     int T, D, H, E, k, e_first, E_local, score, renorm, n_group, topk_group;
     int rows;  // pairs of an entry, at most
@@ -776,10 +778,12 @@ few_layer_kernel(const FewParams p) {
             const int mine = tid == 0 ? cut[0] : cut[1];
             if (mine >= 0) {
                 fence_acq_rel_gpu();
-                const int before = atomicAdd(&p.tile_count[mine], 1);
+                const int from = tid == 0 ? ca[0] : ca[1], others = (tid == 0 ? cb[0] : cb[1]) - from;
+                const int shift = 16 * (from & 1);
+                const unsigned before = atomicAdd(&p.tile_count[from >> 1], 1u << shift);
                 fence_acq_rel_gpu();
-                s_last[tid] = before == (tid == 0 ? cb[0] - ca[0] : cb[1] - ca[1]);
-                if (s_last[tid]) p.tile_count[mine] = 0;
+                s_last[tid] = (before >> shift & 0xffffu) == (unsigned)others;
+                if (s_last[tid]) atomicSub(&p.tile_count[from >> 1], (unsigned)(others + 1) << shift);
             }
         }
         __syncthreads();
@@ -814,7 +818,7 @@ few_layer_kernel(const FewParams p) {
             if (atomicAdd(&p.bars[2], 1) == G - 1) {
                 fence_acq_rel_gpu();
                 if (atomicOr(p.status, 0) & FLAG_TIMEOUT)  // some parts never came
-                    for (int i = 0; i < nt2; ++i) p.tile_count[i] = 0;
+                    for (int i = 0; i < kFewMaxCtas / 2; ++i) p.tile_count[i] = 0;
                 p.bars[0] = p.bars[1] = p.bars[2] = 0;
             }
         }
@@ -823,7 +827,11 @@ few_layer_kernel(const FewParams p) {
 
 }  // namespace
 
-int64_t few_scratch_ints(int D) { return 64 + (D + FW_M - 1) / FW_M; }
+// The barriers' counts, polled, on a line of their own, and the tiles': one length
+// for all layers, so that what one keeps at zero is not another one's scratch.
+constexpr int FW_BARS = 32;
+static_assert(kFewMaxCtas % 2 == 0, "two counts to a word");
+int few_scratch_ints() { return FW_BARS + kFewMaxCtas / 2; }
 int64_t few_part_floats(int T) { return (int64_t)kFewMaxCtas * 2 * T * FW_M; }
 
 cudaError_t launch_few_layer(const FewLayer &f, cudaStream_t stream) {
@@ -839,7 +847,7 @@ cudaError_t launch_few_layer(const FewLayer &f, cudaStream_t stream) {
     p.logits = f.logits;
     p.part = f.part;
     p.bars = f.counters;
-    p.tile_count = f.counters + 64;
+    p.tile_count = reinterpret_cast<unsigned *>(f.counters + FW_BARS);
     p.status = f.status;
     p.T = f.T;
     p.D = f.D;

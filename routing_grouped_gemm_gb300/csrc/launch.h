@@ -258,7 +258,7 @@ cudaError_t launch_grouped_swiglu_bf16(const void *x_perm, const int *seg_offset
                                        int64_t rows_alloc, int *status, cudaStream_t stream);
 
 // The whole layer for at most kFewMaxTokens tokens in one cooperative launch.
-// counters: few_scratch_ints(D) ints, zero before the first call and left zero;
+// counters: few_scratch_ints() ints, zero before the first call and left zero;
 // h [T k, H_local] (fp32, or two bf16 for each), logits [T, E] and part
 // (few_part_floats(T)) are scratch.
 constexpr int kFewMaxTokens = 32;
@@ -271,7 +271,7 @@ struct FewLayer {
     int *counters, *status;
     int T, D, H_local, E, k, e_first, E_local, score, renorm, n_group, topk_group, is_bf16;
 };
-int64_t few_scratch_ints(int D);
+int few_scratch_ints();
 int64_t few_part_floats(int T);
 cudaError_t launch_few_layer(const FewLayer &f, cudaStream_t stream);
 

@@ -1260,7 +1260,7 @@ static int64_t few_ws_layout(const moe_config *c, char *base, moe::FewLayer *f) 
         off += align_up(bytes);
         return p;
     };
-    char *p_ctr = take(4 * moe::few_scratch_ints(c->D));
+    char *p_ctr = take(4 * moe::few_scratch_ints());
     char *p_lg = take((int64_t)c->T * c->E * 4);
     char *p_h = take((int64_t)c->T * c->k * c->H_local * 4);  // fp32, or two bf16
     char *p_part = take(4 * moe::few_part_floats(c->T));

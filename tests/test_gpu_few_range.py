@@ -50,3 +50,14 @@ def test_h_next_to_the_largest_bf16(moe):
     out, _ = _call(moe, c, dict(x=x, wg=z[0, :1].clone(), bias=None, w1=w1, w3=w3, w2=w2))
     assert out[0, 0].item() == (h - first) * 2.0 ** -112
     assert (out[0, 1:] == 0).all()
+
+
+def test_one_workspace_for_layers_of_different_width(moe):
+    """What one width leaves in the workspace is not taken for another one's counters."""
+    cfgs = [moe.Config(T=T, D=D, H_local=H, E=8, k=2, renorm=1, dtype=dt)
+            for T, D, H, dt in ((4, 4104, 2048, 1), (9, 264, 2048, 1), (3, 8, 4096, 0), (32, 1048, 1032, 1), (1, 2056, 4104, 1))]
+    ws = torch.zeros(max(moe.layer_few_workspace_size(c) for c in cfgs), dtype=torch.uint8, device="cuda")
+    t = [_inputs(moe, c) for c in cfgs]
+    want = [_call(moe, c, v)[0] for c, v in zip(cfgs, t)]
+    for i in (1, 0, 2, 3, 4, 0, 4, 2, 1, 3):
+        assert torch.equal(_call(moe, cfgs[i], t[i], ws)[0], want[i]), cfgs[i]
