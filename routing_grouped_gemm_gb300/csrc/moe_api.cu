@@ -1240,7 +1240,16 @@ MOE_EXPORT moe_status moe_get_device_status(const void *ws, size_t ws_bytes, moe
 // ---------------------------------------------------------------------
 // The layer for a few tokens: status | counters | logits | h | parts
 // ---------------------------------------------------------------------
-static moe_status few_supported(const moe_config *c) {
+static moe_status few_supported(const moe_config *cfg) {
+    if (!cfg) return arg_fail("config is NULL");
+    // nothing is permuted: whatever the layout's fields hold
+    moe_config own = *cfg;
+    own.layout = MOE_LAYOUT_CONTIGUOUS;
+    own.align_m = 1;
+    own.capacity = 0;
+    const moe_config *c = &own;
+    const moe_status st = validate(c);
+    if (st != MOE_OK) return st;
     if (c->T > moe::kFewMaxTokens)
         return arg_fail("moe_layer_forward_few: at most 32 tokens", MOE_ERR_UNSUPPORTED);
     // the kernel numbers (16 rows of out, pair, 2 KB of a row of w2), tiles and weight
@@ -1275,7 +1284,7 @@ static int64_t few_ws_layout(const moe_config *c, char *base, moe::FewLayer *f) 
 }
 
 MOE_EXPORT int64_t moe_layer_few_workspace_size(const moe_config *cfg) {
-    if (validate(cfg) != MOE_OK || few_supported(cfg) != MOE_OK) return -1;
+    if (few_supported(cfg) != MOE_OK) return -1;
     return few_ws_layout(cfg, nullptr, nullptr);
 }
 
@@ -1283,9 +1292,8 @@ MOE_EXPORT moe_status moe_layer_forward_few(const moe_config *cfg, const void *x
                                             const float *bias, const void *w1, const void *w3,
                                             const void *w2, void *out, void *ws, size_t ws_bytes,
                                             moe_stream_t stream) {
-    moe_status st = validate(cfg);
+    const moe_status st = few_supported(cfg);
     if (st != MOE_OK) return st;
-    if ((st = few_supported(cfg)) != MOE_OK) return st;
     if (!ws) return arg_fail("workspace is NULL", MOE_ERR_WORKSPACE);
     if (!aligned(ws, kAlign)) return arg_fail("workspace must be 256-byte aligned", MOE_ERR_WORKSPACE);
     if ((int64_t)ws_bytes < few_ws_layout(cfg, nullptr, nullptr))
