@@ -295,9 +295,9 @@ cudaError_t launch_combine_residual_norm(const ResidualNorm &r, const void *y_pe
                                          int64_t rows_alloc, const void *resid, void *y_out,
                                          void *resid_out, void *norm_out, int *status,
                                          cudaStream_t stream);
-// Gradient; `part`: 2 * residual_parts(T, D) * D floats for the CTAs' column sums
+// Gradient; `part`: 2 * residual_parts(T) * D floats for the CTAs' column sums
 // behind the gains' and a channel gate's gradients.
-int residual_parts(int T, int D);
+int residual_parts(int T);
 cudaError_t launch_residual_norm_backward(const ResidualNorm &r, const void *s, const void *y,
                                           const void *dresid_out, const void *dnorm_out,
                                           void *dresid, void *dy, float *dpost, void *dgate,

@@ -1432,7 +1432,7 @@ MOE_EXPORT moe_status moe_combine_residual_norm(
 
 MOE_EXPORT int64_t moe_residual_workspace_size(const moe_residual_config *rc) {
     if (validate_residual(rc) != MOE_OK) return -1;
-    return align_up((int64_t)2 * 4 * moe::residual_parts(rc->T, rc->D) * rc->D);
+    return align_up((int64_t)2 * 4 * moe::residual_parts(rc->T) * rc->D);
 }
 
 MOE_EXPORT moe_status moe_residual_norm_backward(

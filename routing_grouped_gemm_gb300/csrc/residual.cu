@@ -279,12 +279,11 @@ template <bool BF16, int NV> struct Ring {
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
     }
     __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-    // the oldest of `depth` committed rows is there
+    // the oldest of `depth` (2 or 3) committed rows is there
     __device__ __forceinline__ void wait() {
         switch (depth) {
         case 2: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-        case 3: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-        default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+        default: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
         }
         if (!BF16) __syncwarp();
     }
@@ -1059,6 +1058,8 @@ struct GradientShape {
 
 namespace {
 
+constexpr int kMaxParts = 4 * 152;  // of the column sums: what a workspace has room for
+
 // A row per warp up to 512 columns, else per CTA, with as few vectors a thread as
 // 256 threads allow (4096 x 2048: one 22.9 us, two 25.0).  Two rows in the ring
 // where a thread has two vectors, else three (16384 x 4096: 133 us with two, 145
@@ -1088,13 +1089,13 @@ GradientShape gradient_shape(int T, int D, int is_bf16, int gate_kind, bool drop
         per_sm = 1;
     }
     const int rows = g.warp ? 8 : 1;  // at a time in a CTA
-    g.ctas = std::min((T + rows - 1) / rows, 152 * per_sm);
+    g.ctas = std::min((T + rows - 1) / rows, std::min(sm_count() * per_sm, kMaxParts));
     return g;
 }
 
 }  // namespace
 
-int residual_parts(int T, int D) { return std::min(T, 4 * 152); }
+int residual_parts(int T) { return std::min(T, kMaxParts); }
 
 cudaError_t launch_residual_norm_backward(const ResidualNorm &r, const void *s, const void *y,
                                           const void *dresid_out, const void *dnorm_out,
