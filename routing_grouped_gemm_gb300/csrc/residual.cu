@@ -1089,7 +1089,7 @@ GradientShape gradient_shape(int T, int D, int is_bf16, int gate_kind, bool drop
         per_sm = 1;
     }
     const int rows = g.warp ? 8 : 1;  // at a time in a CTA
-    g.ctas = std::min((T + rows - 1) / rows, std::min(sm_count() * per_sm, kMaxParts));
+    g.ctas = std::min(T / rows + (T % rows != 0), std::min(sm_count() * per_sm, kMaxParts));
     return g;
 }
 

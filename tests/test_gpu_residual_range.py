@@ -7,7 +7,8 @@ holds at any scale) plus half a step of the output's type.
 import pytest
 import torch
 
-from test_gpu_residual_norm import GATES, _case, _check_gradient, _forward, _gradient, _keep, moe  # noqa: F401
+from test_gpu_residual_norm import (GATES, _case, _check_forward, _check_gradient, _forward, _gradient, _keep,
+                                    moe)  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -126,3 +127,28 @@ def test_combine_dropped_element(moe, dtype):
         return out
     got = call(t["gate"].masked_fill((_keep(rc, t) == 0).cuda(), float("inf")))
     assert all(torch.equal(a, b) for a, b in zip(got, call(t["gate"])))
+
+
+def test_the_most_rows(moe):
+    """2^31 - 1 rows, as many as a config can say: the norm alone and its gradient."""
+    T, D = 2 ** 31 - 1, 8
+    if torch.cuda.mem_get_info()[0] < 90e9:
+        pytest.skip("two tensors of 34 GB")
+    rc = moe.ResidualConfig(T=T, D=D)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    s, d = (torch.zeros(T, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    pre = torch.randn(D, generator=g, device="cuda").bfloat16()
+    rows = [slice(0, 40), slice(1 << 30, (1 << 30) + 40), slice(T - 41, T)]
+    for r in rows:
+        s[r].normal_(generator=g)
+        d[r].normal_(generator=g)
+    few = [torch.cat([v[r] for r in rows]) for v in (s, d)]
+    small = moe.ResidualConfig(T=len(few[0]), D=D)
+    t = dict(resid=few[0], y=None, post=None, gate=None, pre=pre, rng=None)
+    dpre = torch.empty(D, device="cuda")
+    moe.moe_residual_norm_backward(rc, s, None, None, None, pre, None, None, d, d, None, None, None, dpre,
+                                   moe.alloc_residual_workspace(rc))
+    got = dict(dresid=torch.cat([d[r] for r in rows]), dy=None, dpost_gain=None, dgate=None, dpre_gain=dpre)
+    _check_gradient(small, t, "none", None, few[1], got)
+    moe.moe_residual_norm(rc, s, None, None, None, pre, None, None, d)
+    _check_forward(small, t, "none", None, torch.cat([d[r] for r in rows]))
