@@ -444,9 +444,7 @@ residual_norm_row_kernel(const ForwardArgs a) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) y[i][e] = y[i][e] * r1 * g[e];
                 }
-                uint32_t bits = 0xffu;
                 if (a.drop.cut) {
-                    bits = keep_bits(base + v, a.drop.cut, seed, offset);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) y[i][e] *= a.drop.scale;
                 }
@@ -456,9 +454,14 @@ residual_norm_row_kernel(const ForwardArgs a) {
                     for (int e = 0; e < 8; ++e) y[i][e] *= g[e];
                 }
 #pragma unroll
-                for (int e = 0; e < 8; ++e)  // nothing of a dropped element, be it infinite
-                    s[i][e] = fmaf(a.res_scale, s[i][e],
-                                   bits >> e & 1u ? a.branch_scale * (gt * y[i][e]) : 0.f);
+                for (int e = 0; e < 8; ++e) y[i][e] = a.branch_scale * (gt * y[i][e]);
+                if (a.drop.cut) {  // last: nothing of a dropped element, be it infinite
+                    const uint32_t bits = keep_bits(base + v, a.drop.cut, seed, offset);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[i][e] = bits >> e & 1u ? y[i][e] : 0.f;
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s[i][e] = fmaf(a.res_scale, s[i][e], y[i][e]);
                 store8<BF16>(a.resid_out, base + v, s[i]);
             }
         }
@@ -828,10 +831,11 @@ residual_norm_backward_kernel(const BackwardArgs a) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) ge[e] = kept(ge[e], bits[i], e);
             }
-            f2 dg[4];
+            f2 dg[4], yr[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const f2 sr = mul2(s[e], r2_2), yr = mul2(y[e], g_2);
+                const f2 sr = mul2(s[e], r2_2);
+                yr[e] = mul2(y[e], g_2);
                 const f2 ds = fma2(sr, c_2, fma2(mul2(n[e], w[e]), r2_2, d[e]));
                 P[i][e] = fma2(n[e], sr, P[i][e]);
                 f2 k = drops ? kept(ds, bits[i], e) : ds;
@@ -839,10 +843,13 @@ residual_norm_backward_kernel(const BackwardArgs a) {
                     dg[e] = mul2(mul2(k, coef[i][e]), mul2(y[e], r1_2));
                     k = mul2(k, ge[e]);
                 }
-                G[i][e] = fma2(k, yr, G[i][e]);
+                G[i][e] = fma2(k, yr[e], G[i][e]);
                 d[e] = mul2(ds, res_2);
-                const f2 dv = mul2(mul2(k, coef[i][e]), g_2);
-                y[e] = a.post ? fma2(yr, c1_2, dv) : dv;  // no mean without a norm, whatever y holds
+                y[e] = mul2(mul2(k, coef[i][e]), g_2);
+            }
+            if (a.post) {  // no mean without a norm, whatever y holds
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = fma2(yr[e], c1_2, y[e]);
             }
             store8<BF16>(a.dresid, base + v, d);
             if (branch) store8<BF16>(a.dy, base + v, y);
