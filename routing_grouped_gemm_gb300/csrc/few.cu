@@ -3,7 +3,7 @@
 //   key = x Wg^T + b, top-k and weights w;  h_j = SiLU(w1_e x) * (w3_e x);
 //   out[t] = sum_j w_j (w2_e h_j),  e = the token's j-th expert.
 //
-// With T <= 32 tokens every weight of a chosen expert is used for a handful of
+// With T <= 32 tokens a weight of a chosen expert is mostly used for a handful of
 // rows, so the layer is bound by streaming the chosen experts' weights from HBM
 // (3 D H values each), and by the latency of whatever stands before that stream.
 // Launched as five steps, the steps' launches and tails cost about as much as
@@ -36,20 +36,26 @@
 // fp32 layers use the same tiles with fused multiply-adds.
 //
 // Measured (GB300, bf16): 16 tokens over 256 experts of 7168 x 2048, 9.0 GB of
-// weights, 1.22-1.28 ms (7.0-7.4 TB/s, the copy rate is 6.8); 8 tokens of the
-// fine-grained layer, 0.60 GB, 103-108 us (5.6-5.9 TB/s); one token of it, 104 MB,
-// 32.9 us, of which the stream's floor is 15.3.  The rest is latency: keys 2 us,
+// weights, 1.24-1.29 ms (7.0-7.3 TB/s, the copy rate is 6.8); 8 tokens of the
+// fine-grained layer, 0.60 GB, 108-110 us (5.5-5.6 TB/s); one token of it, 104 MB,
+// 33.0 us, of which the stream's floor is 15.3.  The rest is latency: keys 2 us,
 // barrier 1.3, top-k 2.4, entries 1.2, 4-6 until the first weights are there
 // (address translation and DRAM), the second barrier 2, and all of it run once, so
-// that its instructions come from L2.  (The layer's own calls take 63 us.)
+// that its instructions come from L2.  (The layer's own calls take 64 us.)
+// An expert with more pairs than an entry holds is streamed again, and GEMM1 runs
+// an entry's tiles before the next entry, so from HBM where its weights are large:
+// 8 experts of 4096 x 14336, two a token, take 416 us for 8 tokens, 505 for 12 and
+// 810 for 32, where the layer's own calls take 430, 468 and 471.
 //
 // Rounding: keys, weights, both products' sums and the sum over experts are
 // fp32; out is rounded once.  h of a bf16 layer goes to the second product as the
 // sum of two bf16 (16 significant bits): four pairs' second parts take the columns
-// that an entry of four leaves free, so they cost no instruction of the product,
-// and out is off by its own rounding alone (h in one bf16: 0.0023-0.0027 of the
-// RMS against 64 bits, in two 0.0017).  Every sum has a fixed order for a given grid, so results do not change
-// from run to run.
+// that an entry of four leaves free, and out is off by its own rounding alone (h
+// in one bf16: 0.0023-0.0027 of the RMS against 64 bits, in two 0.0017).  That
+// holds an entry to four pairs, in the first product too: 32 tokens on 13 of 20
+// experts of 1048 x 424 take 43.5 us, with entries of eight and h in one bf16 they
+// took 33.4.  Where w2 is infinite the first part alone counts.  Every sum has a
+// fixed order for a given grid, so results do not change from run to run.
 #include <algorithm>
 
 #include <stdlib.h>
@@ -479,7 +485,8 @@ few_layer_kernel(const FewParams p) {
     // Both products run the same loops (the second finds them in the instruction
     // cache): a SEGMENT is a tile's rows against one entry, nc chunks long.  Where a
     // row is short, fewer than all warps share it and the groups of `ks` warps take
-    // different segments (24 tokens, D = 160, H = 880: 39 us, with all 8 on a row 47).
+    // different segments (24 tokens, D = 160, H = 880: 39 us when
+    // this was chosen, with all 8 on a row 47).
     //   GEMM1: tile = 8 hidden units; the U nt tiles over all CTAs' groups, tiles of
     //          an entry running fastest
     //   GEMM2: tile = 16 rows of out; this CTA's part of the line of chunks, entries

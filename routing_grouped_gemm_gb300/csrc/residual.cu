@@ -15,11 +15,14 @@
 // dy out), and close behind by instructions: at 2 bytes an element the copy rate
 // leaves about 20 per element and warp lane.  A row's values stay on the SM
 // between its sums, and the next row is on its way meanwhile.  Measured on GB300
-// (bf16, of the copy rate): 16384 x 4096 forward 86.5 us (92%), its gradient 132
-// (90%), gradient of 8192 x 7168 113.6 (92%); dropout's generator adds 13 us to
-// 44 at 16384 x 2048; fp32 8192 x 2048 forward 45.9 (86%), gradient 70.5 (84%).  Behind the combine (16384 x 2048, 6 rows a token) 118 us
-// (84%): a row's loads wait for its places, and more of them in flight per thread
+// (bf16, of the copy rate; inputs larger than L2): 16384 x 4096 forward 86.4-87.5 us
+// (91%), its gradient 134 (88%), gradient of 8192 x 7168 115.8 (90%); dropout's
+// generator adds 12 us to 45 at 16384 x 2048; fp32 8192 x 2048 forward 47 (84%),
+// gradient 74 (80%).  Behind the combine (16384 x 2048, 6 rows a token) 119 us
+// (83%): a row's loads wait for its places, and more of them in flight per thread
 // or in a shared ring measured slower (8192 x 4096, 4 rows: 101 us, a ring 134).
+// The order of a row's sums and products goes by the kernel and its threads, so
+// by T and D: among more rows the same row may differ in its last bits.
 #include <algorithm>
 
 #include "common.cuh"
@@ -678,7 +681,10 @@ struct BackwardArgs {
 // A row per CTA (WARP: per warp, narrow rows), rows over the grid, in a Ring from
 // which each thread reads its columns twice, before and behind the reduction
 // (registers are short).  Rows too wide for two in shared memory are read from global memory
-// instead, the second time from L2 (RING false).
+// instead, the second time from L2 (RING false: fp32 from D = 6664, or 5640 with a
+// gate for every element, and all from 8200).  One CTA per SM, nothing copied
+// ahead and registers spilled: 4096 x 7168 fp32 298 us (floor 104), 4096 x 12288
+// bf16 289 (89), 2048 x 24576 bf16 537 (89).
 //
 // The kernel is as much bound by instructions as by bytes (per vector of 8 about
 // 100 to unpack five operands twice, 80 of arithmetic two values at a time), so
@@ -1068,11 +1074,11 @@ namespace {
 constexpr int kMaxParts = 4 * 152;  // of the column sums: what a workspace has room for
 
 // A row per warp up to 512 columns, else per CTA, with as few vectors a thread as
-// 256 threads allow (4096 x 2048: one 22.9 us, two 25.0).  Two rows in the ring
-// where a thread has two vectors, else three (16384 x 4096: 133 us with two, 145
-// with three; 16384 x 2048: 70.9 and 67.3): more in flight than DRAM needs costs.
+// 256 threads allow (4096 x 2048: one 24.7 us, two 27.1).  Two rows in the ring
+// where a thread has two vectors, else three (16384 x 4096: 134.5 us with two, 147
+// with three; 16384 x 2048: 73.8 and 70.5): more in flight than DRAM needs costs.
 // With dropout a row's instructions bound it, and over many rows two vectors a
-// thread share them (16384 x 2048: 84.6 us, one 97.1; 4096 rows: 32.6 and 31.1).
+// thread share them (16384 x 2048: 86.1 us, one 100.8; 4096 rows: 34.5 and 32.0).
 GradientShape gradient_shape(int T, int D, int is_bf16, int gate_kind, bool drops) {
     GradientShape g = {};
     const int V = D / 8;

@@ -152,3 +152,14 @@ def test_the_most_rows(moe):
     _check_gradient(small, t, "none", None, few[1], got)
     moe.moe_residual_norm(rc, s, None, None, None, pre, None, None, d)
     _check_forward(small, t, "none", None, torch.cat([d[r] for r in rows]))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("gate", ["channel", "element"])
+@pytest.mark.parametrize("T,D", [(11003, 72), (7001, 392), (5003, 520), (1501, 4104), (331, 12296)])
+def test_gradient_in_place_over_many_rows(moe, T, D, gate, dtype):
+    """dresid over dnorm_out and dy over dresid_out, with later rows on their way while one is stored."""
+    rc, t, n = _case(moe, T, D, dtype, gate, p=0.1)
+    dso, dn = n(T, D), n(T, D)
+    want, got = _gradient(moe, rc, t, gate, dso, dn), _gradient(moe, rc, t, gate, dso, dn, in_place=True)
+    assert all(torch.equal(got[k], want[k]) for k in want)
